@@ -526,6 +526,102 @@ int eqtp_check_graph(int64_t N, int64_t E, const int32_t* row_ptr, const int32_t
  */
 int eqtp_set_debug(int on);
 
+/* ---------------------------------------------------------------------------
+ * Parts of a transformer block around the convolution: a norm, dropout and
+ * attention over the graph.  Features are [N, C, K] as above with any number
+ * of channels C >= 1 and lmax 0..6; K = 1 (lmax 0) is the ordinary layout of
+ * rows of width C.  Every one of them commutes with rotations: the norm
+ * scales whole degrees, dropout drops whole channels, and the attention's
+ * logits are inner products over all components of a head.
+ *
+ * Random numbers come from a counter: rng points to two int64 words on the
+ * device, a seed and an offset, read when the kernel runs (so a captured
+ * graph sees the values of the moment).  Channel c of node n has number
+ * j = n C + c; its random word is word j mod 4 of the ten-round Philox 4x32
+ * block j / 4 (Salmon, Moraes, Dror and Shaw, "Parallel random numbers: as
+ * easy as 1, 2, 3", 2011) with key = seed (low word first) and counter =
+ * (block, offset) (low words first).  The channel is kept if that word is at
+ * least floor(p 2^32).  The mask is a function of (seed, offset, n, c) alone
+ * and is never stored: the backward pass makes it again.  Use another offset
+ * (or seed) for each place and step.
+ *
+ * Buffers need the alignment of their elements only.  Outputs must not
+ * overlap inputs or each other unless said otherwise.
+ * ------------------------------------------------------------------------ */
+
+typedef struct eqtp_norm_desc {
+  int32_t struct_size; /* = sizeof(eqtp_norm_desc) */
+  int32_t lmax;        /* 0..6 */
+  int32_t C;           /* channels, C K <= 16384 (more: EQTP_EUNSUPPORTED) */
+  int32_t x_dtype;     /* EQTP_F32 or EQTP_BF16: x, residual, total and the gradients of all three */
+  int32_t out_dtype;   /* EQTP_F32 or EQTP_BF16: out and its gradient */
+  float eps;           /* > 0, finite */
+  double p;            /* dropout probability, 0 <= p < 1; eqtp_layer_norm takes 0 only */
+} eqtp_norm_desc;
+
+/*
+ * Layer norm by degree, each node by itself:
+ *   z = x; degree 0: centred, zc[c] = x[c] - mean_c x[c]; degree l > 0: zc = x;
+ *   r_l = 1 / sqrt(mean over the C (2l+1) values of zc^2 + eps);
+ *   out[n, c, l m] = zc[c, l m] r_l weight[l, c]  (+ bias[c] for l = 0).
+ * At lmax 0 this is the layer norm of rows of width C.
+ *   x      [N, C, K] (x_dtype);  out [N, C, K] (out_dtype), fully overwritten.
+ *   weight [lmax+1, C] fp32, or NULL (ones);  bias [C] fp32, or NULL (none).
+ *   stats  [N, lmax+2] fp32 out: mean, r_0, .., r_lmax of each node, what
+ *          eqtp_layer_norm_backward needs; or NULL.
+ * Sums are held in fp32 (the variance from centred values).  A NaN or an
+ * infinity spoils its own node (or degree) only.  0 <= N < 2^31.
+ */
+int eqtp_layer_norm(const eqtp_norm_desc* d, int64_t N, const void* x, const float* weight, const float* bias,
+                    void* out, float* stats, void* stream);
+
+/*
+ * The residual branch's end and the next norm in one pass:
+ *   total = residual + keep x / (1 - p)   (rounded to x_dtype once),
+ *   out   = eqtp_layer_norm(total),
+ * with the same bits as eqtp_dropout followed by eqtp_layer_norm.
+ *   x, residual, total [N, C, K] (x_dtype); rng: see above (NULL allowed when
+ *   p = 0); the rest as for eqtp_layer_norm.
+ */
+int eqtp_dropout_add_norm(const eqtp_norm_desc* d, int64_t N, const void* x, const void* residual,
+                          const int64_t* rng, const float* weight, const float* bias, void* total, void* out,
+                          float* stats, void* stream);
+
+/*
+ * Gradients of both.  With zhat = zc r_l and a = weight grad_out:
+ *   grad_residual = grad_total + r_l (a - [l = 0] mean_c a - zhat mean_l(a zhat)),
+ *   grad_x        = keep grad_residual / (1 - p),
+ *   grad_weight[l, c] = sum_{n, m} grad_out zhat,  grad_bias[c] = sum_n grad_out[n, c, 0].
+ *   total      [N, C, K] (x_dtype): eqtp_dropout_add_norm's total, or
+ *              eqtp_layer_norm's x;  stats: as written by the forward call.
+ *   grad_out   [N, C, K] (out_dtype);  weight as in the forward call.
+ *   grad_total [N, C, K] (x_dtype): what reaches total by other ways; or NULL.
+ *   grad_residual, grad_x [N, C, K] (x_dtype) out: each may be NULL.  For
+ *              eqtp_layer_norm grad_residual is x's gradient.  grad_x needs
+ *              rng (the forward call's values) unless p = 0.
+ *   grad_weight [lmax+1, C], grad_bias [C] fp32 out: each may be NULL.  N = 0
+ *              writes zeros.  Summed in a fixed order: the same from call to call.
+ *   workspace  eqtp_layer_norm_workspace_bytes(d, N) bytes, 16-byte aligned
+ *              (may be NULL when neither grad_weight nor grad_bias is asked).
+ */
+int64_t eqtp_layer_norm_workspace_bytes(const eqtp_norm_desc* d, int64_t N);
+int eqtp_layer_norm_backward(const eqtp_norm_desc* d, int64_t N, const void* total, const float* stats,
+                             const float* weight, const void* grad_out, const void* grad_total, const int64_t* rng,
+                             void* grad_residual, void* grad_x, float* grad_weight, float* grad_bias,
+                             void* workspace, int64_t workspace_bytes, void* stream);
+
+/*
+ * Dropout of whole channels, with an optional residual sum:
+ *   out = residual + keep x / (1 - p)   (residual NULL: keep x / (1 - p)).
+ * The gradient of x is the same call on the gradient (no residual) with the
+ * same rng.  A dropped channel contributes exactly 0, whatever x holds.
+ *   x, residual, out [N, C, K] of dtype EQTP_F32 or EQTP_BF16; out may be x
+ *   or residual.  0 <= p < 1; rng may be NULL when p = 0.  0 <= N < 2^31,
+ *   C >= 1, N C K < 2^61.
+ */
+int eqtp_dropout(int64_t N, int C, int lmax, int dtype, double p, const void* x, const void* residual,
+                 const int64_t* rng, void* out, void* stream);
+
 /*
  * Test-only: walks the dst-sorted edges with exactly the row -> wave ->
  * lane -> step schedule that eqtp_conv_fused uses for the given (C, lmax,

@@ -753,6 +753,162 @@ const char* eqtp_status_string(int status) {
   }
 }
 
+}  // extern "C"
+
+namespace {
+
+constexpr int kMaxNormRow = 16384;  // elements of a node that the norm's kernels hold in registers
+
+bool dtype_ok(int t) { return t == EQTP_F32 || t == EQTP_BF16; }
+bool aligned_as(const void* p, int dtype) {
+  return (reinterpret_cast<uintptr_t>(p) & (dtype == EQTP_BF16 ? 1u : 3u)) == 0;
+}
+bool aligned8(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
+bool prob_ok(double p) { return p >= 0.0 && p < 1.0; }  // false for NaN
+uint32_t drop_threshold(double p) { return (uint32_t)(p * 4294967296.0); }
+
+int norm_check(const eqtp_norm_desc* d, int64_t N) {
+  if (!d || d->struct_size != (int32_t)sizeof(eqtp_norm_desc)) return EQTP_EINVAL;
+  if (d->lmax < 0 || d->C <= 0 || !dtype_ok(d->x_dtype) || !dtype_ok(d->out_dtype)) return EQTP_EINVAL;
+  if (!(d->eps > 0.0f) || d->eps > 3.4028235e38f || !prob_ok(d->p)) return EQTP_EINVAL;
+  if (N < 0 || N > kMaxIndex) return EQTP_EINVAL;
+  if (d->lmax > eqtp::kSo2MaxL || (int64_t)d->C * eqtp::num_comp(d->lmax) > kMaxNormRow) return EQTP_EUNSUPPORTED;
+  return EQTP_OK;
+}
+
+eqtp::NormArgs norm_args(const eqtp_norm_desc* d, int64_t N, const void* x, const float* weight, const float* bias,
+                         void* out, float* stats, void* stream) {
+  eqtp::NormArgs a = {};
+  a.N = N;
+  a.C = d->C;
+  a.K = eqtp::num_comp(d->lmax);
+  a.lmax = d->lmax;
+  a.x_bf16 = d->x_dtype == EQTP_BF16;
+  a.out_bf16 = d->out_dtype == EQTP_BF16;
+  a.eps = d->eps;
+  a.x = x;
+  a.scale = 1.0f;
+  a.weight = weight;
+  a.bias = bias;
+  a.out = out;
+  a.stats = stats;
+  a.stream = (hipStream_t)stream;
+  return a;
+}
+
+}  // namespace
+
+extern "C" {
+
+int eqtp_layer_norm(const eqtp_norm_desc* d, int64_t N, const void* x, const float* weight, const float* bias,
+                    void* out, float* stats, void* stream) {
+  const int rc = norm_check(d, N);
+  if (rc != EQTP_OK) return rc;
+  if (d->p != 0.0) return EQTP_EINVAL;
+  if (N == 0) return EQTP_OK;
+  if (!x || !out || !aligned_as(x, d->x_dtype) || !aligned_as(out, d->out_dtype)) return EQTP_EINVAL;
+  if (!aligned4(weight) || !aligned4(bias) || !aligned4(stats)) return EQTP_EINVAL;
+  return status_of(eqtp::launch_norm(norm_args(d, N, x, weight, bias, out, stats, stream)));
+}
+
+int eqtp_dropout_add_norm(const eqtp_norm_desc* d, int64_t N, const void* x, const void* residual,
+                          const int64_t* rng, const float* weight, const float* bias, void* total, void* out,
+                          float* stats, void* stream) {
+  const int rc = norm_check(d, N);
+  if (rc != EQTP_OK) return rc;
+  if (N == 0) return EQTP_OK;
+  if (!x || !residual || !total || !out || !aligned_as(x, d->x_dtype) || !aligned_as(residual, d->x_dtype) ||
+      !aligned_as(total, d->x_dtype) || !aligned_as(out, d->out_dtype))
+    return EQTP_EINVAL;
+  if (!aligned4(weight) || !aligned4(bias) || !aligned4(stats)) return EQTP_EINVAL;
+  if (d->p > 0.0 && (!rng || !aligned8(rng))) return EQTP_EINVAL;
+  eqtp::NormArgs a = norm_args(d, N, x, weight, bias, out, stats, stream);
+  a.residual = residual;
+  a.total = total;
+  if (d->p > 0.0) {
+    a.rng = rng;
+    a.thr = drop_threshold(d->p);
+    a.scale = (float)(1.0 / (1.0 - d->p));
+  }
+  return status_of(eqtp::launch_norm(a));
+}
+
+int64_t eqtp_layer_norm_workspace_bytes(const eqtp_norm_desc* d, int64_t N) {
+  const int rc = norm_check(d, N);
+  if (rc != EQTP_OK) return -rc;
+  return eqtp::norm_workspace_floats(N, d->C, d->lmax) * 4;
+}
+
+int eqtp_layer_norm_backward(const eqtp_norm_desc* d, int64_t N, const void* total, const float* stats,
+                             const float* weight, const void* grad_out, const void* grad_total, const int64_t* rng,
+                             void* grad_residual, void* grad_x, float* grad_weight, float* grad_bias,
+                             void* workspace, int64_t workspace_bytes, void* stream) {
+  const int rc = norm_check(d, N);
+  if (rc != EQTP_OK) return rc;
+  if (!grad_residual && !grad_x && !grad_weight && !grad_bias && N > 0) return EQTP_EINVAL;
+  if (!aligned4(grad_weight) || !aligned4(grad_bias)) return EQTP_EINVAL;
+  if (N > 0) {
+    if (!total || !stats || !grad_out || !aligned_as(total, d->x_dtype) || !aligned4(stats) ||
+        !aligned_as(grad_out, d->out_dtype) || !aligned4(weight) || !aligned_as(grad_total, d->x_dtype) ||
+        !aligned_as(grad_residual, d->x_dtype) || !aligned_as(grad_x, d->x_dtype))
+      return EQTP_EINVAL;
+    if (grad_x && d->p > 0.0 && (!rng || !aligned8(rng))) return EQTP_EINVAL;
+  }
+  const bool sums = grad_weight || grad_bias;
+  if (sums && (!workspace || !aligned16(workspace) ||
+               workspace_bytes < eqtp::norm_workspace_floats(N, d->C, d->lmax) * 4))
+    return EQTP_EINVAL;
+  eqtp::NormGradArgs a = {};
+  a.N = N;
+  a.C = d->C;
+  a.K = eqtp::num_comp(d->lmax);
+  a.lmax = d->lmax;
+  a.x_bf16 = d->x_dtype == EQTP_BF16;
+  a.out_bf16 = d->out_dtype == EQTP_BF16;
+  a.total = total;
+  a.stats = stats;
+  a.weight = weight;
+  a.gout = grad_out;
+  a.gtotal = grad_total;
+  a.scale = 1.0f;
+  if (grad_x && d->p > 0.0) {
+    a.rng = rng;
+    a.thr = drop_threshold(d->p);
+    a.scale = (float)(1.0 / (1.0 - d->p));
+  }
+  a.gres = grad_residual;
+  a.gx = grad_x;
+  a.gw = grad_weight;
+  a.gb = grad_bias;
+  a.ws = static_cast<float*>(workspace);
+  a.stream = (hipStream_t)stream;
+  return status_of(eqtp::launch_norm_grad(a));
+}
+
+int eqtp_dropout(int64_t N, int C, int lmax, int dtype, double p, const void* x, const void* residual,
+                 const int64_t* rng, void* out, void* stream) {
+  if (lmax < 0 || C <= 0 || N < 0 || N > kMaxIndex || !dtype_ok(dtype) || !prob_ok(p)) return EQTP_EINVAL;
+  if (lmax > eqtp::kSo2MaxL) return EQTP_EUNSUPPORTED;
+  if (N * C > (int64_t(1) << 62) / (2 * eqtp::num_comp(lmax))) return EQTP_EINVAL;
+  if (N == 0) return EQTP_OK;
+  if (!x || !out || !aligned_as(x, dtype) || !aligned_as(residual, dtype) || !aligned_as(out, dtype))
+    return EQTP_EINVAL;
+  if (p > 0.0 && (!rng || !aligned8(rng))) return EQTP_EINVAL;
+  eqtp::DropArgs a = {};
+  a.N = N;
+  a.C = C;
+  a.K = eqtp::num_comp(lmax);
+  a.bf16 = dtype == EQTP_BF16;
+  a.x = x;
+  a.residual = residual;
+  a.rng = p > 0.0 ? rng : nullptr;
+  a.thr = drop_threshold(p);
+  a.scale = (float)(1.0 / (1.0 - p));
+  a.out = out;
+  a.stream = (hipStream_t)stream;
+  return status_of(eqtp::launch_dropout(a));
+}
+
 int eqtp_check_graph(int64_t N, int64_t E, const int32_t* row_ptr, const int32_t* src, const int32_t* dst,
                      const float* vec, int32_t* report, void* stream) {
   if (N < 0 || E < 0 || N > kMaxIndex || E > kMaxIndex) return EQTP_EINVAL;

@@ -60,6 +60,62 @@ struct BwdArgs {
   const int32_t* perm = nullptr;
 };
 
+// layer norm by degree; with total: of residual + dropout(x), written there
+struct NormArgs {
+  int64_t N;
+  int C, K, lmax;
+  bool x_bf16, out_bf16;
+  float eps;
+  const void* x;
+  const void* residual;   // with total
+  const int64_t* rng;     // nullptr: nothing is dropped
+  uint32_t thr;           // floor(p 2^32)
+  float scale;            // 1 / (1 - p)
+  const float* weight;    // or nullptr
+  const float* bias;      // or nullptr
+  void* total;            // or nullptr
+  void* out;
+  float* stats;           // or nullptr
+  hipStream_t stream;
+};
+
+struct NormGradArgs {
+  int64_t N;
+  int C, K, lmax;
+  bool x_bf16, out_bf16;
+  const void* total;
+  const float* stats;
+  const float* weight;    // or nullptr
+  const void* gout;
+  const void* gtotal;     // or nullptr
+  const int64_t* rng;     // nullptr: nothing was dropped
+  uint32_t thr;
+  float scale;
+  void* gres;             // or nullptr
+  void* gx;               // or nullptr
+  float* gw;              // or nullptr
+  float* gb;              // or nullptr
+  float* ws;              // norm_workspace_floats floats when gw or gb is given
+  hipStream_t stream;
+};
+
+struct DropArgs {
+  int64_t N;
+  int C, K;
+  bool bf16;
+  const void* x;
+  const void* residual;   // or nullptr
+  const int64_t* rng;     // nullptr: nothing is dropped
+  uint32_t thr;
+  float scale;
+  void* out;
+  hipStream_t stream;
+};
+
+hipError_t launch_norm(const NormArgs& a);
+int64_t norm_workspace_floats(int64_t N, int C, int lmax);
+hipError_t launch_norm_grad(const NormGradArgs& a);
+hipError_t launch_dropout(const DropArgs& a);
 hipError_t launch_sh(const float* vec, int64_t E, int lmax, float* Y, hipStream_t stream);
 hipError_t launch_conv_node(const ConvArgs& a);   // sorted edges, fixed weights, matrix cores
 hipError_t launch_conv_edge(const ConvArgs& a);   // any order / weights, vector ALUs

@@ -1,0 +1,56 @@
+// philox.hpp -- the counter-based random words of dropout: Philox 4x32 with
+// ten rounds (Salmon, Moraes, Dror and Shaw, "Parallel random numbers: as
+// easy as 1, 2, 3", 2011).  One block of four 32-bit words for a 128-bit
+// counter (block, offset) under a 64-bit key (seed); channel number j uses
+// word j mod 4 of block j / 4.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include <stdint.h>
+
+namespace eqtp {
+
+struct DropState {
+  uint32_t k0, k1, c2, c3;  // key, and the counter's high half
+  uint32_t thr;             // keep if word >= thr = floor(p 2^32)
+  float scale;              // 1 / (1 - p)
+};
+
+__device__ __forceinline__ DropState drop_state(const int64_t* __restrict__ rng, uint32_t thr, float scale) {
+  const uint64_t seed = (uint64_t)rng[0], off = (uint64_t)rng[1];
+  return {(uint32_t)seed, (uint32_t)(seed >> 32), (uint32_t)off, (uint32_t)(off >> 32), thr, scale};
+}
+
+// One round multiplies words 0 and 2 by the method's constants and crosses the
+// halves of the products over; the key moves by two Weyl constants a round.
+__device__ __forceinline__ void philox_words(const DropState& s, uint64_t block, uint32_t (&w)[4]) {
+  uint32_t c0 = (uint32_t)block, c1 = (uint32_t)(block >> 32), c2 = s.c2, c3 = s.c3, k0 = s.k0, k1 = s.k1;
+#pragma unroll
+  for (int r = 0; r < 10; ++r) {
+    const uint64_t a = (uint64_t)0xD2511F53u * c0, b = (uint64_t)0xCD9E8D57u * c2;
+    c0 = (uint32_t)(b >> 32) ^ c1 ^ k0;
+    c2 = (uint32_t)(a >> 32) ^ c3 ^ k1;
+    c1 = (uint32_t)b;
+    c3 = (uint32_t)a;
+    k0 += 0x9E3779B9u;
+    k1 += 0xBB67AE85u;
+  }
+  w[0] = c0, w[1] = c1, w[2] = c2, w[3] = c3;
+}
+
+// Bit i set: channel 4 block + i is kept.
+__device__ __forceinline__ uint32_t keep_nibble(const DropState& s, uint64_t block) {
+  uint32_t w[4];
+  philox_words(s, block, w);
+  return (uint32_t)(w[0] >= s.thr) | (uint32_t)(w[1] >= s.thr) << 1 | (uint32_t)(w[2] >= s.thr) << 2 |
+         (uint32_t)(w[3] >= s.thr) << 3;
+}
+
+// The value of a kept or dropped x beside its residual; the norm's kernels and
+// the dropout kernel share this expression, so their sums have the same bits.
+__device__ __forceinline__ float drop_add(bool keep, float x, float scale, float residual) {
+  return keep ? fmaf(x, scale, residual) : residual;
+}
+
+}  // namespace eqtp

@@ -31,6 +31,8 @@ EXPORTED = ("eqtp_num_paths", "eqtp_path_table", "eqtp_sh", "eqtp_conv_fused", "
             "eqtp_conv_backward", "eqtp_conv_backward_by_source", "eqtp_edge_rows", "eqtp_sort_edges",
             "eqtp_sort_workspace_bytes", "eqtp_sort_edges_stable",
             "eqtp_linear", "eqtp_interaction_workspace_bytes", "eqtp_interaction",
+            "eqtp_layer_norm", "eqtp_dropout_add_norm", "eqtp_layer_norm_workspace_bytes",
+            "eqtp_layer_norm_backward", "eqtp_dropout",
             "eqtp_status_string", "eqtp_check_graph", "eqtp_set_debug", "eqtp_test_segment_probe")
 
 
@@ -51,6 +53,12 @@ class _InteractionDesc(ctypes.Structure):
     _fields_ = [("struct_size", ctypes.c_int32), ("lmax", ctypes.c_int32), ("C", ctypes.c_int32),
                 ("path_set", ctypes.c_int32), ("r_cut", ctypes.c_float), ("n_basis", ctypes.c_int32),
                 ("hidden", ctypes.c_int32), ("norm", ctypes.c_float)]
+
+
+class _NormDesc(ctypes.Structure):
+    _fields_ = [("struct_size", ctypes.c_int32), ("lmax", ctypes.c_int32), ("C", ctypes.c_int32),
+                ("x_dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("p", ctypes.c_double)]
 
 
 _lib = None
@@ -102,6 +110,16 @@ def load_library(path: str = LIB_PATH):
             lib.eqtp_interaction_workspace_bytes.restype = i64
             lib.eqtp_interaction.argtypes = [ctypes.POINTER(_InteractionDesc), i64, i64] + [vp] * 11 + [i64, vp]
             lib.eqtp_interaction.restype = i32
+            lib.eqtp_layer_norm.argtypes = [ctypes.POINTER(_NormDesc), i64] + [vp] * 6
+            lib.eqtp_layer_norm.restype = i32
+            lib.eqtp_dropout_add_norm.argtypes = [ctypes.POINTER(_NormDesc), i64] + [vp] * 9
+            lib.eqtp_dropout_add_norm.restype = i32
+            lib.eqtp_layer_norm_workspace_bytes.argtypes = [ctypes.POINTER(_NormDesc), i64]
+            lib.eqtp_layer_norm_workspace_bytes.restype = i64
+            lib.eqtp_layer_norm_backward.argtypes = [ctypes.POINTER(_NormDesc), i64] + [vp] * 11 + [i64, vp]
+            lib.eqtp_layer_norm_backward.restype = i32
+            lib.eqtp_dropout.argtypes = [i64, i32, i32, i32, ctypes.c_double] + [vp] * 5
+            lib.eqtp_dropout.restype = i32
             lib.eqtp_status_string.argtypes = [i32]
             lib.eqtp_status_string.restype = ctypes.c_char_p
             lib.eqtp_check_graph.argtypes = [i64, i64] + [vp] * 6
@@ -610,6 +628,180 @@ def eqtp_interaction(vec, src, row_ptr, h, W_up, W1, W2, W3, W_out, lmax: int, r
                                          _ptr(W_up), _ptr(W1), _ptr(W2), _ptr(W3), _ptr(W_out), _ptr(out),
                                          _ptr(workspace), workspace.numel(), _stream())
     _raise(rc, "eqtp_interaction")
+    return out
+
+
+def _rows(x, name, lmax):
+    """(element type code, N, C) of features [N, C, K], or [N, C] at lmax 0."""
+    import torch
+
+    code = EQTP_BF16 if x.dtype is torch.bfloat16 else EQTP_F32
+    _check(x, name, torch.bfloat16 if code == EQTP_BF16 else torch.float32)
+    if x.dim() == 3:
+        N, C, K = x.shape
+        if K != (lmax + 1) ** 2:
+            raise ValueError("%s has %d components, lmax %d needs %d" % (name, K, lmax, (lmax + 1) ** 2))
+    elif x.dim() == 2 and lmax == 0:
+        N, C = x.shape
+    else:
+        raise ValueError("%s must be [N, C, K] (or [N, C] at lmax 0)" % name)
+    return code, N, C
+
+
+def _check_rng(rng, p):
+    import torch
+
+    if p == 0.0:
+        return
+    if rng is None:
+        raise ValueError("p > 0 needs rng, an int64 tensor (seed, offset) on the GPU")
+    _check(rng, "rng", torch.int64, (2,))
+
+
+@functools.lru_cache(maxsize=256)
+def _norm_desc(lmax, C, x_dtype, out_dtype, eps, p):
+    # read by the library during a call only, so one instance per distinct descriptor is shared
+    d = _NormDesc(ctypes.sizeof(_NormDesc), lmax, C, x_dtype, out_dtype, eps, p)
+    need = load_library().eqtp_layer_norm_workspace_bytes(ctypes.byref(d), 0)  # checks the descriptor
+    if need < 0:
+        raise EqtpError(int(-need), "eqtp_norm_desc")
+    return ctypes.byref(d), d
+
+
+def _check_affine(weight, bias, lmax, C):
+    import torch
+
+    if weight is not None:
+        _check(weight, "weight", torch.float32, (lmax + 1, C))
+    if bias is not None:
+        _check(bias, "bias", torch.float32, (C,))
+
+
+def _torch_dtype(code):
+    import torch
+
+    if code not in (EQTP_F32, EQTP_BF16):
+        raise ValueError("out_dtype must be EQTP_F32 or EQTP_BF16")
+    return torch.bfloat16 if code == EQTP_BF16 else torch.float32
+
+
+def eqtp_layer_norm(x, lmax: int, weight=None, bias=None, eps: float = 1e-5, out_dtype: int = None, out=None,
+                    stats=None):
+    """out [N, C, K] = layer norm by degree of x (see include/eqtp.h); x float32 or bfloat16, [N, C, K] or, at
+    lmax 0, [N, C].  ``weight`` [lmax+1, C], ``bias`` [C] float32.  ``out_dtype``: EQTP_F32 or EQTP_BF16 (x's by
+    default).  ``stats``: a float32 [N, lmax+2] tensor to fill, for eqtp_layer_norm_backward."""
+    import torch
+
+    code, N, C = _rows(x, "x", lmax)
+    ocode = code if out_dtype is None else out_dtype
+    odt = _torch_dtype(ocode)
+    _check_affine(weight, bias, lmax, C)
+    d, _ = _norm_desc(lmax, C, code, ocode, float(eps), 0.0)
+    if out is None:
+        out = torch.empty(x.shape, dtype=odt, device=x.device)
+    else:
+        _check(out, "out", odt, x.shape)
+    if stats is not None:
+        _check(stats, "stats", torch.float32, (N, lmax + 2))
+    _raise(load_library().eqtp_layer_norm(d, N, _ptr(x), _ptr(weight), _ptr(bias), _ptr(out), _ptr(stats), _stream()),
+           "eqtp_layer_norm")
+    return out
+
+
+def eqtp_dropout_add_norm(x, residual, rng, p: float, lmax: int, weight=None, bias=None, eps: float = 1e-5,
+                          out_dtype: int = None, out=None, total=None, stats=None):
+    """(out, total): total = residual + dropout(x), out = eqtp_layer_norm(total), in one pass.  ``rng``: int64
+    (seed, offset) on the GPU, or None when p is 0.  The rest as for eqtp_layer_norm."""
+    import torch
+
+    code, N, C = _rows(x, "x", lmax)
+    _check(residual, "residual", x.dtype, x.shape)
+    ocode = code if out_dtype is None else out_dtype
+    odt = _torch_dtype(ocode)
+    p = float(p)
+    _check_rng(rng, p)
+    _check_affine(weight, bias, lmax, C)
+    d, _ = _norm_desc(lmax, C, code, ocode, float(eps), p)
+    if out is None:
+        out = torch.empty(x.shape, dtype=odt, device=x.device)
+    else:
+        _check(out, "out", odt, x.shape)
+    if total is None:
+        total = torch.empty_like(x)
+    else:
+        _check(total, "total", x.dtype, x.shape)
+    if stats is not None:
+        _check(stats, "stats", torch.float32, (N, lmax + 2))
+    rc = load_library().eqtp_dropout_add_norm(d, N, _ptr(x), _ptr(residual), _ptr(rng), _ptr(weight), _ptr(bias),
+                                              _ptr(total), _ptr(out), _ptr(stats), _stream())
+    _raise(rc, "eqtp_dropout_add_norm")
+    return out, total
+
+
+def eqtp_layer_norm_workspace_bytes(N: int, C: int, lmax: int) -> int:
+    """Device workspace eqtp_layer_norm_backward needs for the gradients of weight and bias (bytes)."""
+    d, _ = _norm_desc(lmax, C, EQTP_F32, EQTP_F32, 1e-5, 0.0)
+    n = load_library().eqtp_layer_norm_workspace_bytes(d, N)
+    if n < 0:
+        raise EqtpError(int(-n), "eqtp_layer_norm_workspace_bytes")
+    return int(n)
+
+
+def eqtp_layer_norm_backward(total, stats, grad_out, lmax: int, weight=None, grad_total=None, rng=None,
+                             p: float = 0.0, need_residual: bool = True, need_x: bool = None,
+                             need_weight: bool = True, need_bias: bool = True, workspace=None):
+    """(grad_residual, grad_x, grad_weight, grad_bias) of eqtp_dropout_add_norm, each None if not asked for; of
+    eqtp_layer_norm with ``total`` = x, whose gradient is grad_residual.  ``need_x`` defaults to p > 0.
+    ``workspace``: a uint8 tensor of at least eqtp_layer_norm_workspace_bytes bytes, or None to allocate one."""
+    import torch
+
+    code, N, C = _rows(total, "total", lmax)
+    ocode = EQTP_BF16 if grad_out.dtype is torch.bfloat16 else EQTP_F32
+    _check(grad_out, "grad_out", _torch_dtype(ocode), total.shape)
+    _check(stats, "stats", torch.float32, (N, lmax + 2))
+    _check_affine(weight, None, lmax, C)
+    if grad_total is not None:
+        _check(grad_total, "grad_total", total.dtype, total.shape)
+    p = float(p)
+    if need_x is None:
+        need_x = p > 0.0
+    if need_x:
+        _check_rng(rng, p)
+    d, _ = _norm_desc(lmax, C, code, ocode, 1e-5, p)
+    dev = total.device
+    gr = torch.empty_like(total) if need_residual else None
+    gx = torch.empty_like(total) if need_x else None
+    gw = torch.empty((lmax + 1, C), dtype=torch.float32, device=dev) if need_weight else None
+    gb = torch.empty((C,), dtype=torch.float32, device=dev) if need_bias else None
+    if need_weight or need_bias:
+        if workspace is None:
+            workspace = torch.empty(load_library().eqtp_layer_norm_workspace_bytes(d, N), dtype=torch.uint8, device=dev)
+        else:
+            _check(workspace, "workspace", torch.uint8)
+    rc = load_library().eqtp_layer_norm_backward(d, N, _ptr(total), _ptr(stats), _ptr(weight), _ptr(grad_out),
+                                                 _ptr(grad_total), _ptr(rng), _ptr(gr), _ptr(gx), _ptr(gw), _ptr(gb),
+                                                 _ptr(workspace), workspace.numel() if workspace is not None else 0,
+                                                 _stream())
+    _raise(rc, "eqtp_layer_norm_backward")
+    return gr, gx, gw, gb
+
+
+def eqtp_dropout(x, rng, p: float, lmax: int = 0, residual=None, out=None):
+    """out [N, C, K] = residual + dropout(x) of whole channels (see include/eqtp.h); without residual dropout(x),
+    which on a gradient, with the same rng, is the backward pass.  ``out`` may be x or residual."""
+    import torch
+
+    code, N, C = _rows(x, "x", lmax)
+    p = float(p)
+    _check_rng(rng, p)
+    if residual is not None:
+        _check(residual, "residual", x.dtype, x.shape)
+    if out is None:
+        out = torch.empty_like(x)
+    else:
+        _check(out, "out", x.dtype, x.shape)
+    rc = load_library().eqtp_dropout(N, C, lmax, code, p, _ptr(x), _ptr(residual), _ptr(rng), _ptr(out), _stream())
+    _raise(rc, "eqtp_dropout")
     return out
 
 
