@@ -513,7 +513,8 @@ int eqtp_check_graph(int64_t N, int64_t E, const int32_t* row_ptr, const int32_t
 
 /*
  * Debug mode.  When on, every entry point that takes a graph (the
- * convolutions, messages, gradients, edge grouping and the interaction layer)
+ * convolutions, messages, gradients, edge grouping, the interaction layer and
+ * the attention)
  * first runs eqtp_check_graph on the arrays it will read (and on perm for the
  * source-grouped gradients), waits for the report on its stream and returns
  * EQTP_EGRAPH, with nothing else launched, if any count is non-zero.  Debug
@@ -621,6 +622,62 @@ int eqtp_layer_norm_backward(const eqtp_norm_desc* d, int64_t N, const void* tot
  */
 int eqtp_dropout(int64_t N, int C, int lmax, int dtype, double p, const void* x, const void* residual,
                  const int64_t* rng, void* out, void* stream);
+
+typedef struct eqtp_attention_desc {
+  int32_t struct_size; /* = sizeof(eqtp_attention_desc) */
+  int32_t lmax;        /* 0..6 */
+  int32_t C;           /* channels of q: heads times the channels of a head */
+  int32_t heads;       /* divides C; <= 1024, (C / heads) K <= 2048 (more: EQTP_EUNSUPPORTED) */
+  int32_t kv_heads;    /* divides heads; head h reads key and value head h / (heads / kv_heads) */
+  int32_t x_dtype;     /* EQTP_F32 or EQTP_BF16: q, k, v, out and their gradients */
+  float scale;         /* factor of the inner products, finite */
+} eqtp_attention_desc;
+
+/*
+ * Attention of N rows over the edges of a graph (dst-sorted CSR) that lead to
+ * M sources; a readout over the items of each row is the same with src = 0..E-1.
+ *   s[e, h]   = scale sum_{c in head h, m} q[dst_e, c, m] k[src_e, c', m] + bias[e, h],
+ *   w[e, h]   = exp(s[e, h]) / sum over the row's edges,
+ *   out[n, c, m] = sum over row n of w[e, h(c)] v[src_e, c', m],
+ * c' = the same place in the key and value head of h.
+ *   src [E] int32 in [0, M); row_ptr [N+1] int32.
+ *   q, out [N, C, K]; k, v [M, C kv_heads / heads, K] (x_dtype).
+ *   bias   [E, heads] fp32, or NULL.  An edge whose bias is -inf takes no
+ *          part for that head, whatever k and v hold there.
+ *   lse    [N, heads] fp32 out: log of the row's sum of exp(s), -inf if no
+ *          edge takes part (out is 0 there); or NULL.
+ *   workspace eqtp_attention_workspace_bytes(d, N, M, E) bytes, 16-byte
+ *          aligned (may be NULL when that is 0): partial sums where few long
+ *          rows are cut into pieces.
+ * Logits, softmax and sums are fp32; out is rounded once.  The order of every
+ * sum is fixed: the same bits from call to call.  0 <= N, M, E < 2^31 (E > 0
+ * needs N, M > 0).  In debug mode the graph is checked.
+ */
+int64_t eqtp_attention_workspace_bytes(const eqtp_attention_desc* d, int64_t N, int64_t M, int64_t E);
+int eqtp_attention(const eqtp_attention_desc* d, int64_t N, int64_t M, int64_t E, const int32_t* src,
+                   const int32_t* row_ptr, const void* q, const void* k, const void* v, const float* bias, void* out,
+                   float* lse, void* workspace, int64_t workspace_bytes, void* stream);
+
+/*
+ * Gradients of eqtp_attention.  With g = grad_out, a[e, h] = sum over the
+ * head of g[dst_e] v[src_e], t[n, h] = sum over row n of w a, u = w (a - t[dst_e]):
+ *   grad_q[n] = scale sum_{e in row n} u k[src_e];  grad_bias = u;
+ *   grad_k[s] = scale sum_{e: src_e = s} u q[dst_e];  grad_v[s] = sum w g[dst_e],
+ * the last two summed over the heads that share a key and value head too.
+ *   lse: the forward call's; src_ptr [M+1], dst_s [E], perm [E] int32: the
+ *   edges grouped by source (CSR over sources, each edge's row, its index in
+ *   the order of src), needed for grad_k and grad_v only.
+ *   grad_q [N, C, K], grad_k, grad_v [M, C kv_heads / heads, K] (x_dtype),
+ *   grad_bias [E, heads] fp32: each may be NULL; fully overwritten.
+ *   workspace eqtp_attention_backward_workspace_bytes(d, N, M, E) bytes,
+ *   16-byte aligned.  No atomics: the same bits from call to call.
+ */
+int64_t eqtp_attention_backward_workspace_bytes(const eqtp_attention_desc* d, int64_t N, int64_t M, int64_t E);
+int eqtp_attention_backward(const eqtp_attention_desc* d, int64_t N, int64_t M, int64_t E, const int32_t* src,
+                            const int32_t* row_ptr, const void* q, const void* k, const void* v, const float* bias,
+                            const float* lse, const void* grad_out, const int32_t* src_ptr, const int32_t* dst_s,
+                            const int32_t* perm, void* grad_q, void* grad_k, void* grad_v, float* grad_bias,
+                            void* workspace, int64_t workspace_bytes, void* stream);
 
 /*
  * Test-only: walks the dst-sorted edges with exactly the row -> wave ->

@@ -909,6 +909,129 @@ int eqtp_dropout(int64_t N, int C, int lmax, int dtype, double p, const void* x,
   return status_of(eqtp::launch_dropout(a));
 }
 
+}  // extern "C"
+
+namespace {
+
+constexpr int kMaxHeads = 1024;    // of q; bounds the launch grid's second dimension
+constexpr int kMaxHeadRow = 2048;  // elements of a head's row that the attention kernels hold in registers
+
+int attn_check(const eqtp_attention_desc* d, int64_t N, int64_t M, int64_t E) {
+  if (!d || d->struct_size != (int32_t)sizeof(eqtp_attention_desc)) return EQTP_EINVAL;
+  if (d->lmax < 0 || d->C <= 0 || d->heads <= 0 || d->kv_heads <= 0 || !dtype_ok(d->x_dtype)) return EQTP_EINVAL;
+  if (d->C % d->heads != 0 || d->heads % d->kv_heads != 0) return EQTP_EINVAL;
+  if (!(d->scale >= -3.4028235e38f && d->scale <= 3.4028235e38f)) return EQTP_EINVAL;
+  if (N < 0 || M < 0 || E < 0 || N > kMaxIndex || M > kMaxIndex || E > kMaxIndex) return EQTP_EINVAL;
+  if (E > 0 && (N == 0 || M == 0)) return EQTP_EINVAL;
+  if (d->lmax > eqtp::kSo2MaxL || (int64_t)(d->C / d->heads) * eqtp::num_comp(d->lmax) > kMaxHeadRow ||
+      d->heads > kMaxHeads)
+    return EQTP_EUNSUPPORTED;
+  return EQTP_OK;
+}
+
+int attn_head_row(const eqtp_attention_desc* d) { return d->C / d->heads * eqtp::num_comp(d->lmax); }
+
+// Debug mode: the rows' CSR over N, and the sources in [0, M) (two checks: N and M may differ).
+int attn_debug(int64_t N, int64_t M, int64_t E, const int32_t* row_ptr, const int32_t* src, const int32_t* perm,
+               void* stream) {
+  const int rc = debug_check(N, E, row_ptr, nullptr, nullptr, nullptr, perm, stream);
+  return rc != EQTP_OK || E == 0 ? rc : debug_check(M, E, nullptr, src, nullptr, nullptr, nullptr, stream);
+}
+
+}  // namespace
+
+extern "C" {
+
+int64_t eqtp_attention_workspace_bytes(const eqtp_attention_desc* d, int64_t N, int64_t M, int64_t E) {
+  const int rc = attn_check(d, N, M, E);
+  if (rc != EQTP_OK) return -rc;
+  return eqtp::attn_workspace_bytes(N, M, E, attn_head_row(d), d->heads, d->kv_heads);
+}
+
+int eqtp_attention(const eqtp_attention_desc* d, int64_t N, int64_t M, int64_t E, const int32_t* src,
+                   const int32_t* row_ptr, const void* q, const void* k, const void* v, const float* bias, void* out,
+                   float* lse, void* workspace, int64_t workspace_bytes, void* stream) {
+  const int rc = attn_check(d, N, M, E);
+  if (rc != EQTP_OK) return rc;
+  if (N == 0) return EQTP_OK;
+  if (!row_ptr || !aligned4(row_ptr) || !q || !out || !aligned_as(q, d->x_dtype) || !aligned_as(out, d->x_dtype) ||
+      !aligned4(lse) || !aligned4(bias) || !aligned4(src) || !aligned_as(k, d->x_dtype) || !aligned_as(v, d->x_dtype))
+    return EQTP_EINVAL;
+  if (E > 0 && (!src || !k || !v)) return EQTP_EINVAL;
+  const int D = attn_head_row(d);
+  const int64_t need = eqtp::attn_workspace_bytes(N, M, E, D, d->heads, d->kv_heads);
+  if (need > 0 && (!workspace || !aligned16(workspace) || workspace_bytes < need)) return EQTP_EINVAL;
+  const int chk = attn_debug(N, M, E, row_ptr, src, nullptr, stream);
+  if (chk != EQTP_OK) return chk;
+  eqtp::AttnArgs a = {N, M, E, D, d->heads, d->kv_heads, d->x_dtype == EQTP_BF16, d->scale, src, row_ptr, q, k, v,
+                      bias, out, lse, workspace, (hipStream_t)stream};
+  return status_of(eqtp::launch_attention(a));
+}
+
+int64_t eqtp_attention_backward_workspace_bytes(const eqtp_attention_desc* d, int64_t N, int64_t M, int64_t E) {
+  const int rc = attn_check(d, N, M, E);
+  if (rc != EQTP_OK) return -rc;
+  return eqtp::attn_grad_workspace_bytes(N, M, E, attn_head_row(d), d->heads, d->kv_heads);
+}
+
+int eqtp_attention_backward(const eqtp_attention_desc* d, int64_t N, int64_t M, int64_t E, const int32_t* src,
+                            const int32_t* row_ptr, const void* q, const void* k, const void* v, const float* bias,
+                            const float* lse, const void* grad_out, const int32_t* src_ptr, const int32_t* dst_s,
+                            const int32_t* perm, void* grad_q, void* grad_k, void* grad_v, float* grad_bias,
+                            void* workspace, int64_t workspace_bytes, void* stream) {
+  const int rc = attn_check(d, N, M, E);
+  if (rc != EQTP_OK) return rc;
+  const int t = d->x_dtype;
+  if (!aligned4(src) || !aligned4(row_ptr) || !aligned_as(q, t) || !aligned_as(k, t) || !aligned_as(v, t) ||
+      !aligned4(bias) || !aligned4(lse) || !aligned_as(grad_out, t) || !aligned4(src_ptr) ||
+      !aligned4(dst_s) || !aligned4(perm) || !aligned_as(grad_q, t) || !aligned_as(grad_k, t) ||
+      !aligned_as(grad_v, t) || !aligned4(grad_bias))
+    return EQTP_EINVAL;
+  if (N > 0 && (!row_ptr || !q || !lse || !grad_out)) return EQTP_EINVAL;
+  const bool by_source = M > 0 && (grad_k || grad_v);
+  if (E > 0 && (!src || !k || !v || (by_source && (!dst_s || !perm)))) return EQTP_EINVAL;
+  if (by_source && !src_ptr) return EQTP_EINVAL;
+  const int D = attn_head_row(d);
+  const int64_t need = eqtp::attn_grad_workspace_bytes(N, M, E, D, d->heads, d->kv_heads);
+  if (need > 0 && (!workspace || !aligned16(workspace) || workspace_bytes < need)) return EQTP_EINVAL;
+  if (N > 0) {
+    const int chk = attn_debug(N, M, E, row_ptr, src, by_source ? perm : nullptr, stream);
+    if (chk != EQTP_OK) return chk;
+  }
+  if (by_source && E > 0) {
+    int chk = debug_check(M, E, src_ptr, nullptr, nullptr, nullptr, nullptr, stream);
+    if (chk == EQTP_OK) chk = debug_check(N, E, nullptr, nullptr, dst_s, nullptr, nullptr, stream);
+    if (chk != EQTP_OK) return chk;
+  }
+  eqtp::AttnGradArgs a = {};
+  a.N = N;
+  a.M = M;
+  a.E = E;
+  a.D = D;
+  a.heads = d->heads;
+  a.kv_heads = d->kv_heads;
+  a.bf16 = d->x_dtype == EQTP_BF16;
+  a.scale = d->scale;
+  a.src = src;
+  a.row_ptr = row_ptr;
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.bias = bias;
+  a.lse = lse;
+  a.gout = grad_out;
+  a.src_ptr = src_ptr;
+  a.dst_s = dst_s;
+  a.perm = perm;
+  a.gq = grad_q;
+  a.gk = M > 0 ? grad_k : nullptr;
+  a.gv = M > 0 ? grad_v : nullptr;
+  a.gbias = grad_bias;
+  a.ws = workspace;
+  a.stream = (hipStream_t)stream;
+  return status_of(eqtp::launch_attention_grad(a));
+}
+
 int eqtp_check_graph(int64_t N, int64_t E, const int32_t* row_ptr, const int32_t* src, const int32_t* dst,
                      const float* vec, int32_t* report, void* stream) {
   if (N < 0 || E < 0 || N > kMaxIndex || E > kMaxIndex) return EQTP_EINVAL;

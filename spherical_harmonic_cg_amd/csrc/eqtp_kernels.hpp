@@ -112,6 +112,52 @@ struct DropArgs {
   hipStream_t stream;
 };
 
+// attention over a graph; head rows of D = (C / heads) K elements
+struct AttnArgs {
+  int64_t N, M, E;
+  int D, heads, kv_heads;
+  bool bf16;
+  float scale;
+  const int32_t* src;
+  const int32_t* row_ptr;
+  const void* q;
+  const void* k;
+  const void* v;
+  const float* bias;      // or nullptr
+  void* out;
+  float* lse;             // or nullptr
+  void* ws;
+  hipStream_t stream;
+};
+
+struct AttnGradArgs {
+  int64_t N, M, E;
+  int D, heads, kv_heads;
+  bool bf16;
+  float scale;
+  const int32_t* src;
+  const int32_t* row_ptr;
+  const void* q;
+  const void* k;
+  const void* v;
+  const float* bias;      // or nullptr
+  const float* lse;
+  const void* gout;
+  const int32_t* src_ptr; // with gk or gv
+  const int32_t* dst_s;
+  const int32_t* perm;
+  void* gq;               // or nullptr
+  void* gk;               // or nullptr
+  void* gv;               // or nullptr
+  float* gbias;           // or nullptr
+  void* ws;
+  hipStream_t stream;
+};
+
+int64_t attn_workspace_bytes(int64_t N, int64_t M, int64_t E, int D, int heads, int kv_heads);
+hipError_t launch_attention(const AttnArgs& a);
+int64_t attn_grad_workspace_bytes(int64_t N, int64_t M, int64_t E, int D, int heads, int kv_heads);
+hipError_t launch_attention_grad(const AttnGradArgs& a);
 hipError_t launch_norm(const NormArgs& a);
 int64_t norm_workspace_floats(int64_t N, int C, int lmax);
 hipError_t launch_norm_grad(const NormGradArgs& a);

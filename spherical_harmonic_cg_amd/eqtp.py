@@ -33,6 +33,8 @@ EXPORTED = ("eqtp_num_paths", "eqtp_path_table", "eqtp_sh", "eqtp_conv_fused", "
             "eqtp_linear", "eqtp_interaction_workspace_bytes", "eqtp_interaction",
             "eqtp_layer_norm", "eqtp_dropout_add_norm", "eqtp_layer_norm_workspace_bytes",
             "eqtp_layer_norm_backward", "eqtp_dropout",
+            "eqtp_attention_workspace_bytes", "eqtp_attention", "eqtp_attention_backward_workspace_bytes",
+            "eqtp_attention_backward",
             "eqtp_status_string", "eqtp_check_graph", "eqtp_set_debug", "eqtp_test_segment_probe")
 
 
@@ -59,6 +61,12 @@ class _NormDesc(ctypes.Structure):
     _fields_ = [("struct_size", ctypes.c_int32), ("lmax", ctypes.c_int32), ("C", ctypes.c_int32),
                 ("x_dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32), ("eps", ctypes.c_float),
                 ("p", ctypes.c_double)]
+
+
+class _AttentionDesc(ctypes.Structure):
+    _fields_ = [("struct_size", ctypes.c_int32), ("lmax", ctypes.c_int32), ("C", ctypes.c_int32),
+                ("heads", ctypes.c_int32), ("kv_heads", ctypes.c_int32), ("x_dtype", ctypes.c_int32),
+                ("scale", ctypes.c_float)]
 
 
 _lib = None
@@ -120,6 +128,15 @@ def load_library(path: str = LIB_PATH):
             lib.eqtp_layer_norm_backward.restype = i32
             lib.eqtp_dropout.argtypes = [i64, i32, i32, i32, ctypes.c_double] + [vp] * 5
             lib.eqtp_dropout.restype = i32
+            ap = ctypes.POINTER(_AttentionDesc)
+            lib.eqtp_attention_workspace_bytes.argtypes = [ap, i64, i64, i64]
+            lib.eqtp_attention_workspace_bytes.restype = i64
+            lib.eqtp_attention.argtypes = [ap, i64, i64, i64] + [vp] * 9 + [i64, vp]
+            lib.eqtp_attention.restype = i32
+            lib.eqtp_attention_backward_workspace_bytes.argtypes = [ap, i64, i64, i64]
+            lib.eqtp_attention_backward_workspace_bytes.restype = i64
+            lib.eqtp_attention_backward.argtypes = [ap, i64, i64, i64] + [vp] * 16 + [i64, vp]
+            lib.eqtp_attention_backward.restype = i32
             lib.eqtp_status_string.argtypes = [i32]
             lib.eqtp_status_string.restype = ctypes.c_char_p
             lib.eqtp_check_graph.argtypes = [i64, i64] + [vp] * 6
@@ -803,6 +820,131 @@ def eqtp_dropout(x, rng, p: float, lmax: int = 0, residual=None, out=None):
     rc = load_library().eqtp_dropout(N, C, lmax, code, p, _ptr(x), _ptr(residual), _ptr(rng), _ptr(out), _stream())
     _raise(rc, "eqtp_dropout")
     return out
+
+
+@functools.lru_cache(maxsize=256)
+def _attention_desc(lmax, C, heads, kv_heads, x_dtype, scale):
+    # read by the library during a call only, so one instance per distinct descriptor is shared
+    if scale is None:
+        scale = (C // heads * (lmax + 1) ** 2) ** -0.5 if heads > 0 and C >= heads else 1.0
+    d = _AttentionDesc(ctypes.sizeof(_AttentionDesc), lmax, C, heads, kv_heads, x_dtype, scale)
+    need = load_library().eqtp_attention_workspace_bytes(ctypes.byref(d), 0, 0, 0)  # checks the descriptor
+    if need < 0:
+        raise EqtpError(int(-need), "eqtp_attention_desc")
+    return ctypes.byref(d), d
+
+
+def _attention_args(q, k, v, src, row_ptr, lmax, heads, scale, bias):
+    """Checks the attention's tensors; returns (descriptor, N, M, E, element type)."""
+    import torch
+
+    code, N, C = _rows(q, "q", lmax)
+    _check(k, "k", q.dtype)
+    if k.dim() != q.dim() or k.shape[2:] != q.shape[2:]:
+        raise ValueError("k must be [M, C kv_heads / heads, K] as q is [N, C, K]")
+    _check(v, "v", q.dtype, k.shape)
+    M, Ck = k.shape[0], k.shape[1]
+    if heads <= 0 or C % heads != 0:
+        raise ValueError("heads must divide the %d channels of q" % C)
+    width = C // heads
+    if width == 0 or Ck % width != 0 or Ck == 0 or heads % (Ck // width) != 0:
+        raise ValueError("k has %d channels: heads of %d channels, their number a divisor of %d" % (Ck, width, heads))
+    _check(src, "src", torch.int32)
+    E = src.numel()
+    _check(src, "src", torch.int32, (E,))
+    _check(row_ptr, "row_ptr", torch.int32, (N + 1,))
+    if bias is not None:
+        _check(bias, "bias", torch.float32, (E, heads))
+    d, _ = _attention_desc(lmax, C, heads, Ck // width, code, scale)
+    return d, N, M, E
+
+
+def _workspace(workspace, need, dev):
+    import torch
+
+    if need < 0:
+        raise EqtpError(int(-need), "workspace size")
+    if workspace is None:
+        return torch.empty(need, dtype=torch.uint8, device=dev) if need > 0 else None
+    _check(workspace, "workspace", torch.uint8)
+    return workspace
+
+
+def eqtp_attention_workspace_bytes(N: int, M: int, E: int, lmax: int, C: int, heads: int, kv_heads: int = None) -> int:
+    """Device workspace eqtp_attention needs (bytes; often 0)."""
+    d, _ = _attention_desc(lmax, C, heads, heads if kv_heads is None else kv_heads, EQTP_F32, None)
+    n = load_library().eqtp_attention_workspace_bytes(d, N, M, E)
+    if n < 0:
+        raise EqtpError(int(-n), "eqtp_attention_workspace_bytes")
+    return int(n)
+
+
+def eqtp_attention(q, k, v, src, row_ptr, lmax: int, heads: int, scale: float = None, bias=None, out=None, lse=None,
+                   workspace=None):
+    """out [N, C, K] = attention of q's rows over the edges of a dst-sorted graph (see include/eqtp.h).
+
+    q [N, C, K], k and v [M, Ck, K] float32 or bfloat16 ([N, C] and [M, Ck] at lmax 0); Ck = C, or fewer heads of
+    the same width that the heads of q share.  ``src`` [E], ``row_ptr`` [N+1] int32.  ``scale``: 1 / sqrt of the
+    elements of a head by default.  ``bias`` [E, heads] float32, -inf to mask.  ``lse``: a float32 [N, heads]
+    tensor to fill, for eqtp_attention_backward.  ``workspace``: a uint8 tensor of at least
+    eqtp_attention_workspace_bytes bytes, or None to allocate one if it is needed."""
+    import torch
+
+    d, N, M, E = _attention_args(q, k, v, src, row_ptr, lmax, heads, scale, bias)
+    if out is None:
+        out = torch.empty_like(q)
+    else:
+        _check(out, "out", q.dtype, q.shape)
+    if lse is not None:
+        _check(lse, "lse", torch.float32, (N, heads))
+    lib = load_library()
+    workspace = _workspace(workspace, lib.eqtp_attention_workspace_bytes(d, N, M, E), q.device)
+    rc = lib.eqtp_attention(d, N, M, E, _ptr(src), _ptr(row_ptr), _ptr(q), _ptr(k), _ptr(v), _ptr(bias), _ptr(out),
+                            _ptr(lse), _ptr(workspace), workspace.numel() if workspace is not None else 0, _stream())
+    _raise(rc, "eqtp_attention")
+    return out
+
+
+def eqtp_attention_backward_workspace_bytes(N: int, M: int, E: int, lmax: int, C: int, heads: int,
+                                            kv_heads: int = None) -> int:
+    """Device workspace eqtp_attention_backward needs (bytes)."""
+    d, _ = _attention_desc(lmax, C, heads, heads if kv_heads is None else kv_heads, EQTP_F32, None)
+    n = load_library().eqtp_attention_backward_workspace_bytes(d, N, M, E)
+    if n < 0:
+        raise EqtpError(int(-n), "eqtp_attention_backward_workspace_bytes")
+    return int(n)
+
+
+def eqtp_attention_backward(q, k, v, src, row_ptr, lse, grad_out, src_ptr, dst_s, perm, lmax: int, heads: int,
+                            scale: float = None, bias=None, need_q: bool = True, need_k: bool = True,
+                            need_v: bool = True, need_bias: bool = None, workspace=None):
+    """(grad_q, grad_k, grad_v, grad_bias) of eqtp_attention, each None if not asked for.  ``lse`` is the
+    forward call's.  ``src_ptr`` [M+1], ``dst_s`` [E], ``perm`` [E] int32: the edges grouped by source (for grad_k
+    and grad_v; e.g. eqtp_sort_edges_stable on src, carrying eqtp_edge_rows).  ``need_bias`` defaults to whether a
+    bias is given."""
+    import torch
+
+    d, N, M, E = _attention_args(q, k, v, src, row_ptr, lmax, heads, scale, bias)
+    _check(lse, "lse", torch.float32, (N, heads))
+    _check(grad_out, "grad_out", q.dtype, q.shape)
+    if need_k or need_v:
+        _check(src_ptr, "src_ptr", torch.int32, (M + 1,))
+        _check(dst_s, "dst_s", torch.int32, (E,))
+        _check(perm, "perm", torch.int32, (E,))
+    if need_bias is None:
+        need_bias = bias is not None
+    gq = torch.empty_like(q) if need_q else None
+    gk = torch.empty_like(k) if need_k else None
+    gv = torch.empty_like(v) if need_v else None
+    gb = torch.empty((E, heads), dtype=torch.float32, device=q.device) if need_bias else None
+    lib = load_library()
+    workspace = _workspace(workspace, lib.eqtp_attention_backward_workspace_bytes(d, N, M, E), q.device)
+    rc = lib.eqtp_attention_backward(d, N, M, E, _ptr(src), _ptr(row_ptr), _ptr(q), _ptr(k), _ptr(v), _ptr(bias),
+                                     _ptr(lse), _ptr(grad_out), _ptr(src_ptr), _ptr(dst_s), _ptr(perm),
+                                     _ptr(gq), _ptr(gk), _ptr(gv), _ptr(gb), _ptr(workspace),
+                                     workspace.numel() if workspace is not None else 0, _stream())
+    _raise(rc, "eqtp_attention_backward")
+    return gq, gk, gv, gb
 
 
 def eqtp_test_segment_probe(row_ptr, src, C: int, lmax: int, algo: int = EQTP_ALGO_NODE_MFMA):

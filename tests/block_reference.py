@@ -141,3 +141,117 @@ def dropout(x, keep, p, residual=None):
     scale = np.float64(np.float32(1.0 / (1.0 - p)))  # the factor as the library holds it
     out = np.where(keep[:, :, None], x * scale, 0.0)
     return out if residual is None else out + np.asarray(residual, dtype=np.float64)
+
+
+# ---- attention --------------------------------------------------------------
+
+def attention(q, k, v, src, row_ptr, heads, scale, bias=None):
+    """(out [N, C, K], w [E, heads], lse [N, heads], s [E, heads]); q [N, C, K], k, v [M, Ck, K]."""
+    q, k, v = (np.asarray(t, dtype=np.float64) for t in (q, k, v))
+    N = q.shape[0]
+    D = q.shape[1] * q.shape[2] // heads
+    G = k.shape[1] * k.shape[2] // D
+    qh, kh, vh = q.reshape(N, heads, D), k.reshape(-1, G, D), v.reshape(-1, G, D)
+    E = len(src)
+    out, w = np.zeros((N, heads, D)), np.zeros((E, heads))
+    lse, logits = np.full((N, heads), -np.inf), np.full((E, heads), -np.inf)
+    for n in range(N):
+        for h in range(heads):
+            e = np.arange(row_ptr[n], row_ptr[n + 1])
+            if bias is not None:
+                e = e[np.asarray(bias)[e, h] != -np.inf]
+            if len(e) == 0:
+                continue
+            s = scale * (kh[src[e], h * G // heads] @ qh[n, h]) + (np.asarray(bias, dtype=np.float64)[e, h] if bias is not None else 0.0)
+            top = s.max()
+            p = np.exp(s - top)
+            logits[e, h], w[e, h] = s, p / p.sum()
+            lse[n, h] = top + math.log(p.sum())
+            out[n, h] = w[e, h] @ vh[src[e], h * G // heads]
+    return out.reshape(q.shape), w, lse, logits
+
+
+def attention_backward(q, k, v, src, row_ptr, heads, scale, g, bias=None):
+    """(gq, gk, gv, gbias)."""
+    out, w, _, _ = attention(q, k, v, src, row_ptr, heads, scale, bias)
+    q, k, v, g = (np.asarray(t, dtype=np.float64) for t in (q, k, v, g))
+    N = q.shape[0]
+    D = q.shape[1] * q.shape[2] // heads
+    G = k.shape[1] * k.shape[2] // D
+    qh, gh, oh, kh, vh = (t.reshape(t.shape[0], -1, D) for t in (q, g, out, k, v))
+    gq, gk, gv, u = np.zeros_like(qh), np.zeros_like(kh), np.zeros_like(vh), np.zeros_like(w)
+    for n in range(N):
+        for h in range(heads):
+            t = gh[n, h] @ oh[n, h]
+            for e in range(row_ptr[n], row_ptr[n + 1]):
+                if w[e, h] == 0.0:
+                    continue
+                m, j = src[e], h * G // heads
+                u[e, h] = w[e, h] * (gh[n, h] @ vh[m, j] - t)
+                gq[n, h] += scale * u[e, h] * kh[m, j]
+                gk[m, j] += scale * u[e, h] * qh[n, h]
+                gv[m, j] += w[e, h] * gh[n, h]
+    return gq.reshape(q.shape), gk.reshape(k.shape), gv.reshape(v.shape), u
+
+
+def attention_bounds(q, k, v, src, row_ptr, heads, scale, g, bias, half_step):
+    """Elementwise bounds of |kernel - exact| for (out, lse, gq, gk, gv, gbias), from above, by running absolute
+    values through the same formulas.  half_step: of the outputs' type.
+
+    A dot product of D terms is off by at most (D / 16 + 16) u of the sum of its terms' sizes (a lane adds at most
+    D / 16 of them; trees follow), a logit by that times scale and one rounding of |s| and of the bias; exp turns an absolute error of
+    its argument into a relative one and adds its own 4 u (and 2 u |argument|: the hardware's exponential is of
+    base 2, and its argument is rounded).  Sums over a row or a source of n edges are off by at most (n + 16) u."""
+    q, k, v, g = (np.asarray(t, dtype=np.float64) for t in (q, k, v, g))
+    out, w, lse, s = attention(q, k, v, src, row_ptr, heads, scale, bias)
+    N = q.shape[0]
+    D = q.shape[1] * q.shape[2] // heads
+    G = k.shape[1] * k.shape[2] // D
+    u = U32
+    qh, gh, oh, kh, vh = (np.abs(t.reshape(t.shape[0], -1, D)) for t in (q, g, out, k, v))
+    sg, so, sv = (t.reshape(t.shape[0], -1, D) for t in (g, out, v))
+    bo, bl = np.zeros_like(oh), np.zeros_like(lse)
+    bq, bk, bv, bb = np.zeros_like(qh), np.zeros_like(kh), np.zeros_like(vh), np.zeros_like(w)
+    cd = (D / 16 + 16) * u
+    sources = np.bincount(src, minlength=k.shape[0]) * (heads // G)
+    for n in range(N):
+        for h in range(heads):
+            e = np.arange(row_ptr[n], row_ptr[n + 1])
+            e = e[w[e, h] > 0] if len(e) else e
+            live = np.arange(row_ptr[n], row_ptr[n + 1])
+            if len(e) == 0:
+                continue
+            j, m = h * G // heads, src[e]
+            cn = (len(live) + 16) * u
+            size = abs(scale) * (kh[m, j] @ qh[n, h])
+            ds = cd * size + 2 * u * np.abs(s[e, h]) + (u * np.abs(np.asarray(bias, dtype=np.float64)[e, h]) if bias is not None else 0.0)
+            top = s[e, h].max()
+            dw = ds + 4 * u + 2 * u * np.abs(s[e, h] - top)       # relative, of the unnormalised weight
+            dsum = (w[e, h] * dw).sum() + cn
+            rel = dw + dsum + 4 * u + ds.max()
+            bl[n, h] = dsum + 4 * u + 4 * u * abs(lse[n, h]) + 2 * u * abs(top)
+            # backward: w again from lse
+            relb = ds + bl[n, h] + 4 * u + 2 * u * np.abs(s[e, h] - lse[n, h])
+            terms = w[e, h][:, None] * vh[m, j]
+            bo[n, h] = (terms * (rel + cn + 2 * u)[:, None]).sum(axis=0)
+            bo[n, h] += half_step * (oh[n, h] + bo[n, h])
+            dv = vh[m, j] @ gh[n, h]
+            a = np.abs(sv[m, j] @ sg[n, h])
+            t = abs(sg[n, h] @ so[n, h])
+            dt = (w[e, h] * (cd * dv + (relb + cn) * a)).sum()
+            along = np.abs(sv[m, j] @ sg[n, h] - sg[n, h] @ so[n, h])
+            eu = w[e, h] * (cd * dv + dt + 2 * u * along + relb * along)
+            bb[e, h] = eu + u * w[e, h] * along
+            # sum u k as sum w a k - t sum w k: both sums round
+            bq[n, h] = abs(scale) * (eu[:, None] * kh[m, j] + (w[e, h] * (a + t) * (cn + 4 * u))[:, None] * kh[m, j]).sum(axis=0)
+            for i, ei in enumerate(e):
+                cs = (sources[src[ei]] + 16) * u
+                bk[src[ei], j] += abs(scale) * (eu[i] + w[ei, h] * along[i] * (cs + 4 * u)) * qh[n, h]
+                bv[src[ei], j] += w[ei, h] * (relb[i] + cs + 4 * u) * gh[n, h]
+    want = attention_backward(q, k, v, src, row_ptr, heads, scale, g, bias)
+    res = [bo.reshape(q.shape), bl]
+    for b, t in zip((bq, bk, bv), want):
+        b = b.reshape(t.shape)
+        res.append(b + half_step * (np.abs(t) + b))
+    res.append(bb)
+    return [b + 1e-37 for b in res]

@@ -121,3 +121,81 @@ def test_binding_refusals():
         e.eqtp_layer_norm_backward(x, x, x, 1)
     with pytest.raises(TypeError, match="torch.Tensor"):
         e._check([1.0], "x", torch.float32)
+
+
+def _attn_desc(e, **kw):
+    d = dict(lmax=3, C=64, heads=4, kv_heads=2, x_dtype=0, scale=0.1)
+    d.update(kw)
+    return e._AttentionDesc(ctypes.sizeof(e._AttentionDesc), d["lmax"], d["C"], d["heads"], d["kv_heads"], d["x_dtype"],
+                            d["scale"])
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(lmax=-1), 1), (dict(lmax=7), 2), (dict(C=0), 1), (dict(heads=0), 1), (dict(heads=5), 1), (dict(kv_heads=3), 1),
+    (dict(kv_heads=0), 1), (dict(kv_heads=8), 1), (dict(C=1024, heads=4), 2), (dict(lmax=0, C=2049, heads=1, kv_heads=1), 2),
+    (dict(lmax=0, C=2048, heads=2048, kv_heads=1), 2), (dict(x_dtype=2), 1), (dict(scale=float("nan")), 1),
+    (dict(scale=float("inf")), 1)])
+def test_attention_descriptor(kw, want):
+    e = _lib()
+    lib = e.load_library()
+    d = ctypes.byref(_attn_desc(e, **kw))
+    assert lib.eqtp_attention_workspace_bytes(d, 4, 4, 8) == -want
+    assert lib.eqtp_attention_backward_workspace_bytes(d, 4, 4, 8) == -want
+    assert lib.eqtp_attention(d, 4, 4, 8, *[FAKE] * 9, 1 << 40, NULL) == want
+    assert lib.eqtp_attention_backward(d, 4, 4, 8, *[FAKE] * 16, 1 << 40, NULL) == want
+
+
+def test_attention_pointers_and_sizes():
+    e = _lib()
+    lib = e.load_library()
+    d = ctypes.byref(_attn_desc(e))
+    bad = _attn_desc(e)
+    bad.struct_size += 4
+    assert lib.eqtp_attention(ctypes.byref(bad), 4, 4, 8, *[FAKE] * 9, 1 << 40, NULL) == 1
+    assert lib.eqtp_attention(None, 4, 4, 8, *[FAKE] * 9, 1 << 40, NULL) == 1
+    # src row_ptr q k v bias out lse workspace
+    ok = [FAKE] * 9
+    put = lambda k, v: ok[:k] + [v] + ok[k + 1:]
+    f = lambda N, M, E, a, size=1 << 40: lib.eqtp_attention(d, N, M, E, *a, size, NULL)
+    for N, M, E in ((-1, 4, 8), (4, -1, 8), (4, 4, -8), (1 << 31, 4, 8), (4, 1 << 31, 8), (4, 4, 1 << 31), (0, 4, 8), (4, 0, 8)):
+        assert f(N, M, E, ok) == 1
+    assert f(0, 4, 0, [NULL] * 9) == 0
+    for k in (0, 1, 2, 3, 4, 6):
+        assert f(4, 4, 8, put(k, NULL)) == 1
+    for k in range(8):
+        assert f(4, 4, 8, put(k, ODD2)) == 1
+    # few long rows need a workspace
+    need = lib.eqtp_attention_workspace_bytes(d, 1, 100000, 100000)
+    if need > 0:
+        assert f(1, 100000, 100000, put(8, NULL)) == 1 and f(1, 100000, 100000, ok, need - 1) == 1
+        assert f(1, 100000, 100000, put(8, ctypes.c_void_p(0x10008))) == 1
+
+
+def test_attention_backward_refusals():
+    e = _lib()
+    lib = e.load_library()
+    d = ctypes.byref(_attn_desc(e))
+    # src row_ptr q k v bias lse grad_out src_ptr dst_s perm grad_q grad_k grad_v grad_bias workspace
+    ok = [FAKE] * 16
+    put = lambda k, v: ok[:k] + [v] + ok[k + 1:]
+    need = lib.eqtp_attention_backward_workspace_bytes(d, 4, 4, 8)
+    assert need > 0
+    f = lambda N, M, E, a, size=need: lib.eqtp_attention_backward(d, N, M, E, *a, size, NULL)
+    assert f(4, 4, 8, ok, need - 1) == 1 and f(-1, 4, 8, ok) == 1 and f(4, 4, 1 << 31, ok) == 1
+    for k in (0, 1, 2, 3, 4, 6, 7, 8, 9, 10, 15):
+        assert f(4, 4, 8, put(k, NULL)) == 1
+    for k in range(15):
+        assert f(4, 4, 8, put(k, ODD2)) == 1
+    assert f(4, 4, 8, put(15, ctypes.c_void_p(0x10008))) == 1
+
+
+def test_attention_binding_refusals():
+    import torch
+
+    e = _lib()
+    x = torch.zeros(4, 8, 4)
+    i = torch.zeros(5, dtype=torch.int32)
+    with pytest.raises(ValueError, match="on the GPU"):
+        e.eqtp_attention(x, x, x, i, i, 1, 2)
+    with pytest.raises(ValueError, match="on the GPU"):
+        e.eqtp_attention_backward(x, x, x, i, i, x, x, i, i, i, 1, 2)

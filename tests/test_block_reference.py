@@ -50,3 +50,43 @@ def test_keep_mask_rate():
     keep = ref.keep_mask(7, 9, 100, 100, 0.3)
     assert abs(keep.mean() - 0.7) < 5 * np.sqrt(0.21 / 1e4)
     assert ref.keep_mask(7, 9, 3, 5, 0.0).all()
+
+
+def _small(seed, heads, kv_heads, D, masked=False):
+    r = np.random.default_rng(seed)
+    N, M = 4, 5
+    row_ptr = np.array([0, 3, 3, 7, 9])
+    src = r.integers(0, M, 9)
+    q, g = (r.standard_normal((N, heads * D, 1)) for _ in range(2))
+    k, v = (r.standard_normal((M, kv_heads * D, 1)) for _ in range(2))
+    bias = r.standard_normal((9, heads))
+    if masked:
+        bias[4] = -np.inf
+        bias[7:] = -np.inf
+    return q, k, v, src, row_ptr, bias, g
+
+
+@pytest.mark.parametrize("heads,kv_heads", [(1, 1), (4, 2), (3, 1)])
+@pytest.mark.parametrize("masked", [False, True])
+def test_attention_gradient_against_differences(heads, kv_heads, masked):
+    q, k, v, src, rp, bias, g = _small(7, heads, kv_heads, 6, masked)
+    grads = ref.attention_backward(q, k, v, src, rp, heads, 0.4, g, bias)
+    args = [q, k, v, bias]
+    r = np.random.default_rng(2)
+    for i in range(4):
+        d = r.standard_normal(args[i].shape)
+        d[~np.isfinite(args[i])] = 0.0
+
+        def f(t):
+            a = list(args)
+            a[i] = t
+            return (ref.attention(a[0], a[1], a[2], src, rp, heads, 0.4, a[3])[0] * g).sum()
+
+        assert np.isclose((grads[i] * d).sum(), _directional(f, args[i], d), rtol=1e-6, atol=1e-9), i
+
+
+def test_attention_of_equal_logits_is_the_mean():
+    q, k, v, src, rp, _, _ = _small(8, 2, 2, 5)
+    out, w, lse, _ = ref.attention(np.zeros_like(q), k, v, src, rp, 2, 1.0)
+    assert np.allclose(out[0], v[src[:3]].mean(axis=0)) and np.allclose(lse[0], np.log(3))
+    assert (out[1] == 0).all() and np.isneginf(lse[1]).all()
