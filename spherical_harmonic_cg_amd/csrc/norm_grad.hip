@@ -1,0 +1,213 @@
+// norm_grad.hip -- gradients of the layer norm by degree (and of the residual
+// sum and dropout before it):
+//   a = weight g,  zhat = zc r_l,
+//   gz = r_l (a - [l = 0] mean_c a - zhat mean_l(a zhat)) (+ grad_total),
+//   gx = keep gz / (1 - p),  gweight[l, c] = sum g zhat,  gbias[c] = sum g[0].
+// Bound by HBM like the forward pass: z, g (and grad_total) are read once, the
+// gradients written once.  Rows lie in groups of threads as there.  The sums
+// over nodes are kept at each thread's own places while its group walks over
+// the rows; at the end a workgroup adds its groups and the components of a
+// degree through LDS, in a fixed order, into its line of part
+// [workgroups][(lmax+2) C], and a second kernel adds the lines.
+#include "norm_device.hpp"
+
+namespace eqtp {
+
+template <class E, class O, int T, int NV, int KT>
+__global__ __launch_bounds__(norm_threads(T)) void norm_grad_kernel(NormGradArgs a, int A, float* part) {
+  constexpr int TH = norm_threads(T), R = TH / T;
+  constexpr bool HOLD = T < 1024;  // weights in registers (1024 threads: too few of them)
+  __shared__ float red[T > 64 ? 2 * (T / 64) * (kMaxDeg + 1) : 1];
+  __shared__ uint8_t nib[R * (T * NV + 2)];
+  __shared__ float pos[R * T * NV * 4];  // per group: a value for each place of a row
+  const int C = a.C, D = C * a.K, deg = KT == 0 ? 1 : a.lmax + 1;
+  Slots<T, KT> sl(C, a.K, A);
+  const int g = threadIdx.x / T;
+  int turn = 0;
+  constexpr int NB = KT == 0 ? 4 : 1;  // component 0 fills every slot (K = 1), or at most one of a quad
+  float w[NV][4], aw[NV][4] = {}, ab[NV][NB] = {};
+  auto weights = [&]() {
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int c = sl.channel(q, j);
+        w[j][q] = a.weight && sl.on && c < C ? a.weight[sl.l(q) * C + c] : 1.0f;
+      }
+  };
+  if constexpr (HOLD) weights();
+  DropState ds = {};
+  if (a.rng) ds = drop_state(a.rng, a.thr, a.scale);
+  for (int64_t n = (int64_t)blockIdx.x * R + g; n < a.N; n += (int64_t)gridDim.x * R) {
+    sl.row();
+    forget_keys(ds);
+    if constexpr (!HOLD) weights();
+    float z[NV][4], go[NV][4];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int i = 4 * (sl.t + A * j);
+      load4((const E*)a.total + n * D + i, sl.on ? D - i : 0, z[j]);
+      load4((const O*)a.gout + n * D + i, sl.on ? D - i : 0, go[j]);
+    }
+    const float* st = a.stats + n * (a.lmax + 2);
+    const float mu = st[0];
+    float rq[4], sq[4] = {}, v[kMaxDeg + 1] = {};
+#pragma unroll
+    for (int q = 0; q < 4; ++q) rq[q] = st[1 + sl.l(q)];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int i = 4 * (sl.t + A * j);
+      float av[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        z[j][q] = (z[j][q] - (sl.l(q) == 0 ? mu : 0.0f)) * rq[q];
+        if (KT == 1 ? i >= D : i + q >= D) z[j][q] = 0.0f;
+        aw[j][q] = fmaf(go[j][q], z[j][q], aw[j][q]);
+        av[q] = go[j][q] * w[j][q];
+        sq[q] = fmaf(av[q], z[j][q], sq[q]);
+      }
+      v[0] += sl.scalars(av);
+      if constexpr (KT == 0) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) ab[j][q] += go[j][q];
+      } else {
+        ab[j][0] += sl.scalars(go[j]);
+      }
+    }
+    if (a.gres || a.gx) {
+      if (!sl.on)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) sq[q] = 0.0f;
+      sl.by_degree(sq, deg, v + 1);
+      group_sums<T, kMaxDeg + 1>(v, deg + 1, red, turn);
+      const float am = v[0] / (float)C;
+#pragma unroll
+      for (int d = 0; d < kMaxDeg; ++d)
+        if (d < deg) v[1 + d] /= (float)(C * (2 * d + 1));
+      float mq[4];
+      sl.of_degree(v + 1, deg, mq);
+      KeepBits<T, KT> kb;
+      if (a.rng) kb.begin(ds, n, C, sl.t, nib + g * (T * NV + 2));
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const int i = 4 * (sl.t + A * j);
+        if (sl.on && i < D) {
+          float gz[4], gt[4] = {};
+          if (a.gtotal) load4((const E*)a.gtotal + n * D + i, D - i, gt);
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            gz[q] = fmaf(rq[q], (go[j][q] * w[j][q] - (sl.l(q) == 0 ? am : 0.0f)) - z[j][q] * mq[q], gt[q]);
+          if (a.gres) store4((E*)a.gres + n * D + i, D - i, gz);
+          if (a.gx) {
+            int c[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) c[q] = min(sl.channel(q, j), C - 1);
+            const uint32_t keep = a.rng ? kb.quad(ds, c) : 15u;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) gz[q] = drop_add(keep >> q & 1, gz[q], a.scale, 0.0f);
+            store4((E*)a.gx + n * D + i, D - i, gz);
+          }
+        }
+      }
+    }
+  }
+  if (part == nullptr) return;
+  const int cols = (a.lmax + 2) * C, wcols = cols - C;
+  part += (int64_t)blockIdx.x * cols;
+  float* mine = pos + g * (T * NV * 4);
+  if (sl.on)
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) mine[4 * (sl.t + A * j) + q] = aw[j][q];
+  __syncthreads();
+  for (int col = threadIdx.x; col < wcols; col += TH) {
+    const int l = col / C, c = col - l * C;
+    float s = 0.0f;
+    for (int k = 0; k < R; ++k)
+      for (int m = l * l; m < (l + 1) * (l + 1); ++m) s += pos[k * (T * NV * 4) + c * a.K + m];
+    part[col] = s;
+  }
+  __syncthreads();
+  if (sl.on)
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        if (sl.l(q) == 0 && sl.channel(q, j) < C) mine[sl.channel(q, j)] = ab[j][KT == 0 ? q : 0];
+  __syncthreads();
+  for (int c = threadIdx.x; c < C; c += TH) {
+    float s = 0.0f;
+    for (int k = 0; k < R; ++k) s += pos[k * (T * NV * 4) + c];
+    part[wcols + c] = s;
+  }
+}
+
+// Sums of the lines of part: 16 columns and 64 stretches of lines a workgroup.
+__global__ __launch_bounds__(1024) void norm_weight_sum_kernel(int cols, int wcols, int parts,
+                                                               const float* __restrict__ part, float* gw, float* gb) {
+  __shared__ float red[64][17];
+  const int cc = threadIdx.x & 15, k = threadIdx.x >> 4, col = blockIdx.x * 16 + cc;
+  float s = 0.0f;
+  if (col < cols) {
+#pragma unroll 8
+    for (int p = k; p < parts; p += 64) s += part[(int64_t)p * cols + col];
+  }
+  red[k][cc] = s;
+  __syncthreads();
+  if (k == 0 && col < cols) {
+    s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 64; ++i) s += red[i][cc];
+    if (col < wcols) {
+      if (gw) gw[col] = s;
+    } else if (gb) {
+      gb[col - wcols] = s;
+    }
+  }
+}
+
+constexpr int kGradBlocks = 4;
+
+int64_t norm_workspace_floats(int64_t N, int C, int lmax) {
+  // a line for each workgroup of the gradient kernel: at most one a node and kGradBlocks a compute unit (of 256)
+  const int64_t most = (int64_t)kGradBlocks * 256;
+  return (N < most ? (N > 0 ? N : 1) : most) * (lmax + 2) * C;
+}
+
+template <class E, class O, int KT>
+static hipError_t norm_grad_t(const NormGradArgs& a) {
+  const bool sums = a.gw || a.gb;
+  int parts = 0;
+  if (a.N > 0) {
+    const NormShape s = norm_shape(a.C, a.K);
+    parts = norm_grid(a.N, s.T, kGradBlocks);
+    if (parts > 256 * kGradBlocks) parts = 256 * kGradBlocks;
+    const dim3 grid(parts), block(norm_threads(s.T));
+    float* part = sums ? a.ws : nullptr;
+#define EQTP_NORM(T_, NV_) \
+  (norm_grad_kernel<E, O, T_, NV_, KT><<<grid, block, 0, a.stream>>>(a, s.A, part), hipGetLastError())
+    const hipError_t e = EQTP_NORM_SHAPES(s, EQTP_NORM);
+#undef EQTP_NORM
+    if (e != hipSuccess) return e;
+  }
+  if (sums) {
+    const int cols = (a.lmax + 2) * a.C;
+    hipLaunchKernelGGL(norm_weight_sum_kernel, dim3((cols + 15) / 16), dim3(1024), 0, a.stream, cols, cols - a.C, parts,
+                       a.ws, a.gw, a.gb);
+    return hipGetLastError();
+  }
+  return hipSuccess;
+}
+
+template <class E, class O>
+static hipError_t norm_grad_k(const NormGradArgs& a) {
+  return a.K == 1 ? norm_grad_t<E, O, 0>(a) : (a.K % 4 == 0 ? norm_grad_t<E, O, 1>(a) : norm_grad_t<E, O, 2>(a));
+}
+
+hipError_t launch_norm_grad(const NormGradArgs& a) {
+  if (a.x_bf16) return a.out_bf16 ? norm_grad_k<__bf16, __bf16>(a) : norm_grad_k<__bf16, float>(a);
+  return a.out_bf16 ? norm_grad_k<float, __bf16>(a) : norm_grad_k<float, float>(a);
+}
+
+}  // namespace eqtp

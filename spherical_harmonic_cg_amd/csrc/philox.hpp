@@ -19,8 +19,11 @@ struct DropState {
 
 __device__ __forceinline__ DropState drop_state(const int64_t* __restrict__ rng, uint32_t thr, float scale) {
   const uint64_t seed = (uint64_t)rng[0], off = (uint64_t)rng[1];
-  return {(uint32_t)seed, (uint32_t)(seed >> 32), (uint32_t)off, (uint32_t)(off >> 32), thr, scale};
+  auto uni = [](uint64_t v) { return (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)v); };
+  return {uni(seed), uni(seed >> 32), uni(off), uni(off >> 32), thr, scale};
 }
+// At the head of a loop: the ten rounds' keys are made again instead of being kept in scalar registers.
+__device__ __forceinline__ void forget_keys(DropState& s) { asm volatile("" : "+s"(s.k0), "+s"(s.k1)); }
 
 // One round multiplies words 0 and 2 by the method's constants and crosses the
 // halves of the products over; the key moves by two Weyl constants a round.
