@@ -1,36 +1,142 @@
 // dropout.hip -- dropout of whole channels from a counter-based generator,
 // with an optional residual sum: out = residual + keep(n, c) x / (1 - p).
+//
+// Bound by HBM (each element read and written once) next to the vector ALUs
+// that make the random words: one Philox block (ten rounds) serves four
+// channels, 4 K elements.  A wave takes a stretch of 4 x 64 units of 16 bytes.
+// With K = 1 a thread's four (eight, bf16) elements are one (two) whole blocks and it
+// makes its own bits.  With K > 1 the stretch touches few channels: the lanes
+// make one block each, once, leave the keep bits in LDS and read them back
+// element by element; made by every thread for itself, the words would take
+// K times the work.
+#include <type_traits>
+
 #include "eqtp_device.hpp"
 #include "eqtp_kernels.hpp"
 #include "philox.hpp"
 
 namespace eqtp {
 
-// One element a thread.
 template <class T>
-__global__ __launch_bounds__(256) void dropout_kernel(int64_t total, int K, const T* x, const T* residual,
+struct Unit {  // 16 bytes of elements, aligned as one element only
+  static constexpr int VE = 16 / (int)sizeof(T);
+  typedef T V __attribute__((ext_vector_type(VE), aligned(sizeof(T))));
+  static __device__ __forceinline__ void load(const T* p, int left, float (&v)[VE]) {
+    if (left >= VE) {
+      const V t = *reinterpret_cast<const V*>(p);
+#pragma unroll
+      for (int q = 0; q < VE; ++q) v[q] = (float)t[q];
+    } else {
+#pragma unroll
+      for (int q = 0; q < VE; ++q) v[q] = q < left ? (float)p[q] : 0.0f;
+    }
+  }
+  static __device__ __forceinline__ void store(T* p, int left, const float (&v)[VE]) {
+    if (left >= VE) {
+      V t;
+#pragma unroll
+      for (int q = 0; q < VE; ++q) t[q] = (T)v[q];
+      *reinterpret_cast<V*>(p) = t;
+    } else {
+#pragma unroll
+      for (int q = 0; q < VE; ++q)
+        if (q < left) p[q] = (T)v[q];
+    }
+  }
+};
+
+template <class T, int K>
+__global__ __launch_bounds__(256) void dropout_kernel(int64_t total, const T* x, const T* residual,
                                                       const int64_t* __restrict__ rng, uint32_t thr, float scale,
                                                       T* out) {
-  const DropState s = rng ? drop_state(rng, thr, scale) : DropState{0, 0, 0, 0, 0, scale};
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
-    const int64_t j = i / K;
-    const bool keep = rng == nullptr || (keep_nibble(s, (uint64_t)j >> 2) >> (j & 3) & 1);
-    out[i] = (T)drop_add(keep, (float)x[i], scale, residual ? (float)residual[i] : 0.0f);
+  using U = Unit<T>;
+  constexpr int VE = U::VE, NJ = 4, STRETCH = 64 * NJ * VE;
+  __shared__ uint8_t nib[4][K == 1 ? 1 : STRETCH / (4 * K) + 3];
+  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
+  for (int64_t base = ((int64_t)blockIdx.x * 4 + wv) * STRETCH; base < total; base += (int64_t)gridDim.x * 4 * STRETCH) {
+    const int64_t room = total - base;
+    const int have = room < STRETCH ? (int)room : STRETCH;
+    float v[NJ][VE], r[NJ][VE];
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) U::load(x + base + VE * (lane + 64 * j), have - VE * (lane + 64 * j), v[j]);
+    if (residual) {
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) U::load(residual + base + VE * (lane + 64 * j), have - VE * (lane + 64 * j), r[j]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < NJ; ++j)
+#pragma unroll
+        for (int q = 0; q < VE; ++q) r[j][q] = 0.0f;
+    }
+    if (rng) {
+      const DropState s = drop_state(rng, thr, scale);
+      if constexpr (K == 1) {
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+          if (VE * (lane + 64 * j) >= have) break;
+#pragma unroll
+          for (int h = 0; h < VE; h += 4) {
+            const uint32_t keep = keep_nibble(s, (uint64_t)(base + VE * (lane + 64 * j) + h) >> 2);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) v[j][h + q] = drop_add(keep >> q & 1, v[j][h + q], scale, r[j][h + q]);
+          }
+        }
+      } else {
+        const int64_t c0 = base / K;                 // first channel number of the stretch
+        const int shift = (int)(base - c0 * K);      // elements of it before the stretch
+        const int64_t b0 = c0 >> 2;
+        const int blocks = (int)(((base + have - 1) / K >> 2) - b0) + 1, first = (int)(c0 & 3);
+        wave_lds_sync();  // the stretch before has been read
+        for (int i = lane; i < blocks; i += 64) nib[wv][i] = (uint8_t)keep_nibble(s, (uint64_t)(b0 + i));
+        wave_lds_sync();
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+          const int i = VE * (lane + 64 * j);
+          if (i >= have) break;
+#pragma unroll
+          for (int q = 0; q < VE; q += (K % 4 == 0 ? 4 : 1)) {  // K a multiple of 4: four elements share a channel
+            const int c = first + (shift + min(i + q, have - 1)) / K;
+            const bool keep = nib[wv][c >> 2] >> (c & 3) & 1;
+#pragma unroll
+            for (int k = q; k < q + (K % 4 == 0 ? 4 : 1); ++k) v[j][k] = drop_add(keep, v[j][k], scale, r[j][k]);
+          }
+        }
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < NJ; ++j)
+#pragma unroll
+        for (int q = 0; q < VE; ++q) v[j][q] = drop_add(true, v[j][q], scale, r[j][q]);
+    }
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) U::store(out + base + VE * (lane + 64 * j), have - VE * (lane + 64 * j), v[j]);
   }
 }
 
-hipError_t launch_dropout(const DropArgs& a) {
-  const int64_t total = a.N * a.C * a.K;
+template <class T, int K>
+static hipError_t dropout_t(const DropArgs& a) {
+  const int64_t total = a.N * a.C * K, stretch = 4 * 64 * 4 * Unit<T>::VE;
   if (total == 0) return hipSuccess;
-  const int64_t want = (total + 255) / 256, most = 1 << 20;
-  const dim3 grid((unsigned)(want < most ? want : most));
-  if (a.bf16)
-    hipLaunchKernelGGL((dropout_kernel<__bf16>), grid, dim3(256), 0, a.stream, total, a.K, (const __bf16*)a.x,
-                       (const __bf16*)a.residual, a.rng, a.thr, a.scale, (__bf16*)a.out);
-  else
-    hipLaunchKernelGGL((dropout_kernel<float>), grid, dim3(256), 0, a.stream, total, a.K, (const float*)a.x,
-                       (const float*)a.residual, a.rng, a.thr, a.scale, (float*)a.out);
+  const int64_t want = (total + stretch - 1) / stretch, most = 1 << 20;
+  dropout_kernel<T, K><<<dim3((unsigned)(want < most ? want : most)), dim3(256), 0, a.stream>>>(
+      total, (const T*)a.x, (const T*)a.residual, a.rng, a.thr, a.scale, (T*)a.out);
   return hipGetLastError();
 }
+
+template <class T>
+static hipError_t dropout_k(const DropArgs& a) {
+  switch (a.K) {
+    case 1: return dropout_t<T, 1>(a);
+    case 4: return dropout_t<T, 4>(a);
+    case 9: return dropout_t<T, 9>(a);
+    case 16: return dropout_t<T, 16>(a);
+    case 25: return dropout_t<T, 25>(a);
+    case 36: return dropout_t<T, 36>(a);
+    case 49: return dropout_t<T, 49>(a);
+    default: return hipErrorInvalidValue;
+  }
+}
+
+hipError_t launch_dropout(const DropArgs& a) { return a.bf16 ? dropout_k<__bf16>(a) : dropout_k<float>(a); }
 
 }  // namespace eqtp
