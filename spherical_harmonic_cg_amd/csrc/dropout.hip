@@ -45,77 +45,89 @@ struct Unit {  // 16 bytes of elements, aligned as one element only
   }
 };
 
+constexpr int kDropUnits = 4;  // units a thread in a stretch
+
+// One stretch of `have` elements from `base` on; FULL: all of its units are whole.
+template <class T, int K, bool FULL>
+__device__ __forceinline__ void drop_stretch(int64_t base, int have, int lane, uint8_t* nib, const T* x,
+                                             const T* residual, const int64_t* __restrict__ rng, uint32_t thr,
+                                             float scale, T* out) {
+  using U = Unit<T>;
+  constexpr int VE = U::VE, NJ = kDropUnits;
+  float v[NJ][VE], r[NJ][VE];
+#pragma unroll
+  for (int j = 0; j < NJ; ++j) U::load(x + base + VE * (lane + 64 * j), FULL ? VE : have - VE * (lane + 64 * j), v[j]);
+  if (residual) {
+#pragma unroll
+    for (int j = 0; j < NJ; ++j)
+      U::load(residual + base + VE * (lane + 64 * j), FULL ? VE : have - VE * (lane + 64 * j), r[j]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < NJ; ++j)
+#pragma unroll
+      for (int q = 0; q < VE; ++q) r[j][q] = 0.0f;
+  }
+  if (rng) {
+    const DropState s = drop_state(rng, thr, scale);
+    if constexpr (K == 1) {
+#pragma unroll
+      for (int j = 0; j < NJ; ++j)
+#pragma unroll
+        for (int h = 0; h < VE; h += 4) {
+          const uint32_t keep = keep_nibble(s, (uint64_t)(base + VE * (lane + 64 * j) + h) >> 2);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) v[j][h + q] = drop_add(keep, q, v[j][h + q], scale, r[j][h + q]);
+        }
+    } else {
+      const int64_t c0 = base / K;             // first channel number of the stretch
+      const int shift = (int)(base - c0 * K);  // elements of it before the stretch
+      const int64_t b0 = c0 >> 2;
+      const int blocks = (int)(((base + have - 1) / K >> 2) - b0) + 1, first = (int)(c0 & 3);
+      wave_lds_sync();  // the stretch before has been read
+#pragma unroll 1
+      for (int i = lane; i < blocks; i += 64) nib[i] = (uint8_t)keep_nibble(s, (uint64_t)(b0 + i));
+      wave_lds_sync();
+      constexpr int G = K % 4 == 0 ? 4 : 1;  // elements that surely share a channel
+#pragma unroll
+      for (int j = 0; j < NJ; ++j)
+#pragma unroll
+        for (int q = 0; q < VE; q += G) {
+          int i = VE * (lane + 64 * j) + q;
+          if (!FULL) i = min(i, have - 1);
+          const int c = first + (shift + i) / K;
+          const uint32_t keep = nib[c >> 2] >> (c & 3);
+#pragma unroll
+          for (int k = q; k < q + G; ++k) v[j][k] = drop_add(keep, 0, v[j][k], scale, r[j][k]);
+        }
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < NJ; ++j)
+#pragma unroll
+      for (int q = 0; q < VE; ++q) v[j][q] = drop_add(1, 0, v[j][q], scale, r[j][q]);
+  }
+#pragma unroll
+  for (int j = 0; j < NJ; ++j) U::store(out + base + VE * (lane + 64 * j), FULL ? VE : have - VE * (lane + 64 * j), v[j]);
+}
+
 template <class T, int K>
 __global__ __launch_bounds__(256) void dropout_kernel(int64_t total, const T* x, const T* residual,
                                                       const int64_t* __restrict__ rng, uint32_t thr, float scale,
                                                       T* out) {
-  using U = Unit<T>;
-  constexpr int VE = U::VE, NJ = 4, STRETCH = 64 * NJ * VE;
+  constexpr int STRETCH = 64 * kDropUnits * Unit<T>::VE;
   __shared__ uint8_t nib[4][K == 1 ? 1 : STRETCH / (4 * K) + 3];
-  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   for (int64_t base = ((int64_t)blockIdx.x * 4 + wv) * STRETCH; base < total; base += (int64_t)gridDim.x * 4 * STRETCH) {
-    const int64_t room = total - base;
-    const int have = room < STRETCH ? (int)room : STRETCH;
-    float v[NJ][VE], r[NJ][VE];
-#pragma unroll
-    for (int j = 0; j < NJ; ++j) U::load(x + base + VE * (lane + 64 * j), have - VE * (lane + 64 * j), v[j]);
-    if (residual) {
-#pragma unroll
-      for (int j = 0; j < NJ; ++j) U::load(residual + base + VE * (lane + 64 * j), have - VE * (lane + 64 * j), r[j]);
-    } else {
-#pragma unroll
-      for (int j = 0; j < NJ; ++j)
-#pragma unroll
-        for (int q = 0; q < VE; ++q) r[j][q] = 0.0f;
-    }
-    if (rng) {
-      const DropState s = drop_state(rng, thr, scale);
-      if constexpr (K == 1) {
-#pragma unroll
-        for (int j = 0; j < NJ; ++j) {
-          if (VE * (lane + 64 * j) >= have) break;
-#pragma unroll
-          for (int h = 0; h < VE; h += 4) {
-            const uint32_t keep = keep_nibble(s, (uint64_t)(base + VE * (lane + 64 * j) + h) >> 2);
-#pragma unroll
-            for (int q = 0; q < 4; ++q) v[j][h + q] = drop_add(keep >> q & 1, v[j][h + q], scale, r[j][h + q]);
-          }
-        }
-      } else {
-        const int64_t c0 = base / K;                 // first channel number of the stretch
-        const int shift = (int)(base - c0 * K);      // elements of it before the stretch
-        const int64_t b0 = c0 >> 2;
-        const int blocks = (int)(((base + have - 1) / K >> 2) - b0) + 1, first = (int)(c0 & 3);
-        wave_lds_sync();  // the stretch before has been read
-        for (int i = lane; i < blocks; i += 64) nib[wv][i] = (uint8_t)keep_nibble(s, (uint64_t)(b0 + i));
-        wave_lds_sync();
-#pragma unroll
-        for (int j = 0; j < NJ; ++j) {
-          const int i = VE * (lane + 64 * j);
-          if (i >= have) break;
-#pragma unroll
-          for (int q = 0; q < VE; q += (K % 4 == 0 ? 4 : 1)) {  // K a multiple of 4: four elements share a channel
-            const int c = first + (shift + min(i + q, have - 1)) / K;
-            const bool keep = nib[wv][c >> 2] >> (c & 3) & 1;
-#pragma unroll
-            for (int k = q; k < q + (K % 4 == 0 ? 4 : 1); ++k) v[j][k] = drop_add(keep, v[j][k], scale, r[j][k]);
-          }
-        }
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < NJ; ++j)
-#pragma unroll
-        for (int q = 0; q < VE; ++q) v[j][q] = drop_add(true, v[j][q], scale, r[j][q]);
-    }
-#pragma unroll
-    for (int j = 0; j < NJ; ++j) U::store(out + base + VE * (lane + 64 * j), have - VE * (lane + 64 * j), v[j]);
+    if (total - base >= STRETCH)
+      drop_stretch<T, K, true>(base, STRETCH, lane, nib[wv], x, residual, rng, thr, scale, out);
+    else
+      drop_stretch<T, K, false>(base, (int)(total - base), lane, nib[wv], x, residual, rng, thr, scale, out);
   }
 }
 
 template <class T, int K>
 static hipError_t dropout_t(const DropArgs& a) {
-  const int64_t total = a.N * a.C * K, stretch = 4 * 64 * 4 * Unit<T>::VE;
+  const int64_t total = a.N * a.C * K, stretch = 4 * 64 * kDropUnits * Unit<T>::VE;
   if (total == 0) return hipSuccess;
   const int64_t want = (total + stretch - 1) / stretch, most = 1 << 20;
   dropout_kernel<T, K><<<dim3((unsigned)(want < most ? want : most)), dim3(256), 0, a.stream>>>(

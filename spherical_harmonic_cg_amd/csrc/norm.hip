@@ -19,13 +19,14 @@
 namespace eqtp {
 
 template <class E, class O, int T, int NV, int KT, bool ADD>
-__global__ __launch_bounds__(norm_threads(T)) void norm_kernel(NormArgs a, int A) {
+__global__ __launch_bounds__(norm_threads(T)) void norm_kernel(NormArgs a, int A, NormInv inv) {
   constexpr int R = norm_threads(T) / T;  // rows at a time in a workgroup
   __shared__ float red[T > 64 ? 2 * (T / 64) * (kMaxDeg + 1) : 1];
   __shared__ uint8_t nib[ADD ? R * (T * NV + 2) : 1];
   const int C = a.C, D = C * a.K, deg = KT == 0 ? 1 : a.lmax + 1;
-  Slots<T, KT> sl(C, a.K, A);
-  const int g = threadIdx.x / T;
+  Slots<T, KT> sl(a.K, A);
+  const int g = T < 64 ? threadIdx.x / T : __builtin_amdgcn_readfirstlane(threadIdx.x / T);
+  const bool tail = KT != 1 && (D & 3) != 0;
   int turn = 0;
   constexpr int NB = KT == 0 ? 4 : 1;  // component 0 fills every slot (K = 1), or at most one of a quad
   float w[NV][4], b[NV][NB];
@@ -50,14 +51,14 @@ __global__ __launch_bounds__(norm_threads(T)) void norm_kernel(NormArgs a, int A
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int i = 4 * (sl.t + A * j);
-      load4(x + i, sl.on ? D - i : 0, z[j]);
+      load4(x + i, sl.on ? D - i : 0, tail, z[j]);
     }
     if constexpr (ADD) {
       float res[NV][4];
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
         const int i = 4 * (sl.t + A * j);
-        load4((const E*)a.residual + n * D + i, sl.on ? D - i : 0, res[j]);
+        load4((const E*)a.residual + n * D + i, sl.on ? D - i : 0, tail, res[j]);
       }
       KeepBits<T, KT> kb;
       if (a.rng) kb.begin(ds, n, C, sl.t, nib + g * (T * NV + 2));
@@ -71,8 +72,8 @@ __global__ __launch_bounds__(norm_threads(T)) void norm_kernel(NormArgs a, int A
           const uint32_t keep = a.rng ? kb.quad(ds, c) : 15u;
 #pragma unroll
           for (int q = 0; q < 4; ++q)  // the norm is that of the sum as it is written
-            z[j][q] = (float)(E)drop_add(keep >> q & 1, z[j][q], a.scale, res[j][q]);
-          store4((E*)a.total + n * D + i, D - i, z[j]);
+            z[j][q] = (float)(E)drop_add(keep, q, z[j][q], a.scale, res[j][q]);
+          store4((E*)a.total + n * D + i, D - i, tail, z[j]);
         }
       }
     }
@@ -80,7 +81,7 @@ __global__ __launch_bounds__(norm_threads(T)) void norm_kernel(NormArgs a, int A
 #pragma unroll
     for (int j = 0; j < NV; ++j) mu[0] += sl.scalars(z[j]);
     group_sums<T, 1>(mu, 1, red, turn);
-    mu[0] /= (float)C;
+    mu[0] *= inv.v[0];
     float sq[4] = {};
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
@@ -100,7 +101,7 @@ __global__ __launch_bounds__(norm_threads(T)) void norm_kernel(NormArgs a, int A
     group_sums<T, kMaxDeg>(r, deg, red, turn);
 #pragma unroll
     for (int d = 0; d < kMaxDeg; ++d)
-      if (d < deg) r[d] = 1.0f / sqrtf(r[d] / (float)(C * (2 * d + 1)) + a.eps);
+      if (d < deg) r[d] = rsqrtf(fmaf(r[d], inv.v[d], a.eps));
     float rq[4];
     sl.of_degree(r, deg, rq);
 #pragma unroll
@@ -110,7 +111,7 @@ __global__ __launch_bounds__(norm_threads(T)) void norm_kernel(NormArgs a, int A
 #pragma unroll
       for (int q = 0; q < 4; ++q)
         o[q] = fmaf(z[j][q] * rq[q], w[j][q], KT == 0 ? b[j][q % NB] : (sl.l(q) == 0 ? b[j][0] : 0.0f));
-      if (sl.on) store4((O*)a.out + n * D + i, D - i, o);
+      if (sl.on) store4((O*)a.out + n * D + i, D - i, tail, o);
     }
     if (a.stats && sl.t == 0) {
       float* st = a.stats + n * (a.lmax + 2);
@@ -129,7 +130,7 @@ static hipError_t norm_t(const NormArgs& a) {
   const NormShape s = norm_shape(a.C, a.K);
   const dim3 grid(norm_grid(a.N, s.T, kNormBlocks)), block(norm_threads(s.T));
 #define EQTP_NORM(T_, NV_) \
-  (norm_kernel<E, O, T_, NV_, KT, ADD><<<grid, block, 0, a.stream>>>(a, s.A), hipGetLastError())
+  (norm_kernel<E, O, T_, NV_, KT, ADD><<<grid, block, 0, a.stream>>>(a, s.A, norm_inv(a.C)), hipGetLastError())
   return EQTP_NORM_SHAPES(s, EQTP_NORM);
 #undef EQTP_NORM
 }

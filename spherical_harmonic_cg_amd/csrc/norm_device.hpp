@@ -19,42 +19,46 @@ __device__ __forceinline__ int degree_of(int m) {
 typedef float f4u __attribute__((ext_vector_type(4), aligned(4)));
 typedef __bf16 b4u __attribute__((ext_vector_type(4), aligned(2)));
 
-__device__ __forceinline__ void load4(const float* p, int left, float (&v)[4]) {
-  if (left >= 4) {
-    const f4u t = *reinterpret_cast<const f4u*>(p);
+// `left` elements of the row are left from p on (0 or less: none); `tail`: there are rows whose last quad is short
+// (the same for every thread).
+__device__ __forceinline__ void widen4(const float* p, float (&v)[4]) {
+  const f4u t = *reinterpret_cast<const f4u*>(p);
 #pragma unroll
-    for (int q = 0; q < 4; ++q) v[q] = t[q];
+  for (int q = 0; q < 4; ++q) v[q] = t[q];
+}
+__device__ __forceinline__ void widen4(const __bf16* p, float (&v)[4]) {
+  const b4u t = *reinterpret_cast<const b4u*>(p);
+#pragma unroll
+  for (int q = 0; q < 4; ++q) v[q] = (float)t[q];
+}
+template <class T>
+__device__ __forceinline__ void load4(const T* p, int left, bool tail, float (&v)[4]) {
+#pragma unroll
+  for (int q = 0; q < 4; ++q) v[q] = 0.0f;
+  if (left <= 0) return;
+  if (tail && left < 4) {
+#pragma unroll
+    for (int q = 0; q < 3; ++q)
+      if (q < left) v[q] = (float)p[q];
   } else {
-#pragma unroll
-    for (int q = 0; q < 4; ++q) v[q] = q < left ? p[q] : 0.0f;
+    widen4(p, v);
   }
 }
-__device__ __forceinline__ void load4(const __bf16* p, int left, float (&v)[4]) {
-  if (left >= 4) {
-    const b4u t = *reinterpret_cast<const b4u*>(p);
-#pragma unroll
-    for (int q = 0; q < 4; ++q) v[q] = (float)t[q];
-  } else {
-#pragma unroll
-    for (int q = 0; q < 4; ++q) v[q] = q < left ? (float)p[q] : 0.0f;
-  }
+__device__ __forceinline__ void narrow4(float* p, const float (&v)[4]) {
+  *reinterpret_cast<f4u*>(p) = f4u{v[0], v[1], v[2], v[3]};
 }
-__device__ __forceinline__ void store4(float* p, int left, const float (&v)[4]) {
-  if (left >= 4) {
-    *reinterpret_cast<f4u*>(p) = f4u{v[0], v[1], v[2], v[3]};
-  } else {
-#pragma unroll
-    for (int q = 0; q < 4; ++q)
-      if (q < left) p[q] = v[q];
-  }
+__device__ __forceinline__ void narrow4(__bf16* p, const float (&v)[4]) {
+  *reinterpret_cast<b4u*>(p) = b4u{(__bf16)v[0], (__bf16)v[1], (__bf16)v[2], (__bf16)v[3]};
 }
-__device__ __forceinline__ void store4(__bf16* p, int left, const float (&v)[4]) {
-  if (left >= 4) {
-    *reinterpret_cast<b4u*>(p) = b4u{(__bf16)v[0], (__bf16)v[1], (__bf16)v[2], (__bf16)v[3]};
-  } else {
+template <class T>
+__device__ __forceinline__ void store4(T* p, int left, bool tail, const float (&v)[4]) {
+  if (left <= 0) return;
+  if (tail && left < 4) {
 #pragma unroll
-    for (int q = 0; q < 4; ++q)
-      if (q < left) p[q] = (__bf16)v[q];
+    for (int q = 0; q < 3; ++q)
+      if (q < left) p[q] = (T)v[q];
+  } else {
+    narrow4(p, v);
   }
 }
 
@@ -126,6 +130,7 @@ struct KeepBits {
     const uint64_t b0 = first >> 2;
     const int blocks = (int)(((first + C - 1) >> 2) - b0) + 1;
     sync();  // the row before has been read
+#pragma unroll 1
     for (int i = t; i < blocks; i += T) nib[i] = (uint8_t)keep_nibble(s, b0 + i);
     sync();
   }
@@ -133,14 +138,21 @@ struct KeepBits {
     if constexpr (T > 64) __syncthreads();
     else wave_lds_sync();
   }
-  // keep bits of the channels of slots 0..3 of a quad (c: their channels)
+  // keep bits of a quad's slots (c: their channels, below C)
   __device__ __forceinline__ uint32_t quad(const DropState& s, const int (&c)[4]) const {
     if (direct) return keep_nibble(s, (first + c[0]) >> 2);
     const int off = (int)(first & 3);
-    if constexpr (KT == 1) return (nib[(off + c[0]) >> 2] >> ((off + c[0]) & 3) & 1) ? 15u : 0u;
+    if constexpr (KT == 1) return 0u - (nib[(off + c[0]) >> 2] >> ((off + c[0]) & 3) & 1u);
     uint32_t bits = 0;
+    if constexpr (KT == 2) {  // two channels at most
+      const uint32_t a = nib[(off + c[0]) >> 2] >> ((off + c[0]) & 3) & 1u;
+      const uint32_t b = nib[(off + c[3]) >> 2] >> ((off + c[3]) & 3) & 1u;
 #pragma unroll
-    for (int q = 0; q < 4; ++q) bits |= (uint32_t)(nib[(off + c[q]) >> 2] >> ((off + c[q]) & 3) & 1) << q;
+      for (int q = 0; q < 4; ++q) bits |= (c[q] == c[0] ? a : b) << q;
+    } else {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) bits |= (nib[(off + c[q]) >> 2] >> ((off + c[q]) & 3) & 1u) << q;
+    }
     return bits;
   }
 };
@@ -151,22 +163,24 @@ struct KeepBits {
 // scalar registers several times over.  Component 0 is the one of degree 0.
 template <int T, int KT>
 struct Slots {
-  int t, degrees, step, C, K;
+  int t, degrees, c0, wrap, step;
   bool on;  // takes quads
-  __device__ __forceinline__ Slots(int C_, int K_, int A) : C(C_), K(K_) {
+  __device__ __forceinline__ Slots(int K, int A) {
     t = threadIdx.x % T;
     on = t < A;
     step = 4 * A / K;
     degrees = 0;
+    c0 = 4 * t / K;
+    wrap = K - (4 * t - c0 * K);  // the first slot of the next channel (K > 4: there is one at most)
     if constexpr (KT != 0)
 #pragma unroll
       for (int q = 0; q < 4; ++q) degrees |= degree_of((4 * t + q) % K) << (8 * q);
   }
   // at the head of a row: keeps what follows from t and the degrees out of the registers between rows
-  __device__ __forceinline__ void row() { asm volatile("" : "+v"(t), "+v"(degrees)); }
+  __device__ __forceinline__ void row() { asm volatile("" : "+v"(t), "+v"(degrees), "+v"(c0), "+v"(wrap)); }
   __device__ __forceinline__ int l(int q) const { return KT == 0 ? 0 : degrees >> (8 * q) & 255; }
   __device__ __forceinline__ int channel(int q, int j) const {
-    return (KT == 0 ? 4 * t + q : (KT == 1 ? 4 * t / K : (4 * t + q) / K)) + j * step;
+    return c0 + j * step + (KT == 0 ? q : (KT == 1 ? 0 : (q >= wrap ? 1 : 0)));
   }
   // sums of slot values by degree, added into s
   __device__ __forceinline__ void by_degree(const float (&v)[4], int deg, float* s) const {
@@ -200,42 +214,56 @@ struct Slots {
   }
 };
 
-constexpr int norm_threads(int T) { return T > 256 ? T : 256; }
+// threads of a workgroup: several rows of up to 64 threads, or one
+constexpr int norm_threads(int T) { return T > 64 ? T : 256; }
+
+// 1 / (C (2 d + 1)): what turns a degree's sum into a mean
+struct NormInv {
+  float v[kMaxDeg];
+};
+inline NormInv norm_inv(int C) {
+  NormInv r;
+  for (int d = 0; d < kMaxDeg; ++d) r.v[d] = (float)(1.0 / ((double)C * (2 * d + 1)));
+  return r;
+}
 
 // ---- choice of the group ----------------------------------------------------
-// The smallest group whose threads hold the row in at most four quads (five
-// for 1024 threads, so that every row of up to 16384 elements fits).
+// The smallest group whose threads hold the row in four quads or fewer (512
+// threads take the rest, up to nine: every row of up to 16384 elements).  The
+// work beside the elements (two sums over the group, a square root for each
+// degree) is the same for every thread of a group, so fewer threads do less of
+// it; more quads a thread cost registers, and with them waves in flight.
 struct NormShape {
   int T, NV, A;
 };
 inline NormShape norm_shape(int C, int K) {
   const int D = C * K, Q = (D + 3) / 4;
   const int P = K % 4 == 0 ? K / 4 : K;
-  NormShape s = {1024, 5, 1024 / P * P};
-  for (int T : {16, 64, 256, 1024}) {
+  NormShape s = {512, 0, 512 / P * P};
+  for (int T : {16, 64, 128, 256}) {
     const int A = T / P * P;
-    if (A == 0) continue;
-    const int nv = (Q + A - 1) / A;
-    if (nv <= 4) {
-      s = {T, nv, A};
+    if (A > 0 && (Q + A - 1) / A <= 4) {
+      s = {T, 0, A};
       break;
     }
   }
+  s.NV = (Q + s.A - 1) / s.A;
   return s;
 }
 
-// workgroups that walk over the rows: at most per_cu of 256 threads a compute unit
+// workgroups that walk over the rows: at most per_cu times four waves a compute unit
 inline int norm_grid(int64_t N, int T, int per_cu) {
   const int64_t rows = norm_threads(T) / T;
-  const int64_t want = (N + rows - 1) / rows, most = (int64_t)num_cus() * (T > 256 ? per_cu / 4 : per_cu);
+  const int64_t want = (N + rows - 1) / rows, most = (int64_t)num_cus() * per_cu * 256 / norm_threads(T);
   return (int)(want < most ? want : most);
 }
 
-// Calls F<T, NV> for a shape: NV is the next of the built sizes.
-#define EQTP_NORM_SHAPES(s, F)                                            \
-  ((s).T == 16   ? ((s).NV <= 1 ? F(16, 1) : ((s).NV <= 2 ? F(16, 2) : F(16, 4))) \
-   : (s).T == 64  ? ((s).NV <= 2 ? F(64, 2) : F(64, 4))                   \
-   : (s).T == 256 ? ((s).NV <= 2 ? F(256, 2) : F(256, 4))                 \
-                  : ((s).NV <= 2 ? F(1024, 2) : F(1024, 5)))
+// Calls F(T, NV) for a shape: NV is the next of the built sizes.
+#define EQTP_NORM_SHAPES(s, F)                                                     \
+  ((s).T == 16    ? ((s).NV <= 1 ? F(16, 1) : ((s).NV <= 2 ? F(16, 2) : F(16, 4))) \
+   : (s).T == 64  ? ((s).NV <= 2 ? F(64, 2) : F(64, 4))                            \
+   : (s).T == 128 ? ((s).NV <= 2 ? F(128, 2) : F(128, 4))                          \
+   : (s).T == 256 ? F(256, 4)                                                      \
+                  : ((s).NV <= 5 ? F(512, 5) : F(512, 9)))
 
 }  // namespace eqtp

@@ -14,15 +14,16 @@
 namespace eqtp {
 
 template <class E, class O, int T, int NV, int KT>
-__global__ __launch_bounds__(norm_threads(T)) void norm_grad_kernel(NormGradArgs a, int A, float* part) {
+__global__ __launch_bounds__(norm_threads(T)) void norm_grad_kernel(NormGradArgs a, int A, NormInv inv, float* part) {
   constexpr int TH = norm_threads(T), R = TH / T;
-  constexpr bool HOLD = T < 1024;  // weights in registers (1024 threads: too few of them)
+  constexpr bool HOLD = NV < 9;  // weights in registers
   __shared__ float red[T > 64 ? 2 * (T / 64) * (kMaxDeg + 1) : 1];
   __shared__ uint8_t nib[R * (T * NV + 2)];
   __shared__ float pos[R * T * NV * 4];  // per group: a value for each place of a row
   const int C = a.C, D = C * a.K, deg = KT == 0 ? 1 : a.lmax + 1;
-  Slots<T, KT> sl(C, a.K, A);
-  const int g = threadIdx.x / T;
+  Slots<T, KT> sl(a.K, A);
+  const int g = T < 64 ? threadIdx.x / T : __builtin_amdgcn_readfirstlane(threadIdx.x / T);
+  const bool tail = KT != 1 && (D & 3) != 0;
   int turn = 0;
   constexpr int NB = KT == 0 ? 4 : 1;  // component 0 fills every slot (K = 1), or at most one of a quad
   float w[NV][4], aw[NV][4] = {}, ab[NV][NB] = {};
@@ -46,9 +47,16 @@ __global__ __launch_bounds__(norm_threads(T)) void norm_grad_kernel(NormGradArgs
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int i = 4 * (sl.t + A * j);
-      load4((const E*)a.total + n * D + i, sl.on ? D - i : 0, z[j]);
-      load4((const O*)a.gout + n * D + i, sl.on ? D - i : 0, go[j]);
+      load4((const E*)a.total + n * D + i, sl.on ? D - i : 0, tail, z[j]);
+      load4((const O*)a.gout + n * D + i, sl.on ? D - i : 0, tail, go[j]);
     }
+    float gt[NV][4] = {};
+    if (a.gtotal)
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const int i = 4 * (sl.t + A * j);
+        load4((const E*)a.gtotal + n * D + i, sl.on ? D - i : 0, tail, gt[j]);
+      }
     const float* st = a.stats + n * (a.lmax + 2);
     const float mu = st[0];
     float rq[4], sq[4] = {}, v[kMaxDeg + 1] = {};
@@ -80,10 +88,10 @@ __global__ __launch_bounds__(norm_threads(T)) void norm_grad_kernel(NormGradArgs
         for (int q = 0; q < 4; ++q) sq[q] = 0.0f;
       sl.by_degree(sq, deg, v + 1);
       group_sums<T, kMaxDeg + 1>(v, deg + 1, red, turn);
-      const float am = v[0] / (float)C;
+      const float am = v[0] * inv.v[0];
 #pragma unroll
       for (int d = 0; d < kMaxDeg; ++d)
-        if (d < deg) v[1 + d] /= (float)(C * (2 * d + 1));
+        if (d < deg) v[1 + d] *= inv.v[d];
       float mq[4];
       sl.of_degree(v + 1, deg, mq);
       KeepBits<T, KT> kb;
@@ -92,20 +100,19 @@ __global__ __launch_bounds__(norm_threads(T)) void norm_grad_kernel(NormGradArgs
       for (int j = 0; j < NV; ++j) {
         const int i = 4 * (sl.t + A * j);
         if (sl.on && i < D) {
-          float gz[4], gt[4] = {};
-          if (a.gtotal) load4((const E*)a.gtotal + n * D + i, D - i, gt);
+          float gz[4];
 #pragma unroll
           for (int q = 0; q < 4; ++q)
-            gz[q] = fmaf(rq[q], (go[j][q] * w[j][q] - (sl.l(q) == 0 ? am : 0.0f)) - z[j][q] * mq[q], gt[q]);
-          if (a.gres) store4((E*)a.gres + n * D + i, D - i, gz);
+            gz[q] = fmaf(rq[q], (go[j][q] * w[j][q] - (sl.l(q) == 0 ? am : 0.0f)) - z[j][q] * mq[q], gt[j][q]);
+          if (a.gres) store4((E*)a.gres + n * D + i, D - i, tail, gz);
           if (a.gx) {
             int c[4];
 #pragma unroll
             for (int q = 0; q < 4; ++q) c[q] = min(sl.channel(q, j), C - 1);
             const uint32_t keep = a.rng ? kb.quad(ds, c) : 15u;
 #pragma unroll
-            for (int q = 0; q < 4; ++q) gz[q] = drop_add(keep >> q & 1, gz[q], a.scale, 0.0f);
-            store4((E*)a.gx + n * D + i, D - i, gz);
+            for (int q = 0; q < 4; ++q) gz[q] = drop_add(keep, q, gz[q], a.scale, 0.0f);
+            store4((E*)a.gx + n * D + i, D - i, tail, gz);
           }
         }
       }
@@ -168,11 +175,11 @@ __global__ __launch_bounds__(1024) void norm_weight_sum_kernel(int cols, int wco
 }
 
 constexpr int kGradBlocks = 4;
+constexpr int kMaxParts = 2048;
 
 int64_t norm_workspace_floats(int64_t N, int C, int lmax) {
-  // a line for each workgroup of the gradient kernel: at most one a node and kGradBlocks a compute unit (of 256)
-  const int64_t most = (int64_t)kGradBlocks * 256;
-  return (N < most ? (N > 0 ? N : 1) : most) * (lmax + 2) * C;
+  // a line for each workgroup of the gradient kernel: at most kMaxParts, and one a node
+  return (N < kMaxParts ? (N > 0 ? N : 1) : kMaxParts) * (lmax + 2) * C;
 }
 
 template <class E, class O, int KT>
@@ -182,11 +189,11 @@ static hipError_t norm_grad_t(const NormGradArgs& a) {
   if (a.N > 0) {
     const NormShape s = norm_shape(a.C, a.K);
     parts = norm_grid(a.N, s.T, kGradBlocks);
-    if (parts > 256 * kGradBlocks) parts = 256 * kGradBlocks;
+    if (parts > kMaxParts) parts = kMaxParts;
     const dim3 grid(parts), block(norm_threads(s.T));
     float* part = sums ? a.ws : nullptr;
 #define EQTP_NORM(T_, NV_) \
-  (norm_grad_kernel<E, O, T_, NV_, KT><<<grid, block, 0, a.stream>>>(a, s.A, part), hipGetLastError())
+  (norm_grad_kernel<E, O, T_, NV_, KT><<<grid, block, 0, a.stream>>>(a, s.A, norm_inv(a.C), part), hipGetLastError())
     const hipError_t e = EQTP_NORM_SHAPES(s, EQTP_NORM);
 #undef EQTP_NORM
     if (e != hipSuccess) return e;

@@ -50,10 +50,13 @@ __device__ __forceinline__ uint32_t keep_nibble(const DropState& s, uint64_t blo
          (uint32_t)(w[3] >= s.thr) << 3;
 }
 
-// The value of a kept or dropped x beside its residual; the norm's kernels and
-// the dropout kernel share this expression, so their sums have the same bits.
-__device__ __forceinline__ float drop_add(bool keep, float x, float scale, float residual) {
-  return keep ? fmaf(x, scale, residual) : residual;
+// The value of x at place q of a quad with these keep bits, beside its residual; the norm's kernels and the dropout
+// kernel share this expression, so their sums have the same bits.  The choice goes through a mask in a vector
+// register: lane masks for every place of a row would not fit in the scalar registers.
+__device__ __forceinline__ float drop_add(uint32_t keep, int q, float x, float scale, float residual) {
+  const uint32_t m = (uint32_t)__builtin_amdgcn_sbfe((int)keep, q, 1);
+  const uint32_t in = __builtin_bit_cast(uint32_t, fmaf(x, scale, residual));
+  return __builtin_bit_cast(float, (in & m) | (__builtin_bit_cast(uint32_t, residual) & ~m));
 }
 
 }  // namespace eqtp
