@@ -2,16 +2,92 @@
 // backward; no per-edge vectors are formed in memory.
 //   s = scale q[dst] . k[src] + bias,  w = softmax of s over the row,
 //   out[n] = sum w v[src].
-// One wave a (row, head); the softmax runs along the row with a running
-// maximum and sum.
+//
+// Every edge reads a row of k and one of v by its source (backward: by rows k
+// and v again, by sources q and the output's gradient), 2 E C K elements that
+// come from the caches next to memory; a row of q meets each of them once, so
+// the products stay on the vector ALUs and the gathers bound the kernels.
+//
+// A head's row of D elements is a line of 16-byte units.  G lanes hold it, NU
+// units each (unit lig + G j), beside the q and sums of the same places; dot
+// products are added over the G lanes by register moves.  A wave takes HW
+// heads of a row side by side and, where they do not fill it, ES edges at a
+// time (their partial results are joined at the row's end).  EU edges are
+// loaded together, with the next ones' indexes and biases on the way.  The
+// softmax runs along the row in one pass: a running maximum and sum, one
+// rescaling for each EU edges.
+//
+// Few long rows (a readout) are cut into S pieces of about equal length, whose
+// partial results go through the workspace and are added by a second kernel.
+#include <type_traits>
+
 #include "eqtp_device.hpp"
 #include "eqtp_kernels.hpp"
 
 namespace eqtp {
 
-__device__ __forceinline__ float wave_sum(float v) {
+constexpr float kLog2E = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+// Differences of logits are taken before the change to base 2: biases of the type's lowest value would overflow in it.
+__device__ __forceinline__ float exp_of(float v) { return __builtin_amdgcn_exp2f(v * kLog2E); }
+
+// ---- 16 bytes of a row --------------------------------------------------------
+typedef uint32_t u4u __attribute__((ext_vector_type(4), aligned(2)));
+typedef uint32_t u4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+
+template <class T>
+struct El;
+template <>
+struct El<float> {
+  static constexpr int VE = 4;
+  static __device__ __forceinline__ float at(const u4& r, int i) {
+    const uint32_t w = r[i];  // a value: the cast of a vector's element itself takes element 0
+    return __builtin_bit_cast(float, w);
+  }
+  static __device__ __forceinline__ float dot(const u4& a, const u4& b, float c) {
 #pragma unroll
-  for (int off = 32; off; off >>= 1) v += __shfl_xor(v, off, 64);
+    for (int i = 0; i < 4; ++i) c = fmaf(at(a, i), at(b, i), c);
+    return c;
+  }
+};
+template <>
+struct El<__bf16> {
+  static constexpr int VE = 8;
+  static __device__ __forceinline__ float at(const u4& r, int i) {
+    return __builtin_bit_cast(float, i & 1 ? r[i >> 1] & 0xffff0000u : r[i >> 1] << 16);
+  }
+  // pairs of products, summed in fp32
+  static __device__ __forceinline__ float dot(const u4& a, const u4& b, float c) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t x = a[i], y = b[i];
+      c = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, x), __builtin_bit_cast(bf16x2, y), c, false);
+    }
+    return c;
+  }
+};
+
+// Sums over groups of G consecutive lanes, the same bits in each of them.
+template <int CTRL>
+__device__ __forceinline__ float dpp_plus(float v) {
+  return v + __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xf, 0xf, false));
+}
+template <int G>
+__device__ __forceinline__ float lane_sum(float v) {
+  if constexpr (G >= 2) v = dpp_plus<0xB1>(v);    // lanes 1 0 3 2
+  if constexpr (G >= 4) v = dpp_plus<0x4E>(v);    // lanes 2 3 0 1
+  if constexpr (G >= 8) v = dpp_plus<0x141>(v);   // mirrored in 8
+  if constexpr (G >= 16) v = dpp_plus<0x140>(v);  // mirrored in 16
+  if constexpr (G >= 32) {
+    const unsigned a = __builtin_bit_cast(unsigned, v);
+    const auto r = __builtin_amdgcn_permlane16_swap(a, a, false, false);
+    v = __builtin_bit_cast(float, (unsigned)r[0]) + __builtin_bit_cast(float, (unsigned)r[1]);
+  }
+  if constexpr (G >= 64) {
+    const unsigned a = __builtin_bit_cast(unsigned, v);
+    const auto r = __builtin_amdgcn_permlane32_swap(a, a, false, false);
+    v = __builtin_bit_cast(float, (unsigned)r[0]) + __builtin_bit_cast(float, (unsigned)r[1]);
+  }
   return v;
 }
 
@@ -25,194 +101,717 @@ __device__ __forceinline__ RowRange row_range(const int32_t* __restrict__ ptr, i
   e = e < b ? b : (e > E ? E : e);
   return {b, e};
 }
+// Piece s of S of it.
+__device__ __forceinline__ RowRange piece(RowRange r, int s, int S) {
+  const int64_t len = r.e - r.b;
+  return {r.b + len * s / S, r.b + len * (s + 1) / S};
+}
 
-template <class T, int NE>
-__global__ __launch_bounds__(256) void attn_kernel(AttnArgs a) {
-  const int lane = threadIdx.x & 63;
-  const int64_t task = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (task >= a.N * a.heads) return;
-  const int64_t n = task / a.heads;
-  const int h = (int)(task - n * a.heads), hk = h / (a.heads / a.kv_heads);
-  const T* q = (const T*)a.q + task * a.D;
-  float qr[NE], acc[NE];
+// How a wave's lanes lie over (edge, head, place in the head's row).  MODE 0:
+// the units fill the G lanes and rows are whole units; 1: units past the row
+// are masked and the row's last unit ends at its end (its first elements, which
+// the unit before holds, are masked); 2: rows shorter than a unit.
+template <class T, int G, int NU, int MODE>
+struct Lanes {
+  static constexpr int VE = El<T>::VE;
+  int lig, hs, es;
+  int off[NU];               // first element of each unit
+  u4 mask[MODE == 1 ? NU : 1];
+  __device__ __forceinline__ Lanes(int D, int HW) {
+    const int lane = threadIdx.x & 63;
+    lig = lane & (G - 1);
+    hs = lane / G & (HW - 1);
+    es = lane / (G * HW);
 #pragma unroll
-  for (int i = 0; i < NE; ++i) {
-    const int d = lane + 64 * i;
-    qr[i] = d < a.D ? (float)q[d] : 0.0f;
-    acc[i] = 0.0f;
+    for (int j = 0; j < NU; ++j) {
+      off[j] = VE * (lig + G * j);
+      if constexpr (MODE == 1) {
+        const int at = min(off[j], D - VE), lo = off[j] < D ? off[j] - at : VE;  // elements below lo are not this unit's
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if constexpr (VE == 4) mask[j][i] = i >= lo ? ~0u : 0u;
+          else mask[j][i] = (2 * i >= lo ? 0xffffu : 0u) | (2 * i + 1 >= lo ? 0xffff0000u : 0u);
+        }
+        off[j] = at;
+      }
+    }
   }
-  const RowRange r = row_range(a.row_ptr, n, a.E);
+  __device__ __forceinline__ u4 load(const T* row, int j, int D) const {
+    if constexpr (MODE == 2) {
+      u4 r = {0u, 0u, 0u, 0u};
+#pragma unroll
+      for (int i = 0; i < VE; ++i)
+        if (i < D) {
+          if constexpr (VE == 4) r[i] = __builtin_bit_cast(uint32_t, row[i]);
+          else r[i >> 1] |= (uint32_t)__builtin_bit_cast(uint16_t, row[i]) << (16 * (i & 1));
+        }
+      return r;
+    } else {
+      u4 r = *reinterpret_cast<const u4u*>(row + off[j]);
+      if constexpr (MODE == 1) r &= mask[j];
+      return r;
+    }
+  }
+  // stores f(i) at the unit's own elements
+  template <class F>
+  __device__ __forceinline__ void store(T* row, int j, int D, F f) const {
+    if constexpr (MODE == 0) {
+      u4 r = {0u, 0u, 0u, 0u};
+#pragma unroll
+      for (int i = 0; i < VE; ++i) {
+        const T t = (T)f(i);
+        if constexpr (VE == 4) r[i] = __builtin_bit_cast(uint32_t, t);
+        else r[i >> 1] |= (uint32_t)__builtin_bit_cast(uint16_t, t) << (16 * (i & 1));
+      }
+      *reinterpret_cast<u4u*>(row + off[j]) = r;
+    } else {
+#pragma unroll
+      for (int i = 0; i < VE; ++i) {
+        const bool own = MODE == 2 ? i < D : (VE == 4 ? mask[MODE == 1 ? j : 0][i & 3] != 0u
+                                                      : (mask[MODE == 1 ? j : 0][i >> 1] >> (16 * (i & 1)) & 1u) != 0u);
+        if (own) row[off[j] + i] = (T)f(i);
+      }
+    }
+  }
+  template <class F>
+  __device__ __forceinline__ void store_f32(float* row, int j, int D, F f) const {
+#pragma unroll
+    for (int i = 0; i < VE; ++i) {
+      const bool own = MODE == 0 || (MODE == 2 ? i < D : (VE == 4 ? mask[MODE == 1 ? j : 0][i & 3] != 0u
+                                                                  : (mask[MODE == 1 ? j : 0][i >> 1] >> (16 * (i & 1)) & 1u) != 0u));
+      if (own) row[off[j] + i] = f(i);
+    }
+  }
+};
+
+// What a launch fixes for its waves.
+struct Tiling {
+  int HW, ES;       // heads and edges of a wave side by side (powers of two)
+  int blocks;       // of HW heads
+  int S;            // pieces of a row
+  int64_t first;    // task of the launch's first wave, and the end of the tasks
+  int64_t end;
+  float* part;      // S > 1: partial results
+};
+
+__device__ __forceinline__ u4 keep_if(const u4& v, bool keep) {
+  const uint32_t m = keep ? ~0u : 0u;
+  return v & u4{m, m, m, m};
+}
+
+// One wave: heads hb HW .. of row n, piece s.
+template <class T, int G, int NU, int MODE, int EU>
+__global__ __launch_bounds__(256) void attn_kernel(AttnArgs a, Tiling t) {
+  constexpr int VE = El<T>::VE;
+  const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t task = t.first + (int64_t)blockIdx.x * 4 + wv;
+  if (task >= t.end) return;
+  const int64_t row = task / t.blocks, n = t.S == 1 ? row : row / t.S;
+  const int hb = (int)(task - row * t.blocks), sp = (int)(row - n * t.S), D = a.D, H = a.heads;
+  const Lanes<T, G, NU, MODE> ln(D, t.HW);
+  const int h = min(hb * t.HW + ln.hs, H - 1), R = H / a.kv_heads;
+  const bool mine = hb * t.HW + ln.hs < H;
+  const int64_t rowlen = (int64_t)a.kv_heads * D;
+  const T* kb = (const T*)a.k + (int64_t)(h / R) * D;
+  const T* vb = (const T*)a.v + (int64_t)(h / R) * D;
+  u4 q[NU];
+  float acc[NU][VE] = {};
+#pragma unroll
+  for (int j = 0; j < NU; ++j) q[j] = ln.load((const T*)a.q + (n * H + h) * D, j, D);
+  const RowRange r = piece(row_range(a.row_ptr, n, a.E), sp, t.S);
   float top = -INFINITY, sum = 0.0f;
-  for (int64_t e = r.b; e < r.e; ++e) {
-    const float bias = a.bias ? a.bias[e * a.heads + h] : 0.0f;
-    if (bias == -INFINITY) continue;
-    const int64_t at = ((int64_t)clamp_index(a.src[e], (int)a.M) * a.kv_heads + hk) * a.D;
-    float dot = 0.0f;
+  int idx[EU];
+  float bias[EU];
+  auto fetch = [&](int64_t e0) {
 #pragma unroll
-    for (int i = 0; i < NE; ++i) {
-      const int d = lane + 64 * i;
-      if (d < a.D) dot = fmaf(qr[i], (float)((const T*)a.k)[at + d], dot);
+    for (int i = 0; i < EU; ++i) {
+      int64_t e = e0 + i * t.ES + ln.es;
+      e = e < r.e ? e : r.e - 1;
+      idx[i] = a.src[e];
+      bias[i] = a.bias ? a.bias[e * H + h] : 0.0f;
     }
-    const float s = fmaf(a.scale, wave_sum(dot), bias);
-    const float t = fmaxf(top, s);
-    const float w = s == -INFINITY ? 0.0f : __expf(s - t), keep = top == -INFINITY ? 0.0f : __expf(top - t);
-    top = t;
-    sum = fmaf(sum, keep, w);
+  };
+  if (r.b < r.e) fetch(r.b);
+  for (int64_t e0 = r.b; e0 < r.e; e0 += EU * t.ES) {
+    u4 k[EU][NU], v[EU][NU];
+    float s[EU];
+    bool live[EU], all = true;
 #pragma unroll
-    for (int i = 0; i < NE; ++i) {
-      const int d = lane + 64 * i;
-      if (d < a.D) acc[i] = fmaf(acc[i], keep, w * (float)((const T*)a.v)[at + d]);
+    for (int i = 0; i < EU; ++i) {
+      const int64_t at = (int64_t)clamp_index(idx[i], (int)a.M) * rowlen;
+#pragma unroll
+      for (int j = 0; j < NU; ++j) k[i][j] = ln.load(kb + at, j, D);
+#pragma unroll
+      for (int j = 0; j < NU; ++j) v[i][j] = ln.load(vb + at, j, D);
+      s[i] = bias[i];
+      live[i] = bias[i] != -INFINITY && e0 + i * t.ES + ln.es < r.e;
+      all = all && live[i];
+    }
+    if (e0 + EU * t.ES < r.e) fetch(e0 + EU * t.ES);
+    float m = top;
+#pragma unroll
+    for (int i = 0; i < EU; ++i) {
+      float d = 0.0f;
+#pragma unroll
+      for (int j = 0; j < NU; ++j) d = El<T>::dot(q[j], k[i][j], d);
+      s[i] = fmaf(a.scale, lane_sum<G>(d), s[i]);
+    }
+    if (!__all(all)) {  // masked edges and places past the row take no part, whatever they hold
+#pragma unroll
+      for (int i = 0; i < EU; ++i) {
+        s[i] = live[i] ? s[i] : -INFINITY;
+#pragma unroll
+        for (int j = 0; j < NU; ++j) v[i][j] = keep_if(v[i][j], live[i]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < EU; ++i) m = fmaxf(m, s[i]);
+    const float base = m == -INFINITY ? 0.0f : m;
+    const float down = exp_of(top - base);
+    top = m;
+    sum *= down;
+#pragma unroll
+    for (int j = 0; j < NU; ++j)
+#pragma unroll
+      for (int x = 0; x < VE; ++x) acc[j][x] *= down;
+#pragma unroll
+    for (int i = 0; i < EU; ++i) {
+      const float w = exp_of(s[i] - base);
+      sum += w;
+#pragma unroll
+      for (int j = 0; j < NU; ++j)
+#pragma unroll
+        for (int x = 0; x < VE; ++x) acc[j][x] = fmaf(w, El<T>::at(v[i][j], x), acc[j][x]);
     }
   }
-  const bool any = !(sum == 0.0f);
+  // join the edges that ran side by side
+  for (int d = G * t.HW; d < 64; d <<= 1) {
+    const float other = __shfl_xor(top, d, 64), m = fmaxf(top, other), base = m == -INFINITY ? 0.0f : m;
+    const float down = exp_of(top - base), od = exp_of(other - base);
+    top = m;
+    sum = fmaf(sum, down, __shfl_xor(sum, d, 64) * od);
 #pragma unroll
-  for (int i = 0; i < NE; ++i) {
-    const int d = lane + 64 * i;
-    if (d < a.D) ((T*)a.out)[task * a.D + d] = (T)(any ? acc[i] / sum : 0.0f);
+    for (int j = 0; j < NU; ++j)
+#pragma unroll
+      for (int x = 0; x < VE; ++x) acc[j][x] = fmaf(acc[j][x], down, __shfl_xor(acc[j][x], d, 64) * od);
   }
-  if (a.lse && lane == 0) a.lse[task] = any ? top + logf(sum) : -INFINITY;
+  if (!mine || ln.es != 0) return;
+  if (t.S > 1) {
+    float* ml = t.part + (int64_t)a.N * t.S * H * D;
+#pragma unroll
+    for (int j = 0; j < NU; ++j) ln.store_f32(t.part + (row * H + h) * D, j, D, [&](int x) { return acc[j][x]; });
+    if (ln.lig == 0) {
+      ml[(row * H + h) * 2] = top;
+      ml[(row * H + h) * 2 + 1] = sum;
+    }
+    return;
+  }
+  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+#pragma unroll
+  for (int j = 0; j < NU; ++j) ln.store((T*)a.out + (n * H + h) * D, j, D, [&](int x) { return acc[j][x] * inv; });
+  if (a.lse && ln.lig == 0) a.lse[n * H + h] = sum == 0.0f ? -INFINITY : top + __builtin_amdgcn_logf(sum) * kLn2;
 }
 
-// Row pass of the gradients: grad_q, and per edge and head the weight w and
-// u = w (a - t), a = g . v, which the source pass reads.  t = sum w a is known
-// only at the row's end, so sum u k is formed as sum w a k - t sum w k, and a
-// waits in u's place until then.
-template <class T, int NE>
-__global__ __launch_bounds__(256) void attn_grad_row_kernel(AttnGradArgs a, float* wts, float* us) {
-  const int lane = threadIdx.x & 63;
-  const int64_t task = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (task >= a.N * a.heads) return;
-  const int64_t n = task / a.heads;
-  const int h = (int)(task - n * a.heads), hk = h / (a.heads / a.kv_heads);
-  float qr[NE], g[NE], wak[NE], wk[NE], t = 0.0f;
-#pragma unroll
-  for (int i = 0; i < NE; ++i) {
-    const int d = lane + 64 * i;
-    qr[i] = d < a.D ? (float)((const T*)a.q)[task * a.D + d] : 0.0f;
-    g[i] = d < a.D ? (float)((const T*)a.gout)[task * a.D + d] : 0.0f;
-    wak[i] = wk[i] = 0.0f;
+// Joins the pieces of the rows: a workgroup a (row, head); its threads lie over the pieces and the places.
+template <class T>
+__global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, Tiling t, int L) {
+  __shared__ float red[256];
+  const int H = a.heads, D = a.D, S = t.S;
+  const int64_t n = blockIdx.x / H;
+  const int h = (int)(blockIdx.x - n * H), d0 = threadIdx.x & (L - 1), k = threadIdx.x / L, W = 256 / L;
+  const float* part = t.part + (n * S * H + h) * D;
+  const float* ml = t.part + a.N * S * H * (int64_t)D + (n * S * H + h) * 2;
+  float top = -INFINITY, sum = 0.0f;
+  for (int s = 0; s < S; ++s) top = fmaxf(top, ml[(int64_t)s * H * 2]);
+  const float base = top == -INFINITY ? 0.0f : top;
+  for (int s = 0; s < S; ++s) sum = fmaf(ml[(int64_t)s * H * 2 + 1], exp_of(ml[(int64_t)s * H * 2] - base), sum);
+  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+  for (int d = d0; d < D; d += L) {
+    float acc = 0.0f;
+#pragma unroll 4
+    for (int s = k; s < S; s += W)
+      acc = fmaf(part[(int64_t)s * H * D + d], exp_of(ml[(int64_t)s * H * 2] - base), acc);
+    __syncthreads();
+    red[threadIdx.x] = acc;
+    __syncthreads();
+    if (k == 0) {
+      for (int i = 1; i < W; ++i) acc += red[i * L + d0];
+      ((T*)a.out)[(n * H + h) * D + d] = (T)(acc * inv);
+    }
   }
-  const float lse = a.lse[task];
-  const RowRange r = row_range(a.row_ptr, n, a.E);
-  for (int64_t e = r.b; e < r.e; ++e) {
-    const float bias = a.bias ? a.bias[e * a.heads + h] : 0.0f;
-    float w = 0.0f, av = 0.0f;
-    if (bias != -INFINITY) {
-      const int64_t at = ((int64_t)clamp_index(a.src[e], (int)a.M) * a.kv_heads + hk) * a.D;
-      float kr[NE], dot = 0.0f;
+  if (a.lse && threadIdx.x == 0) a.lse[n * H + h] = sum == 0.0f ? -INFINITY : top + __builtin_amdgcn_logf(sum) * kLn2;
+}
+
+// ---- gradients ------------------------------------------------------------------
+// Row pass: grad_q, and per edge and head the weight w and u = w (a - t),
+// a = g . v, which the source pass reads.  t = sum w a is known only at the
+// row's end, so sum u k is formed as sum w a k - t sum w k, and a waits in u's
+// place until then.  The weights exp(s - lse) are summed and divided by their
+// sum again: it is 1 but for lse's rounding, which counts where the logits are
+// so large that the sum's logarithm is lost in lse (biases of the lowest value).
+__device__ __forceinline__ void grad_of_logit(float* wts, float* us, int64_t at, float t, float inv) {
+  const float w = wts[at] * inv;
+  wts[at] = w;
+  us[at] = w == 0.0f ? 0.0f : w * (us[at] - t);
+}
+
+template <class T, int G, int NU, int MODE, int EU>
+__global__ __launch_bounds__(256) void attn_grad_row_kernel(AttnGradArgs a, Tiling t, float* wts, float* us) {
+  constexpr int VE = El<T>::VE;
+  const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t task = t.first + (int64_t)blockIdx.x * 4 + wv;
+  if (task >= t.end) return;
+  const int64_t row = task / t.blocks, n = t.S == 1 ? row : row / t.S;
+  const int hb = (int)(task - row * t.blocks), sp = (int)(row - n * t.S), D = a.D, H = a.heads;
+  const Lanes<T, G, NU, MODE> ln(D, t.HW);
+  const int h = min(hb * t.HW + ln.hs, H - 1), R = H / a.kv_heads;
+  const bool mine = hb * t.HW + ln.hs < H;
+  const int64_t rowlen = (int64_t)a.kv_heads * D;
+  const T* kb = (const T*)a.k + (int64_t)(h / R) * D;
+  const T* vb = (const T*)a.v + (int64_t)(h / R) * D;
+  u4 q[NU], g[NU];
+  float wak[NU][VE] = {}, wk[NU][VE] = {}, tt = 0.0f, total = 0.0f;
 #pragma unroll
-      for (int i = 0; i < NE; ++i) {
-        const int d = lane + 64 * i;
-        kr[i] = d < a.D ? (float)((const T*)a.k)[at + d] : 0.0f;
-        dot = fmaf(qr[i], kr[i], dot);
-        av = d < a.D ? fmaf(g[i], (float)((const T*)a.v)[at + d], av) : av;
-      }
-      const float s = fmaf(a.scale, wave_sum(dot), bias);
-      av = wave_sum(av);
-      if (s != -INFINITY) {
-        w = __expf(s - lse);
-        t = fmaf(w, av, t);
+  for (int j = 0; j < NU; ++j) {
+    q[j] = ln.load((const T*)a.q + (n * H + h) * D, j, D);
+    g[j] = ln.load((const T*)a.gout + (n * H + h) * D, j, D);
+  }
+  const float lse = a.lse[n * H + h];
+  const RowRange r = piece(row_range(a.row_ptr, n, a.E), sp, t.S);
+  int idx[EU];
+  float bias[EU];
+  auto fetch = [&](int64_t e0) {
 #pragma unroll
-        for (int i = 0; i < NE; ++i) {
-          wak[i] = fmaf(w * av, kr[i], wak[i]);
-          wk[i] = fmaf(w, kr[i], wk[i]);
+    for (int i = 0; i < EU; ++i) {
+      int64_t e = e0 + i * t.ES + ln.es;
+      e = e < r.e ? e : r.e - 1;
+      idx[i] = a.src[e];
+      bias[i] = a.bias ? a.bias[e * H + h] : 0.0f;
+    }
+  };
+  if (r.b < r.e) fetch(r.b);
+  for (int64_t e0 = r.b; e0 < r.e; e0 += EU * t.ES) {
+    u4 k[EU][NU], v[EU][NU];
+    float s[EU];
+    bool live[EU], in[EU], all = true;
+#pragma unroll
+    for (int i = 0; i < EU; ++i) {
+      const int64_t at = (int64_t)clamp_index(idx[i], (int)a.M) * rowlen;
+#pragma unroll
+      for (int j = 0; j < NU; ++j) k[i][j] = ln.load(kb + at, j, D);
+#pragma unroll
+      for (int j = 0; j < NU; ++j) v[i][j] = ln.load(vb + at, j, D);
+      s[i] = bias[i];
+      in[i] = e0 + i * t.ES + ln.es < r.e;
+      live[i] = bias[i] != -INFINITY && in[i];
+      all = all && live[i];
+    }
+    if (e0 + EU * t.ES < r.e) fetch(e0 + EU * t.ES);
+    if (!__all(all)) {
+#pragma unroll
+      for (int i = 0; i < EU; ++i) {
+        s[i] = live[i] ? s[i] : -INFINITY;
+#pragma unroll
+        for (int j = 0; j < NU; ++j) {
+          k[i][j] = keep_if(k[i][j], live[i]);
+          v[i][j] = keep_if(v[i][j], live[i]);
         }
       }
     }
-    if (lane == 0) {
-      wts[e * a.heads + h] = w;
-      us[e * a.heads + h] = av;
+#pragma unroll
+    for (int i = 0; i < EU; ++i) {
+      float d = 0.0f, av = 0.0f;
+#pragma unroll
+      for (int j = 0; j < NU; ++j) {
+        d = El<T>::dot(q[j], k[i][j], d);
+        av = El<T>::dot(g[j], v[i][j], av);
+      }
+      s[i] = s[i] == -INFINITY ? s[i] : fmaf(a.scale, lane_sum<G>(d), s[i]);
+      av = lane_sum<G>(av);
+      const bool none = s[i] == -INFINITY;
+      const float w = none ? 0.0f : exp_of(s[i] - lse), wa = none ? 0.0f : w * av;
+      tt += wa;
+      total += w;
+#pragma unroll
+      for (int j = 0; j < NU; ++j)
+#pragma unroll
+        for (int x = 0; x < VE; ++x) {
+          const float kx = El<T>::at(k[i][j], x);
+          wak[j][x] = fmaf(wa, kx, wak[j][x]);
+          wk[j][x] = fmaf(w, kx, wk[j][x]);
+        }
+      if (mine && in[i] && ln.lig == 0) {
+        const int64_t at = (e0 + i * t.ES + ln.es) * H + h;
+        wts[at] = w;
+        us[at] = none ? 0.0f : av;
+      }
     }
   }
-  if (lane == 0)  // the lane that wrote them
-    for (int64_t e = r.b; e < r.e; ++e) {
-      const float w = wts[e * a.heads + h];
-      us[e * a.heads + h] = w == 0.0f ? 0.0f : w * (us[e * a.heads + h] - t);
+  for (int d = G * t.HW; d < 64; d <<= 1) {
+    tt += __shfl_xor(tt, d, 64);
+    total += __shfl_xor(total, d, 64);
+#pragma unroll
+    for (int j = 0; j < NU; ++j)
+#pragma unroll
+      for (int x = 0; x < VE; ++x) {
+        wak[j][x] += __shfl_xor(wak[j][x], d, 64);
+        wk[j][x] += __shfl_xor(wk[j][x], d, 64);
+      }
+  }
+  if (t.S > 1) {
+    if (!mine || ln.es != 0) return;
+    const int64_t all = a.N * t.S * H * (int64_t)D;
+#pragma unroll
+    for (int j = 0; j < NU; ++j) {
+      ln.store_f32(t.part + (row * H + h) * D, j, D, [&](int x) { return wak[j][x]; });
+      ln.store_f32(t.part + all + (row * H + h) * D, j, D, [&](int x) { return wk[j][x]; });
     }
+    if (ln.lig == 0) {
+      t.part[2 * all + (row * H + h) * 2] = tt;
+      t.part[2 * all + (row * H + h) * 2 + 1] = total;
+    }
+    return;
+  }
+  const float inv = total == 0.0f ? 0.0f : 1.0f / total;
+  tt *= inv;
+  if (a.gq && mine && ln.es == 0)
+#pragma unroll
+    for (int j = 0; j < NU; ++j)
+      ln.store((T*)a.gq + (n * H + h) * D, j, D, [&](int x) { return fmaf(-tt, wk[j][x], wak[j][x]) * (inv * a.scale); });
+  // u of the row's edges: lanes over (edge, head), once the wave's own stores above are done
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "workgroup");
+  const int hh = (threadIdx.x & 63) & (t.HW - 1);
+  const float th = __shfl(tt, hh * G, 64), ih = __shfl(inv, hh * G, 64);
+  if (hb * t.HW + hh < H)
+    for (int64_t e = r.b + (threadIdx.x & 63) / t.HW; e < r.e; e += 64 / t.HW) grad_of_logit(wts, us, e * H + hb * t.HW + hh, th, ih);
+}
+
+// Joins the pieces of the row pass: t and the weights' sum, then grad_q.
+template <class T>
+__global__ __launch_bounds__(256) void attn_grad_join_kernel(AttnGradArgs a, Tiling t, int L) {
+  __shared__ float red[2][256];
+  const int H = a.heads, D = a.D, S = t.S;
+  const int64_t n = blockIdx.x / H, all = a.N * S * H * (int64_t)D;
+  const int h = (int)(blockIdx.x - n * H), d0 = threadIdx.x & (L - 1), k = threadIdx.x / L, W = 256 / L;
+  const float* tp = t.part + 2 * all + (n * S * H + h) * 2;
+  float tt = 0.0f, total = 0.0f;
+  for (int s = 0; s < S; ++s) {
+    tt += tp[(int64_t)s * H * 2];
+    total += tp[(int64_t)s * H * 2 + 1];
+  }
+  const float inv = total == 0.0f ? 0.0f : 1.0f / total;
+  tt *= inv;
+  if (threadIdx.x == 0) {
+    float* o = t.part + 2 * all + (a.N * S * H + n * H + h) * 2;
+    o[0] = tt;
+    o[1] = inv;
+  }
   if (a.gq)
-#pragma unroll
-    for (int i = 0; i < NE; ++i) {
-      const int d = lane + 64 * i;
-      if (d < a.D) ((T*)a.gq)[task * a.D + d] = (T)(fmaf(-t, wk[i], wak[i]) * a.scale);
-    }
-}
-
-// Source pass: grad_k and grad_v of one (source, key and value head).
-template <class T, int NE>
-__global__ __launch_bounds__(256) void attn_grad_source_kernel(AttnGradArgs a, const float* wts, const float* us) {
-  const int lane = threadIdx.x & 63;
-  const int64_t task = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (task >= a.M * a.kv_heads) return;
-  const int64_t m = task / a.kv_heads;
-  const int R = a.heads / a.kv_heads, h0 = (int)(task - m * a.kv_heads) * R;
-  float ka[NE] = {}, va[NE] = {};
-  const RowRange r = row_range(a.src_ptr, m, a.E);
-  for (int64_t i = r.b; i < r.e; ++i) {
-    const int64_t e = clamp_index(a.perm[i], (int)a.E), n = clamp_index(a.dst_s[i], (int)a.N);
-    for (int j = 0; j < R; ++j) {
-      const float w = wts[e * a.heads + h0 + j], u = us[e * a.heads + h0 + j] * a.scale;
-      if (w == 0.0f && u == 0.0f) continue;  // masked: whatever the row holds
-      const int64_t at = (n * a.heads + h0 + j) * a.D;
-#pragma unroll
-      for (int x = 0; x < NE; ++x) {
-        const int d = lane + 64 * x;
-        if (d < a.D) {
-          ka[x] = fmaf(u, (float)((const T*)a.q)[at + d], ka[x]);
-          va[x] = fmaf(w, (float)((const T*)a.gout)[at + d], va[x]);
-        }
+    for (int d = d0; d < D; d += L) {
+      const float* p = t.part + (n * S * H + h) * D + d;
+      float x = 0.0f, y = 0.0f;
+#pragma unroll 4
+      for (int s = k; s < S; s += W) {
+        x += p[(int64_t)s * H * D];
+        y += p[all + (int64_t)s * H * D];
+      }
+      __syncthreads();
+      red[0][threadIdx.x] = x;
+      red[1][threadIdx.x] = y;
+      __syncthreads();
+      if (k == 0) {
+        for (int i = 1; i < W; ++i) x += red[0][i * L + d0], y += red[1][i * L + d0];
+        ((T*)a.gq)[(n * H + h) * D + d] = (T)(fmaf(-tt, y, x) * (inv * a.scale));
       }
     }
+}
+
+// w and u of every edge of the pieces, from their rows' joined sums: a workgroup a (row, piece).
+__global__ __launch_bounds__(256) void attn_grad_fix_kernel(AttnGradArgs a, Tiling t, float* wts, float* us) {
+  const int H = a.heads;
+  const int64_t n = blockIdx.x / t.S;
+  const RowRange r = piece(row_range(a.row_ptr, n, a.E), (int)(blockIdx.x - n * t.S), t.S);
+  const float* tt = t.part + 2 * (a.N * t.S * H * (int64_t)a.D) + (a.N * t.S + n) * H * 2;
+  for (int64_t i = threadIdx.x; i < (r.e - r.b) * H; i += 256)
+    grad_of_logit(wts, us, r.b * H + i, tt[i % H * 2], tt[i % H * 2 + 1]);
+}
+
+// Source pass: grad_k = scale sum u q, grad_v = sum w g over a source's edges
+// (and the heads that share a key and value head).
+template <class T, int G, int NU, int MODE, int EU>
+__global__ __launch_bounds__(256) void attn_grad_source_kernel(AttnGradArgs a, Tiling t, const float* __restrict__ wts,
+                                                               const float* __restrict__ us) {
+  constexpr int VE = El<T>::VE;
+  const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t task = t.first + (int64_t)blockIdx.x * 4 + wv;
+  if (task >= t.end) return;
+  const int64_t row = task / t.blocks, m = t.S == 1 ? row : row / t.S;
+  const int hb = (int)(task - row * t.blocks), sp = (int)(row - m * t.S), D = a.D, H = a.heads, HK = a.kv_heads;
+  const Lanes<T, G, NU, MODE> ln(D, t.HW);
+  const int hk = min(hb * t.HW + ln.hs, HK - 1), R = H / HK;
+  const bool mine = hb * t.HW + ln.hs < HK;
+  float ka[NU][VE] = {}, va[NU][VE] = {};
+  const RowRange r = piece(row_range(a.src_ptr, m, a.E), sp, t.S);
+  int edge[EU], dst[EU];
+  auto fetch = [&](int64_t i0) {
+#pragma unroll
+    for (int i = 0; i < EU; ++i) {
+      int64_t e = i0 + i * t.ES + ln.es;
+      e = e < r.e ? e : r.e - 1;
+      edge[i] = a.perm[e];
+      dst[i] = a.dst_s[e];
+    }
+  };
+  if (r.b < r.e) fetch(r.b);
+  for (int64_t i0 = r.b; i0 < r.e; i0 += EU * t.ES) {
+    int64_t eh[EU], nh[EU];
+#pragma unroll
+    for (int i = 0; i < EU; ++i) {
+      eh[i] = (int64_t)clamp_index(edge[i], (int)a.E) * H + hk * R;
+      nh[i] = ((int64_t)clamp_index(dst[i], (int)a.N) * H + hk * R) * D;
+    }
+    if (i0 + EU * t.ES < r.e) fetch(i0 + EU * t.ES);
+    for (int h = 0; h < R; ++h) {
+      u4 q[EU][NU], g[EU][NU];
+      float w[EU], u[EU];
+      bool all = true;
+#pragma unroll
+      for (int i = 0; i < EU; ++i) {
+        const bool in = i0 + i * t.ES + ln.es < r.e;
+        w[i] = in ? wts[eh[i] + h] : 0.0f;
+        u[i] = in ? us[eh[i] + h] : 0.0f;
+#pragma unroll
+        for (int j = 0; j < NU; ++j) q[i][j] = ln.load((const T*)a.q + nh[i] + (int64_t)h * D, j, D);
+#pragma unroll
+        for (int j = 0; j < NU; ++j) g[i][j] = ln.load((const T*)a.gout + nh[i] + (int64_t)h * D, j, D);
+      }
+#pragma unroll
+      for (int i = 0; i < EU; ++i) all = all && (w[i] != 0.0f || u[i] != 0.0f);
+      if (!__all(all)) {  // masked edges and places past the row: whatever the rows hold
+#pragma unroll
+        for (int i = 0; i < EU; ++i)
+#pragma unroll
+          for (int j = 0; j < NU; ++j) {
+            q[i][j] = keep_if(q[i][j], w[i] != 0.0f || u[i] != 0.0f);
+            g[i][j] = keep_if(g[i][j], w[i] != 0.0f || u[i] != 0.0f);
+          }
+      }
+#pragma unroll
+      for (int i = 0; i < EU; ++i)
+#pragma unroll
+        for (int j = 0; j < NU; ++j)
+#pragma unroll
+          for (int x = 0; x < VE; ++x) {
+            ka[j][x] = fmaf(u[i], El<T>::at(q[i][j], x), ka[j][x]);
+            va[j][x] = fmaf(w[i], El<T>::at(g[i][j], x), va[j][x]);
+          }
+    }
+  }
+  for (int d = G * t.HW; d < 64; d <<= 1)
+#pragma unroll
+    for (int j = 0; j < NU; ++j)
+#pragma unroll
+      for (int x = 0; x < VE; ++x) {
+        ka[j][x] += __shfl_xor(ka[j][x], d, 64);
+        va[j][x] += __shfl_xor(va[j][x], d, 64);
+      }
+  if (!mine || ln.es != 0) return;
+  if (t.S > 1) {
+    const int64_t all = a.M * t.S * HK * (int64_t)D;
+#pragma unroll
+    for (int j = 0; j < NU; ++j) {
+      ln.store_f32(t.part + (row * HK + hk) * D, j, D, [&](int x) { return ka[j][x]; });
+      ln.store_f32(t.part + all + (row * HK + hk) * D, j, D, [&](int x) { return va[j][x]; });
+    }
+    return;
   }
 #pragma unroll
-  for (int x = 0; x < NE; ++x) {
-    const int d = lane + 64 * x;
-    if (d < a.D) {
-      if (a.gk) ((T*)a.gk)[task * a.D + d] = (T)ka[x];
-      if (a.gv) ((T*)a.gv)[task * a.D + d] = (T)va[x];
+  for (int j = 0; j < NU; ++j) {
+    if (a.gk) ln.store((T*)a.gk + (m * HK + hk) * D, j, D, [&](int x) { return ka[j][x] * a.scale; });
+    if (a.gv) ln.store((T*)a.gv + (m * HK + hk) * D, j, D, [&](int x) { return va[j][x]; });
+  }
+}
+
+template <class T>
+__global__ __launch_bounds__(256) void attn_source_join_kernel(AttnGradArgs a, Tiling t, int L) {
+  __shared__ float red[2][256];
+  const int HK = a.kv_heads, D = a.D, S = t.S;
+  const int64_t m = blockIdx.x / HK, all = a.M * S * HK * (int64_t)D;
+  const int h = (int)(blockIdx.x - m * HK), d0 = threadIdx.x & (L - 1), k = threadIdx.x / L, W = 256 / L;
+  for (int d = d0; d < D; d += L) {
+    const float* p = t.part + (m * S * HK + h) * D + d;
+    float x = 0.0f, y = 0.0f;
+#pragma unroll 4
+    for (int s = k; s < S; s += W) {
+      x += p[(int64_t)s * HK * D];
+      y += p[all + (int64_t)s * HK * D];
+    }
+    __syncthreads();
+    red[0][threadIdx.x] = x;
+    red[1][threadIdx.x] = y;
+    __syncthreads();
+    if (k == 0) {
+      for (int i = 1; i < W; ++i) x += red[0][i * L + d0], y += red[1][i * L + d0];
+      if (a.gk) ((T*)a.gk)[(m * HK + h) * D + d] = (T)(x * a.scale);
+      if (a.gv) ((T*)a.gv)[(m * HK + h) * D + d] = (T)y;
     }
   }
 }
 
-int64_t attn_workspace_bytes(int64_t, int64_t, int64_t, int, int, int) { return 0; }
-
-int64_t attn_grad_workspace_bytes(int64_t, int64_t, int64_t E, int, int heads, int) { return 2 * 4 * E * heads; }
-
-template <class T, int NE>
-static hipError_t attn_t(const AttnArgs& a) {
-  hipLaunchKernelGGL((attn_kernel<T, NE>), dim3((unsigned)((a.N * a.heads + 3) / 4)), dim3(256), 0, a.stream, a);
-  return hipGetLastError();
+// ---- launch ---------------------------------------------------------------------
+static int pow2_from(int v) {
+  int p = 1;
+  while (p < v) p <<= 1;
+  return p;
 }
 
-template <class T, int NE>
-static hipError_t attn_grad_t(const AttnGradArgs& a) {
-  float* wts = (float*)a.ws;
-  float* us = a.gbias ? a.gbias : wts + a.E * a.heads;
-  if (a.N > 0) {
-    hipLaunchKernelGGL((attn_grad_row_kernel<T, NE>), dim3((unsigned)((a.N * a.heads + 3) / 4)), dim3(256), 0, a.stream, a,
-                       wts, us);
+// Pieces of a row: where the rows alone give fewer than kMinWaves waves, as many as bring them there, of kMinPiece
+// edges on average or more.
+constexpr int64_t kMinWaves = 1024, kMinPiece = 64, kMaxPieces = 512;
+static int pieces(int64_t rows, int64_t E) {
+  if (rows <= 0 || rows >= kMinWaves) return 1;
+  int64_t s = (kMinWaves + rows - 1) / rows;
+  const int64_t by_length = E / rows / kMinPiece;
+  s = s < by_length ? s : by_length;
+  s = s < kMaxPieces ? s : kMaxPieces;
+  return s < 2 ? 1 : (int)s;
+}
+
+int64_t attn_workspace_bytes(int64_t N, int64_t, int64_t E, int D, int heads, int) {
+  const int S = pieces(N, E);
+  return S == 1 ? 0 : 4 * N * S * heads * ((int64_t)D + 2);
+}
+
+static int64_t grad_tables(int64_t E, int heads) { return (2 * 4 * E * heads + 15) / 16 * 16; }
+
+int64_t attn_grad_workspace_bytes(int64_t N, int64_t M, int64_t E, int D, int heads, int kv_heads) {
+  const int S = pieces(N, E), Z = pieces(M, E);
+  const int64_t rows = S == 1 ? 0 : 4 * N * heads * (S * (2 * (int64_t)D + 2) + 2);
+  const int64_t sources = Z == 1 ? 0 : 4 * M * Z * kv_heads * 2 * (int64_t)D;
+  return grad_tables(E, heads) + (rows > sources ? rows : sources);
+}
+
+// Lanes and units of a head's row: up to 8 units one a lane, then two, four, eight a lane.
+struct HeadShape {
+  int G, NU, mode;
+};
+static HeadShape head_shape(int D, int VE) {
+  const int U = (D + VE - 1) / VE;
+  HeadShape s;
+  s.NU = U <= 8 ? 1 : (U <= 32 ? 2 : (U <= 256 ? 4 : 8));
+  s.G = pow2_from((U + s.NU - 1) / s.NU);
+  s.mode = D < VE ? 2 : (D == s.G * s.NU * VE ? 0 : 1);
+  return s;
+}
+static Tiling tiling(const HeadShape& s, int heads, int S, float* part) {
+  Tiling t;
+  const int room = 64 / s.G;
+  t.HW = pow2_from(heads) < room ? pow2_from(heads) : room;
+  t.ES = room / t.HW;
+  t.blocks = (heads + t.HW - 1) / t.HW;
+  t.S = S;
+  t.first = t.end = 0;
+  t.part = part;
+  return t;
+}
+
+// Launches F<T, G, NU, MODE, EU> for a shape over all tasks; a launch holds at most 2^24 waves (2^32 threads is the
+// grid's limit).  EU(NU): edges loaded together.
+template <class L>
+static hipError_t over_tasks(int64_t tasks, Tiling& t, L launch) {
+  constexpr int64_t kMost = (int64_t)1 << 24;
+  t.end = tasks;
+  for (t.first = 0; t.first < tasks; t.first += kMost) {
+    const int64_t n = tasks - t.first < kMost ? tasks - t.first : kMost;
+    launch(dim3((unsigned)((n + 3) / 4)));
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  if (a.M > 0 && (a.gk || a.gv))
-    hipLaunchKernelGGL((attn_grad_source_kernel<T, NE>), dim3((unsigned)((a.M * a.kv_heads + 3) / 4)), dim3(256), 0,
-                       a.stream, a, wts, us);
+  return hipSuccess;
+}
+// Calls f(G, NU, MODE) as constants.  Of eight units a lane there are fp32 rows only (2048 bf16 elements fill 64
+// lanes of four); a single unit a row is whole or short.
+template <class T, class F>
+static void with_shape(const HeadShape& s, F f) {
+  auto modes = [&](auto G, auto NU) {
+    if (s.mode == 0) f(G, NU, std::integral_constant<int, 0>());
+    else f(G, NU, std::integral_constant<int, 1>());
+  };
+  typedef std::integral_constant<int, 1> I1;
+  typedef std::integral_constant<int, 2> I2;
+  typedef std::integral_constant<int, 4> I4;
+  typedef std::integral_constant<int, 8> I8;
+  typedef std::integral_constant<int, 16> I16;
+  typedef std::integral_constant<int, 32> I32;
+  typedef std::integral_constant<int, 64> I64;
+  if (s.mode == 2) f(I1(), I1(), I2());
+  else if (s.NU == 1 && s.G == 1) f(I1(), I1(), std::integral_constant<int, 0>());
+  else if (s.NU == 1 && s.G == 2) modes(I2(), I1());
+  else if (s.NU == 1 && s.G == 4) modes(I4(), I1());
+  else if (s.NU == 1) modes(I8(), I1());
+  else if (s.NU == 2 && s.G == 8) modes(I8(), I2());
+  else if (s.NU == 2) modes(I16(), I2());
+  else if (s.NU == 4 && s.G == 16) modes(I16(), I4());
+  else if (s.NU == 4 && s.G == 32) modes(I32(), I4());
+  else if (s.NU == 4) modes(I64(), I4());
+  else if constexpr (El<T>::VE == 4) modes(I64(), I8());
+}
+
+static int join_lanes(int D) { return pow2_from(D) < 256 ? pow2_from(D) : 256; }
+
+template <class T>
+static hipError_t attn_t(const AttnArgs& a) {
+  const HeadShape s = head_shape(a.D, El<T>::VE);
+  Tiling t = tiling(s, a.heads, pieces(a.N, a.E), (float*)a.ws);
+  const hipError_t e = over_tasks(a.N * t.blocks * t.S, t, [&](dim3 grid) {
+    with_shape<T>(s, [&](auto G, auto NU, auto MODE) {
+      attn_kernel<T, G(), NU(), MODE(), 8 / NU()><<<grid, dim3(256), 0, a.stream>>>(a, t);
+    });
+  });
+  if (e != hipSuccess || t.S == 1) return e;
+  attn_join_kernel<T><<<dim3((unsigned)(a.N * a.heads)), dim3(256), 0, a.stream>>>(a, t, join_lanes(a.D));
   return hipGetLastError();
 }
 
-#define EQTP_BY_WIDTH(F, T, a)              \
-  ((a).D <= 64     ? F<T, 1>(a)             \
-   : (a).D <= 128  ? F<T, 2>(a)             \
-   : (a).D <= 256  ? F<T, 4>(a)             \
-   : (a).D <= 512  ? F<T, 8>(a)             \
-   : (a).D <= 1024 ? F<T, 16>(a)            \
-                   : F<T, 32>(a))
-
-hipError_t launch_attention(const AttnArgs& a) {
-  return a.bf16 ? EQTP_BY_WIDTH(attn_t, __bf16, a) : EQTP_BY_WIDTH(attn_t, float, a);
+template <class T>
+static hipError_t attn_grad_t(const AttnGradArgs& a) {
+  float* wts = (float*)a.ws;
+  float* us = a.gbias ? a.gbias : wts + a.E * a.heads;
+  float* part = (float*)((unsigned char*)a.ws + grad_tables(a.E, a.heads));
+  const HeadShape s = head_shape(a.D, El<T>::VE);
+  if (a.N > 0) {
+    Tiling t = tiling(s, a.heads, pieces(a.N, a.E), part);
+    hipError_t e = over_tasks(a.N * t.blocks * t.S, t, [&](dim3 grid) {
+      with_shape<T>(s, [&](auto G, auto NU, auto MODE) {
+        attn_grad_row_kernel<T, G(), NU(), MODE(), (NU() >= 4 ? 1 : 4 / NU())><<<grid, dim3(256), 0, a.stream>>>(a, t, wts, us);
+      });
+    });
+    if (e != hipSuccess) return e;
+    if (t.S > 1) {
+      attn_grad_join_kernel<T><<<dim3((unsigned)(a.N * a.heads)), dim3(256), 0, a.stream>>>(a, t, join_lanes(a.D));
+      e = hipGetLastError();
+      if (e != hipSuccess) return e;
+      attn_grad_fix_kernel<<<dim3((unsigned)(a.N * t.S)), dim3(256), 0, a.stream>>>(a, t, wts, us);
+      e = hipGetLastError();
+      if (e != hipSuccess) return e;
+    }
+  }
+  if (a.M == 0 || (!a.gk && !a.gv)) return hipSuccess;
+  Tiling t = tiling(s, a.kv_heads, pieces(a.M, a.E), part);
+  const hipError_t e = over_tasks(a.M * t.blocks * t.S, t, [&](dim3 grid) {
+    with_shape<T>(s, [&](auto G, auto NU, auto MODE) {
+      attn_grad_source_kernel<T, G(), NU(), MODE(), (NU() >= 4 ? 1 : 4 / NU())><<<grid, dim3(256), 0, a.stream>>>(a, t, wts, us);
+    });
+  });
+  if (e != hipSuccess || t.S == 1) return e;
+  attn_source_join_kernel<T><<<dim3((unsigned)(a.M * a.kv_heads)), dim3(256), 0, a.stream>>>(a, t, join_lanes(a.D));
+  return hipGetLastError();
 }
 
+hipError_t launch_attention(const AttnArgs& a) { return a.bf16 ? attn_t<__bf16>(a) : attn_t<float>(a); }
+
 hipError_t launch_attention_grad(const AttnGradArgs& a) {
-  return a.bf16 ? EQTP_BY_WIDTH(attn_grad_t, __bf16, a) : EQTP_BY_WIDTH(attn_grad_t, float, a);
+  return a.bf16 ? attn_grad_t<__bf16>(a) : attn_grad_t<float>(a);
 }
 
 }  // namespace eqtp

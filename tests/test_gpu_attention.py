@@ -186,6 +186,26 @@ def test_attention_masks():
     assert torch.equal(c.forward(eq)[0], clean[0])
 
 
+@pytest.mark.parametrize("bias", [float(np.finfo(np.float32).min), -1e30, 3e6])
+@pytest.mark.parametrize("N,E", [(4, 24), (2, 3000)])
+def test_attention_common_bias_cancels(bias, N, E):
+    """A bias that all edges of a row share, the type's lowest value among them, changes neither the weights nor any
+    gradient; logits that it rounds away leave equal weights."""
+    eq = _eq()
+    _say("attention common bias %g N=%d" % (bias, N))
+    c = Case(N, 9, [E // N] * N, 8, 1, 2, 1, bias=True, masked=0.0, seed=18)
+    c.q = _put(np.zeros(c.q[1].shape))     # equal logits, whatever the bias
+    c.bias = _put(np.full((E, 2), bias))
+    args = (c.q[1], c.k[1], c.v[1], c.src, c.row_ptr, 2, c.scale)
+    want = ref.attention(*args)[0]
+    bounds = ref.attention_bounds(*args, c.g[1], None, ref.U32)
+    out, lse = c.forward(eq)
+    _within(_get(out), want, bounds[0], "out")
+    grads = c.backward(eq, lse)
+    for name, t, w, e in zip(("gq", "gk", "gv", "gbias"), grads, ref.attention_backward(*args, c.g[1]), bounds[2:]):
+        _within(_get(t), w, e, name)
+
+
 def test_attention_not_finite():
     """A NaN in one source reaches the rows that read it and no others."""
     eq = _eq()
