@@ -186,13 +186,58 @@ struct Lanes {
 
 // What a launch fixes for its waves.
 struct Tiling {
-  int HW, ES;       // heads and edges of a wave side by side (powers of two)
+  int HW, ES;       // heads and edges (or, SHORT, rows) of a wave side by side (powers of two)
   int blocks;       // of HW heads
   int S;            // pieces of a row
-  int64_t first;    // task of the launch's first wave, and the end of the tasks
+  int step;         // distance of a lane's next edge: ES, or 1 where lanes side by side have rows of their own
+  int spread;       // head blocks are dealt to the XCDs: 8 / blocks of them for each; 0: not
+  int64_t first;    // task of the launch's first wave, and the end of the tasks (one head block's, where spread)
   int64_t end;
   float* part;      // S > 1: partial results
 };
+
+// A wave's task: its row, piece and head block, the same for all lanes, but the row where lanes have their own.
+struct Task {
+  int64_t row, n;  // row S + piece, row
+  int sp, hb;
+  bool in;         // a row of the graph (a wave's last rows may lie past the end)
+};
+__device__ __forceinline__ bool find_task(const Tiling& t, int64_t rows, int es, Task& k) {
+  const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  int64_t task;
+  if (t.spread) {
+    // workgroups go to the XCDs in turn: an XCD sees one block of heads only, and keeps more of its rows in its L2
+    const int x = blockIdx.x & 7;
+    k.hb = x / t.spread;
+    task = (((int64_t)(blockIdx.x >> 3) * t.spread) + (x & (t.spread - 1))) * 4 + wv;
+    if (task >= t.end) return false;
+  } else {
+    task = t.first + (int64_t)blockIdx.x * 4 + wv;
+    if (task >= t.end) return false;
+    if (t.blocks == 1) {
+      k.hb = 0;
+    } else {
+      const int64_t r = task / t.blocks;
+      k.hb = (int)(task - r * t.blocks);
+      task = r;
+    }
+  }
+  k.in = true;
+  k.sp = 0;
+  if (t.S > 1) {
+    k.row = task;
+    k.n = task / t.S;
+    k.sp = (int)(task - k.n * t.S);
+  } else if (t.step != t.ES) {
+    k.n = task * t.ES + es;
+    k.in = k.n < rows;
+    k.n = k.in ? k.n : rows - 1;
+    k.row = k.n;
+  } else {
+    k.row = k.n = task;
+  }
+  return true;
+}
 
 __device__ __forceinline__ u4 keep_if(const u4& v, bool keep) {
   const uint32_t m = keep ? ~0u : 0u;
@@ -203,12 +248,12 @@ __device__ __forceinline__ u4 keep_if(const u4& v, bool keep) {
 template <class T, int G, int NU, int MODE, int EU>
 __global__ __launch_bounds__(256) void attn_kernel(AttnArgs a, Tiling t) {
   constexpr int VE = El<T>::VE;
-  const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t task = t.first + (int64_t)blockIdx.x * 4 + wv;
-  if (task >= t.end) return;
-  const int64_t row = task / t.blocks, n = t.S == 1 ? row : row / t.S;
-  const int hb = (int)(task - row * t.blocks), sp = (int)(row - n * t.S), D = a.D, H = a.heads;
+  const int D = a.D, H = a.heads;
   const Lanes<T, G, NU, MODE> ln(D, t.HW);
+  Task task;
+  if (!find_task(t, a.N, ln.es, task)) return;
+  const int64_t row = task.row, n = task.n;
+  const int hb = task.hb;
   const int h = min(hb * t.HW + ln.hs, H - 1), R = H / a.kv_heads;
   const bool mine = hb * t.HW + ln.hs < H;
   const int64_t rowlen = (int64_t)a.kv_heads * D;
@@ -218,21 +263,23 @@ __global__ __launch_bounds__(256) void attn_kernel(AttnArgs a, Tiling t) {
   float acc[NU][VE] = {};
 #pragma unroll
   for (int j = 0; j < NU; ++j) q[j] = ln.load((const T*)a.q + (n * H + h) * D, j, D);
-  const RowRange r = piece(row_range(a.row_ptr, n, a.E), sp, t.S);
+  RowRange r = piece(row_range(a.row_ptr, n, a.E), task.sp, t.S);
+  if (!task.in) r.e = r.b;
+  const int es = t.step == t.ES ? ln.es : 0;
   float top = -INFINITY, sum = 0.0f;
   int idx[EU];
   float bias[EU];
   auto fetch = [&](int64_t e0) {
 #pragma unroll
     for (int i = 0; i < EU; ++i) {
-      int64_t e = e0 + i * t.ES + ln.es;
-      e = e < r.e ? e : r.e - 1;
+      int64_t e = e0 + i * t.step + es;
+      e = e < r.e ? e : (r.e > 0 ? r.e - 1 : 0);  // (r.e = 0: a row of its own beside others that have edges)
       idx[i] = a.src[e];
       bias[i] = a.bias ? a.bias[e * H + h] : 0.0f;
     }
   };
-  if (r.b < r.e) fetch(r.b);
-  for (int64_t e0 = r.b; e0 < r.e; e0 += EU * t.ES) {
+  if (__any(r.b < r.e)) fetch(r.b);
+  for (int64_t e0 = r.b; __any(e0 < r.e); e0 += EU * t.step) {
     u4 k[EU][NU], v[EU][NU];
     float s[EU];
     bool live[EU], all = true;
@@ -244,10 +291,10 @@ __global__ __launch_bounds__(256) void attn_kernel(AttnArgs a, Tiling t) {
 #pragma unroll
       for (int j = 0; j < NU; ++j) v[i][j] = ln.load(vb + at, j, D);
       s[i] = bias[i];
-      live[i] = bias[i] != -INFINITY && e0 + i * t.ES + ln.es < r.e;
+      live[i] = bias[i] != -INFINITY && e0 + i * t.step + es < r.e;
       all = all && live[i];
     }
-    if (e0 + EU * t.ES < r.e) fetch(e0 + EU * t.ES);
+    if (__any(e0 + EU * t.step < r.e)) fetch(e0 + EU * t.step);
     float m = top;
 #pragma unroll
     for (int i = 0; i < EU; ++i) {
@@ -285,7 +332,7 @@ __global__ __launch_bounds__(256) void attn_kernel(AttnArgs a, Tiling t) {
     }
   }
   // join the edges that ran side by side
-  for (int d = G * t.HW; d < 64; d <<= 1) {
+  for (int d = t.step == t.ES ? G * t.HW : 64; d < 64; d <<= 1) {
     const float other = __shfl_xor(top, d, 64), m = fmaxf(top, other), base = m == -INFINITY ? 0.0f : m;
     const float down = exp_of(top - base), od = exp_of(other - base);
     top = m;
@@ -295,7 +342,7 @@ __global__ __launch_bounds__(256) void attn_kernel(AttnArgs a, Tiling t) {
 #pragma unroll
       for (int x = 0; x < VE; ++x) acc[j][x] = fmaf(acc[j][x], down, __shfl_xor(acc[j][x], d, 64) * od);
   }
-  if (!mine || ln.es != 0) return;
+  if (!mine || !task.in || es != 0) return;
   if (t.S > 1) {
     float* ml = t.part + (int64_t)a.N * t.S * H * D;
 #pragma unroll
@@ -312,32 +359,62 @@ __global__ __launch_bounds__(256) void attn_kernel(AttnArgs a, Tiling t) {
   if (a.lse && ln.lig == 0) a.lse[n * H + h] = sum == 0.0f ? -INFINITY : top + __builtin_amdgcn_logf(sum) * kLn2;
 }
 
+constexpr int kMaxPieces = 512;
+
+// Sums of v over a workgroup of 256, or the largest, the same in every thread.
+template <bool MAX>
+__device__ __forceinline__ float over_group(float v, float* red) {
+  for (int d = 32; d; d >>= 1) {
+    const float o = __shfl_xor(v, d, 64);
+    v = MAX ? fmaxf(v, o) : v + o;
+  }
+  __syncthreads();
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+  __syncthreads();
+  return MAX ? fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3])) : (red[0] + red[1]) + (red[2] + red[3]);
+}
+
+// sum over the pieces k, k + W, .. of f(piece), then over the W threads of a place; the result in the threads with
+// k = 0.
+template <class F>
+__device__ __forceinline__ float over_pieces(int S, int k, int W, int L, float* red, F f) {
+  float acc = 0.0f;
+#pragma unroll 4
+  for (int s = k; s < S; s += W) acc += f(s);
+  __syncthreads();
+  red[threadIdx.x] = acc;
+  for (int w = W; w > 1; w >>= 1) {
+    __syncthreads();
+    if (k < w / 2) red[threadIdx.x] += red[threadIdx.x + w / 2 * L];
+  }
+  return red[threadIdx.x];
+}
+
 // Joins the pieces of the rows: a workgroup a (row, head); its threads lie over the pieces and the places.
 template <class T>
 __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, Tiling t, int L) {
-  __shared__ float red[256];
+  __shared__ float red[256], w[kMaxPieces], four[4];
   const int H = a.heads, D = a.D, S = t.S;
   const int64_t n = blockIdx.x / H;
   const int h = (int)(blockIdx.x - n * H), d0 = threadIdx.x & (L - 1), k = threadIdx.x / L, W = 256 / L;
   const float* part = t.part + (n * S * H + h) * D;
   const float* ml = t.part + a.N * S * H * (int64_t)D + (n * S * H + h) * 2;
   float top = -INFINITY, sum = 0.0f;
-  for (int s = 0; s < S; ++s) top = fmaxf(top, ml[(int64_t)s * H * 2]);
+  for (int s = threadIdx.x; s < S; s += 256) {
+    w[s] = ml[(int64_t)s * H * 2];
+    top = fmaxf(top, w[s]);
+  }
+  top = over_group<true>(top, four);
   const float base = top == -INFINITY ? 0.0f : top;
-  for (int s = 0; s < S; ++s) sum = fmaf(ml[(int64_t)s * H * 2 + 1], exp_of(ml[(int64_t)s * H * 2] - base), sum);
+  for (int s = threadIdx.x; s < S; s += 256) {
+    w[s] = exp_of(w[s] - base);
+    sum = fmaf(ml[(int64_t)s * H * 2 + 1], w[s], sum);
+  }
+  sum = over_group<false>(sum, four);
   const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-  for (int d = d0; d < D; d += L) {
-    float acc = 0.0f;
-#pragma unroll 4
-    for (int s = k; s < S; s += W)
-      acc = fmaf(part[(int64_t)s * H * D + d], exp_of(ml[(int64_t)s * H * 2] - base), acc);
-    __syncthreads();
-    red[threadIdx.x] = acc;
-    __syncthreads();
-    if (k == 0) {
-      for (int i = 1; i < W; ++i) acc += red[i * L + d0];
-      ((T*)a.out)[(n * H + h) * D + d] = (T)(acc * inv);
-    }
+  for (int d = d0; d < (D + L - 1) / L * L; d += L) {
+    const float acc = over_pieces(S, k, W, L, red, [&](int s) { return d < D ? part[(int64_t)s * H * D + d] * w[s] : 0.0f; });
+    if (k == 0 && d < D) ((T*)a.out)[(n * H + h) * D + d] = (T)(acc * inv);
   }
   if (a.lse && threadIdx.x == 0) a.lse[n * H + h] = sum == 0.0f ? -INFINITY : top + __builtin_amdgcn_logf(sum) * kLn2;
 }
@@ -358,12 +435,12 @@ __device__ __forceinline__ void grad_of_logit(float* wts, float* us, int64_t at,
 template <class T, int G, int NU, int MODE, int EU>
 __global__ __launch_bounds__(256) void attn_grad_row_kernel(AttnGradArgs a, Tiling t, float* wts, float* us) {
   constexpr int VE = El<T>::VE;
-  const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t task = t.first + (int64_t)blockIdx.x * 4 + wv;
-  if (task >= t.end) return;
-  const int64_t row = task / t.blocks, n = t.S == 1 ? row : row / t.S;
-  const int hb = (int)(task - row * t.blocks), sp = (int)(row - n * t.S), D = a.D, H = a.heads;
+  const int D = a.D, H = a.heads;
   const Lanes<T, G, NU, MODE> ln(D, t.HW);
+  Task task;
+  if (!find_task(t, a.N, ln.es, task)) return;
+  const int64_t row = task.row, n = task.n;
+  const int hb = task.hb;
   const int h = min(hb * t.HW + ln.hs, H - 1), R = H / a.kv_heads;
   const bool mine = hb * t.HW + ln.hs < H;
   const int64_t rowlen = (int64_t)a.kv_heads * D;
@@ -377,20 +454,22 @@ __global__ __launch_bounds__(256) void attn_grad_row_kernel(AttnGradArgs a, Tili
     g[j] = ln.load((const T*)a.gout + (n * H + h) * D, j, D);
   }
   const float lse = a.lse[n * H + h];
-  const RowRange r = piece(row_range(a.row_ptr, n, a.E), sp, t.S);
+  RowRange r = piece(row_range(a.row_ptr, n, a.E), task.sp, t.S);
+  if (!task.in) r.e = r.b;
+  const int es = t.step == t.ES ? ln.es : 0;
   int idx[EU];
   float bias[EU];
   auto fetch = [&](int64_t e0) {
 #pragma unroll
     for (int i = 0; i < EU; ++i) {
-      int64_t e = e0 + i * t.ES + ln.es;
-      e = e < r.e ? e : r.e - 1;
+      int64_t e = e0 + i * t.step + es;
+      e = e < r.e ? e : (r.e > 0 ? r.e - 1 : 0);  // (r.e = 0: a row of its own beside others that have edges)
       idx[i] = a.src[e];
       bias[i] = a.bias ? a.bias[e * H + h] : 0.0f;
     }
   };
-  if (r.b < r.e) fetch(r.b);
-  for (int64_t e0 = r.b; e0 < r.e; e0 += EU * t.ES) {
+  if (__any(r.b < r.e)) fetch(r.b);
+  for (int64_t e0 = r.b; __any(e0 < r.e); e0 += EU * t.step) {
     u4 k[EU][NU], v[EU][NU];
     float s[EU];
     bool live[EU], in[EU], all = true;
@@ -402,11 +481,11 @@ __global__ __launch_bounds__(256) void attn_grad_row_kernel(AttnGradArgs a, Tili
 #pragma unroll
       for (int j = 0; j < NU; ++j) v[i][j] = ln.load(vb + at, j, D);
       s[i] = bias[i];
-      in[i] = e0 + i * t.ES + ln.es < r.e;
+      in[i] = e0 + i * t.step + es < r.e;
       live[i] = bias[i] != -INFINITY && in[i];
       all = all && live[i];
     }
-    if (e0 + EU * t.ES < r.e) fetch(e0 + EU * t.ES);
+    if (__any(e0 + EU * t.step < r.e)) fetch(e0 + EU * t.step);
     if (!__all(all)) {
 #pragma unroll
       for (int i = 0; i < EU; ++i) {
@@ -441,13 +520,13 @@ __global__ __launch_bounds__(256) void attn_grad_row_kernel(AttnGradArgs a, Tili
           wk[j][x] = fmaf(w, kx, wk[j][x]);
         }
       if (mine && in[i] && ln.lig == 0) {
-        const int64_t at = (e0 + i * t.ES + ln.es) * H + h;
+        const int64_t at = (e0 + i * t.step + es) * H + h;
         wts[at] = w;
         us[at] = none ? 0.0f : av;
       }
     }
   }
-  for (int d = G * t.HW; d < 64; d <<= 1) {
+  for (int d = t.step == t.ES ? G * t.HW : 64; d < 64; d <<= 1) {
     tt += __shfl_xor(tt, d, 64);
     total += __shfl_xor(total, d, 64);
 #pragma unroll
@@ -459,7 +538,7 @@ __global__ __launch_bounds__(256) void attn_grad_row_kernel(AttnGradArgs a, Tili
       }
   }
   if (t.S > 1) {
-    if (!mine || ln.es != 0) return;
+    if (!mine || es != 0) return;
     const int64_t all = a.N * t.S * H * (int64_t)D;
 #pragma unroll
     for (int j = 0; j < NU; ++j) {
@@ -474,31 +553,37 @@ __global__ __launch_bounds__(256) void attn_grad_row_kernel(AttnGradArgs a, Tili
   }
   const float inv = total == 0.0f ? 0.0f : 1.0f / total;
   tt *= inv;
-  if (a.gq && mine && ln.es == 0)
+  if (a.gq && mine && task.in && es == 0)
 #pragma unroll
     for (int j = 0; j < NU; ++j)
       ln.store((T*)a.gq + (n * H + h) * D, j, D, [&](int x) { return fmaf(-tt, wk[j][x], wak[j][x]) * (inv * a.scale); });
-  // u of the row's edges: lanes over (edge, head), once the wave's own stores above are done
+  // w and u of the row's edges: lanes over (edge, head), once the wave's own stores above are done
   __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "workgroup");
-  const int hh = (threadIdx.x & 63) & (t.HW - 1);
-  const float th = __shfl(tt, hh * G, 64), ih = __shfl(inv, hh * G, 64);
-  if (hb * t.HW + hh < H)
-    for (int64_t e = r.b + (threadIdx.x & 63) / t.HW; e < r.e; e += 64 / t.HW) grad_of_logit(wts, us, e * H + hb * t.HW + hh, th, ih);
+  if (t.step == t.ES) {
+    const int hh = (threadIdx.x & 63) & (t.HW - 1);
+    const float th = __shfl(tt, hh * G, 64), ih = __shfl(inv, hh * G, 64);
+    if (hb * t.HW + hh < H)
+      for (int64_t e = r.b + (threadIdx.x & 63) / t.HW; e < r.e; e += 64 / t.HW) grad_of_logit(wts, us, e * H + hb * t.HW + hh, th, ih);
+  } else if (mine) {
+    for (int64_t e = r.b + ln.lig; e < r.e; e += G) grad_of_logit(wts, us, e * H + h, tt, inv);
+  }
 }
 
 // Joins the pieces of the row pass: t and the weights' sum, then grad_q.
 template <class T>
 __global__ __launch_bounds__(256) void attn_grad_join_kernel(AttnGradArgs a, Tiling t, int L) {
-  __shared__ float red[2][256];
+  __shared__ float red[256], four[4];
   const int H = a.heads, D = a.D, S = t.S;
   const int64_t n = blockIdx.x / H, all = a.N * S * H * (int64_t)D;
   const int h = (int)(blockIdx.x - n * H), d0 = threadIdx.x & (L - 1), k = threadIdx.x / L, W = 256 / L;
   const float* tp = t.part + 2 * all + (n * S * H + h) * 2;
   float tt = 0.0f, total = 0.0f;
-  for (int s = 0; s < S; ++s) {
+  for (int s = threadIdx.x; s < S; s += 256) {
     tt += tp[(int64_t)s * H * 2];
     total += tp[(int64_t)s * H * 2 + 1];
   }
+  tt = over_group<false>(tt, four);
+  total = over_group<false>(total, four);
   const float inv = total == 0.0f ? 0.0f : 1.0f / total;
   tt *= inv;
   if (threadIdx.x == 0) {
@@ -507,22 +592,11 @@ __global__ __launch_bounds__(256) void attn_grad_join_kernel(AttnGradArgs a, Til
     o[1] = inv;
   }
   if (a.gq)
-    for (int d = d0; d < D; d += L) {
+    for (int d = d0; d < (D + L - 1) / L * L; d += L) {
       const float* p = t.part + (n * S * H + h) * D + d;
-      float x = 0.0f, y = 0.0f;
-#pragma unroll 4
-      for (int s = k; s < S; s += W) {
-        x += p[(int64_t)s * H * D];
-        y += p[all + (int64_t)s * H * D];
-      }
-      __syncthreads();
-      red[0][threadIdx.x] = x;
-      red[1][threadIdx.x] = y;
-      __syncthreads();
-      if (k == 0) {
-        for (int i = 1; i < W; ++i) x += red[0][i * L + d0], y += red[1][i * L + d0];
-        ((T*)a.gq)[(n * H + h) * D + d] = (T)(fmaf(-tt, y, x) * (inv * a.scale));
-      }
+      const float x = over_pieces(S, k, W, L, red, [&](int s) { return d < D ? p[(int64_t)s * H * D] : 0.0f; });
+      const float y = over_pieces(S, k, W, L, red, [&](int s) { return d < D ? p[all + (int64_t)s * H * D] : 0.0f; });
+      if (k == 0 && d < D) ((T*)a.gq)[(n * H + h) * D + d] = (T)(fmaf(-tt, y, x) * (inv * a.scale));
     }
 }
 
@@ -542,42 +616,44 @@ template <class T, int G, int NU, int MODE, int EU>
 __global__ __launch_bounds__(256) void attn_grad_source_kernel(AttnGradArgs a, Tiling t, const float* __restrict__ wts,
                                                                const float* __restrict__ us) {
   constexpr int VE = El<T>::VE;
-  const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t task = t.first + (int64_t)blockIdx.x * 4 + wv;
-  if (task >= t.end) return;
-  const int64_t row = task / t.blocks, m = t.S == 1 ? row : row / t.S;
-  const int hb = (int)(task - row * t.blocks), sp = (int)(row - m * t.S), D = a.D, H = a.heads, HK = a.kv_heads;
+  const int D = a.D, H = a.heads, HK = a.kv_heads;
   const Lanes<T, G, NU, MODE> ln(D, t.HW);
+  Task task;
+  if (!find_task(t, a.M, ln.es, task)) return;
+  const int64_t row = task.row, m = task.n;
+  const int hb = task.hb;
   const int hk = min(hb * t.HW + ln.hs, HK - 1), R = H / HK;
   const bool mine = hb * t.HW + ln.hs < HK;
   float ka[NU][VE] = {}, va[NU][VE] = {};
-  const RowRange r = piece(row_range(a.src_ptr, m, a.E), sp, t.S);
+  RowRange r = piece(row_range(a.src_ptr, m, a.E), task.sp, t.S);
+  if (!task.in) r.e = r.b;
+  const int es = t.step == t.ES ? ln.es : 0;
   int edge[EU], dst[EU];
   auto fetch = [&](int64_t i0) {
 #pragma unroll
     for (int i = 0; i < EU; ++i) {
-      int64_t e = i0 + i * t.ES + ln.es;
-      e = e < r.e ? e : r.e - 1;
+      int64_t e = i0 + i * t.step + es;
+      e = e < r.e ? e : (r.e > 0 ? r.e - 1 : 0);
       edge[i] = a.perm[e];
       dst[i] = a.dst_s[e];
     }
   };
-  if (r.b < r.e) fetch(r.b);
-  for (int64_t i0 = r.b; i0 < r.e; i0 += EU * t.ES) {
+  if (__any(r.b < r.e)) fetch(r.b);
+  for (int64_t i0 = r.b; __any(i0 < r.e); i0 += EU * t.step) {
     int64_t eh[EU], nh[EU];
 #pragma unroll
     for (int i = 0; i < EU; ++i) {
       eh[i] = (int64_t)clamp_index(edge[i], (int)a.E) * H + hk * R;
       nh[i] = ((int64_t)clamp_index(dst[i], (int)a.N) * H + hk * R) * D;
     }
-    if (i0 + EU * t.ES < r.e) fetch(i0 + EU * t.ES);
+    if (__any(i0 + EU * t.step < r.e)) fetch(i0 + EU * t.step);
     for (int h = 0; h < R; ++h) {
       u4 q[EU][NU], g[EU][NU];
       float w[EU], u[EU];
       bool all = true;
 #pragma unroll
       for (int i = 0; i < EU; ++i) {
-        const bool in = i0 + i * t.ES + ln.es < r.e;
+        const bool in = i0 + i * t.step + es < r.e;
         w[i] = in ? wts[eh[i] + h] : 0.0f;
         u[i] = in ? us[eh[i] + h] : 0.0f;
 #pragma unroll
@@ -607,7 +683,7 @@ __global__ __launch_bounds__(256) void attn_grad_source_kernel(AttnGradArgs a, T
           }
     }
   }
-  for (int d = G * t.HW; d < 64; d <<= 1)
+  for (int d = t.step == t.ES ? G * t.HW : 64; d < 64; d <<= 1)
 #pragma unroll
     for (int j = 0; j < NU; ++j)
 #pragma unroll
@@ -615,7 +691,7 @@ __global__ __launch_bounds__(256) void attn_grad_source_kernel(AttnGradArgs a, T
         ka[j][x] += __shfl_xor(ka[j][x], d, 64);
         va[j][x] += __shfl_xor(va[j][x], d, 64);
       }
-  if (!mine || ln.es != 0) return;
+  if (!mine || !task.in || es != 0) return;
   if (t.S > 1) {
     const int64_t all = a.M * t.S * HK * (int64_t)D;
 #pragma unroll
@@ -634,24 +710,15 @@ __global__ __launch_bounds__(256) void attn_grad_source_kernel(AttnGradArgs a, T
 
 template <class T>
 __global__ __launch_bounds__(256) void attn_source_join_kernel(AttnGradArgs a, Tiling t, int L) {
-  __shared__ float red[2][256];
+  __shared__ float red[256];
   const int HK = a.kv_heads, D = a.D, S = t.S;
   const int64_t m = blockIdx.x / HK, all = a.M * S * HK * (int64_t)D;
   const int h = (int)(blockIdx.x - m * HK), d0 = threadIdx.x & (L - 1), k = threadIdx.x / L, W = 256 / L;
-  for (int d = d0; d < D; d += L) {
+  for (int d = d0; d < (D + L - 1) / L * L; d += L) {
     const float* p = t.part + (m * S * HK + h) * D + d;
-    float x = 0.0f, y = 0.0f;
-#pragma unroll 4
-    for (int s = k; s < S; s += W) {
-      x += p[(int64_t)s * HK * D];
-      y += p[all + (int64_t)s * HK * D];
-    }
-    __syncthreads();
-    red[0][threadIdx.x] = x;
-    red[1][threadIdx.x] = y;
-    __syncthreads();
-    if (k == 0) {
-      for (int i = 1; i < W; ++i) x += red[0][i * L + d0], y += red[1][i * L + d0];
+    const float x = over_pieces(S, k, W, L, red, [&](int s) { return d < D ? p[(int64_t)s * HK * D] : 0.0f; });
+    const float y = over_pieces(S, k, W, L, red, [&](int s) { return d < D ? p[all + (int64_t)s * HK * D] : 0.0f; });
+    if (k == 0 && d < D) {
       if (a.gk) ((T*)a.gk)[(m * HK + h) * D + d] = (T)(x * a.scale);
       if (a.gv) ((T*)a.gv)[(m * HK + h) * D + d] = (T)y;
     }
@@ -667,7 +734,7 @@ static int pow2_from(int v) {
 
 // Pieces of a row: where the rows alone give fewer than kMinWaves waves, as many as bring them there, of kMinPiece
 // edges on average or more.
-constexpr int64_t kMinWaves = 1024, kMinPiece = 64, kMaxPieces = 512;
+constexpr int64_t kMinWaves = 1024, kMinPiece = 64;
 static int pieces(int64_t rows, int64_t E) {
   if (rows <= 0 || rows >= kMinWaves) return 1;
   int64_t s = (kMinWaves + rows - 1) / rows;
@@ -691,6 +758,8 @@ int64_t attn_grad_workspace_bytes(int64_t N, int64_t M, int64_t E, int D, int he
   return grad_tables(E, heads) + (rows > sources ? rows : sources);
 }
 
+constexpr int64_t kSpreadBytes = (int64_t)8 << 20, kShortRow = 8;
+
 // Lanes and units of a head's row: up to 8 units one a lane, then two, four, eight a lane.
 struct HeadShape {
   int G, NU, mode;
@@ -703,26 +772,52 @@ static HeadShape head_shape(int D, int VE) {
   s.mode = D < VE ? 2 : (D == s.G * s.NU * VE ? 0 : 1);
   return s;
 }
-static Tiling tiling(const HeadShape& s, int heads, int S, float* part) {
+static bool is_pow2(int v) { return (v & (v - 1)) == 0; }
+
+// heads of the pass (of q, or of k and v), share of them that read the same rows, rows and edges of the pass, bytes
+// of the two gathered tensors.
+static Tiling tiling(const HeadShape& s, int heads, int share, int64_t rows, int64_t E, int64_t gathered, float* part) {
   Tiling t;
-  const int room = 64 / s.G;
+  const int room = 64 / s.G, kv = heads / share;
+  t.S = pieces(rows, E);
   t.HW = pow2_from(heads) < room ? pow2_from(heads) : room;
+  // Gathers out of tensors that an L2 of 4 MiB does not hold run at about 7.5 TB/s whatever the tensors' size below
+  // the L2's misses; heads dealt to the XCDs leave each L2 a part of them.
+  t.spread = 0;
+  const int nb = kv < 8 ? kv : 8;
+  if (t.S == 1 && gathered > kSpreadBytes && kv > 1 && is_pow2(kv) && is_pow2(share) && heads / nb <= room &&
+      rows < ((int64_t)1 << 24)) {
+    t.HW = heads / nb;
+    t.spread = 8 / nb;
+  }
   t.ES = room / t.HW;
   t.blocks = (heads + t.HW - 1) / t.HW;
-  t.S = S;
+  // rows of few edges: lanes side by side take rows of their own
+  t.step = t.S == 1 && t.ES > 1 && E < rows * kShortRow ? 1 : t.ES;
   t.first = t.end = 0;
   t.part = part;
   return t;
 }
+static int64_t wave_tasks(const Tiling& t, int64_t rows) {
+  if (t.S > 1) return rows * t.S;
+  return t.step != t.ES ? (rows + t.ES - 1) / t.ES : rows;
+}
 
-// Launches F<T, G, NU, MODE, EU> for a shape over all tasks; a launch holds at most 2^24 waves (2^32 threads is the
-// grid's limit).  EU(NU): edges loaded together.
+// Launches over all tasks; a launch holds at most 2^24 waves (2^32 threads is the
+// grid's limit).
 template <class L>
-static hipError_t over_tasks(int64_t tasks, Tiling& t, L launch) {
+static hipError_t over_tasks(int64_t rows, Tiling& t, L launch) {
   constexpr int64_t kMost = (int64_t)1 << 24;
-  t.end = tasks;
-  for (t.first = 0; t.first < tasks; t.first += kMost) {
-    const int64_t n = tasks - t.first < kMost ? tasks - t.first : kMost;
+  const int64_t tasks = wave_tasks(t, rows);
+  if (t.spread) {
+    t.end = tasks;
+    const int64_t groups = (tasks + 3) / 4;
+    launch(dim3((unsigned)((groups + t.spread - 1) / t.spread * 8)));
+    return hipGetLastError();
+  }
+  t.end = tasks * t.blocks;
+  for (t.first = 0; t.first < t.end; t.first += kMost) {
+    const int64_t n = t.end - t.first < kMost ? t.end - t.first : kMost;
     launch(dim3((unsigned)((n + 3) / 4)));
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
@@ -762,8 +857,8 @@ static int join_lanes(int D) { return pow2_from(D) < 256 ? pow2_from(D) : 256; }
 template <class T>
 static hipError_t attn_t(const AttnArgs& a) {
   const HeadShape s = head_shape(a.D, El<T>::VE);
-  Tiling t = tiling(s, a.heads, pieces(a.N, a.E), (float*)a.ws);
-  const hipError_t e = over_tasks(a.N * t.blocks * t.S, t, [&](dim3 grid) {
+  Tiling t = tiling(s, a.heads, a.heads / a.kv_heads, a.N, a.E, 2 * a.M * a.kv_heads * a.D * (int64_t)sizeof(T), (float*)a.ws);
+  const hipError_t e = over_tasks(a.N, t, [&](dim3 grid) {
     with_shape<T>(s, [&](auto G, auto NU, auto MODE) {
       attn_kernel<T, G(), NU(), MODE(), 8 / NU()><<<grid, dim3(256), 0, a.stream>>>(a, t);
     });
@@ -780,8 +875,8 @@ static hipError_t attn_grad_t(const AttnGradArgs& a) {
   float* part = (float*)((unsigned char*)a.ws + grad_tables(a.E, a.heads));
   const HeadShape s = head_shape(a.D, El<T>::VE);
   if (a.N > 0) {
-    Tiling t = tiling(s, a.heads, pieces(a.N, a.E), part);
-    hipError_t e = over_tasks(a.N * t.blocks * t.S, t, [&](dim3 grid) {
+    Tiling t = tiling(s, a.heads, a.heads / a.kv_heads, a.N, a.E, 2 * a.M * a.kv_heads * a.D * (int64_t)sizeof(T), part);
+    hipError_t e = over_tasks(a.N, t, [&](dim3 grid) {
       with_shape<T>(s, [&](auto G, auto NU, auto MODE) {
         attn_grad_row_kernel<T, G(), NU(), MODE(), (NU() >= 4 ? 1 : 4 / NU())><<<grid, dim3(256), 0, a.stream>>>(a, t, wts, us);
       });
@@ -797,8 +892,8 @@ static hipError_t attn_grad_t(const AttnGradArgs& a) {
     }
   }
   if (a.M == 0 || (!a.gk && !a.gv)) return hipSuccess;
-  Tiling t = tiling(s, a.kv_heads, pieces(a.M, a.E), part);
-  const hipError_t e = over_tasks(a.M * t.blocks * t.S, t, [&](dim3 grid) {
+  Tiling t = tiling(s, a.kv_heads, 1, a.M, a.E, 2 * a.N * a.heads * a.D * (int64_t)sizeof(T), part);
+  const hipError_t e = over_tasks(a.M, t, [&](dim3 grid) {
     with_shape<T>(s, [&](auto G, auto NU, auto MODE) {
       attn_grad_source_kernel<T, G(), NU(), MODE(), (NU() >= 4 ? 1 : 4 / NU())><<<grid, dim3(256), 0, a.stream>>>(a, t, wts, us);
     });
