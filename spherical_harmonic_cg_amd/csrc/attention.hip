@@ -359,9 +359,9 @@ __global__ __launch_bounds__(256) void attn_kernel(AttnArgs a, Tiling t) {
   if (a.lse && ln.lig == 0) a.lse[n * H + h] = sum == 0.0f ? -INFINITY : top + __builtin_amdgcn_logf(sum) * kLn2;
 }
 
-constexpr int kMaxPieces = 512;
+constexpr int kMaxPieces = 1024, kJoin = 1024;  // pieces of a row; threads of a workgroup that joins them
 
-// Sums of v over a workgroup of 256, or the largest, the same in every thread.
+// Sums of v over a workgroup of kJoin threads, or the largest, the same in every thread.
 template <bool MAX>
 __device__ __forceinline__ float over_group(float v, float* red) {
   for (int d = 32; d; d >>= 1) {
@@ -371,7 +371,10 @@ __device__ __forceinline__ float over_group(float v, float* red) {
   __syncthreads();
   if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
   __syncthreads();
-  return MAX ? fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3])) : (red[0] + red[1]) + (red[2] + red[3]);
+  v = red[0];
+#pragma unroll
+  for (int i = 1; i < kJoin / 64; ++i) v = MAX ? fmaxf(v, red[i]) : v + red[i];
+  return v;
 }
 
 // sum over the pieces k, k + W, .. of f(piece), then over the W threads of a place; the result in the threads with
@@ -392,25 +395,25 @@ __device__ __forceinline__ float over_pieces(int S, int k, int W, int L, float* 
 
 // Joins the pieces of the rows: a workgroup a (row, head); its threads lie over the pieces and the places.
 template <class T>
-__global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, Tiling t, int L) {
-  __shared__ float red[256], w[kMaxPieces], four[4];
+__global__ __launch_bounds__(kJoin) void attn_join_kernel(AttnArgs a, Tiling t, int L) {
+  __shared__ float red[kJoin], w[kMaxPieces], few[kJoin / 64];
   const int H = a.heads, D = a.D, S = t.S;
   const int64_t n = blockIdx.x / H;
-  const int h = (int)(blockIdx.x - n * H), d0 = threadIdx.x & (L - 1), k = threadIdx.x / L, W = 256 / L;
+  const int h = (int)(blockIdx.x - n * H), d0 = threadIdx.x & (L - 1), k = threadIdx.x / L, W = kJoin / L;
   const float* part = t.part + (n * S * H + h) * D;
   const float* ml = t.part + a.N * S * H * (int64_t)D + (n * S * H + h) * 2;
   float top = -INFINITY, sum = 0.0f;
-  for (int s = threadIdx.x; s < S; s += 256) {
+  for (int s = threadIdx.x; s < S; s += kJoin) {
     w[s] = ml[(int64_t)s * H * 2];
     top = fmaxf(top, w[s]);
   }
-  top = over_group<true>(top, four);
+  top = over_group<true>(top, few);
   const float base = top == -INFINITY ? 0.0f : top;
-  for (int s = threadIdx.x; s < S; s += 256) {
+  for (int s = threadIdx.x; s < S; s += kJoin) {
     w[s] = exp_of(w[s] - base);
     sum = fmaf(ml[(int64_t)s * H * 2 + 1], w[s], sum);
   }
-  sum = over_group<false>(sum, four);
+  sum = over_group<false>(sum, few);
   const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
   for (int d = d0; d < (D + L - 1) / L * L; d += L) {
     const float acc = over_pieces(S, k, W, L, red, [&](int s) { return d < D ? part[(int64_t)s * H * D + d] * w[s] : 0.0f; });
@@ -571,19 +574,19 @@ __global__ __launch_bounds__(256) void attn_grad_row_kernel(AttnGradArgs a, Tili
 
 // Joins the pieces of the row pass: t and the weights' sum, then grad_q.
 template <class T>
-__global__ __launch_bounds__(256) void attn_grad_join_kernel(AttnGradArgs a, Tiling t, int L) {
-  __shared__ float red[256], four[4];
+__global__ __launch_bounds__(kJoin) void attn_grad_join_kernel(AttnGradArgs a, Tiling t, int L) {
+  __shared__ float red[kJoin], few[kJoin / 64];
   const int H = a.heads, D = a.D, S = t.S;
   const int64_t n = blockIdx.x / H, all = a.N * S * H * (int64_t)D;
-  const int h = (int)(blockIdx.x - n * H), d0 = threadIdx.x & (L - 1), k = threadIdx.x / L, W = 256 / L;
+  const int h = (int)(blockIdx.x - n * H), d0 = threadIdx.x & (L - 1), k = threadIdx.x / L, W = kJoin / L;
   const float* tp = t.part + 2 * all + (n * S * H + h) * 2;
   float tt = 0.0f, total = 0.0f;
-  for (int s = threadIdx.x; s < S; s += 256) {
+  for (int s = threadIdx.x; s < S; s += kJoin) {
     tt += tp[(int64_t)s * H * 2];
     total += tp[(int64_t)s * H * 2 + 1];
   }
-  tt = over_group<false>(tt, four);
-  total = over_group<false>(total, four);
+  tt = over_group<false>(tt, few);
+  total = over_group<false>(total, few);
   const float inv = total == 0.0f ? 0.0f : 1.0f / total;
   tt *= inv;
   if (threadIdx.x == 0) {
@@ -600,7 +603,8 @@ __global__ __launch_bounds__(256) void attn_grad_join_kernel(AttnGradArgs a, Til
     }
 }
 
-// w and u of every edge of the pieces, from their rows' joined sums: a workgroup a (row, piece).
+// w and u of every edge of the pieces, from their rows' joined sums: a workgroup a (row, piece).  (By the joining
+// workgroups themselves, one head each, it took 15 us more for a readout of 50k items and 8 heads: 4 of 32 bytes.)
 __global__ __launch_bounds__(256) void attn_grad_fix_kernel(AttnGradArgs a, Tiling t, float* wts, float* us) {
   const int H = a.heads;
   const int64_t n = blockIdx.x / t.S;
@@ -709,11 +713,11 @@ __global__ __launch_bounds__(256) void attn_grad_source_kernel(AttnGradArgs a, T
 }
 
 template <class T>
-__global__ __launch_bounds__(256) void attn_source_join_kernel(AttnGradArgs a, Tiling t, int L) {
-  __shared__ float red[256];
+__global__ __launch_bounds__(kJoin) void attn_source_join_kernel(AttnGradArgs a, Tiling t, int L) {
+  __shared__ float red[kJoin];
   const int HK = a.kv_heads, D = a.D, S = t.S;
   const int64_t m = blockIdx.x / HK, all = a.M * S * HK * (int64_t)D;
-  const int h = (int)(blockIdx.x - m * HK), d0 = threadIdx.x & (L - 1), k = threadIdx.x / L, W = 256 / L;
+  const int h = (int)(blockIdx.x - m * HK), d0 = threadIdx.x & (L - 1), k = threadIdx.x / L, W = kJoin / L;
   for (int d = d0; d < (D + L - 1) / L * L; d += L) {
     const float* p = t.part + (m * S * HK + h) * D + d;
     const float x = over_pieces(S, k, W, L, red, [&](int s) { return d < D ? p[(int64_t)s * HK * D] : 0.0f; });
@@ -734,7 +738,7 @@ static int pow2_from(int v) {
 
 // Pieces of a row: where the rows alone give fewer than kMinWaves waves, as many as bring them there, of kMinPiece
 // edges on average or more.
-constexpr int64_t kMinWaves = 1024, kMinPiece = 64;
+constexpr int64_t kMinWaves = 2048, kMinPiece = 32;
 static int pieces(int64_t rows, int64_t E) {
   if (rows <= 0 || rows >= kMinWaves) return 1;
   int64_t s = (kMinWaves + rows - 1) / rows;
@@ -758,7 +762,7 @@ int64_t attn_grad_workspace_bytes(int64_t N, int64_t M, int64_t E, int D, int he
   return grad_tables(E, heads) + (rows > sources ? rows : sources);
 }
 
-constexpr int64_t kSpreadBytes = (int64_t)8 << 20, kShortRow = 8;
+constexpr int64_t kSpreadBytes = (int64_t)8 << 20, kSpreadMost = (int64_t)32 << 20, kShortRow = 8;
 
 // Lanes and units of a head's row: up to 8 units one a lane, then two, four, eight a lane.
 struct HeadShape {
@@ -785,7 +789,7 @@ static Tiling tiling(const HeadShape& s, int heads, int share, int64_t rows, int
   // the L2's misses; heads dealt to the XCDs leave each L2 a part of them.
   t.spread = 0;
   const int nb = kv < 8 ? kv : 8;
-  if (t.S == 1 && gathered > kSpreadBytes && kv > 1 && is_pow2(kv) && is_pow2(share) && heads / nb <= room &&
+  if (t.S == 1 && gathered > kSpreadBytes && gathered / nb <= kSpreadMost && kv > 1 && is_pow2(kv) && is_pow2(share) && heads / nb <= room &&
       rows < ((int64_t)1 << 24)) {
     t.HW = heads / nb;
     t.spread = 8 / nb;
@@ -852,7 +856,7 @@ static void with_shape(const HeadShape& s, F f) {
   else if constexpr (El<T>::VE == 4) modes(I64(), I8());
 }
 
-static int join_lanes(int D) { return pow2_from(D) < 256 ? pow2_from(D) : 256; }
+static int join_lanes(int D) { return pow2_from(D) < kJoin ? pow2_from(D) : kJoin; }
 
 template <class T>
 static hipError_t attn_t(const AttnArgs& a) {
@@ -864,7 +868,7 @@ static hipError_t attn_t(const AttnArgs& a) {
     });
   });
   if (e != hipSuccess || t.S == 1) return e;
-  attn_join_kernel<T><<<dim3((unsigned)(a.N * a.heads)), dim3(256), 0, a.stream>>>(a, t, join_lanes(a.D));
+  attn_join_kernel<T><<<dim3((unsigned)(a.N * a.heads)), dim3(kJoin), 0, a.stream>>>(a, t, join_lanes(a.D));
   return hipGetLastError();
 }
 
@@ -883,7 +887,7 @@ static hipError_t attn_grad_t(const AttnGradArgs& a) {
     });
     if (e != hipSuccess) return e;
     if (t.S > 1) {
-      attn_grad_join_kernel<T><<<dim3((unsigned)(a.N * a.heads)), dim3(256), 0, a.stream>>>(a, t, join_lanes(a.D));
+      attn_grad_join_kernel<T><<<dim3((unsigned)(a.N * a.heads)), dim3(kJoin), 0, a.stream>>>(a, t, join_lanes(a.D));
       e = hipGetLastError();
       if (e != hipSuccess) return e;
       attn_grad_fix_kernel<<<dim3((unsigned)(a.N * t.S)), dim3(256), 0, a.stream>>>(a, t, wts, us);
@@ -893,13 +897,19 @@ static hipError_t attn_grad_t(const AttnGradArgs& a) {
   }
   if (a.M == 0 || (!a.gk && !a.gv)) return hipSuccess;
   Tiling t = tiling(s, a.kv_heads, 1, a.M, a.E, 2 * a.N * a.heads * a.D * (int64_t)sizeof(T), part);
+  // sources of one or two edges (a readout's items have one): places for four would stay empty and cost the registers
+  // that more waves need (50k sources of one edge: 27 against 15 us)
+  const bool one = a.E <= 2 * a.M;
   const hipError_t e = over_tasks(a.M, t, [&](dim3 grid) {
     with_shape<T>(s, [&](auto G, auto NU, auto MODE) {
-      attn_grad_source_kernel<T, G(), NU(), MODE(), (NU() >= 4 ? 1 : 4 / NU())><<<grid, dim3(256), 0, a.stream>>>(a, t, wts, us);
+      if (one)
+        attn_grad_source_kernel<T, G(), NU(), MODE(), 1><<<grid, dim3(256), 0, a.stream>>>(a, t, wts, us);
+      else
+        attn_grad_source_kernel<T, G(), NU(), MODE(), (NU() >= 4 ? 1 : 4 / NU())><<<grid, dim3(256), 0, a.stream>>>(a, t, wts, us);
     });
   });
   if (e != hipSuccess || t.S == 1) return e;
-  attn_source_join_kernel<T><<<dim3((unsigned)(a.M * a.kv_heads)), dim3(256), 0, a.stream>>>(a, t, join_lanes(a.D));
+  attn_source_join_kernel<T><<<dim3((unsigned)(a.M * a.kv_heads)), dim3(kJoin), 0, a.stream>>>(a, t, join_lanes(a.D));
   return hipGetLastError();
 }
 
