@@ -123,14 +123,16 @@ __global__ __launch_bounds__(norm_threads(T)) void norm_kernel(NormArgs a, int A
   }
 }
 
-constexpr int kNormBlocks = 8;
+template <auto kernel, int T>
+static hipError_t norm_launch(const NormArgs& a, int A) {
+  kernel<<<dim3(norm_grid<kernel, T>(a.N)), dim3(norm_threads(T)), 0, a.stream>>>(a, A, norm_inv(a.C));
+  return hipGetLastError();
+}
 
 template <class E, class O, int KT, bool ADD>
 static hipError_t norm_t(const NormArgs& a) {
   const NormShape s = norm_shape(a.C, a.K);
-  const dim3 grid(norm_grid(a.N, s.T, kNormBlocks)), block(norm_threads(s.T));
-#define EQTP_NORM(T_, NV_) \
-  (norm_kernel<E, O, T_, NV_, KT, ADD><<<grid, block, 0, a.stream>>>(a, s.A, norm_inv(a.C)), hipGetLastError())
+#define EQTP_NORM(T_, NV_) norm_launch<norm_kernel<E, O, T_, NV_, KT, ADD>, T_>(a, s.A)
   return EQTP_NORM_SHAPES(s, EQTP_NORM);
 #undef EQTP_NORM
 }

@@ -5,6 +5,7 @@
 
 #include "eqtp_device.hpp"
 #include "eqtp_kernels.hpp"
+#include "lane_ops.hpp"
 #include "philox.hpp"
 
 namespace eqtp {
@@ -63,28 +64,6 @@ __device__ __forceinline__ void store4(T* p, int left, bool tail, const float (&
 }
 
 // ---- sums over a group ------------------------------------------------------
-template <int CTRL>
-__device__ __forceinline__ float dpp_add(float v) {
-  return v + __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xf, 0xf, false));
-}
-// over 16 lanes (rotations by 8, 4, 2, 1), every lane the same bits
-__device__ __forceinline__ float sum16(float v) {
-  v = dpp_add<0x128>(v);
-  v = dpp_add<0x124>(v);
-  v = dpp_add<0x122>(v);
-  return dpp_add<0x121>(v);
-}
-// over a wave: the odd 16-lane rows change places with the even ones, then the halves
-__device__ __forceinline__ float sum64(float v) {
-  v = sum16(v);
-  const unsigned a = __builtin_bit_cast(unsigned, v);
-  const auto r = __builtin_amdgcn_permlane16_swap(a, a, false, false);
-  v = __builtin_bit_cast(float, (unsigned)r[0]) + __builtin_bit_cast(float, (unsigned)r[1]);
-  const unsigned b = __builtin_bit_cast(unsigned, v);
-  const auto s = __builtin_amdgcn_permlane32_swap(b, b, false, false);
-  return __builtin_bit_cast(float, (unsigned)s[0]) + __builtin_bit_cast(float, (unsigned)s[1]);
-}
-
 // Sums of the first `count` of v over a group of T threads, the same in each.
 // Groups of more than a wave use red [2][waves * NV]; `turn` alternates its
 // halves, so one barrier a sum suffices.
@@ -92,7 +71,7 @@ template <int T, int NV>
 __device__ __forceinline__ void group_sums(float (&v)[NV], int count, float* red, int& turn) {
 #pragma unroll
   for (int i = 0; i < NV; ++i)
-    if (i < count) v[i] = T == 16 ? sum16(v[i]) : sum64(v[i]);
+    if (i < count) v[i] = lane_sum<(T < 64 ? T : 64)>(v[i]);
   if constexpr (T > 64) {
     constexpr int W = T / 64;
     float* r = red + turn * (W * (kMaxDeg + 1));
@@ -240,7 +219,7 @@ inline NormShape norm_shape(int C, int K) {
   const int D = C * K, Q = (D + 3) / 4;
   const int P = K % 4 == 0 ? K / 4 : K;
   NormShape s = {512, 0, 512 / P * P};
-  for (int T : {16, 64, 128, 256}) {
+  for (int T : {8, 16, 32, 64, 128, 256}) {
     const int A = T / P * P;
     if (A > 0 && (Q + A - 1) / A <= 4) {
       s = {T, 0, A};
@@ -251,16 +230,24 @@ inline NormShape norm_shape(int C, int K) {
   return s;
 }
 
-// workgroups that walk over the rows: at most per_cu times four waves a compute unit
-inline int norm_grid(int64_t N, int T, int per_cu) {
+// Workgroups that walk over the rows: what the card holds at once, so that all of them finish together (with 4 a
+// compute unit where registers allow 3, the last ones ran alone: half as fast).
+template <auto kernel, int T>
+inline int norm_grid(int64_t N) {
+  static const int held = [&] {  // per kernel
+    int n = 0;
+    return hipOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, norm_threads(T), 0) == hipSuccess && n > 0 ? n : 1;
+  }();
   const int64_t rows = norm_threads(T) / T;
-  const int64_t want = (N + rows - 1) / rows, most = (int64_t)num_cus() * per_cu * 256 / norm_threads(T);
+  const int64_t want = (N + rows - 1) / rows, most = (int64_t)num_cus() * held;
   return (int)(want < most ? want : most);
 }
 
 // Calls F(T, NV) for a shape: NV is the next of the built sizes.
 #define EQTP_NORM_SHAPES(s, F)                                                     \
-  ((s).T == 16    ? ((s).NV <= 1 ? F(16, 1) : ((s).NV <= 2 ? F(16, 2) : F(16, 4))) \
+  ((s).T == 8     ? ((s).NV <= 2 ? F(8, 2) : F(8, 4))                              \
+   : (s).T == 16  ? ((s).NV <= 2 ? F(16, 2) : F(16, 4))                            \
+   : (s).T == 32  ? F(32, 4)                                                       \
    : (s).T == 64  ? ((s).NV <= 2 ? F(64, 2) : F(64, 4))                            \
    : (s).T == 128 ? ((s).NV <= 2 ? F(128, 2) : F(128, 4))                          \
    : (s).T == 256 ? F(256, 4)                                                      \

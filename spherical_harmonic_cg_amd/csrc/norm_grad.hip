@@ -174,12 +174,19 @@ __global__ __launch_bounds__(1024) void norm_weight_sum_kernel(int cols, int wco
   }
 }
 
-constexpr int kGradBlocks = 4;
 constexpr int kMaxParts = 2048;
 
 int64_t norm_workspace_floats(int64_t N, int C, int lmax) {
   // a line for each workgroup of the gradient kernel: at most kMaxParts, and one a node
   return (N < kMaxParts ? (N > 0 ? N : 1) : kMaxParts) * (lmax + 2) * C;
+}
+
+template <auto kernel, int T>
+static hipError_t norm_grad_launch(const NormGradArgs& a, int A, float* part, int& parts) {
+  parts = norm_grid<kernel, T>(a.N);
+  if (parts > kMaxParts) parts = kMaxParts;
+  kernel<<<dim3(parts), dim3(norm_threads(T)), 0, a.stream>>>(a, A, norm_inv(a.C), part);
+  return hipGetLastError();
 }
 
 template <class E, class O, int KT>
@@ -188,12 +195,8 @@ static hipError_t norm_grad_t(const NormGradArgs& a) {
   int parts = 0;
   if (a.N > 0) {
     const NormShape s = norm_shape(a.C, a.K);
-    parts = norm_grid(a.N, s.T, kGradBlocks);
-    if (parts > kMaxParts) parts = kMaxParts;
-    const dim3 grid(parts), block(norm_threads(s.T));
     float* part = sums ? a.ws : nullptr;
-#define EQTP_NORM(T_, NV_) \
-  (norm_grad_kernel<E, O, T_, NV_, KT><<<grid, block, 0, a.stream>>>(a, s.A, norm_inv(a.C), part), hipGetLastError())
+#define EQTP_NORM(T_, NV_) norm_grad_launch<norm_grad_kernel<E, O, T_, NV_, KT>, T_>(a, s.A, part, parts)
     const hipError_t e = EQTP_NORM_SHAPES(s, EQTP_NORM);
 #undef EQTP_NORM
     if (e != hipSuccess) return e;
