@@ -13,12 +13,12 @@
 
 namespace eqtp {
 
-template <class E, class O, int T, int NV, int KT>
+template <class E, class O, int T, int NV, int KT, bool DROP>
 __global__ __launch_bounds__(norm_threads(T)) void norm_grad_kernel(NormGradArgs a, int A, NormInv inv, float* part) {
   constexpr int TH = norm_threads(T), R = TH / T;
   constexpr bool HOLD = NV < 9;  // weights in registers
   __shared__ float red[T > 64 ? 2 * (T / 64) * (kMaxDeg + 1) : 1];
-  __shared__ uint8_t nib[R * (T * NV + 2)];
+  __shared__ uint8_t nib[DROP ? R * (T * NV + 2) : 1];
   __shared__ float pos[R * T * NV * 4];  // per group: a value for each place of a row
   const int C = a.C, D = C * a.K, deg = KT == 0 ? 1 : a.lmax + 1;
   Slots<T, KT> sl(a.K, A);
@@ -38,10 +38,10 @@ __global__ __launch_bounds__(norm_threads(T)) void norm_grad_kernel(NormGradArgs
   };
   if constexpr (HOLD) weights();
   DropState ds = {};
-  if (a.rng) ds = drop_state(a.rng, a.thr, a.scale);
+  if constexpr (DROP) ds = drop_state(a.rng, a.thr, a.scale);
   for (int64_t n = (int64_t)blockIdx.x * R + g; n < a.N; n += (int64_t)gridDim.x * R) {
     sl.row();
-    forget_keys(ds);
+    if constexpr (DROP) forget_keys(ds);
     if constexpr (!HOLD) weights();
     float z[NV][4], go[NV][4];
 #pragma unroll
@@ -95,7 +95,7 @@ __global__ __launch_bounds__(norm_threads(T)) void norm_grad_kernel(NormGradArgs
       float mq[4];
       sl.of_degree(v + 1, deg, mq);
       KeepBits<T, KT> kb;
-      if (a.rng) kb.begin(ds, n, C, sl.t, nib + g * (T * NV + 2));
+      if constexpr (DROP) kb.begin(ds, n, C, sl.t, nib + g * (T * NV + 2));
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
         const int i = 4 * (sl.t + A * j);
@@ -106,12 +106,14 @@ __global__ __launch_bounds__(norm_threads(T)) void norm_grad_kernel(NormGradArgs
             gz[q] = fmaf(rq[q], (go[j][q] * w[j][q] - (sl.l(q) == 0 ? am : 0.0f)) - z[j][q] * mq[q], gt[j][q]);
           if (a.gres) store4((E*)a.gres + n * D + i, D - i, tail, gz);
           if (a.gx) {
-            int c[4];
+            if constexpr (DROP) {
+              int c[4];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) c[q] = min(sl.channel(q, j), C - 1);
-            const uint32_t keep = a.rng ? kb.quad(ds, c) : 15u;
+              for (int q = 0; q < 4; ++q) c[q] = min(sl.channel(q, j), C - 1);
+              const uint32_t keep = kb.quad(ds, c);
 #pragma unroll
-            for (int q = 0; q < 4; ++q) gz[q] = drop_add(keep, q, gz[q], a.scale, 0.0f);
+              for (int q = 0; q < 4; ++q) gz[q] = drop_add(keep, q, gz[q], a.scale, 0.0f);
+            }
             store4((E*)a.gx + n * D + i, D - i, tail, gz);
           }
         }
@@ -189,14 +191,14 @@ static hipError_t norm_grad_launch(const NormGradArgs& a, int A, float* part, in
   return hipGetLastError();
 }
 
-template <class E, class O, int KT>
+template <class E, class O, int KT, bool DROP>
 static hipError_t norm_grad_t(const NormGradArgs& a) {
   const bool sums = a.gw || a.gb;
   int parts = 0;
   if (a.N > 0) {
     const NormShape s = norm_shape(a.C, a.K);
     float* part = sums ? a.ws : nullptr;
-#define EQTP_NORM(T_, NV_) norm_grad_launch<norm_grad_kernel<E, O, T_, NV_, KT>, T_>(a, s.A, part, parts)
+#define EQTP_NORM(T_, NV_) norm_grad_launch<norm_grad_kernel<E, O, T_, NV_, KT, DROP>, T_>(a, s.A, part, parts)
     const hipError_t e = EQTP_NORM_SHAPES(s, EQTP_NORM);
 #undef EQTP_NORM
     if (e != hipSuccess) return e;
@@ -212,7 +214,8 @@ static hipError_t norm_grad_t(const NormGradArgs& a) {
 
 template <class E, class O>
 static hipError_t norm_grad_k(const NormGradArgs& a) {
-  return a.K == 1 ? norm_grad_t<E, O, 0>(a) : (a.K % 4 == 0 ? norm_grad_t<E, O, 1>(a) : norm_grad_t<E, O, 2>(a));
+  if (a.rng) return a.K == 1 ? norm_grad_t<E, O, 0, true>(a) : (a.K % 4 == 0 ? norm_grad_t<E, O, 1, true>(a) : norm_grad_t<E, O, 2, true>(a));
+  return a.K == 1 ? norm_grad_t<E, O, 0, false>(a) : (a.K % 4 == 0 ? norm_grad_t<E, O, 1, false>(a) : norm_grad_t<E, O, 2, false>(a));
 }
 
 hipError_t launch_norm_grad(const NormGradArgs& a) {
