@@ -74,7 +74,8 @@ __device__ __forceinline__ void drop_stretch(int64_t base, int have, int lane, u
       for (int j = 0; j < NJ; ++j)
 #pragma unroll
         for (int h = 0; h < VE; h += 4) {
-          const uint32_t keep = keep_nibble(s, (uint64_t)(base + VE * (lane + 64 * j) + h) >> 2);
+          // stretches begin at multiples of their length, a power of two: no carry into the high word
+          const uint32_t keep = keep_nibble(s, (uint32_t)(base >> 2) + (VE * (lane + 64 * j) + h) / 4, (uint32_t)(base >> 34));
 #pragma unroll
           for (int q = 0; q < 4; ++q) v[j][h + q] = drop_add(keep, q, v[j][h + q], scale, r[j][h + q]);
         }

@@ -25,15 +25,22 @@ __device__ __forceinline__ DropState drop_state(const int64_t* __restrict__ rng,
 // At the head of a loop: the ten rounds' keys are made again instead of being kept in scalar registers.
 __device__ __forceinline__ void forget_keys(DropState& s) { asm volatile("" : "+s"(s.k0), "+s"(s.k1)); }
 
+// a ^ b ^ c as one instruction (its truth table is 0x96).
+__device__ __forceinline__ uint32_t xor3(uint32_t a, uint32_t b, uint32_t c) {
+  return (uint32_t)__builtin_amdgcn_bitop3_b32((int)a, (int)b, (int)c, 0x96);
+}
+
 // One round multiplies words 0 and 2 by the method's constants and crosses the
 // halves of the products over; the key moves by two Weyl constants a round.
-__device__ __forceinline__ void philox_words(const DropState& s, uint64_t block, uint32_t (&w)[4]) {
-  uint32_t c0 = (uint32_t)block, c1 = (uint32_t)(block >> 32), c2 = s.c2, c3 = s.c3, k0 = s.k0, k1 = s.k1;
+// The block's high word is an argument of its own: where it is the same for a wave, as the offset is, the first
+// rounds' products of these words are scalar ones.
+__device__ __forceinline__ void philox_words(const DropState& s, uint32_t lo, uint32_t hi, uint32_t (&w)[4]) {
+  uint32_t c0 = lo, c1 = hi, c2 = s.c2, c3 = s.c3, k0 = s.k0, k1 = s.k1;
 #pragma unroll
   for (int r = 0; r < 10; ++r) {
     const uint64_t a = (uint64_t)0xD2511F53u * c0, b = (uint64_t)0xCD9E8D57u * c2;
-    c0 = (uint32_t)(b >> 32) ^ c1 ^ k0;
-    c2 = (uint32_t)(a >> 32) ^ c3 ^ k1;
+    c0 = r == 0 ? (uint32_t)(b >> 32) ^ c1 ^ k0 : xor3((uint32_t)(b >> 32), c1, k0);
+    c2 = xor3((uint32_t)(a >> 32), c3, k1);
     c1 = (uint32_t)b;
     c3 = (uint32_t)a;
     k0 += 0x9E3779B9u;
@@ -43,11 +50,15 @@ __device__ __forceinline__ void philox_words(const DropState& s, uint64_t block,
 }
 
 // Bit i set: channel 4 block + i is kept.
-__device__ __forceinline__ uint32_t keep_nibble(const DropState& s, uint64_t block) {
+__device__ __forceinline__ uint32_t keep_nibble(const DropState& s, uint32_t lo, uint32_t hi) {
   uint32_t w[4];
-  philox_words(s, block, w);
+  philox_words(s, lo, hi, w);
   return (uint32_t)(w[0] >= s.thr) | (uint32_t)(w[1] >= s.thr) << 1 | (uint32_t)(w[2] >= s.thr) << 2 |
          (uint32_t)(w[3] >= s.thr) << 3;
+}
+
+__device__ __forceinline__ uint32_t keep_nibble(const DropState& s, uint64_t block) {
+  return keep_nibble(s, (uint32_t)block, (uint32_t)(block >> 32));
 }
 
 // The value of x at place q of a quad with these keep bits, beside its residual; the norm's kernels and the dropout
