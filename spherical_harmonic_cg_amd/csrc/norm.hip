@@ -28,6 +28,8 @@ __global__ __launch_bounds__(norm_threads(T)) void norm_kernel(NormArgs a, int A
   const int g = T < 64 ? threadIdx.x / T : __builtin_amdgcn_readfirstlane(threadIdx.x / T);
   const bool tail = KT != 1 && (D & 3) != 0;
   int turn = 0;
+  constexpr int G = T < 64 ? T : 64;
+  const float inv_mine = 1.0f / (float)(C * (2 * sum8_index<G>() + 1));
   constexpr int NB = KT == 0 ? 4 : 1;  // component 0 fills every slot (K = 1), or at most one of a quad
   float w[NV][4], b[NV][NB];
 #pragma unroll
@@ -96,14 +98,19 @@ __global__ __launch_bounds__(norm_threads(T)) void norm_kernel(NormArgs a, int A
     if (!sl.on)
 #pragma unroll
       for (int q = 0; q < 4; ++q) sq[q] = 0.0f;
-    float r[kMaxDeg] = {};
-    sl.by_degree(sq, deg, r);
-    group_sums<T, kMaxDeg>(r, deg, red, turn);
+    float rq[4], r;
+    if constexpr (KT == 0) {
+      float v[1] = {(sq[0] + sq[1]) + (sq[2] + sq[3])};
+      group_sums<T, 1>(v, 1, red, turn);
+      r = rsqrtf(fmaf(v[0], inv.v[0], a.eps));
 #pragma unroll
-    for (int d = 0; d < kMaxDeg; ++d)
-      if (d < deg) r[d] = rsqrtf(fmaf(r[d], inv.v[d], a.eps));
-    float rq[4];
-    sl.of_degree(r, deg, rq);
+      for (int q = 0; q < 4; ++q) rq[q] = r;
+    } else {
+      float v[8] = {};
+      sl.by_degree(sq, deg, v);
+      r = rsqrtf(fmaf(group_sums8<T>(v, red, turn), inv_mine, a.eps));
+      sl.of_degree(r, 0, rq);
+    }
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int i = 4 * (sl.t + A * j);
@@ -113,12 +120,15 @@ __global__ __launch_bounds__(norm_threads(T)) void norm_kernel(NormArgs a, int A
         o[q] = fmaf(z[j][q] * rq[q], w[j][q], KT == 0 ? b[j][q % NB] : (sl.l(q) == 0 ? b[j][0] : 0.0f));
       if (sl.on) store4((O*)a.out + n * D + i, D - i, tail, o);
     }
-    if (a.stats && sl.t == 0) {
+    if (a.stats) {
       float* st = a.stats + n * (a.lmax + 2);
-      st[0] = mu[0];
-#pragma unroll
-      for (int d = 0; d < kMaxDeg; ++d)
-        if (d < deg) st[1 + d] = r[d];
+      if (sl.t == 0) st[0] = mu[0];
+      if constexpr (KT == 0) {
+        if (sl.t == 0) st[1] = r;
+      } else {
+        if (T > 64 ? sl.t < 64 && sl.t % 8 == 0 : sl.t % (T / 8) == 0)  // a thread that has a degree's sum first
+          if (const int d = sum8_index<G>(); d < deg) st[1 + d] = r;
+      }
     }
   }
 }

@@ -92,6 +92,25 @@ __device__ __forceinline__ void group_sums(float (&v)[NV], int count, float* red
   }
 }
 
+// Sums of eight values over a group of T threads: a thread ends with that of value sum8_index.
+template <int T>
+__device__ __forceinline__ float group_sums8(const float (&v)[8], float* red, int& turn) {
+  constexpr int G = T < 64 ? T : 64;
+  float mine = lane_sums8<G>(v);
+  if constexpr (T > 64) {
+    constexpr int W = T / 64;
+    float* r = red + turn * (W * (kMaxDeg + 1));
+    turn ^= 1;
+    const int k = sum8_index<64>();
+    if ((threadIdx.x & 7) == 0) r[k * W + (threadIdx.x >> 6)] = mine;
+    __syncthreads();
+    mine = 0.0f;
+#pragma unroll
+    for (int w = 0; w < W; ++w) mine += r[k * W + w];
+  }
+  return mine;
+}
+
 // ---- which channels of a row are kept -------------------------------------
 // A nibble of keep bits for each counter block that the row touches, in LDS.
 // With one component a channel and C a multiple of 4 a thread's quad is one
@@ -173,15 +192,10 @@ struct Slots {
           for (int q = 0; q < 4; ++q) s[d] += l(q) == d ? v[q] : 0.0f;
     }
   }
-  __device__ __forceinline__ void of_degree(const float* s, int deg, float (&v)[4]) const {
+  // the slots' own of values that lie as group_sums8 leaves them, degree l as value first + l
+  __device__ __forceinline__ void of_degree(float mine, int first, float (&v)[4]) const {
 #pragma unroll
-    for (int q = 0; q < 4; ++q) v[q] = s[0];
-    if constexpr (KT != 0)
-#pragma unroll
-      for (int d = 1; d < kMaxDeg; ++d)
-        if (d < deg)
-#pragma unroll
-          for (int q = 0; q < 4; ++q) v[q] = l(q) == d ? s[d] : v[q];
+    for (int q = 0; q < 4; ++q) v[q] = sum8_of<(T < 64 ? T : 64)>(mine, first + l(q));
   }
   // the value at component 0, or the sum of the values there (K = 1)
   __device__ __forceinline__ float scalars(const float (&v)[4]) const {

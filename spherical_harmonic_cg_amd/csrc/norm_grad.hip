@@ -25,6 +25,9 @@ __global__ __launch_bounds__(norm_threads(T)) void norm_grad_kernel(NormGradArgs
   const int g = T < 64 ? threadIdx.x / T : __builtin_amdgcn_readfirstlane(threadIdx.x / T);
   const bool tail = KT != 1 && (D & 3) != 0;
   int turn = 0;
+  constexpr int G = T < 64 ? T : 64;
+  const int place = sum8_index<G>();  // of eight sums: the scalars', then the degrees'
+  const float inv_mine = 1.0f / (float)(C * (place == 0 ? 1 : 2 * place - 1));
   constexpr int NB = KT == 0 ? 4 : 1;  // component 0 fills every slot (K = 1), or at most one of a quad
   float w[NV][4], aw[NV][4] = {}, ab[NV][NB] = {};
   auto weights = [&]() {
@@ -59,7 +62,7 @@ __global__ __launch_bounds__(norm_threads(T)) void norm_grad_kernel(NormGradArgs
       }
     const float* st = a.stats + n * (a.lmax + 2);
     const float mu = st[0];
-    float rq[4], sq[4] = {}, v[kMaxDeg + 1] = {};
+    float rq[4], sq[4] = {}, v[8] = {};
 #pragma unroll
     for (int q = 0; q < 4; ++q) rq[q] = st[1 + sl.l(q)];
 #pragma unroll
@@ -86,14 +89,19 @@ __global__ __launch_bounds__(norm_threads(T)) void norm_grad_kernel(NormGradArgs
       if (!sl.on)
 #pragma unroll
         for (int q = 0; q < 4; ++q) sq[q] = 0.0f;
-      sl.by_degree(sq, deg, v + 1);
-      group_sums<T, kMaxDeg + 1>(v, deg + 1, red, turn);
-      const float am = v[0] * inv.v[0];
+      float am, mq[4];
+      if constexpr (KT == 0) {
+        float two[2] = {v[0], (sq[0] + sq[1]) + (sq[2] + sq[3])};
+        group_sums<T, 2>(two, 2, red, turn);
+        am = two[0] * inv.v[0];
 #pragma unroll
-      for (int d = 0; d < kMaxDeg; ++d)
-        if (d < deg) v[1 + d] *= inv.v[d];
-      float mq[4];
-      sl.of_degree(v + 1, deg, mq);
+        for (int q = 0; q < 4; ++q) mq[q] = two[1] * inv.v[0];
+      } else {
+        sl.by_degree(sq, deg, v + 1);
+        const float mean = group_sums8<T>(v, red, turn) * inv_mine;
+        am = sum8_of<G>(mean, 0);
+        sl.of_degree(mean, 1, mq);
+      }
       KeepBits<T, KT> kb;
       if constexpr (DROP) kb.begin(ds, n, C, sl.t, nib + g * (T * NV + 2));
 #pragma unroll
