@@ -370,13 +370,13 @@ __device__ __forceinline__ float over_pieces(int S, int k, int W, int L, float* 
   return red[threadIdx.x];
 }
 
-// Joins the pieces of the rows: a workgroup a (row, head); its threads lie over the pieces and the places.
+// Joins the pieces of the rows: a workgroup a (row, head) and L places; its threads lie over the pieces and the places.
 template <class T>
 __global__ __launch_bounds__(kJoin) void attn_join_kernel(AttnArgs a, Tiling t, int L) {
   __shared__ float red[kJoin], w[kMaxPieces], few[kJoin / 64];
   const int H = a.heads, D = a.D, S = t.S;
   const int64_t n = blockIdx.x / H;
-  const int h = (int)(blockIdx.x - n * H), d0 = threadIdx.x & (L - 1), k = threadIdx.x / L, W = kJoin / L;
+  const int h = (int)(blockIdx.x - n * H), d = blockIdx.y * L + (threadIdx.x & (L - 1)), k = threadIdx.x / L, W = kJoin / L;
   const float* part = t.part + (n * S * H + h) * D;
   const float* ml = t.part + a.N * S * H * (int64_t)D + (n * S * H + h) * 2;
   float top = -INFINITY, sum = 0.0f;
@@ -392,11 +392,9 @@ __global__ __launch_bounds__(kJoin) void attn_join_kernel(AttnArgs a, Tiling t, 
   }
   sum = over_group<false>(sum, few);
   const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-  for (int d = d0; d < (D + L - 1) / L * L; d += L) {
-    const float acc = over_pieces(S, k, W, L, red, [&](int s) { return d < D ? part[(int64_t)s * H * D + d] * w[s] : 0.0f; });
-    if (k == 0 && d < D) ((T*)a.out)[(n * H + h) * D + d] = (T)(acc * inv);
-  }
-  if (a.lse && threadIdx.x == 0) a.lse[n * H + h] = sum == 0.0f ? -INFINITY : top + __builtin_amdgcn_logf(sum) * kLn2;
+  const float acc = over_pieces(S, k, W, L, red, [&](int s) { return d < D ? part[(int64_t)s * H * D + d] * w[s] : 0.0f; });
+  if (k == 0 && d < D) ((T*)a.out)[(n * H + h) * D + d] = (T)(acc * inv);
+  if (a.lse && threadIdx.x == 0 && blockIdx.y == 0) a.lse[n * H + h] = sum == 0.0f ? -INFINITY : top + __builtin_amdgcn_logf(sum) * kLn2;
 }
 
 // ---- gradients ------------------------------------------------------------------
@@ -555,7 +553,7 @@ __global__ __launch_bounds__(kJoin) void attn_grad_join_kernel(AttnGradArgs a, T
   __shared__ float red[kJoin], few[kJoin / 64];
   const int H = a.heads, D = a.D, S = t.S;
   const int64_t n = blockIdx.x / H, all = a.N * S * H * (int64_t)D;
-  const int h = (int)(blockIdx.x - n * H), d0 = threadIdx.x & (L - 1), k = threadIdx.x / L, W = kJoin / L;
+  const int h = (int)(blockIdx.x - n * H), d = blockIdx.y * L + (threadIdx.x & (L - 1)), k = threadIdx.x / L, W = kJoin / L;
   const float* tp = t.part + 2 * all + (n * S * H + h) * 2;
   float tt = 0.0f, total = 0.0f;
   for (int s = threadIdx.x; s < S; s += kJoin) {
@@ -566,18 +564,17 @@ __global__ __launch_bounds__(kJoin) void attn_grad_join_kernel(AttnGradArgs a, T
   total = over_group<false>(total, few);
   const float inv = total == 0.0f ? 0.0f : 1.0f / total;
   tt *= inv;
-  if (threadIdx.x == 0) {
+  if (threadIdx.x == 0 && blockIdx.y == 0) {
     float* o = t.part + 2 * all + (a.N * S * H + n * H + h) * 2;
     o[0] = tt;
     o[1] = inv;
   }
-  if (a.gq)
-    for (int d = d0; d < (D + L - 1) / L * L; d += L) {
-      const float* p = t.part + (n * S * H + h) * D + d;
-      const float x = over_pieces(S, k, W, L, red, [&](int s) { return d < D ? p[(int64_t)s * H * D] : 0.0f; });
-      const float y = over_pieces(S, k, W, L, red, [&](int s) { return d < D ? p[all + (int64_t)s * H * D] : 0.0f; });
-      if (k == 0 && d < D) ((T*)a.gq)[(n * H + h) * D + d] = (T)(fmaf(-tt, y, x) * (inv * a.scale));
-    }
+  if (a.gq) {
+    const float* p = t.part + (n * S * H + h) * D + d;
+    const float x = over_pieces(S, k, W, L, red, [&](int s) { return d < D ? p[(int64_t)s * H * D] : 0.0f; });
+    const float y = over_pieces(S, k, W, L, red, [&](int s) { return d < D ? p[all + (int64_t)s * H * D] : 0.0f; });
+    if (k == 0 && d < D) ((T*)a.gq)[(n * H + h) * D + d] = (T)(fmaf(-tt, y, x) * (inv * a.scale));
+  }
 }
 
 // w and u of every edge of the pieces, from their rows' joined sums: a workgroup a (row, piece).  (By the joining
@@ -694,15 +691,13 @@ __global__ __launch_bounds__(kJoin) void attn_source_join_kernel(AttnGradArgs a,
   __shared__ float red[kJoin];
   const int HK = a.kv_heads, D = a.D, S = t.S;
   const int64_t m = blockIdx.x / HK, all = a.M * S * HK * (int64_t)D;
-  const int h = (int)(blockIdx.x - m * HK), d0 = threadIdx.x & (L - 1), k = threadIdx.x / L, W = kJoin / L;
-  for (int d = d0; d < (D + L - 1) / L * L; d += L) {
-    const float* p = t.part + (m * S * HK + h) * D + d;
-    const float x = over_pieces(S, k, W, L, red, [&](int s) { return d < D ? p[(int64_t)s * HK * D] : 0.0f; });
-    const float y = over_pieces(S, k, W, L, red, [&](int s) { return d < D ? p[all + (int64_t)s * HK * D] : 0.0f; });
-    if (k == 0 && d < D) {
-      if (a.gk) ((T*)a.gk)[(m * HK + h) * D + d] = (T)(x * a.scale);
-      if (a.gv) ((T*)a.gv)[(m * HK + h) * D + d] = (T)y;
-    }
+  const int h = (int)(blockIdx.x - m * HK), d = blockIdx.y * L + (threadIdx.x & (L - 1)), k = threadIdx.x / L, W = kJoin / L;
+  const float* p = t.part + (m * S * HK + h) * D + d;
+  const float x = over_pieces(S, k, W, L, red, [&](int s) { return d < D ? p[(int64_t)s * HK * D] : 0.0f; });
+  const float y = over_pieces(S, k, W, L, red, [&](int s) { return d < D ? p[all + (int64_t)s * HK * D] : 0.0f; });
+  if (k == 0 && d < D) {
+    if (a.gk) ((T*)a.gk)[(m * HK + h) * D + d] = (T)(x * a.scale);
+    if (a.gv) ((T*)a.gv)[(m * HK + h) * D + d] = (T)y;
   }
 }
 
@@ -739,7 +734,7 @@ int64_t attn_grad_workspace_bytes(int64_t N, int64_t M, int64_t E, int D, int he
   return grad_tables(E, heads) + (rows > sources ? rows : sources);
 }
 
-constexpr int64_t kSpreadBytes = (int64_t)8 << 20, kSpreadMost = (int64_t)32 << 20, kShortRow = 8;
+constexpr int64_t kSpreadLine = 512, kSpreadBytes = (int64_t)8 << 20, kSpreadMost = (int64_t)32 << 20, kShortRow = 8;
 
 // Lanes and units of a head's row: up to 8 units one a lane, then two, four, eight a lane.
 struct HeadShape {
@@ -756,8 +751,8 @@ static HeadShape head_shape(int D, int VE) {
 static bool is_pow2(int v) { return (v & (v - 1)) == 0; }
 
 // heads of the pass (of q, or of k and v), share of them that read the same rows, rows and edges of the pass, bytes
-// of the two gathered tensors.
-static Tiling tiling(const HeadShape& s, int heads, int share, int64_t rows, int64_t E, int64_t gathered, float* part) {
+// of the two gathered tensors and of a head's row in them.
+static Tiling tiling(const HeadShape& s, int heads, int share, int64_t rows, int64_t E, int64_t gathered, int row_bytes, float* part) {
   Tiling t;
   const int room = 64 / s.G, kv = heads / share;
   t.S = pieces(rows, E);
@@ -765,8 +760,9 @@ static Tiling tiling(const HeadShape& s, int heads, int share, int64_t rows, int
   // Gathers out of tensors that an L2 of 4 MiB does not hold run at about 7.5 TB/s whatever the tensors' size below
   // the L2's misses; heads dealt to the XCDs leave each L2 a part of them.
   t.spread = 0;
-  const int nb = kv < 8 ? kv : 8;
-  if (t.S == 1 && gathered > kSpreadBytes && gathered / nb <= kSpreadMost && kv > 1 && is_pow2(kv) && is_pow2(share) && heads / nb <= room &&
+  int nb = kv < 8 ? kv : 8;
+  while (nb > 1 && kv / nb * row_bytes < kSpreadLine) nb >>= 1;  // (pieces of a cache line would fetch all of it)
+  if (t.S == 1 && nb > 1 && gathered > kSpreadBytes && gathered / nb <= kSpreadMost && kv > 1 && is_pow2(kv) && is_pow2(share) && heads / nb <= room &&
       rows < ((int64_t)1 << 24)) {
     t.HW = heads / nb;
     t.spread = 8 / nb;
@@ -833,19 +829,21 @@ static void with_shape(const HeadShape& s, F f) {
   else if constexpr (El<T>::VE == 4) modes(I64(), I8());
 }
 
-static int join_lanes(int D) { return pow2_from(D) < kJoin ? pow2_from(D) : kJoin; }
+// places of a row that a joining workgroup takes: 64 bytes, so that 64 threads share each place's pieces
+static int join_lanes(int D) { return pow2_from(D) < 16 ? pow2_from(D) : 16; }
+static dim3 join_grid(int64_t rows, int D) { return dim3((unsigned)rows, (unsigned)((D + join_lanes(D) - 1) / join_lanes(D))); }
 
 template <class T>
 static hipError_t attn_t(const AttnArgs& a) {
   const HeadShape s = head_shape(a.D, El<T>::VE);
-  Tiling t = tiling(s, a.heads, a.heads / a.kv_heads, a.N, a.E, 2 * a.M * a.kv_heads * a.D * (int64_t)sizeof(T), (float*)a.ws);
+  Tiling t = tiling(s, a.heads, a.heads / a.kv_heads, a.N, a.E, 2 * a.M * a.kv_heads * a.D * (int64_t)sizeof(T), a.D * (int)sizeof(T), (float*)a.ws);
   const hipError_t e = over_tasks(a.N, t, [&](dim3 grid) {
     with_shape<T>(s, [&](auto G, auto NU, auto MODE) {
       attn_kernel<T, G(), NU(), MODE(), 8 / NU()><<<grid, dim3(256), 0, a.stream>>>(a, t);
     });
   });
   if (e != hipSuccess || t.S == 1) return e;
-  attn_join_kernel<T><<<dim3((unsigned)(a.N * a.heads)), dim3(kJoin), 0, a.stream>>>(a, t, join_lanes(a.D));
+  attn_join_kernel<T><<<join_grid(a.N * a.heads, a.D), dim3(kJoin), 0, a.stream>>>(a, t, join_lanes(a.D));
   return hipGetLastError();
 }
 
@@ -856,7 +854,7 @@ static hipError_t attn_grad_t(const AttnGradArgs& a) {
   float* part = (float*)((unsigned char*)a.ws + grad_tables(a.E, a.heads));
   const HeadShape s = head_shape(a.D, El<T>::VE);
   if (a.N > 0) {
-    Tiling t = tiling(s, a.heads, a.heads / a.kv_heads, a.N, a.E, 2 * a.M * a.kv_heads * a.D * (int64_t)sizeof(T), part);
+    Tiling t = tiling(s, a.heads, a.heads / a.kv_heads, a.N, a.E, 2 * a.M * a.kv_heads * a.D * (int64_t)sizeof(T), a.D * (int)sizeof(T), part);
     hipError_t e = over_tasks(a.N, t, [&](dim3 grid) {
       with_shape<T>(s, [&](auto G, auto NU, auto MODE) {
         attn_grad_row_kernel<T, G(), NU(), MODE(), (NU() >= 4 ? 1 : 4 / NU())><<<grid, dim3(256), 0, a.stream>>>(a, t, wts, us);
@@ -864,7 +862,7 @@ static hipError_t attn_grad_t(const AttnGradArgs& a) {
     });
     if (e != hipSuccess) return e;
     if (t.S > 1) {
-      attn_grad_join_kernel<T><<<dim3((unsigned)(a.N * a.heads)), dim3(kJoin), 0, a.stream>>>(a, t, join_lanes(a.D));
+      attn_grad_join_kernel<T><<<join_grid(a.N * a.heads, a.D), dim3(kJoin), 0, a.stream>>>(a, t, join_lanes(a.D));
       e = hipGetLastError();
       if (e != hipSuccess) return e;
       attn_grad_fix_kernel<<<dim3((unsigned)(a.N * t.S)), dim3(256), 0, a.stream>>>(a, t, wts, us);
@@ -873,7 +871,7 @@ static hipError_t attn_grad_t(const AttnGradArgs& a) {
     }
   }
   if (a.M == 0 || (!a.gk && !a.gv)) return hipSuccess;
-  Tiling t = tiling(s, a.kv_heads, 1, a.M, a.E, 2 * a.N * a.heads * a.D * (int64_t)sizeof(T), part);
+  Tiling t = tiling(s, a.kv_heads, 1, a.M, a.E, 2 * a.N * a.heads * a.D * (int64_t)sizeof(T), a.D * (int)sizeof(T), part);
   // sources of one or two edges (a readout's items have one): places for four would stay empty and cost the registers
   // that more waves need (50k sources of one edge: 27 against 15 us)
   const bool one = a.E <= 2 * a.M;
@@ -886,7 +884,7 @@ static hipError_t attn_grad_t(const AttnGradArgs& a) {
     });
   });
   if (e != hipSuccess || t.S == 1) return e;
-  attn_source_join_kernel<T><<<dim3((unsigned)(a.M * a.kv_heads)), dim3(kJoin), 0, a.stream>>>(a, t, join_lanes(a.D));
+  attn_source_join_kernel<T><<<join_grid(a.M * a.kv_heads, a.D), dim3(kJoin), 0, a.stream>>>(a, t, join_lanes(a.D));
   return hipGetLastError();
 }
 

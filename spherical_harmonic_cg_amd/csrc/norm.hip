@@ -39,9 +39,17 @@ __global__ __launch_bounds__(norm_threads(T)) void norm_kernel(NormArgs a, int A
       const int c = sl.channel(q, j);
       w[j][q] = a.weight && sl.on && c < C ? a.weight[sl.l(q) * C + c] : 1.0f;
       if (KT == 0 || q == 0) b[j][KT == 0 ? q : 0] = 0.0f;
-      if (a.bias && sl.on && c < C && sl.l(q) == 0) b[j][KT == 0 ? q : 0] = a.bias[c];
+      if (a.bias && sl.on && c < C && sl.zero(q)) b[j][KT == 0 ? q : 0] = a.bias[c];
     }
   }
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) arrived(w[j][q]);
+#pragma unroll
+    for (int q = 0; q < NB; ++q) arrived(b[j][q]);
+  }
+  const bool full = A == T && D == 4 * T * NV;
   DropState ds = {};
   if constexpr (ADD)
     if (a.rng) ds = drop_state(a.rng, a.thr, a.scale);
@@ -50,20 +58,16 @@ __global__ __launch_bounds__(norm_threads(T)) void norm_kernel(NormArgs a, int A
     forget_keys(ds);
     const E* x = (const E*)a.x + n * D;
     float z[NV][4];
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int i = 4 * (sl.t + A * j);
-      load4(x + i, sl.on ? D - i : 0, tail, z[j]);
-    }
+    RowQuads<E, NV> rows;
+    rows.load(x, sl, A, D);
     if constexpr (ADD) {
       float res[NV][4];
-#pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        const int i = 4 * (sl.t + A * j);
-        load4((const E*)a.residual + n * D + i, sl.on ? D - i : 0, tail, res[j]);
-      }
+      RowQuads<E, NV> more;
+      more.load((const E*)a.residual + n * D, sl, A, D);
       KeepBits<T, KT> kb;
       if (a.rng) kb.begin(ds, n, C, sl.t, nib + g * (T * NV + 2));
+      rows.values(sl, A, D, full, tail, z);
+      more.values(sl, A, D, full, tail, res);
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
         const int i = 4 * (sl.t + A * j);
@@ -78,10 +82,15 @@ __global__ __launch_bounds__(norm_threads(T)) void norm_kernel(NormArgs a, int A
           store4((E*)a.total + n * D + i, D - i, tail, z[j]);
         }
       }
+    } else {
+      rows.values(sl, A, D, full, tail, z);
     }
-    float mu[1] = {0.0f};
+    float slot[4] = {};
 #pragma unroll
-    for (int j = 0; j < NV; ++j) mu[0] += sl.scalars(z[j]);
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) slot[q] += z[j][q];
+    float mu[1] = {sl.scalars(slot)};
     group_sums<T, 1>(mu, 1, red, turn);
     mu[0] *= inv.v[0];
     float sq[4] = {};
@@ -90,8 +99,8 @@ __global__ __launch_bounds__(norm_threads(T)) void norm_kernel(NormArgs a, int A
       const int i = 4 * (sl.t + A * j);
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        z[j][q] -= sl.l(q) == 0 ? mu[0] : 0.0f;
-        if (KT == 1 ? i >= D : i + q >= D) z[j][q] = 0.0f;
+        // (places past the row hold 0 and stay 0)
+        if (KT != 1 || q == 0) z[j][q] -= sl.zero(q) && (KT == 1 ? i < D : i + q < D) ? mu[0] : 0.0f;
         sq[q] = fmaf(z[j][q], z[j][q], sq[q]);
       }
     }
@@ -117,7 +126,7 @@ __global__ __launch_bounds__(norm_threads(T)) void norm_kernel(NormArgs a, int A
       float o[4];
 #pragma unroll
       for (int q = 0; q < 4; ++q)
-        o[q] = fmaf(z[j][q] * rq[q], w[j][q], KT == 0 ? b[j][q % NB] : (sl.l(q) == 0 ? b[j][0] : 0.0f));
+        o[q] = fmaf(z[j][q] * rq[q], w[j][q], KT == 0 ? b[j][q % NB] : (KT == 1 ? (q == 0 ? b[j][0] : 0.0f) : (sl.zero(q) ? b[j][0] : 0.0f)));
       if (sl.on) store4((O*)a.out + n * D + i, D - i, tail, o);
     }
     if (a.stats) {

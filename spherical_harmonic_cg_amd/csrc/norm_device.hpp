@@ -19,38 +19,29 @@ __device__ __forceinline__ int degree_of(int m) {
 // ---- four consecutive elements, aligned as one element only ---------------
 typedef float f4u __attribute__((ext_vector_type(4), aligned(4)));
 typedef __bf16 b4u __attribute__((ext_vector_type(4), aligned(2)));
+typedef __bf16 b4 __attribute__((ext_vector_type(4)));
+
+template <class T>
+struct Quad;
+template <>
+struct Quad<float> {
+  typedef f4 Raw;
+  static __device__ __forceinline__ Raw load(const float* p) { return *reinterpret_cast<const f4u*>(p); }
+  static __device__ __forceinline__ void store(float* p, const float (&v)[4]) {
+    *reinterpret_cast<f4u*>(p) = f4u{v[0], v[1], v[2], v[3]};
+  }
+};
+template <>
+struct Quad<__bf16> {
+  typedef b4 Raw;
+  static __device__ __forceinline__ Raw load(const __bf16* p) { return *reinterpret_cast<const b4u*>(p); }
+  static __device__ __forceinline__ void store(__bf16* p, const float (&v)[4]) {
+    *reinterpret_cast<b4u*>(p) = b4u{(__bf16)v[0], (__bf16)v[1], (__bf16)v[2], (__bf16)v[3]};
+  }
+};
 
 // `left` elements of the row are left from p on (0 or less: none); `tail`: there are rows whose last quad is short
 // (the same for every thread).
-__device__ __forceinline__ void widen4(const float* p, float (&v)[4]) {
-  const f4u t = *reinterpret_cast<const f4u*>(p);
-#pragma unroll
-  for (int q = 0; q < 4; ++q) v[q] = t[q];
-}
-__device__ __forceinline__ void widen4(const __bf16* p, float (&v)[4]) {
-  const b4u t = *reinterpret_cast<const b4u*>(p);
-#pragma unroll
-  for (int q = 0; q < 4; ++q) v[q] = (float)t[q];
-}
-template <class T>
-__device__ __forceinline__ void load4(const T* p, int left, bool tail, float (&v)[4]) {
-#pragma unroll
-  for (int q = 0; q < 4; ++q) v[q] = 0.0f;
-  if (left <= 0) return;
-  if (tail && left < 4) {
-#pragma unroll
-    for (int q = 0; q < 3; ++q)
-      if (q < left) v[q] = (float)p[q];
-  } else {
-    widen4(p, v);
-  }
-}
-__device__ __forceinline__ void narrow4(float* p, const float (&v)[4]) {
-  *reinterpret_cast<f4u*>(p) = f4u{v[0], v[1], v[2], v[3]};
-}
-__device__ __forceinline__ void narrow4(__bf16* p, const float (&v)[4]) {
-  *reinterpret_cast<b4u*>(p) = b4u{(__bf16)v[0], (__bf16)v[1], (__bf16)v[2], (__bf16)v[3]};
-}
 template <class T>
 __device__ __forceinline__ void store4(T* p, int left, bool tail, const float (&v)[4]) {
   if (left <= 0) return;
@@ -59,9 +50,60 @@ __device__ __forceinline__ void store4(T* p, int left, bool tail, const float (&
     for (int q = 0; q < 3; ++q)
       if (q < left) p[q] = (T)v[q];
   } else {
-    narrow4(p, v);
+    Quad<T>::store(p, v);
   }
 }
+
+// A thread's quads of a row as they lie in memory.  All loads of a row are issued before the first value is used, and
+// none stands behind a branch of its own (a conversion inside such a branch waits for its load, and the next load for
+// the conversion: bf16 rows took 1.8 times as long): a quad past the row, or the short one at its end, is loaded from
+// the row's last four elements and put right afterwards.
+template <class T, int NV>
+struct RowQuads {
+  typename Quad<T>::Raw raw[NV];
+  template <class S>
+  __device__ __forceinline__ void load(const T* row, const S& sl, int A, int D) {
+    if (D >= 4) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) raw[j] = Quad<T>::load(row + (sl.on ? min(4 * (sl.t + A * j), D - 4) : 0));
+    } else {  // (a row of one to three elements, in the first thread)
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) raw[j][q] = (T)0.0f;
+      if (sl.t == 0)
+#pragma unroll
+        for (int q = 0; q < 3; ++q)
+          if (q < D) raw[0][q] = row[q];
+    }
+  }
+  // the values, zeros past the row
+  template <class S>
+  __device__ __forceinline__ void values(const S& sl, int A, int D, bool full, bool tail, float (&v)[NV][4]) const {
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) v[j][q] = (float)raw[j][q];
+    if (full || D < 4) return;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int over = sl.on ? 4 * (sl.t + A * j) - (D - 4) : 4;  // places that the quad reaches past the row
+      if (tail) {
+        const float w[7] = {v[j][0], v[j][1], v[j][2], v[j][3], 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          v[j][q] = over <= 0 ? w[q] : (over == 1 ? w[q + 1] : (over == 2 ? w[q + 2] : (over == 3 ? w[q + 3] : 0.0f)));
+      } else {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) v[j][q] = over > 0 ? 0.0f : v[j][q];
+      }
+    }
+  }
+};
+
+// Waits for a value before a loop: left to its first use inside, the wait would be for everything in flight there,
+// the stores of the round before included.
+__device__ __forceinline__ void arrived(float& v) { asm volatile("" : "+v"(v)); }
 
 // ---- sums over a group ------------------------------------------------------
 // Sums of the first `count` of v over a group of T threads, the same in each.
@@ -197,12 +239,15 @@ struct Slots {
 #pragma unroll
     for (int q = 0; q < 4; ++q) v[q] = sum8_of<(T < 64 ? T : 64)>(mine, first + l(q));
   }
+  // slot q holds component 0 (KT = 1: quads begin at multiples of 4, so slot 0 only)
+  __device__ __forceinline__ bool zero(int q) const { return KT == 0 || ((KT == 2 || q == 0) && l(q) == 0); }
   // the value at component 0, or the sum of the values there (K = 1)
   __device__ __forceinline__ float scalars(const float (&v)[4]) const {
     if constexpr (KT == 0) return (v[0] + v[1]) + (v[2] + v[3]);
+    if constexpr (KT == 1) return zero(0) ? v[0] : 0.0f;
     float s = 0.0f;
 #pragma unroll
-    for (int q = 0; q < 4; ++q) s += l(q) == 0 ? v[q] : 0.0f;
+    for (int q = 0; q < 4; ++q) s = zero(q) ? v[q] : s;
     return s;
   }
 };

@@ -39,56 +39,60 @@ __global__ __launch_bounds__(norm_threads(T)) void norm_grad_kernel(NormGradArgs
         w[j][q] = a.weight && sl.on && c < C ? a.weight[sl.l(q) * C + c] : 1.0f;
       }
   };
-  if constexpr (HOLD) weights();
+  if constexpr (HOLD) {
+    weights();
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) arrived(w[j][q]);
+  }
+  const bool full = A == T && D == 4 * T * NV;
   DropState ds = {};
   if constexpr (DROP) ds = drop_state(a.rng, a.thr, a.scale);
   for (int64_t n = (int64_t)blockIdx.x * R + g; n < a.N; n += (int64_t)gridDim.x * R) {
     sl.row();
     if constexpr (DROP) forget_keys(ds);
     if constexpr (!HOLD) weights();
-    float z[NV][4], go[NV][4];
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int i = 4 * (sl.t + A * j);
-      load4((const E*)a.total + n * D + i, sl.on ? D - i : 0, tail, z[j]);
-      load4((const O*)a.gout + n * D + i, sl.on ? D - i : 0, tail, go[j]);
-    }
-    float gt[NV][4] = {};
-    if (a.gtotal)
-#pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        const int i = 4 * (sl.t + A * j);
-        load4((const E*)a.gtotal + n * D + i, sl.on ? D - i : 0, tail, gt[j]);
-      }
+    float z[NV][4], go[NV][4], gt[NV][4] = {};
+    RowQuads<E, NV> rz, rt;
+    RowQuads<O, NV> rg;
+    rz.load((const E*)a.total + n * D, sl, A, D);
+    rg.load((const O*)a.gout + n * D, sl, A, D);
+    if (a.gtotal) rt.load((const E*)a.gtotal + n * D, sl, A, D);
     const float* st = a.stats + n * (a.lmax + 2);
     const float mu = st[0];
-    float rq[4], sq[4] = {}, v[8] = {};
+    float rq[4], sq[4] = {}, slot[4] = {}, v[8] = {};
 #pragma unroll
     for (int q = 0; q < 4; ++q) rq[q] = st[1 + sl.l(q)];
+    rz.values(sl, A, D, full, tail, z);
+    rg.values(sl, A, D, full, tail, go);
+    if (a.gtotal) rt.values(sl, A, D, full, tail, gt);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int i = 4 * (sl.t + A * j);
       float av[4];
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        z[j][q] = (z[j][q] - (sl.l(q) == 0 ? mu : 0.0f)) * rq[q];
-        if (KT == 1 ? i >= D : i + q >= D) z[j][q] = 0.0f;
+        // (places past the row hold 0 and stay 0)
+        if (KT != 1 || q == 0) z[j][q] -= sl.zero(q) && (KT == 1 ? i < D : i + q < D) ? mu : 0.0f;
+        z[j][q] *= rq[q];
         aw[j][q] = fmaf(go[j][q], z[j][q], aw[j][q]);
         av[q] = go[j][q] * w[j][q];
         sq[q] = fmaf(av[q], z[j][q], sq[q]);
+        slot[q] += av[q];
       }
-      v[0] += sl.scalars(av);
       if constexpr (KT == 0) {
 #pragma unroll
         for (int q = 0; q < 4; ++q) ab[j][q] += go[j][q];
       } else {
-        ab[j][0] += sl.scalars(go[j]);
+        ab[j][0] += KT == 1 ? go[j][0] : sl.scalars(go[j]);
       }
     }
     if (a.gres || a.gx) {
       if (!sl.on)
 #pragma unroll
         for (int q = 0; q < 4; ++q) sq[q] = 0.0f;
+      v[0] = sl.scalars(slot);
       float am, mq[4];
       if constexpr (KT == 0) {
         float two[2] = {v[0], (sq[0] + sq[1]) + (sq[2] + sq[3])};
@@ -111,7 +115,7 @@ __global__ __launch_bounds__(norm_threads(T)) void norm_grad_kernel(NormGradArgs
           float gz[4];
 #pragma unroll
           for (int q = 0; q < 4; ++q)
-            gz[q] = fmaf(rq[q], (go[j][q] * w[j][q] - (sl.l(q) == 0 ? am : 0.0f)) - z[j][q] * mq[q], gt[j][q]);
+            gz[q] = fmaf(rq[q], (go[j][q] * w[j][q] - (sl.zero(q) ? am : 0.0f)) - z[j][q] * mq[q], gt[j][q]);
           if (a.gres) store4((E*)a.gres + n * D + i, D - i, tail, gz);
           if (a.gx) {
             if constexpr (DROP) {
@@ -151,7 +155,7 @@ __global__ __launch_bounds__(norm_threads(T)) void norm_grad_kernel(NormGradArgs
     for (int j = 0; j < NV; ++j)
 #pragma unroll
       for (int q = 0; q < 4; ++q)
-        if (sl.l(q) == 0 && sl.channel(q, j) < C) mine[sl.channel(q, j)] = ab[j][KT == 0 ? q : 0];
+        if (sl.zero(q) && sl.channel(q, j) < C) mine[sl.channel(q, j)] = ab[j][KT == 0 ? q : 0];
   __syncthreads();
   for (int c = threadIdx.x; c < C; c += TH) {
     float s = 0.0f;
