@@ -648,10 +648,35 @@ def eqtp_interaction(vec, src, row_ptr, h, W_up, W1, W2, W3, W_out, lmax: int, r
     return out
 
 
+_torch_module = None
+
+
+def _torch():
+    global _torch_module
+    if _torch_module is None:
+        import torch
+
+        _torch_module = torch
+    return _torch_module
+
+
+def _like(x, code, own):
+    """An empty tensor of x's shape and the type of a code; `own` is x's."""
+    torch = _torch()
+    return torch.empty_like(x) if code == own else torch.empty_like(x, dtype=_torch_dtype(code))
+
+
 def _rows(x, name, lmax):
     """(element type code, N, C) of features [N, C, K], or [N, C] at lmax 0."""
-    import torch
-
+    torch = _torch()
+    try:  # the usual case in one test
+        dt = x.dtype
+        if x.is_cuda and x.is_contiguous() and (dt is torch.float32 or dt is torch.bfloat16):
+            N, C, K = x.shape
+            if K == (lmax + 1) ** 2:
+                return (EQTP_F32 if dt is torch.float32 else EQTP_BF16), N, C
+    except (AttributeError, ValueError):
+        pass
     code = EQTP_BF16 if x.dtype is torch.bfloat16 else EQTP_F32
     _check(x, name, torch.bfloat16 if code == EQTP_BF16 else torch.float32)
     if x.dim() == 3:
@@ -666,8 +691,7 @@ def _rows(x, name, lmax):
 
 
 def _check_rng(rng, p):
-    import torch
-
+    torch = _torch()
     if p == 0.0:
         return
     if rng is None:
@@ -686,8 +710,7 @@ def _norm_desc(lmax, C, x_dtype, out_dtype, eps, p):
 
 
 def _check_affine(weight, bias, lmax, C):
-    import torch
-
+    torch = _torch()
     if weight is not None:
         _check(weight, "weight", torch.float32, (lmax + 1, C))
     if bias is not None:
@@ -695,8 +718,7 @@ def _check_affine(weight, bias, lmax, C):
 
 
 def _torch_dtype(code):
-    import torch
-
+    torch = _torch()
     if code not in (EQTP_F32, EQTP_BF16):
         raise ValueError("out_dtype must be EQTP_F32 or EQTP_BF16")
     return torch.bfloat16 if code == EQTP_BF16 else torch.float32
@@ -707,15 +729,14 @@ def eqtp_layer_norm(x, lmax: int, weight=None, bias=None, eps: float = 1e-5, out
     """out [N, C, K] = layer norm by degree of x (see include/eqtp.h); x float32 or bfloat16, [N, C, K] or, at
     lmax 0, [N, C].  ``weight`` [lmax+1, C], ``bias`` [C] float32.  ``out_dtype``: EQTP_F32 or EQTP_BF16 (x's by
     default).  ``stats``: a float32 [N, lmax+2] tensor to fill, for eqtp_layer_norm_backward."""
-    import torch
-
+    torch = _torch()
     code, N, C = _rows(x, "x", lmax)
     ocode = code if out_dtype is None else out_dtype
     odt = _torch_dtype(ocode)
     _check_affine(weight, bias, lmax, C)
     d, _ = _norm_desc(lmax, C, code, ocode, float(eps), 0.0)
     if out is None:
-        out = torch.empty(x.shape, dtype=odt, device=x.device)
+        out = _like(x, ocode, code)
     else:
         _check(out, "out", odt, x.shape)
     if stats is not None:
@@ -729,8 +750,7 @@ def eqtp_dropout_add_norm(x, residual, rng, p: float, lmax: int, weight=None, bi
                           out_dtype: int = None, out=None, total=None, stats=None):
     """(out, total): total = residual + dropout(x), out = eqtp_layer_norm(total), in one pass.  ``rng``: int64
     (seed, offset) on the GPU, or None when p is 0.  The rest as for eqtp_layer_norm."""
-    import torch
-
+    torch = _torch()
     code, N, C = _rows(x, "x", lmax)
     _check(residual, "residual", x.dtype, x.shape)
     ocode = code if out_dtype is None else out_dtype
@@ -740,7 +760,7 @@ def eqtp_dropout_add_norm(x, residual, rng, p: float, lmax: int, weight=None, bi
     _check_affine(weight, bias, lmax, C)
     d, _ = _norm_desc(lmax, C, code, ocode, float(eps), p)
     if out is None:
-        out = torch.empty(x.shape, dtype=odt, device=x.device)
+        out = _like(x, ocode, code)
     else:
         _check(out, "out", odt, x.shape)
     if total is None:
@@ -770,8 +790,7 @@ def eqtp_layer_norm_backward(total, stats, grad_out, lmax: int, weight=None, gra
     """(grad_residual, grad_x, grad_weight, grad_bias) of eqtp_dropout_add_norm, each None if not asked for; of
     eqtp_layer_norm with ``total`` = x, whose gradient is grad_residual.  ``need_x`` defaults to p > 0.
     ``workspace``: a uint8 tensor of at least eqtp_layer_norm_workspace_bytes bytes, or None to allocate one."""
-    import torch
-
+    torch = _torch()
     code, N, C = _rows(total, "total", lmax)
     ocode = EQTP_BF16 if grad_out.dtype is torch.bfloat16 else EQTP_F32
     _check(grad_out, "grad_out", _torch_dtype(ocode), total.shape)
@@ -806,8 +825,7 @@ def eqtp_layer_norm_backward(total, stats, grad_out, lmax: int, weight=None, gra
 def eqtp_dropout(x, rng, p: float, lmax: int = 0, residual=None, out=None):
     """out [N, C, K] = residual + dropout(x) of whole channels (see include/eqtp.h); without residual dropout(x),
     which on a gradient, with the same rng, is the backward pass.  ``out`` may be x or residual."""
-    import torch
-
+    torch = _torch()
     code, N, C = _rows(x, "x", lmax)
     p = float(p)
     _check_rng(rng, p)
@@ -835,33 +853,31 @@ def _attention_desc(lmax, C, heads, kv_heads, x_dtype, scale):
 
 
 def _attention_args(q, k, v, src, row_ptr, lmax, heads, scale, bias):
-    """Checks the attention's tensors; returns (descriptor, N, M, E, element type)."""
-    import torch
-
+    """Checks the attention's tensors; returns (descriptor, N, M, E)."""
+    torch = _torch()
     code, N, C = _rows(q, "q", lmax)
-    _check(k, "k", q.dtype)
-    if k.dim() != q.dim() or k.shape[2:] != q.shape[2:]:
+    dt = q.dtype
+    _check(k, "k", dt)
+    ks = k.shape
+    if len(ks) != q.dim() or (len(ks) == 3 and ks[2] != (lmax + 1) ** 2):
         raise ValueError("k must be [M, C kv_heads / heads, K] as q is [N, C, K]")
-    _check(v, "v", q.dtype, k.shape)
-    M, Ck = k.shape[0], k.shape[1]
+    _check(v, "v", dt, ks)
+    M, Ck = ks[0], ks[1]
     if heads <= 0 or C % heads != 0:
         raise ValueError("heads must divide the %d channels of q" % C)
     width = C // heads
-    if width == 0 or Ck % width != 0 or Ck == 0 or heads % (Ck // width) != 0:
+    if width == 0 or Ck == 0 or Ck % width != 0 or heads % (Ck // width) != 0:
         raise ValueError("k has %d channels: heads of %d channels, their number a divisor of %d" % (Ck, width, heads))
-    _check(src, "src", torch.int32)
     E = src.numel()
     _check(src, "src", torch.int32, (E,))
     _check(row_ptr, "row_ptr", torch.int32, (N + 1,))
     if bias is not None:
         _check(bias, "bias", torch.float32, (E, heads))
-    d, _ = _attention_desc(lmax, C, heads, Ck // width, code, scale)
-    return d, N, M, E
+    return _attention_desc(lmax, C, heads, Ck // width, code, scale)[0], N, M, E
 
 
 def _workspace(workspace, need, dev):
-    import torch
-
+    torch = _torch()
     if need < 0:
         raise EqtpError(int(-need), "workspace size")
     if workspace is None:
@@ -888,8 +904,7 @@ def eqtp_attention(q, k, v, src, row_ptr, lmax: int, heads: int, scale: float = 
     elements of a head by default.  ``bias`` [E, heads] float32, -inf to mask.  ``lse``: a float32 [N, heads]
     tensor to fill, for eqtp_attention_backward.  ``workspace``: a uint8 tensor of at least
     eqtp_attention_workspace_bytes bytes, or None to allocate one if it is needed."""
-    import torch
-
+    torch = _torch()
     d, N, M, E = _attention_args(q, k, v, src, row_ptr, lmax, heads, scale, bias)
     if out is None:
         out = torch.empty_like(q)
@@ -922,8 +937,7 @@ def eqtp_attention_backward(q, k, v, src, row_ptr, lse, grad_out, src_ptr, dst_s
     forward call's.  ``src_ptr`` [M+1], ``dst_s`` [E], ``perm`` [E] int32: the edges grouped by source (for grad_k
     and grad_v; e.g. eqtp_sort_edges_stable on src, carrying eqtp_edge_rows).  ``need_bias`` defaults to whether a
     bias is given."""
-    import torch
-
+    torch = _torch()
     d, N, M, E = _attention_args(q, k, v, src, row_ptr, lmax, heads, scale, bias)
     _check(lse, "lse", torch.float32, (N, heads))
     _check(grad_out, "grad_out", q.dtype, q.shape)
