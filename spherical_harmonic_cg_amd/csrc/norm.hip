@@ -90,7 +90,7 @@ __global__ __launch_bounds__(norm_threads(T)) void norm_kernel(NormArgs a, int A
     for (int j = 0; j < NV; ++j)
 #pragma unroll
       for (int q = 0; q < 4; ++q) slot[q] += z[j][q];
-    float mu[1] = {sl.scalars(slot)};
+    float mu[1] = {sl.on ? sl.scalars(slot) : 0.0f};
     group_sums<T, 1>(mu, 1, red, turn);
     mu[0] *= inv.v[0];
     float sq[4] = {};

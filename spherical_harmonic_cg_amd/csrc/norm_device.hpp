@@ -77,7 +77,7 @@ struct RowQuads {
           if (q < D) raw[0][q] = row[q];
     }
   }
-  // the values, zeros past the row
+  // the values, zeros past the row (in the threads that take quads)
   template <class S>
   __device__ __forceinline__ void values(const S& sl, int A, int D, bool full, bool tail, float (&v)[NV][4]) const {
 #pragma unroll
@@ -87,8 +87,9 @@ struct RowQuads {
     if (full || D < 4) return;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int over = sl.on ? 4 * (sl.t + A * j) - (D - 4) : 4;  // places that the quad reaches past the row
+      const int over = 4 * (sl.t + A * j) - (D - 4);  // places that the quad reaches past the row
       if (tail) {
+        if (!__any(sl.on && over > 0)) continue;
         const float w[7] = {v[j][0], v[j][1], v[j][2], v[j][3], 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int q = 0; q < 4; ++q)

@@ -92,7 +92,7 @@ __global__ __launch_bounds__(norm_threads(T)) void norm_grad_kernel(NormGradArgs
       if (!sl.on)
 #pragma unroll
         for (int q = 0; q < 4; ++q) sq[q] = 0.0f;
-      v[0] = sl.scalars(slot);
+      v[0] = sl.on ? sl.scalars(slot) : 0.0f;
       float am, mq[4];
       if constexpr (KT == 0) {
         float two[2] = {v[0], (sq[0] + sq[1]) + (sq[2] + sq[3])};
