@@ -734,7 +734,8 @@ int64_t attn_grad_workspace_bytes(int64_t N, int64_t M, int64_t E, int D, int he
   return grad_tables(E, heads) + (rows > sources ? rows : sources);
 }
 
-constexpr int64_t kSpreadLine = 512, kSpreadBytes = (int64_t)8 << 20, kSpreadMost = (int64_t)32 << 20, kShortRow = 8;
+constexpr int64_t kSpreadLine = 512, kSpreadBytes = (int64_t)8 << 20, kSpreadMost = (int64_t)32 << 20, kShortRow = 8,
+                  kShortPlaces = 4;
 
 // Lanes and units of a head's row: up to 8 units one a lane, then two, four, eight a lane.
 struct HeadShape {
@@ -769,8 +770,9 @@ static Tiling tiling(const HeadShape& s, int heads, int share, int64_t rows, int
   }
   t.ES = room / t.HW;
   t.blocks = (heads + t.HW - 1) / t.HW;
-  // rows of few edges: lanes side by side take rows of their own
-  t.step = t.S == 1 && t.ES > 1 && E < rows * kShortRow ? 1 : t.ES;
+  // rows of few edges beside the places for edges: lanes side by side take rows of their own
+  const bool few = E < rows * kShortRow || (E < rows * t.ES * kShortPlaces && rows / t.ES >= kMinWaves / 4);
+  t.step = t.S == 1 && t.ES > 1 && few ? 1 : t.ES;
   t.first = t.end = 0;
   t.part = part;
   return t;
