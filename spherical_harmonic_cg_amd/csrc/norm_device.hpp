@@ -87,6 +87,7 @@ struct RowQuads {
     if (full || D < 4) return;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
+      if (4 * A * (j + 1) <= D) continue;             // all threads' quads lie in the row
       const int over = 4 * (sl.t + A * j) - (D - 4);  // places that the quad reaches past the row
       if (tail) {
         if (!__any(sl.on && over > 0)) continue;
@@ -227,6 +228,13 @@ struct Slots {
   __device__ __forceinline__ void by_degree(const float (&v)[4], int deg, float* s) const {
     if constexpr (KT == 0) {
       s[0] += (v[0] + v[1]) + (v[2] + v[3]);
+    } else if constexpr (KT == 1) {
+      // degrees begin at squares, which are 0 or 1 modulo 4: slots 1 to 3 share one, slot 0 may have another
+      const int a = l(0), b = l(1);
+      const float rest = (v[1] + v[2]) + (v[3] + (a == b ? v[0] : 0.0f));
+#pragma unroll
+      for (int d = 0; d < kMaxDeg; ++d)
+        if (d < deg) s[d] += b == d ? rest : (a == d ? v[0] : 0.0f);
     } else {
 #pragma unroll
       for (int d = 0; d < kMaxDeg; ++d)
@@ -308,7 +316,7 @@ inline int norm_grid(int64_t N) {
   ((s).T == 8     ? ((s).NV <= 2 ? F(8, 2) : F(8, 4))                              \
    : (s).T == 16  ? ((s).NV <= 2 ? F(16, 2) : F(16, 4))                            \
    : (s).T == 32  ? F(32, 4)                                                       \
-   : (s).T == 64  ? ((s).NV <= 2 ? F(64, 2) : F(64, 4))                            \
+   : (s).T == 64  ? ((s).NV <= 2 ? F(64, 2) : ((s).NV <= 3 ? F(64, 3) : F(64, 4))) \
    : (s).T == 128 ? ((s).NV <= 2 ? F(128, 2) : F(128, 4))                          \
    : (s).T == 256 ? F(256, 4)                                                      \
                   : ((s).NV <= 5 ? F(512, 5) : F(512, 9)))
