@@ -1,8 +1,9 @@
 """MI355X (gfx950) equivariant convolution: fused real spherical harmonics ->
 Clebsch-Gordan tensor product -> destination sum, a per-l channel linear, and
-the standalone harmonics, as hand-written HIP kernels behind a C ABI
-(include/eqtp.h).  ``eqtp`` is the Python binding, ``autograd`` wraps the
-convolution and its gradients as a torch.autograd.Function; ``synth`` builds
+the standalone harmonics, and around them layer norm by degree, counter-based
+dropout and attention over the graph, as hand-written HIP kernels behind a C
+ABI (include/eqtp.h).  ``eqtp`` is the Python binding, ``autograd`` wraps the
+operators and their gradients as torch.autograd.Functions; ``synth`` builds
 seeded synthetic workloads."""
 from .eqtp import (EQTP_ALGO_AUTO, EQTP_ALGO_EDGE_SO2, EQTP_ALGO_EDGE_VALU, EQTP_ALGO_NODE_MFMA, EQTP_BF16, EQTP_EDGES_DST_SORTED,
                    EQTP_CHECK_WORDS, EQTP_EDGES_UNSORTED, EQTP_EGRAPH, EQTP_EHIP, EQTP_EINVAL, EQTP_ETOOLARGE, EQTP_EUNSUPPORTED, EQTP_F32, EQTP_F32_BF16, EQTP_OK,

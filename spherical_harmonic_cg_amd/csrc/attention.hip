@@ -4,9 +4,13 @@
 //   out[n] = sum w v[src].
 //
 // Every edge reads a row of k and one of v by its source (backward: by rows k
-// and v again, by sources q and the output's gradient), 2 E C K elements that
-// come from the caches next to memory; a row of q meets each of them once, so
-// the products stay on the vector ALUs and the gathers bound the kernels.
+// and v again, by sources q and the output's gradient), 2 E C K elements each
+// time.  A query meets each of them once, so the products stay on the vector
+// ALUs and the gathers bound the kernels: rows outside an XCD's L2 (4 MiB)
+// arrive at 7.4 to 8.2 TB/s, whatever holds them.  10k atoms, 266k edges,
+// 4 heads of 256 fp32 elements: 2.18 GB a pass, forward 250, by rows 267, by
+// sources 285 us (8.7, 8.2, 7.7 TB/s, a fifth of it L2 hits); 100k atoms,
+// 5.2M edges, bf16, 2 key and value heads of 128: 5.37 GB, 715 us (7.5 TB/s).
 //
 // A head's row of D elements is a line of 16-byte units.  G lanes hold it, NU
 // units each (unit lig + G j), beside the q and sums of the same places; dot
@@ -404,14 +408,28 @@ __global__ __launch_bounds__(kJoin) void attn_join_kernel(AttnArgs a, Tiling t, 
 // place until then.  The weights exp(s - lse) are summed and divided by their
 // sum again: it is 1 but for lse's rounding, which counts where the logits are
 // so large that the sum's logarithm is lost in lse (biases of the lowest value).
-__device__ __forceinline__ void grad_of_logit(float* wts, float* us, int64_t at, float t, float inv) {
-  const float w = wts[at] * inv;
-  wts[at] = w;
-  us[at] = w == 0.0f ? 0.0f : w * (us[at] - t);
-}
+//
+// Both lie in tables of E heads numbers, edge by edge, or head by head where
+// heads are dealt to the XCDs: each then writes and reads stretches of its own
+// (edge by edge, four of them wrote to every line: 120 MB written instead of
+// 50, and 8.5 MB of tables beside the gathered rows in each L2 instead of 2).
+struct EdgeTables {
+  float* w;
+  float* u;
+  float* gbias;    // u also goes here, edge by edge; or nullptr (u is the caller's, or not asked for)
+  int64_t se, sh;  // distance of edges and of heads
+  __device__ __forceinline__ int64_t at(int64_t e, int h) const { return e * se + h * sh; }
+  __device__ __forceinline__ void finish(int64_t e, int h, int H, float t, float inv) const {
+    const int64_t i = at(e, h);
+    const float weight = w[i] * inv, v = weight == 0.0f ? 0.0f : weight * (u[i] - t);
+    w[i] = weight;
+    u[i] = v;
+    if (gbias) gbias[e * H + h] = v;
+  }
+};
 
 template <class T, int G, int NU, int MODE, int EU>
-__global__ __launch_bounds__(256) void attn_grad_row_kernel(AttnGradArgs a, Tiling t, float* wts, float* us) {
+__global__ __launch_bounds__(256) void attn_grad_row_kernel(AttnGradArgs a, Tiling t, EdgeTables tab) {
   constexpr int VE = El<T>::VE;
   const int D = a.D, H = a.heads;
   const Lanes<T, G, NU, MODE> ln(D, t.HW);
@@ -498,9 +516,9 @@ __global__ __launch_bounds__(256) void attn_grad_row_kernel(AttnGradArgs a, Tili
           wk[j][x] = fmaf(w, kx, wk[j][x]);
         }
       if (mine && in[i] && ln.lig == 0) {
-        const int64_t at = (e0 + i * t.step + es) * H + h;
-        wts[at] = w;
-        us[at] = none ? 0.0f : av;
+        const int64_t at = tab.at(e0 + i * t.step + es, h);
+        tab.w[at] = w;
+        tab.u[at] = none ? 0.0f : av;
       }
     }
   }
@@ -541,9 +559,9 @@ __global__ __launch_bounds__(256) void attn_grad_row_kernel(AttnGradArgs a, Tili
     const int hh = (threadIdx.x & 63) & (t.HW - 1);
     const float th = __shfl(tt, hh * G, 64), ih = __shfl(inv, hh * G, 64);
     if (hb * t.HW + hh < H)
-      for (int64_t e = r.b + (threadIdx.x & 63) / t.HW; e < r.e; e += 64 / t.HW) grad_of_logit(wts, us, e * H + hb * t.HW + hh, th, ih);
+      for (int64_t e = r.b + (threadIdx.x & 63) / t.HW; e < r.e; e += 64 / t.HW) tab.finish(e, hb * t.HW + hh, H, th, ih);
   } else if (mine) {
-    for (int64_t e = r.b + ln.lig; e < r.e; e += G) grad_of_logit(wts, us, e * H + h, tt, inv);
+    for (int64_t e = r.b + ln.lig; e < r.e; e += G) tab.finish(e, h, H, tt, inv);
   }
 }
 
@@ -579,20 +597,21 @@ __global__ __launch_bounds__(kJoin) void attn_grad_join_kernel(AttnGradArgs a, T
 
 // w and u of every edge of the pieces, from their rows' joined sums: a workgroup a (row, piece).  (By the joining
 // workgroups themselves, one head each, it took 15 us more for a readout of 50k items and 8 heads: 4 of 32 bytes.)
-__global__ __launch_bounds__(256) void attn_grad_fix_kernel(AttnGradArgs a, Tiling t, float* wts, float* us) {
+__global__ __launch_bounds__(256) void attn_grad_fix_kernel(AttnGradArgs a, Tiling t, EdgeTables tab) {
   const int H = a.heads;
   const int64_t n = blockIdx.x / t.S;
   const RowRange r = piece(row_range(a.row_ptr, n, a.E), (int)(blockIdx.x - n * t.S), t.S);
   const float* tt = t.part + 2 * (a.N * t.S * H * (int64_t)a.D) + (a.N * t.S + n) * H * 2;
-  for (int64_t i = threadIdx.x; i < (r.e - r.b) * H; i += 256)
-    grad_of_logit(wts, us, r.b * H + i, tt[i % H * 2], tt[i % H * 2 + 1]);
+  for (int64_t i = threadIdx.x; i < (r.e - r.b) * H; i += 256) {
+    const int h = (int)(i % H);
+    tab.finish(r.b + i / H, h, H, tt[h * 2], tt[h * 2 + 1]);
+  }
 }
 
 // Source pass: grad_k = scale sum u q, grad_v = sum w g over a source's edges
 // (and the heads that share a key and value head).
 template <class T, int G, int NU, int MODE, int EU>
-__global__ __launch_bounds__(256) void attn_grad_source_kernel(AttnGradArgs a, Tiling t, const float* __restrict__ wts,
-                                                               const float* __restrict__ us) {
+__global__ __launch_bounds__(256) void attn_grad_source_kernel(AttnGradArgs a, Tiling t, EdgeTables tab) {
   constexpr int VE = El<T>::VE;
   const int D = a.D, H = a.heads, HK = a.kv_heads;
   const Lanes<T, G, NU, MODE> ln(D, t.HW);
@@ -621,7 +640,7 @@ __global__ __launch_bounds__(256) void attn_grad_source_kernel(AttnGradArgs a, T
     int64_t eh[EU], nh[EU];
 #pragma unroll
     for (int i = 0; i < EU; ++i) {
-      eh[i] = (int64_t)clamp_index(edge[i], (int)a.E) * H + hk * R;
+      eh[i] = tab.at(clamp_index(edge[i], (int)a.E), hk * R);
       nh[i] = ((int64_t)clamp_index(dst[i], (int)a.N) * H + hk * R) * D;
     }
     if (__any(i0 + EU * t.step < r.e)) fetch(i0 + EU * t.step);
@@ -632,8 +651,8 @@ __global__ __launch_bounds__(256) void attn_grad_source_kernel(AttnGradArgs a, T
 #pragma unroll
       for (int i = 0; i < EU; ++i) {
         const bool in = i0 + i * t.step + es < r.e;
-        w[i] = in ? wts[eh[i] + h] : 0.0f;
-        u[i] = in ? us[eh[i] + h] : 0.0f;
+        w[i] = in ? tab.w[eh[i] + h * tab.sh] : 0.0f;
+        u[i] = in ? tab.u[eh[i] + h * tab.sh] : 0.0f;
 #pragma unroll
         for (int j = 0; j < NU; ++j) q[i][j] = ln.load((const T*)a.q + nh[i] + (int64_t)h * D, j, D);
 #pragma unroll
@@ -709,7 +728,8 @@ static int pow2_from(int v) {
 }
 
 // Pieces of a row: where the rows alone give fewer than kMinWaves waves, as many as bring them there, of kMinPiece
-// edges on average or more.
+// edges on average or more (7 rows over 50k items, 8 heads of 16: one wave a row 15 ms, 292 pieces 14 us and 6 to join).
+// (1024 waves of 64 edges or more: 15 and 19 us forward and by rows; 2048 of 32: 14 and 15; 4096: the same.)
 constexpr int64_t kMinWaves = 2048, kMinPiece = 32;
 static int pieces(int64_t rows, int64_t E) {
   if (rows <= 0 || rows >= kMinWaves) return 1;
@@ -753,24 +773,29 @@ static bool is_pow2(int v) { return (v & (v - 1)) == 0; }
 
 // heads of the pass (of q, or of k and v), share of them that read the same rows, rows and edges of the pass, bytes
 // of the two gathered tensors and of a head's row in them.
-static Tiling tiling(const HeadShape& s, int heads, int share, int64_t rows, int64_t E, int64_t gathered, int row_bytes, float* part) {
+static Tiling tiling(const HeadShape& s, int heads, int share, int64_t rows, int64_t E, int64_t gathered,
+                     int row_bytes, float* part) {
   Tiling t;
   const int room = 64 / s.G, kv = heads / share;
   t.S = pieces(rows, E);
   t.HW = pow2_from(heads) < room ? pow2_from(heads) : room;
-  // Gathers out of tensors that an L2 of 4 MiB does not hold run at about 7.5 TB/s whatever the tensors' size below
-  // the L2's misses; heads dealt to the XCDs leave each L2 a part of them.
+  // Heads dealt to the XCDs: each L2 then sees one slice of the gathered tensors and finds more of it (10k atoms,
+  // 4 heads, 82 MB: slices of 20 MB, a fifth of the reads; 308 -> 250 us forward).  Not where the tensors fit the L2s
+  // anyway, nor where a slice is so large that hardly anything is found (51 MB: 718 -> 726 us), nor with slices of
+  // less than some cache lines a row (64-byte pieces of 512-byte rows: 69 -> 250 us).
   t.spread = 0;
   int nb = kv < 8 ? kv : 8;
-  while (nb > 1 && kv / nb * row_bytes < kSpreadLine) nb >>= 1;  // (pieces of a cache line would fetch all of it)
-  if (t.S == 1 && nb > 1 && gathered > kSpreadBytes && gathered / nb <= kSpreadMost && kv > 1 && is_pow2(kv) && is_pow2(share) && heads / nb <= room &&
-      rows < ((int64_t)1 << 24)) {
+  while (nb > 1 && kv / nb * row_bytes < kSpreadLine) nb >>= 1;
+  if (t.S == 1 && nb > 1 && gathered > kSpreadBytes && gathered / nb <= kSpreadMost && is_pow2(kv) && is_pow2(share) &&
+      heads / nb <= room &&
+      rows < ((int64_t)1 << 22)) {  // (eight workgroups for four rows: below 2^32 threads)
     t.HW = heads / nb;
     t.spread = 8 / nb;
   }
   t.ES = room / t.HW;
   t.blocks = (heads + t.HW - 1) / t.HW;
-  // rows of few edges beside the places for edges: lanes side by side take rows of their own
+  // Rows of few edges beside the places for edges (ES by EU): lanes side by side take rows of their own.  50k rows of
+  // 20 edges, 4 heads of one element (ES 16): forward 77 -> 25 us; 50k sources of one edge: 46 -> 27 us.
   const bool few = E < rows * kShortRow || (E < rows * t.ES * kShortPlaces && rows / t.ES >= kMinWaves / 4);
   t.step = t.S == 1 && t.ES > 1 && few ? 1 : t.ES;
   t.first = t.end = 0;
@@ -851,15 +876,15 @@ static hipError_t attn_t(const AttnArgs& a) {
 
 template <class T>
 static hipError_t attn_grad_t(const AttnGradArgs& a) {
-  float* wts = (float*)a.ws;
-  float* us = a.gbias ? a.gbias : wts + a.E * a.heads;
+  EdgeTables tab = {(float*)a.ws, a.gbias ? a.gbias : (float*)a.ws + a.E * a.heads, nullptr, a.heads, 1};
   float* part = (float*)((unsigned char*)a.ws + grad_tables(a.E, a.heads));
   const HeadShape s = head_shape(a.D, El<T>::VE);
   if (a.N > 0) {
     Tiling t = tiling(s, a.heads, a.heads / a.kv_heads, a.N, a.E, 2 * a.M * a.kv_heads * a.D * (int64_t)sizeof(T), a.D * (int)sizeof(T), part);
+    if (t.spread) tab = {tab.w, tab.w + a.E * a.heads, a.gbias, 1, a.E};
     hipError_t e = over_tasks(a.N, t, [&](dim3 grid) {
       with_shape<T>(s, [&](auto G, auto NU, auto MODE) {
-        attn_grad_row_kernel<T, G(), NU(), MODE(), (NU() >= 4 ? 1 : 4 / NU())><<<grid, dim3(256), 0, a.stream>>>(a, t, wts, us);
+        attn_grad_row_kernel<T, G(), NU(), MODE(), (NU() >= 4 ? 1 : 4 / NU())><<<grid, dim3(256), 0, a.stream>>>(a, t, tab);
       });
     });
     if (e != hipSuccess) return e;
@@ -867,7 +892,7 @@ static hipError_t attn_grad_t(const AttnGradArgs& a) {
       attn_grad_join_kernel<T><<<join_grid(a.N * a.heads, a.D), dim3(kJoin), 0, a.stream>>>(a, t, join_lanes(a.D));
       e = hipGetLastError();
       if (e != hipSuccess) return e;
-      attn_grad_fix_kernel<<<dim3((unsigned)(a.N * t.S)), dim3(256), 0, a.stream>>>(a, t, wts, us);
+      attn_grad_fix_kernel<<<dim3((unsigned)(a.N * t.S)), dim3(256), 0, a.stream>>>(a, t, tab);
       e = hipGetLastError();
       if (e != hipSuccess) return e;
     }
@@ -880,9 +905,9 @@ static hipError_t attn_grad_t(const AttnGradArgs& a) {
   const hipError_t e = over_tasks(a.M, t, [&](dim3 grid) {
     with_shape<T>(s, [&](auto G, auto NU, auto MODE) {
       if (one)
-        attn_grad_source_kernel<T, G(), NU(), MODE(), 1><<<grid, dim3(256), 0, a.stream>>>(a, t, wts, us);
+        attn_grad_source_kernel<T, G(), NU(), MODE(), 1><<<grid, dim3(256), 0, a.stream>>>(a, t, tab);
       else
-        attn_grad_source_kernel<T, G(), NU(), MODE(), (NU() >= 4 ? 1 : 4 / NU())><<<grid, dim3(256), 0, a.stream>>>(a, t, wts, us);
+        attn_grad_source_kernel<T, G(), NU(), MODE(), (NU() >= 4 ? 1 : 4 / NU())><<<grid, dim3(256), 0, a.stream>>>(a, t, tab);
     });
   });
   if (e != hipSuccess || t.S == 1) return e;

@@ -8,7 +8,9 @@
 // makes its own bits.  With K > 1 the stretch touches few channels: the lanes
 // make one block each, once, leave the keep bits in LDS and read them back
 // element by element; made by every thread for itself, the words would take
-// K times the work.
+// K times the work.  266k x 64 bf16 (K = 1): 12 to 14 us, 68 MB, the words'
+// multiplications (18 of four passes a block) about as long as the memory;
+// fp32 with K = 49: 5.4 TB/s.
 #include <type_traits>
 
 #include "eqtp_device.hpp"

@@ -5,15 +5,18 @@
 //   out = zc r_l weight[l, c] + [l = 0] bias[c].
 //
 // Bound by HBM: each element is read and written once.  A group of T threads
-// (16, 64, 256 or 1024) holds a node's row of D = C K elements in registers, NV
-// quads of four consecutive elements a thread, so the row is read once for
-// both the statistics and the result.  Only the first A threads of a group
-// take quads, A a multiple of K / gcd(K, 4): quad j of thread t begins at
-// 4 (t + A j), so a thread's four slots keep their components m, degrees and
-// factors for every j and every row, whatever K is, and loads stay coalesced.
-// Groups walk over the rows, weights stay in registers.  Sums by degree go
-// over a thread's quads, then over 16 lanes by row rotations and over a wave
-// by lane swaps (register moves, no LDS), then over waves through LDS.
+// (8 to 512) holds a node's row of D = C K elements in registers, NV quads of
+// four consecutive elements a thread, so the row is read once for both the
+// statistics and the result.  Only the first A threads of a group take quads,
+// A a multiple of K / gcd(K, 4): quad j of thread t begins at 4 (t + A j), so a
+// thread's four slots keep their components m, degrees and factors for every j
+// and every row, whatever K is, and loads stay coalesced.  Groups walk over
+// the rows, as many as the card holds at once; weights stay in registers.
+// Sums by degree are folded over the lanes together (register moves, no LDS),
+// then over a group's waves through LDS.
+// 100k nodes, 32 channels, lmax 3, with dropout and residual: 146 us (819 MB,
+// 5.6 TB/s; a large copy reaches 5.4); 10k x 64 x 16 to bf16: 13 us (61 MB);
+// lmax 4 and 6 with few channels: the vector ALUs (the fixed work of a row).
 #include "norm_device.hpp"
 
 namespace eqtp {

@@ -280,6 +280,8 @@ inline NormInv norm_inv(int C) {
 // work beside the elements (two sums over the group, a square root for each
 // degree) is the same for every thread of a group, so fewer threads do less of
 // it; more quads a thread cost registers, and with them waves in flight.
+// 825 fp32 elements, gradients: 128 threads of two quads 25 us, 64 of six 30;
+// 64 bf16 elements, forward: 16 threads of one 17 us, 8 of two 16, 4 of four 21.
 struct NormShape {
   int T, NV, A;
 };

@@ -9,6 +9,10 @@
 // the rows; at the end a workgroup adds its groups and the components of a
 // degree through LDS, in a fixed order, into its line of part
 // [workgroups][(lmax+2) C], and a second kernel adds the lines.
+// 100k nodes, 32 channels, lmax 3, five tensors of 205 MB: 189 us (5.4 TB/s)
+// and 5 for the lines; 266k rows of 64 bf16: 23 and 4.4 us (102 MB).  Dropout
+// makes kernels of its own: its words cost registers, and with them waves
+// (bf16 rows of 64: 34 us with, 24 without).
 #include "norm_device.hpp"
 
 namespace eqtp {

@@ -412,3 +412,35 @@ def test_attention_graph_capture():
                 assert torch.equal(a, b)
             step()
             torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("x,heads,kv_heads,width,lmax,N,M,each", [
+    ("f32", 4, 4, 16, 3, 350, 1500, 21),    # each XCD has one head's slice of k and v, four edges side by side
+    ("f32", 4, 2, 16, 3, 350, 3000, 19),    # two heads to each key and value head
+    ("bf16", 8, 8, 16, 3, 300, 1400, 17),   # eight slices
+    ("f32", 4, 4, 16, 3, 900, 1500, 4),     # rows of few edges side by side
+    ("f32", 2, 2, 33, 3, 300, 1300, 18)])   # rows that are not whole units
+@pytest.mark.parametrize("bias", [False, True])
+def test_attention_dealt_heads(x, heads, kv_heads, width, lmax, N, M, each, bias):
+    """Keys, values, queries and gradients of more than an L2: heads are dealt to the XCDs and the tables of weights
+    lie head by head."""
+    eq = _eq()
+    _say("attention dealt heads %s %d/%d width=%d each=%d bias=%s" % (x, heads, kv_heads, width, each, bias))
+    r = np.random.default_rng(each)
+    lengths = r.integers(0, 2 * each + 1, N)
+    Case(N, M, lengths, width, lmax, heads, kv_heads, x, bias=bias, seed=each).check(eq)
+
+
+@pytest.mark.parametrize("heads,kv_heads,width,lmax,x", [(4, 4, 1, 0, "f32"), (1, 1, 1, 2, "f32"), (2, 1, 5, 0, "bf16"), (3, 3, 4, 0, "f32")])
+def test_attention_many_short_rows(heads, kv_heads, width, lmax, x):
+    """Enough rows of some twenty edges that each wave takes several side by side, sources among them with one edge."""
+    eq = _eq()
+    _say("attention many rows heads=%d/%d width=%d %s" % (heads, kv_heads, width, x))
+    r = np.random.default_rng(7)
+    N = 9000
+    lengths = np.zeros(N, dtype=np.int64)
+    lengths[r.integers(0, N, 700)] = r.integers(1, 60, 700)
+    lengths[:64] = 20
+    lengths[N - 1] = 33
+    c = Case(N, 12000, lengths, width, lmax, heads, kv_heads, x, seed=8)
+    c.check(eq)

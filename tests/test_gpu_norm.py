@@ -351,3 +351,36 @@ def test_norm_side_stream_and_graph():
             assert torch.equal(a, b), off
         step()
         torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("lmax,C,N", [(0, 130, 5), (0, 256, 9), (0, 301, 4), (0, 512, 5), (0, 600, 3), (0, 1500, 3), (0, 2048, 2),
+                                      (0, 3001, 2), (0, 9000, 2), (1, 16, 40), (1, 33, 9), (1, 100, 6), (1, 3000, 2), (2, 3, 70),
+                                      (2, 14, 9), (2, 28, 5), (2, 60, 4), (2, 300, 2), (3, 4, 30), (3, 8, 17), (4, 3, 20), (4, 16, 6),
+                                      (4, 600, 2), (5, 1, 40), (5, 7, 9), (5, 20, 5), (6, 4, 9), (6, 10, 6), (6, 330, 2)])
+@pytest.mark.parametrize("x", ["f32", "bf16"])
+@pytest.mark.parametrize("p", [0.0, 0.25])
+def test_norm_more_widths(lmax, C, N, x, p):
+    """Widths on both sides of every change of the group of threads, with and without dropout, both directions."""
+    eq = _eq()
+    _say("norm widths lmax=%d C=%d N=%d %s p=%g" % (lmax, C, N, x, p))
+    import torch
+
+    d = _inputs(N, C, lmax, 90 + C, x, x)
+    rng = torch.tensor(RNG, device="cuda")
+    stats = torch.empty((N, lmax + 2), device="cuda")
+    o, t = eq.eqtp_dropout_add_norm(d["x"][0], d["res"][0], rng, p, lmax, d["w"][0], d["b"][0], eps=EPS, stats=stats)
+    keep = ref.keep_mask(RNG[0], RNG[1], N, C, p)
+    want = ref.dropout(d["x"][1], keep, p, d["res"][1])
+    _within(_get(t), want, (ref.U16 if x == "bf16" else ref.U32) * np.abs(want) * (1 + 1e-6) + 1e-37, "total")
+    tt = _get(t)
+    _within(_get(o), ref.norm(tt, lmax, d["w"][1], d["b"][1], EPS)[0],
+            ref.norm_bound(tt, lmax, d["w"][1], d["b"][1], EPS, x == "bf16"), "out")
+    gr, gx, gw, gb = eq.eqtp_layer_norm_backward(t, stats, d["g"][0], lmax, d["w"][0], grad_total=d["gt"][0], rng=rng, p=p,
+                                                 need_x=True)
+    wr, ww, wb = ref.norm_backward(tt, lmax, d["g"][1], d["w"][1], EPS)
+    br, bw, bb = ref.norm_backward_bounds(tt, lmax, d["g"][1], d["w"][1], EPS, x == "bf16", extra=d["gt"][1])
+    wr, scale = wr + d["gt"][1], 1.0 / (1.0 - p)
+    _within(_get(gr), wr, br, "grad_residual")
+    _within(_get(gx), np.where(keep[:, :, None], wr * scale, 0.0), 1.001 * scale * br, "grad_x")
+    _within(_get(gw), ww, bw, "gweight")
+    _within(_get(gb), wb, bb, "gbias")
