@@ -578,7 +578,8 @@ int eqtp_layer_norm(const eqtp_norm_desc* d, int64_t N, const void* x, const flo
 
 /*
  * The residual branch's end and the next norm in one pass:
- *   total = residual + keep x / (1 - p)   (rounded to x_dtype once),
+ *   total = residual + keep x / (1 - p)   (rounded to x_dtype once; the sum as
+ *                                          eqtp_dropout forms it),
  *   out   = eqtp_layer_norm(total),
  * with the same bits as eqtp_dropout followed by eqtp_layer_norm.
  *   x, residual, total [N, C, K] (x_dtype); rng: see above (NULL allowed when
@@ -614,6 +615,9 @@ int eqtp_layer_norm_backward(const eqtp_norm_desc* d, int64_t N, const void* tot
 /*
  * Dropout of whole channels, with an optional residual sum:
  *   out = residual + keep x / (1 - p)   (residual NULL: keep x / (1 - p)).
+ * fp32: one rounding.  bf16: the product rounded to fp32, the sum in fp32, and
+ * one rounding to bf16, the bits of the separate operations; a sum that cancels
+ * to less than 1/64 of the residual is formed without the product's rounding.
  * The gradient of x is the same call on the gradient (no residual) with the
  * same rng.  A dropped channel contributes exactly 0, whatever x holds.
  *   x, residual, out [N, C, K] of dtype EQTP_F32 or EQTP_BF16; out may be x

@@ -8,9 +8,9 @@
 // makes its own bits.  With K > 1 the stretch touches few channels: the lanes
 // make one block each, once, leave the keep bits in LDS and read them back
 // element by element; made by every thread for itself, the words would take
-// K times the work.  266k x 64 bf16 (K = 1): 12 to 14 us, 68 MB, the words'
-// multiplications (18 of four passes a block) about as long as the memory;
-// fp32 with K = 49: 5.4 TB/s.
+// K times the work.  266k x 64 bf16 (K = 1): 16 us (68 MB), 20 us beside a
+// residual (102 MB), the words' multiplications (18 of four passes a block)
+// about as long as the memory; fp32 with K = 49: 5.8 TB/s.
 #include <type_traits>
 
 #include "eqtp_device.hpp"
@@ -23,15 +23,12 @@ template <class T>
 struct Unit {  // 16 bytes of elements, aligned as one element only
   static constexpr int VE = 16 / (int)sizeof(T);
   typedef T V __attribute__((ext_vector_type(VE), aligned(sizeof(T))));
-  static __device__ __forceinline__ void load(const T* p, int left, float (&v)[VE]) {
-    if (left >= VE) {
-      const V t = *reinterpret_cast<const V*>(p);
+  static __device__ __forceinline__ V load(const T* p, int left) {
+    if (left >= VE) return *reinterpret_cast<const V*>(p);
+    V t;
 #pragma unroll
-      for (int q = 0; q < VE; ++q) v[q] = (float)t[q];
-    } else {
-#pragma unroll
-      for (int q = 0; q < VE; ++q) v[q] = q < left ? (float)p[q] : 0.0f;
-    }
+    for (int q = 0; q < VE; ++q) t[q] = q < left ? p[q] : (T)0.0f;
+    return t;
   }
   static __device__ __forceinline__ void store(T* p, int left, const float (&v)[VE]) {
     if (left >= VE) {
@@ -49,26 +46,28 @@ struct Unit {  // 16 bytes of elements, aligned as one element only
 
 constexpr int kDropUnits = 4;  // units a thread in a stretch
 
-// One stretch of `have` elements from `base` on; FULL: all of its units are whole.
-template <class T, int K, bool FULL>
+// One stretch of `have` elements from `base` on; FULL: all of its units are whole, RES: with a residual.
+template <class T, int K, bool FULL, bool RES>
 __device__ __forceinline__ void drop_stretch(int64_t base, int have, int lane, uint8_t* nib, const T* x,
                                              const T* residual, const int64_t* __restrict__ rng, uint32_t thr,
                                              float scale, T* out) {
   using U = Unit<T>;
   constexpr int VE = U::VE, NJ = kDropUnits;
-  float v[NJ][VE], r[NJ][VE];
+  typename U::V v[NJ], r[RES ? NJ : 1];  // as they lie in memory: all are on their way before the first is converted
 #pragma unroll
-  for (int j = 0; j < NJ; ++j) U::load(x + base + VE * (lane + 64 * j), FULL ? VE : have - VE * (lane + 64 * j), v[j]);
-  if (residual) {
-#pragma unroll
-    for (int j = 0; j < NJ; ++j)
-      U::load(residual + base + VE * (lane + 64 * j), FULL ? VE : have - VE * (lane + 64 * j), r[j]);
-  } else {
+  for (int j = 0; j < NJ; ++j) v[j] = U::load(x + base + VE * (lane + 64 * j), FULL ? VE : have - VE * (lane + 64 * j));
+  if constexpr (RES) {
 #pragma unroll
     for (int j = 0; j < NJ; ++j)
-#pragma unroll
-      for (int q = 0; q < VE; ++q) r[j][q] = 0.0f;
+      r[j] = U::load(residual + base + VE * (lane + 64 * j), FULL ? VE : have - VE * (lane + 64 * j));
   }
+  float o[NJ][VE];
+  auto put = [&](uint32_t keep, int place, int j, int q) {
+    if constexpr (RES)
+      o[j][q] = drop_add<T>(keep, place, (float)v[j][q], scale, (float)r[j][q]);
+    else
+      o[j][q] = drop(keep, place, (float)v[j][q], scale);
+  };
   if (rng) {
     const DropState s = drop_state(rng, thr, scale);
     if constexpr (K == 1) {
@@ -79,7 +78,7 @@ __device__ __forceinline__ void drop_stretch(int64_t base, int have, int lane, u
           // stretches begin at multiples of their length, a power of two: no carry into the high word
           const uint32_t keep = keep_nibble(s, (uint32_t)(base >> 2) + (VE * (lane + 64 * j) + h) / 4, (uint32_t)(base >> 34));
 #pragma unroll
-          for (int q = 0; q < 4; ++q) v[j][h + q] = drop_add(keep, q, v[j][h + q], scale, r[j][h + q]);
+          for (int q = 0; q < 4; ++q) put(keep, q, j, h + q);
         }
     } else {
       const int64_t c0 = base / K;             // first channel number of the stretch
@@ -100,20 +99,20 @@ __device__ __forceinline__ void drop_stretch(int64_t base, int have, int lane, u
           const int c = first + (shift + i) / K;
           const uint32_t keep = nib[c >> 2] >> (c & 3);
 #pragma unroll
-          for (int k = q; k < q + G; ++k) v[j][k] = drop_add(keep, 0, v[j][k], scale, r[j][k]);
+          for (int k = q; k < q + G; ++k) put(keep, 0, j, k);
         }
     }
   } else {
 #pragma unroll
     for (int j = 0; j < NJ; ++j)
 #pragma unroll
-      for (int q = 0; q < VE; ++q) v[j][q] = drop_add(1, 0, v[j][q], scale, r[j][q]);
+      for (int q = 0; q < VE; ++q) put(1, 0, j, q);
   }
 #pragma unroll
-  for (int j = 0; j < NJ; ++j) U::store(out + base + VE * (lane + 64 * j), FULL ? VE : have - VE * (lane + 64 * j), v[j]);
+  for (int j = 0; j < NJ; ++j) U::store(out + base + VE * (lane + 64 * j), FULL ? VE : have - VE * (lane + 64 * j), o[j]);
 }
 
-template <class T, int K>
+template <class T, int K, bool RES>
 __global__ __launch_bounds__(256) void dropout_kernel(int64_t total, const T* x, const T* residual,
                                                       const int64_t* __restrict__ rng, uint32_t thr, float scale,
                                                       T* out) {
@@ -122,9 +121,9 @@ __global__ __launch_bounds__(256) void dropout_kernel(int64_t total, const T* x,
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   for (int64_t base = ((int64_t)blockIdx.x * 4 + wv) * STRETCH; base < total; base += (int64_t)gridDim.x * 4 * STRETCH) {
     if (total - base >= STRETCH)
-      drop_stretch<T, K, true>(base, STRETCH, lane, nib[wv], x, residual, rng, thr, scale, out);
+      drop_stretch<T, K, true, RES>(base, STRETCH, lane, nib[wv], x, residual, rng, thr, scale, out);
     else
-      drop_stretch<T, K, false>(base, (int)(total - base), lane, nib[wv], x, residual, rng, thr, scale, out);
+      drop_stretch<T, K, false, RES>(base, (int)(total - base), lane, nib[wv], x, residual, rng, thr, scale, out);
   }
 }
 
@@ -133,7 +132,8 @@ static hipError_t dropout_t(const DropArgs& a) {
   const int64_t total = a.N * a.C * K, stretch = 4 * 64 * kDropUnits * Unit<T>::VE;
   if (total == 0) return hipSuccess;
   const int64_t want = (total + stretch - 1) / stretch, most = 1 << 20;
-  dropout_kernel<T, K><<<dim3((unsigned)(want < most ? want : most)), dim3(256), 0, a.stream>>>(
+  auto* kernel = a.residual ? dropout_kernel<T, K, true> : dropout_kernel<T, K, false>;
+  kernel<<<dim3((unsigned)(want < most ? want : most)), dim3(256), 0, a.stream>>>(
       total, (const T*)a.x, (const T*)a.residual, a.rng, a.thr, a.scale, (T*)a.out);
   return hipGetLastError();
 }

@@ -81,7 +81,7 @@ __global__ __launch_bounds__(norm_threads(T)) void norm_kernel(NormArgs a, int A
           const uint32_t keep = a.rng ? kb.quad(ds, c) : 15u;
 #pragma unroll
           for (int q = 0; q < 4; ++q)  // the norm is that of the sum as it is written
-            z[j][q] = (float)(E)drop_add(keep, q, z[j][q], a.scale, res[j][q]);
+            z[j][q] = (float)(E)drop_add<E>(keep, q, z[j][q], a.scale, res[j][q]);
           store4((E*)a.total + n * D + i, D - i, tail, z[j]);
         }
       }

@@ -128,7 +128,7 @@ __global__ __launch_bounds__(norm_threads(T)) void norm_grad_kernel(NormGradArgs
               for (int q = 0; q < 4; ++q) c[q] = min(sl.channel(q, j), C - 1);
               const uint32_t keep = kb.quad(ds, c);
 #pragma unroll
-              for (int q = 0; q < 4; ++q) gz[q] = drop_add(keep, q, gz[q], a.scale, 0.0f);
+              for (int q = 0; q < 4; ++q) gz[q] = drop(keep, q, gz[q], a.scale);
             }
             store4((E*)a.gx + n * D + i, D - i, tail, gz);
           }

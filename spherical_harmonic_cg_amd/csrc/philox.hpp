@@ -61,13 +61,32 @@ __device__ __forceinline__ uint32_t keep_nibble(const DropState& s, uint64_t blo
   return keep_nibble(s, (uint32_t)block, (uint32_t)(block >> 32));
 }
 
-// The value of x at place q of a quad with these keep bits, beside its residual; the norm's kernels and the dropout
-// kernel share this expression, so their sums have the same bits.  The choice goes through a mask in a vector
-// register: lane masks for every place of a row would not fit in the scalar registers.
-__device__ __forceinline__ float drop_add(uint32_t keep, int q, float x, float scale, float residual) {
+// The value at place q of a quad with these keep bits.  The choice goes through a mask in a vector register: lane
+// masks for every place of a row would not fit in the scalar registers.
+__device__ __forceinline__ float drop_choose(uint32_t keep, int q, float kept, float dropped) {
   const uint32_t m = (uint32_t)__builtin_amdgcn_sbfe((int)keep, q, 1);
-  const uint32_t in = __builtin_bit_cast(uint32_t, fmaf(x, scale, residual));
-  return __builtin_bit_cast(float, (in & m) | (__builtin_bit_cast(uint32_t, residual) & ~m));
+  return __builtin_bit_cast(float, (__builtin_bit_cast(uint32_t, kept) & m) | (__builtin_bit_cast(uint32_t, dropped) & ~m));
+}
+
+__device__ __forceinline__ float drop(uint32_t keep, int q, float x, float scale) {
+  return __builtin_bit_cast(float, __builtin_bit_cast(uint32_t, x * scale) & (uint32_t)__builtin_amdgcn_sbfe((int)keep, q, 1));
+}
+
+// The same beside a residual; the norm's kernels and the dropout kernel share this expression, so their sums have
+// the same bits.  fp32 values (E) take one rounding.  bf16 values take the rounded product and then the sum, as the
+// separate fp32 operations do: 1 / (1 - p) is often a short fraction (10/9), multiples of its denominator then fall
+// on exact ties of the bf16 steps, and a last bit more or less in fp32 would send them the other way (of bf16
+// normal values at p = 0.1 about one sum in 2000, 1.3e-4 of an fp32 norm behind it).  Only where the sum cancels to
+// less than 1/64 of the residual, and the product's rounding would weigh more than 2^-18 of it, the fused one.
+template <class E>
+__device__ __forceinline__ float drop_add(uint32_t keep, int q, float x, float scale, float residual) {
+#pragma clang fp contract(off)
+  float sum = fmaf(x, scale, residual);
+  if constexpr (sizeof(E) == 2) {
+    const float kept = x * scale, apart = kept + residual;
+    sum = fabsf(apart) < 0.015625f * fabsf(residual) ? sum : apart;
+  }
+  return drop_choose(keep, q, sum, residual);
 }
 
 }  // namespace eqtp

@@ -65,6 +65,30 @@ def test_dropout_unaligned_and_in_place(shift, lmax, C, x):
     assert torch.equal(t, plain)
 
 
+@pytest.mark.parametrize("p", [0.05, 0.1, 0.3, 0.5])
+@pytest.mark.parametrize("lmax,C,N", [(0, 64, 300), (0, 7, 999), (1, 10, 200), (3, 32, 41), (6, 5, 37)])
+def test_dropout_bf16_sums_fall_as_those_of_the_separate_operations(lmax, C, N, p):
+    """In bf16 a kept sum has the bits of the fp32 product, the fp32 sum and one rounding: where 1 / (1 - p) is a
+    short fraction many sums are exact ties, which the last bit of fp32 decides.  The fused call writes the same.
+    Sums that cancel to less than 1/64 of the residual are within half a step of the formula instead."""
+    eq = _eq()
+    _say("bf16 dropout sums lmax=%d C=%d N=%d p=%g" % (lmax, C, N, p))
+    import torch
+
+    r = np.random.default_rng(17)
+    x, s = (_put(r.standard_normal((N, C, (lmax + 1) ** 2)), "bf16")[0] for _ in range(2))
+    keep = torch.from_numpy(ref.keep_mask(8, 9, N, C, p)).cuda()[:, :, None]
+    kept = x.float() * (1.0 / (1.0 - p))
+    want = torch.where(keep, kept + s.float(), s.float()).to(torch.bfloat16)
+    got = eq.eqtp_dropout(x, _rng(8, 9), p, lmax, residual=s)
+    apart = ~keep | ((kept + s.float()).abs() >= s.float().abs() / 64)
+    assert apart.float().mean() > 0.9 and torch.equal(got[apart], want[apart])
+    true = x.double() * float(np.float32(1.0 / (1.0 - p))) + s.double()  # the factor as the library holds it
+    assert ((got.double() - true).abs() <= 1.001 * (ref.U16 + ref.U32) * true.abs())[~apart].all()
+    assert torch.equal(eq.eqtp_dropout_add_norm(x, s, _rng(8, 9), p, lmax)[1], got)
+    assert torch.equal(eq.eqtp_dropout(x, _rng(8, 9), p, lmax), torch.where(keep, kept, 0.0).to(torch.bfloat16))
+
+
 def test_dropout_drops_what_is_not_finite():
     """A dropped channel contributes nothing, NaN and infinities included; kept ones pass them on."""
     eq = _eq()
