@@ -930,15 +930,32 @@ def eqtp_attention_backward_workspace_bytes(N: int, M: int, E: int, lmax: int, C
     return int(n)
 
 
+def _output_before_lse(f):
+    """Lets the forward call's output stand between row_ptr and lse: perm is then where lmax is without it."""
+    @functools.wraps(f)
+    def call(*args, **named):
+        if len(args) > 10 and (args[10] is None or isinstance(args[10], _torch().Tensor)):
+            return f(*args[:5], *args[6:], out=args[5], **named)
+        return f(*args, **named)
+    return call
+
+
+@_output_before_lse
 def eqtp_attention_backward(q, k, v, src, row_ptr, lse, grad_out, src_ptr, dst_s, perm, lmax: int, heads: int,
                             scale: float = None, bias=None, need_q: bool = True, need_k: bool = True,
-                            need_v: bool = True, need_bias: bool = None, workspace=None):
+                            need_v: bool = True, need_bias: bool = None, workspace=None, out=None):
     """(grad_q, grad_k, grad_v, grad_bias) of eqtp_attention, each None if not asked for.  ``lse`` is the
     forward call's.  ``src_ptr`` [M+1], ``dst_s`` [E], ``perm`` [E] int32: the edges grouped by source (for grad_k
     and grad_v; e.g. eqtp_sort_edges_stable on src, carrying eqtp_edge_rows).  ``need_bias`` defaults to whether a
-    bias is given."""
+    bias is given.
+
+    The forward call's output may stand between ``row_ptr`` and ``lse`` (or be given as ``out``), for programs that
+    keep both.  Its shape and type are checked, its values are not read: the row sums that it could stand for are
+    formed again in fp32, because a bf16 output rounds them at 2^-9."""
     torch = _torch()
     d, N, M, E = _attention_args(q, k, v, src, row_ptr, lmax, heads, scale, bias)
+    if out is not None:
+        _check(out, "out", q.dtype, q.shape)
     _check(lse, "lse", torch.float32, (N, heads))
     _check(grad_out, "grad_out", q.dtype, q.shape)
     if need_k or need_v:
