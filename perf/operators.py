@@ -211,7 +211,7 @@ def _own_attn(st):
     lse = torch.empty((c["N"], c["heads"]), dtype=torch.float32, device="cuda")
     out = eq.eqtp_attention(st["q"], st["k"], st["v"], st["src"], st["row_ptr"], c["lmax"], c["heads"],
                             bias=st["bias"], lse=lse)
-    gq, gk, gv, gb = eq.eqtp_attention_backward(st["q"], st["k"], st["v"], st["src"], st["row_ptr"], lse,
+    gq, gk, gv, gb = eq.eqtp_attention_backward(st["q"], st["k"], st["v"], st["src"], st["row_ptr"], out, lse,
                                                 st["grad_out"], st["src_ptr"], st["dst_s"], st["perm"], c["lmax"],
                                                 c["heads"], bias=st["bias"])
     return (out, gq, gk, gv, gb) if c["bias"] else (out, gq, gk, gv)
