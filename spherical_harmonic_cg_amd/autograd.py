@@ -193,6 +193,7 @@ class GraphAttentionFunction(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, q, k, v, bias, src, row_ptr, lmax, heads, scale, plan):
+        scale = None if scale is None else float(scale)  # its value now, for both passes
         lse = torch.empty((q.shape[0], heads), dtype=torch.float32, device=q.device)
         out = _eq.eqtp_attention(q, k, v, src, row_ptr, lmax, heads, scale=scale, bias=bias, lse=lse)
         ctx.save_for_backward(q, k, v, bias, src, row_ptr, lse, *(plan if plan is not None else ()))
@@ -245,5 +246,5 @@ def dropout_add_norm(x, residual, rng, p: float, lmax: int, weight=None, bias=No
 
 def graph_attention(q, k, v, src, row_ptr, lmax: int, heads: int, scale: float = None, bias=None, plan=None):
     """Differentiable attention over a graph (see eqtp_attention).  ``plan``: attention_plan's result, or None to
-    group the edges in each backward pass."""
+    group the edges in each backward pass.  ``scale`` is a number and gets no gradient (scale q to learn one)."""
     return GraphAttentionFunction.apply(q, k, v, bias, src, row_ptr, lmax, heads, scale, plan)

@@ -873,7 +873,8 @@ def _attention_args(q, k, v, src, row_ptr, lmax, heads, scale, bias):
     _check(row_ptr, "row_ptr", torch.int32, (N + 1,))
     if bias is not None:
         _check(bias, "bias", torch.float32, (E, heads))
-    return _attention_desc(lmax, C, heads, Ck // width, code, scale)[0], N, M, E
+    # the scale as a number: a tensor would be found in the descriptors' cache by its identity, whatever it holds by now
+    return _attention_desc(lmax, C, heads, Ck // width, code, None if scale is None else float(scale))[0], N, M, E
 
 
 def _workspace(workspace, need, dev):

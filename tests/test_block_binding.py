@@ -85,3 +85,25 @@ def test_attention_backward_checks_the_output(recorded):
         e.eqtp_attention_backward(*head, t["out"].double(), *rest)
     with pytest.raises(TypeError):  # given twice
         e.eqtp_attention_backward(*head, t["out"], *rest, out=t["out"])
+
+
+def test_attention_scale_is_taken_by_value(recorded):
+    """A scale held in a tensor (a learned one) counts as it is at the call, not as it was at an earlier one."""
+    import numpy as np
+    import torch
+
+    e, rec = recorded
+    t = _tensors()
+    head = [t[n] for n in ("q", "k", "v", "src", "row_ptr")]
+    back = [t[n] for n in ("lse", "grad_out", "src_ptr", "dst_s", "perm")] + [1, 2]
+    s = torch.tensor(0.5)
+    for value in (0.5, 0.25, -2.0):
+        s.fill_(value)
+        e.eqtp_attention(*head, 1, 2, scale=s)
+        e.eqtp_attention_backward(*head, *back, scale=s)
+        assert rec.scales[-1] == value and rec.calls[-1][0] == value
+    a = np.array(0.125)  # not hashable
+    e.eqtp_attention(*head, 1, 2, scale=a)
+    assert rec.scales[-1] == 0.125
+    e.eqtp_attention(*head, 1, 2)
+    assert rec.scales[-1] == 0.25  # 1 / sqrt(4 channels of 4 components)
