@@ -8,7 +8,11 @@
 // over nodes are kept at each thread's own places while its group walks over
 // the rows; at the end a workgroup adds its groups and the components of a
 // degree through LDS, in a fixed order, into its line of part
-// [workgroups][(lmax+2) C], and a second kernel adds the lines.
+// [workgroups][(lmax+2) C], and a second kernel adds the lines.  Both add in
+// 64 bits and round once: at 1000 nodes of 32 x 16 the results are 6e-8 off
+// the exact sums (fp32 additions one after the other: 1.9e-7; a pairwise fp32
+// sum: 1.3e-7), in the same time.  A thread's own sum, over the rows of its
+// group, is fp32.
 // 100k nodes, 32 channels, lmax 3, five tensors of 205 MB: 189 us (5.4 TB/s)
 // and 5 for the lines; 266k rows of 64 bf16: 23 and 4.4 us (102 MB).  Dropout
 // makes kernels of its own: its words cost registers, and with them waves
@@ -148,10 +152,10 @@ __global__ __launch_bounds__(norm_threads(T)) void norm_grad_kernel(NormGradArgs
   __syncthreads();
   for (int col = threadIdx.x; col < wcols; col += TH) {
     const int l = col / C, c = col - l * C;
-    float s = 0.0f;
+    double s = 0.0;
     for (int k = 0; k < R; ++k)
       for (int m = l * l; m < (l + 1) * (l + 1); ++m) s += pos[k * (T * NV * 4) + c * a.K + m];
-    part[col] = s;
+    part[col] = (float)s;
   }
   __syncthreads();
   if (sl.on)
@@ -162,18 +166,18 @@ __global__ __launch_bounds__(norm_threads(T)) void norm_grad_kernel(NormGradArgs
         if (sl.zero(q) && sl.channel(q, j) < C) mine[sl.channel(q, j)] = ab[j][KT == 0 ? q : 0];
   __syncthreads();
   for (int c = threadIdx.x; c < C; c += TH) {
-    float s = 0.0f;
+    double s = 0.0;
     for (int k = 0; k < R; ++k) s += pos[k * (T * NV * 4) + c];
-    part[wcols + c] = s;
+    part[wcols + c] = (float)s;
   }
 }
 
 // Sums of the lines of part: 16 columns and 64 stretches of lines a workgroup.
 __global__ __launch_bounds__(1024) void norm_weight_sum_kernel(int cols, int wcols, int parts,
                                                                const float* __restrict__ part, float* gw, float* gb) {
-  __shared__ float red[64][17];
+  __shared__ double red[64][17];
   const int cc = threadIdx.x & 15, k = threadIdx.x >> 4, col = blockIdx.x * 16 + cc;
-  float s = 0.0f;
+  double s = 0.0;
   if (col < cols) {
 #pragma unroll 8
     for (int p = k; p < parts; p += 64) s += part[(int64_t)p * cols + col];
@@ -181,13 +185,13 @@ __global__ __launch_bounds__(1024) void norm_weight_sum_kernel(int cols, int wco
   red[k][cc] = s;
   __syncthreads();
   if (k == 0 && col < cols) {
-    s = 0.0f;
+    s = 0.0;
 #pragma unroll
     for (int i = 0; i < 64; ++i) s += red[i][cc];
     if (col < wcols) {
-      if (gw) gw[col] = s;
+      if (gw) gw[col] = (float)s;
     } else if (gb) {
-      gb[col - wcols] = s;
+      gb[col - wcols] = (float)s;
     }
   }
 }
