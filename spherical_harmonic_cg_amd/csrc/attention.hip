@@ -32,8 +32,19 @@
 namespace eqtp {
 
 constexpr float kLog2E = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-// Differences of logits are taken before the change to base 2: biases of the type's lowest value would overflow in it.
-__device__ __forceinline__ float exp_of(float v) { return __builtin_amdgcn_exp2f(v * kLog2E); }
+constexpr float kLog2ELow = (float)(1.4426950408889634 - (double)kLog2E);
+// exp v for a difference of logits (taken before the change to base 2: biases of the type's lowest value would
+// overflow in it).  The hardware's exponential is of base 2; of its argument v log2 e the whole part is taken off first
+// and the rest, at most 1/2, formed with log2 e in two parts.  Rounded as one product the argument would cost |v| half
+// steps of the result (57 of them measured at v = -57, against 2.6 at most); the cases' times are the same, a single
+// wave's long row takes a tenth longer.  Below -150 the result is 0 in any case, and no infinity enters the
+// differences; NaN stays NaN.
+__device__ __forceinline__ float exp_of(float v) {
+  v = v < -150.0f ? -150.0f : v;
+  const float whole = __builtin_rintf(v * kLog2E);
+  const float rest = fmaf(v, kLog2ELow, fmaf(v, kLog2E, -whole));
+  return __builtin_ldexpf(__builtin_amdgcn_exp2f(rest), (int)whole);
+}
 
 // ---- 16 bytes of a row --------------------------------------------------------
 typedef uint32_t u4u __attribute__((ext_vector_type(4), aligned(2)));
@@ -225,9 +236,16 @@ __device__ __forceinline__ u4 keep_if(const u4& v, bool keep) {
   return v & u4{m, m, m, m};
 }
 
+// Waves a SIMD that the compiler is held to where it comes to a few registers more than three leave it (168): whole
+// units, and fp32 rows of four units a lane.  Masked units take 178 and more; those are left to it.
+template <class T, int NU, int MODE>
+constexpr int attn_waves() {
+  return MODE == 0 || (El<T>::VE == 4 && NU == 4) ? 3 : 1;
+}
+
 // One wave: heads hb HW .. of row n, piece s.
 template <class T, int G, int NU, int MODE, int EU>
-__global__ __launch_bounds__(256) void attn_kernel(AttnArgs a, Tiling t) {
+__global__ __launch_bounds__(256, (attn_waves<T, NU, MODE>())) void attn_kernel(AttnArgs a, Tiling t) {
   constexpr int VE = El<T>::VE;
   const int D = a.D, H = a.heads;
   const Lanes<T, G, NU, MODE> ln(D, t.HW);
