@@ -59,3 +59,139 @@ def test_attention_scale():
         assert torch.equal(y, out)
         for t, g in zip(leaves, grads):
             assert torch.equal(t.grad, g)
+
+
+@pytest.mark.parametrize("N,M,lengths", [(3, 700, [900, 0, 1400]), (9, 7, [3, 0, 5, 1, 4, 2, 6, 0, 3])])
+def test_attention_workspace_of_the_caller(N, M, lengths):
+    """A workspace of exactly the size that is asked for gives the same bits, and nothing behind it is written."""
+    eq = _eq()
+    _say("attention with the caller's workspace, N=%d" % N)
+    import torch
+
+    c = Case(N, M, lengths, 4, 1, 4, 2, seed=33)
+    sizes = [f(c.N, c.M, c.E, 1, 16, 4, 2) for f in (eq.eqtp_attention_workspace_bytes, eq.eqtp_attention_backward_workspace_bytes)]
+    assert sizes[1] > 0 and (sizes[0] > 0) == (N == 3)
+    out, lse = c.forward(eq)
+    grads = c.backward(eq, lse)
+    spaces = [torch.full((s + 512,), 0xA5, dtype=torch.uint8, device="cuda") for s in sizes]
+    got = c.forward(eq, workspace=spaces[0][:sizes[0]])
+    assert torch.equal(got[0], out) and torch.equal(got[1], lse)
+    for a, b in zip(c.backward(eq, lse, workspace=spaces[1][:sizes[1]]), grads):
+        assert torch.equal(a, b)
+    for s, n in zip(spaces, sizes):
+        assert (s[n:] == 0xA5).all()
+    if N == 3:
+        with pytest.raises(eq.EqtpError):
+            c.forward(eq, workspace=spaces[0][:sizes[0] - 1])
+    with pytest.raises(eq.EqtpError):
+        c.backward(eq, lse, workspace=spaces[1][:sizes[1] - 1])
+
+
+def test_norm_workspace_of_the_caller():
+    eq = _eq()
+    _say("norm with the caller's workspace")
+    import torch
+
+    d = _inputs(300, 12, 2, 1)
+    stats = torch.empty((300, 4), device="cuda")
+    eq.eqtp_layer_norm(d["x"][0], 2, d["w"][0], d["b"][0], stats=stats)
+    need = eq.eqtp_layer_norm_workspace_bytes(300, 12, 2)
+    space = torch.full((need + 512,), 0xA5, dtype=torch.uint8, device="cuda")
+    want = eq.eqtp_layer_norm_backward(d["x"][0], stats, d["g"][0], 2, d["w"][0])
+    got = eq.eqtp_layer_norm_backward(d["x"][0], stats, d["g"][0], 2, d["w"][0], workspace=space[:need])
+    for k in (0, 2, 3):
+        assert torch.equal(got[k], want[k])
+    assert (space[need:] == 0xA5).all()
+    with pytest.raises(eq.EqtpError):
+        eq.eqtp_layer_norm_backward(d["x"][0], stats, d["g"][0], 2, d["w"][0], workspace=space[:need - 1])
+
+
+def test_calls_on_another_stream():
+    """Inputs made, and every operator run, on a stream of its own: the bits of the default stream's calls."""
+    eq = _eq()
+    _say("block operators on another stream")
+    import torch
+
+    cases = [Case(40, 40, [9] * 40, 8, 3, 4, 4, seed=16), Case(2, 4000, [1500, 2500], 16, 0, 4, 4, seed=17)]
+    d = _inputs(500, 24, 2, 5)
+    rng = torch.tensor(RNG, device="cuda")
+
+    def all_calls(scale):
+        """The inputs times a power of two, made here, so that they exist on this stream only."""
+        m = lambda t: t * scale  # noqa: E731
+        res = []
+        for c in cases:
+            src, rp = _i32(c.src), _i32(c.row_ptr)
+            plan = [_i32(t) for t in c.plan]
+            lse = torch.empty((c.N, c.heads), device="cuda")
+            q, k, v, g = m(c.q[0]), m(c.k[0]), m(c.v[0]), m(c.g[0])
+            res.append(eq.eqtp_attention(q, k, v, src, rp, c.lmax, c.heads, bias=c.bias[0], lse=lse))
+            res.extend(eq.eqtp_attention_backward(q, k, v, src, rp, lse, g, *plan, c.lmax, c.heads, bias=c.bias[0]))
+        stats = torch.empty((500, 4), device="cuda")
+        out, total = eq.eqtp_dropout_add_norm(m(d["x"][0]), m(d["res"][0]), rng, 0.3, 2, d["w"][0], d["b"][0], stats=stats)
+        res += [out, total, eq.eqtp_dropout(m(d["x"][0]), rng, 0.3, 2)]
+        res += eq.eqtp_layer_norm_backward(total, stats, m(d["g"][0]), 2, d["w"][0], rng=rng, p=0.3)
+        return res
+
+    want = all_calls(0.5)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        got = all_calls(0.5)
+    side.synchronize()
+    assert len(got) == len(want)
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+
+
+def test_autograd_in_bf16():
+    """The wrappers on bf16 tensors: gradients come in bf16 (the affine ones in fp32), within the bounds of their
+    statements."""
+    _eq()
+    _say("autograd in bf16")
+    import torch
+
+    from spherical_harmonic_cg_amd import autograd as ag
+
+    d = _inputs(21, 10, 2, 1, "bf16", "bf16")
+    x, w, b = (d[n][0].clone().requires_grad_() for n in ("x", "w", "b"))
+    ag.equivariant_layer_norm(x, 2, w, b).backward(d["g"][0])
+    want = ref.norm_backward(d["x"][1], 2, d["g"][1], d["w"][1])
+    bound = ref.norm_backward_bounds(d["x"][1], 2, d["g"][1], d["w"][1], 1e-5, True)
+    assert x.grad.dtype is torch.bfloat16 and w.grad.dtype is b.grad.dtype is torch.float32
+    for t, e, o in zip((x, w, b), want, bound):
+        _within(_get(t.grad), e, o, "norm gradient")
+
+    rng = torch.tensor(RNG, device="cuda")
+    x, r = (d[n][0].clone().requires_grad_() for n in ("x", "res"))
+    w = d["w"][0].clone().requires_grad_()
+    out, total = ag.dropout_add_norm(x, r, rng, 0.3, 2, w)
+    torch.autograd.backward([out, total], [d["g"][0], d["gt"][0]])
+    t64 = _get(total.detach())
+    keep = ref.keep_mask(RNG[0], RNG[1], 21, 10, 0.3)[:, :, None]
+    gr, gw, _ = ref.norm_backward(t64, 2, d["g"][1], d["w"][1])
+    gr = gr + d["gt"][1]
+    br, bw, _ = ref.norm_backward_bounds(t64, 2, d["g"][1], d["w"][1], 1e-5, True, extra=d["gt"][1])
+    _within(_get(r.grad), gr, br, "residual")
+    # grad_x is rounded on its own, from the fp32 sum: its bound is that of the fp32 sum and one more rounding
+    b32 = ref.norm_backward_bounds(t64, 2, d["g"][1], d["w"][1], 1e-5, False, extra=d["gt"][1])[0]
+    bx = (1.001 * b32 + 3 * ref.U32 * np.abs(gr)) / 0.7
+    _within(_get(x.grad), np.where(keep, gr / 0.7, 0.0), bx + ref.U16 * (np.abs(gr) / 0.7 + bx), "x")
+    _within(_get(w.grad), gw, bw, "weight")
+
+    x = d["x"][0].clone().requires_grad_()
+    ag.equivariant_dropout(x, rng, 0.25, 2).backward(d["g"][0])
+    keep = ref.keep_mask(RNG[0], RNG[1], 21, 10, 0.25)[:, :, None]
+    want = np.where(keep, d["g"][1] / 0.75, 0.0)
+    # the factor is held in fp32, the product rounds to fp32 and then to bf16
+    _within(_get(x.grad), want, np.abs(want) * (ref.U16 + 3 * ref.U32), "dropout")
+
+    c = Case(9, 7, [3, 0, 5, 1, 4, 2, 6, 0, 3], 4, 1, 4, 2, "bf16", seed=5)
+    leaves = [t[0].clone().requires_grad_() for t in (c.q, c.k, c.v, c.bias)]
+    src, rp = _i32(c.src), _i32(c.row_ptr)
+    ag.graph_attention(*leaves[:3], src, rp, 1, 4, bias=leaves[3], plan=ag.attention_plan(src, rp, 7)).backward(c.g[0])
+    args = (c.q[1], c.k[1], c.v[1], c.src, c.row_ptr, 4, c.scale)
+    bounds = ref.attention_bounds(*args, c.g[1], c.bias[1], ref.U16)[2:]
+    for t, e, o in zip(leaves, ref.attention_backward(*args, c.g[1], c.bias[1]), bounds):
+        assert t.grad.dtype is t.dtype
+        _within(_get(t.grad), e, o, "attention gradient")
