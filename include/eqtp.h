@@ -544,7 +544,10 @@ int eqtp_set_debug(int on);
  * (block, offset) (low words first).  The channel is kept if that word is at
  * least floor(p 2^32).  The mask is a function of (seed, offset, n, c) alone
  * and is never stored: the backward pass makes it again.  Use another offset
- * (or seed) for each place and step.
+ * (or seed) for each place and step.  Whatever runs again (the backward pass,
+ * a forward pass recomputed under activation checkpointing) needs the words of
+ * the first run: give each place two words of its own rather than moving one
+ * pair along.
  *
  * Buffers need the alignment of their elements only.  Outputs must not
  * overlap inputs or each other unless said otherwise.

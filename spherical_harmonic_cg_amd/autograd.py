@@ -19,7 +19,14 @@ graph_attention keep what their backward calls need: the norm its input and
 (lmax+2) numbers a node, dropout two integers (the mask is made again), the
 attention q, k, v and one number a row and head.  Each takes its gradients
 from entry points that give the same bits from call to call.  Their backward
-passes cannot be differentiated again.  To capture a training step into a
+passes cannot be differentiated again.  A forward pass that is run again
+(activation checkpointing) reads rng again: it must still hold what it held
+the first time, or the activations made then belong to another mask than the
+output did, and no error says so.  Do not move one rng along between places;
+give each place of a step a row of its own, made from seed and offset before
+the step and left alone until its backward pass is over:
+    places = torch.stack((rng[0].expand(n), rng[1] + torch.arange(n, device=rng.device)), 1)
+To capture a training step into a
 graph, drop every eager graph over the same leaves first (torch ends the
 process when a captured backward pass meets one).
 """
@@ -233,14 +240,15 @@ def equivariant_layer_norm(x, lmax: int, weight=None, bias=None, eps: float = 1e
 
 def equivariant_dropout(x, rng, p: float, lmax: int, residual=None):
     """Differentiable dropout of whole channels, with an optional residual sum (see eqtp_dropout).  ``rng``: int64
-    (seed, offset) on the GPU; its values at this call are kept for the backward pass."""
+    (seed, offset) on the GPU; its values at this call are kept for the backward pass.  Under activation checkpointing
+    the call is made twice: rng must not change in between (see the head of this module)."""
     return EquivariantDropoutFunction.apply(x, residual, rng, float(p), lmax)
 
 
 def dropout_add_norm(x, residual, rng, p: float, lmax: int, weight=None, bias=None, eps: float = 1e-5,
                      out_dtype: int = None):
     """Differentiable (out, total): total = residual + dropout(x), out = layer norm of total, one pass each way
-    (see eqtp_dropout_add_norm)."""
+    (see eqtp_dropout_add_norm).  ``rng`` as for equivariant_dropout."""
     return DropoutAddNormFunction.apply(x, residual, weight, bias, rng, float(p), lmax, eps, out_dtype)
 
 

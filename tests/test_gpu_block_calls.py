@@ -195,3 +195,36 @@ def test_autograd_in_bf16():
     for t, e, o in zip(leaves, ref.attention_backward(*args, c.g[1], c.bias[1]), bounds):
         assert t.grad.dtype is t.dtype
         _within(_get(t.grad), e, o, "attention gradient")
+
+
+@pytest.mark.parametrize("reentrant", [False, True])
+def test_dropout_under_checkpointing(reentrant):
+    """A row of rng for each place, left alone while the step's own offset moves on: a recomputed forward pass makes
+    the first one's masks, and the gradients have the bits of a run without checkpoints."""
+    _eq()
+    _say("dropout under activation checkpointing, reentrant=%s" % reentrant)
+    import torch
+    from torch.utils.checkpoint import checkpoint
+
+    from spherical_harmonic_cg_amd import autograd as ag
+
+    d = _inputs(40, 8, 1, 3)
+
+    def grads(kept):
+        rng = torch.tensor(RNG, device="cuda")
+        places = torch.stack((rng[0].expand(3), rng[1] + torch.arange(3, device="cuda")), 1)
+        x, w = d["x"][0].clone().requires_grad_(), d["w"][0].clone().requires_grad_()
+
+        def layer(h, place):
+            n, t = ag.dropout_add_norm(torch.tanh(h), h, place, 0.4, 1, w)
+            return ag.equivariant_dropout(n, place, 0.2, 1, residual=t) * n
+
+        h = x
+        for i in range(3):
+            h = layer(h, places[i]) if kept else checkpoint(layer, h, places[i], use_reentrant=reentrant)
+            rng[1] += 1
+        h.backward(d["g"][0])
+        return h.detach(), x.grad, w.grad
+
+    for a, b in zip(grads(True), grads(False)):
+        assert torch.equal(a, b)
