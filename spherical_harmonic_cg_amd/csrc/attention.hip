@@ -33,17 +33,17 @@ namespace eqtp {
 
 constexpr float kLog2E = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kLog2ELow = (float)(1.4426950408889634 - (double)kLog2E);
-// exp v for a difference of logits (taken before the change to base 2: biases of the type's lowest value would
-// overflow in it).  The hardware's exponential is of base 2; of its argument v log2 e the whole part is taken off first
-// and the rest, at most 1/2, formed with log2 e in two parts.  Rounded as one product the argument would cost |v| half
-// steps of the result (57 of them measured at v = -57, against 2.6 at most); the cases' times are the same, a single
-// wave's long row takes a tenth longer.  Below -150 the result is 0 in any case, and no infinity enters the
-// differences; NaN stays NaN.
-__device__ __forceinline__ float exp_of(float v) {
-  v = v < -150.0f ? -150.0f : v;
+// exp(v) / 2^down for a difference of logits (taken before the change to base 2: biases of the type's lowest value
+// would overflow in it).  The hardware's exponential is of base 2; of its argument v log2 e the whole part is taken off
+// first and the rest, at most 1/2, formed with log2 e in two parts.  Rounded as one product the argument would cost |v|
+// half steps of the result (57 of them measured at v = -57, against 2.6 at most); the cases' times are the same, a
+// single wave's long row takes a tenth longer.  Below -300 the result is 0 in any case (|down| < 100), and no infinity
+// enters the differences; NaN stays NaN.
+__device__ __forceinline__ float exp_of(float v, int down = 0) {
+  v = v < -300.0f ? -300.0f : v;
   const float whole = __builtin_rintf(v * kLog2E);
   const float rest = fmaf(v, kLog2ELow, fmaf(v, kLog2E, -whole));
-  return __builtin_ldexpf(__builtin_amdgcn_exp2f(rest), (int)whole);
+  return __builtin_ldexpf(__builtin_amdgcn_exp2f(rest), (int)whole - down);
 }
 
 // ---- 16 bytes of a row --------------------------------------------------------
@@ -426,6 +426,9 @@ __global__ __launch_bounds__(kJoin) void attn_join_kernel(AttnArgs a, Tiling t, 
 // place until then.  The weights exp(s - lse) are summed and divided by their
 // sum again: it is 1 but for lse's rounding, which counts where the logits are
 // so large that the sum's logarithm is lost in lse (biases of the lowest value).
+// It allows any other factor near 1 too: a moderate lse is taken off as a whole
+// power of two instead of in the difference, which would round (8 half steps of
+// a weight in a row of 4096 edges).
 //
 // Both lie in tables of E heads numbers, edge by edge, or head by head where
 // heads are dealt to the XCDs: each then writes and reads stretches of its own
@@ -468,6 +471,9 @@ __global__ __launch_bounds__(256) void attn_grad_row_kernel(AttnGradArgs a, Tili
     g[j] = ln.load((const T*)a.gout + (n * H + h) * D, j, D);
   }
   const float lse = a.lse[n * H + h];
+  const bool moderate = fabsf(lse) < 64.0f;
+  const float from = moderate ? 0.0f : lse;
+  const int down = moderate ? (int)__builtin_rintf(lse * kLog2E) : 0;
   RowRange r = piece(row_range(a.row_ptr, n, a.E), task.sp, t.S);
   if (!task.in) r.e = r.b;
   const int es = t.step == t.ES ? ln.es : 0;
@@ -522,7 +528,7 @@ __global__ __launch_bounds__(256) void attn_grad_row_kernel(AttnGradArgs a, Tili
       s[i] = s[i] == -INFINITY ? s[i] : fmaf(a.scale, lane_sum<G>(d), s[i]);
       av = lane_sum<G>(av);
       const bool none = s[i] == -INFINITY;
-      const float w = none ? 0.0f : exp_of(s[i] - lse), wa = none ? 0.0f : w * av;
+      const float w = none ? 0.0f : exp_of(s[i] - from, down), wa = none ? 0.0f : w * av;
       tt += wa;
       total += w;
 #pragma unroll

@@ -59,3 +59,33 @@ def test_weights_of_far_logits(heads):
     off = np.abs(_get(gv)[:n] - want) / want / ref.U32
     _say("largest error of a gradient's weight, half steps: %.2f" % off.max())
     assert (off <= 17.0).all(), (off.max(), a.ravel()[off.argmax()])
+
+
+@pytest.mark.parametrize("shift", [0.0, 20.0, -50.0])
+def test_gradient_weights_of_long_rows(shift):
+    """Rows of 4096 edges, whose lse lies some 8 above the logits: the gradient's weights are formed from s and lse
+    without rounding their difference (half a step of it is 8 u and more).  Every edge has a source of its own and the
+    output's gradient is 1, so grad_v is the row's weights; over that of an edge at the row's largest logit the row's
+    sum cancels.  Each of the two is off by 3 u for the exponential and one for the quotient's product: 8 u."""
+    eq = _eq()
+    _say("attention gradient weights of long rows, shift %g" % shift)
+    import torch
+
+    n, rows, heads = 4096, 2, 2
+    r = np.random.default_rng(6)
+    bias = (-5.0 * r.random((rows, n, heads))).astype(np.float32) + np.float32(shift)
+    bias[:, 17] = shift
+    E = n * rows
+    row_ptr = (n * np.arange(rows + 1)).astype(np.int32)
+    every = np.arange(E, dtype=np.int32)
+    q, k = torch.zeros((rows, heads), device="cuda"), torch.zeros((E, heads), device="cuda")
+    lse = torch.empty((rows, heads), device="cuda")
+    b = torch.from_numpy(bias.reshape(E, heads)).cuda()
+    eq.eqtp_attention(q, k, k, _i32(every), _i32(row_ptr), 0, heads, bias=b, lse=lse)
+    gv = eq.eqtp_attention_backward(q, k, k, _i32(every), _i32(row_ptr), lse, torch.ones_like(q), _i32(np.arange(E + 1)),
+                                    _i32(np.repeat(np.arange(rows), n)), _i32(every), 0, heads, bias=b)[2]
+    w = _get(gv).reshape(rows, n, heads)
+    want = np.exp(bias.astype(np.float64) - shift)
+    off = np.abs(w / w[:, 17:18] - want) / want / ref.U32
+    _say("largest error of a weight's ratio, half steps: %.2f" % off.max())
+    assert (off <= 8.0).all(), off.max()
