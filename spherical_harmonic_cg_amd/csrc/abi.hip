@@ -913,7 +913,6 @@ int eqtp_dropout(int64_t N, int C, int lmax, int dtype, double p, const void* x,
 
 namespace {
 
-constexpr int kMaxHeads = 1024;    // of q; bounds the launch grid's second dimension
 constexpr int kMaxHeadRow = 2048;  // elements of a head's row that the attention kernels hold in registers
 
 int attn_check(const eqtp_attention_desc* d, int64_t N, int64_t M, int64_t E) {
@@ -924,7 +923,7 @@ int attn_check(const eqtp_attention_desc* d, int64_t N, int64_t M, int64_t E) {
   if (N < 0 || M < 0 || E < 0 || N > kMaxIndex || M > kMaxIndex || E > kMaxIndex) return EQTP_EINVAL;
   if (E > 0 && (N == 0 || M == 0)) return EQTP_EINVAL;
   if (d->lmax > eqtp::kSo2MaxL || (int64_t)(d->C / d->heads) * eqtp::num_comp(d->lmax) > kMaxHeadRow ||
-      d->heads > kMaxHeads)
+      d->heads > eqtp::kMaxAttnHeads)
     return EQTP_EUNSUPPORTED;
   return EQTP_OK;
 }

@@ -72,7 +72,9 @@ struct El<__bf16> {
   static __device__ __forceinline__ float at(const u4& r, int i) {
     return __builtin_bit_cast(float, i & 1 ? r[i >> 1] & 0xffff0000u : r[i >> 1] << 16);
   }
-  // pairs of products, summed in fp32
+  // Pairs of exact products, added to the running sum by one instruction with one rounding; what lies below the
+  // largest of the three by more than a few bits of an fp32 value is cut off first, as separate fp32 additions would
+  // round it off.  Subnormals are kept; a product past fp32's range is infinite.
   static __device__ __forceinline__ float dot(const u4& a, const u4& b, float c) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -423,7 +425,10 @@ __global__ __launch_bounds__(kJoin) void attn_join_kernel(AttnArgs a, Tiling t, 
 // Row pass: grad_q, and per edge and head the weight w and u = w (a - t),
 // a = g . v, which the source pass reads.  t = sum w a is known only at the
 // row's end, so sum u k is formed as sum w a k - t sum w k, and a waits in u's
-// place until then.  The weights exp(s - lse) are summed and divided by their
+// place until then.  (Where a's share a large part the two sums cancel: 1.25
+// to 1.45 times the error of the direct sum; 3.0e-7 against 2.4e-7 for heads
+// of one element, 20 edges a row.  Where they do not, nothing is lost: 1.4e-7
+// against 1.8e-7 for heads of 16.)  The weights exp(s - lse) are summed and divided by their
 // sum again: it is 1 but for lse's rounding, which counts where the logits are
 // so large that the sum's logarithm is lost in lse (biases of the lowest value).
 // It allows any other factor near 1 too: a moderate lse is taken off as a whole
@@ -754,7 +759,12 @@ static int pow2_from(int v) {
 // Pieces of a row: where the rows alone give fewer than kMinWaves waves, as many as bring them there, of kMinPiece
 // edges on average or more (7 rows over 50k items, 8 heads of 16: one wave a row 15 ms, 292 pieces 14 us and 6 to join).
 // (1024 waves of 64 edges or more: 15 and 19 us forward and by rows; 2048 of 32: 14 and 15; 4096: the same.)
+// The rule knows the rows' number and their mean length, not the longest: among kMinWaves rows and more a row is one
+// wave's (or, beside short ones, one lane group's) however long it is.  10k rows, 300k edges, 4 heads of 16, trained: 84
+// us with even rows, 14 ms with 100k of the edges in one row, 6 ms with 100k at one source.
 constexpr int64_t kMinWaves = 2048, kMinPiece = 32;
+// (a join's grid is a workgroup of kJoin threads for each of fewer than kMinWaves rows and each head)
+static_assert((kMinWaves - 1) * kMaxAttnHeads * kJoin < ((int64_t)1 << 32), "a grid holds fewer than 2^32 threads");
 static int pieces(int64_t rows, int64_t E) {
   if (rows <= 0 || rows >= kMinWaves) return 1;
   int64_t s = (kMinWaves + rows - 1) / rows;
@@ -804,9 +814,11 @@ static Tiling tiling(const HeadShape& s, int heads, int share, int64_t rows, int
   t.S = pieces(rows, E);
   t.HW = pow2_from(heads) < room ? pow2_from(heads) : room;
   // Heads dealt to the XCDs: each L2 then sees one slice of the gathered tensors and finds more of it (10k atoms,
-  // 4 heads, 82 MB: slices of 20 MB, a fifth of the reads; 308 -> 250 us forward).  Not where the tensors fit the L2s
-  // anyway, nor where a slice is so large that hardly anything is found (51 MB: 718 -> 726 us), nor with slices of
-  // less than some cache lines a row (64-byte pieces of 512-byte rows: 69 -> 250 us).
+  // 4 heads, 82 MB: slices of 20 MB, a fifth of the reads; 308 -> 250 us forward).  Not up to 8 MB, where much is
+  // found by whatever XCD (10k rows of 27 edges, 4 heads of 256; 4 MB: fp32 forward 99 us, 104 if dealt, bf16 66 and 90;
+  // 6 MB: 132 and 104, trained 838 and 838, bf16 75 and 91; 8 MB: 171 and 105, trained 959 and 880, bf16 92 and 91), nor
+  // where a slice is so large that hardly anything is found (51 MB: 718 -> 726 us), nor with slices of less than some
+  // cache lines a row (64-byte pieces of 512-byte rows: 69 -> 250 us).
   t.spread = 0;
   int nb = kv < 8 ? kv : 8;
   while (nb > 1 && kv / nb * row_bytes < kSpreadLine) nb >>= 1;

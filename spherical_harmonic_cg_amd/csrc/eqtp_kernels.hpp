@@ -112,6 +112,8 @@ struct DropArgs {
   hipStream_t stream;
 };
 
+constexpr int kMaxAttnHeads = 1024;  // heads of q: bounds the grids of the attention's joins
+
 // attention over a graph; head rows of D = (C / heads) K elements
 struct AttnArgs {
   int64_t N, M, E;

@@ -1,5 +1,5 @@
-// norm.hip -- layer norm by degree of features [N, C, K], forward and
-// backward, with the residual branch's dropout and sum in the same pass:
+// norm.hip -- layer norm by degree of features [N, C, K] (gradients are in
+// norm_grad.hip), with the residual branch's dropout and sum in the same pass:
 //   z = x, or residual + keep x / (1 - p);
 //   zc = z - [l = 0] mean_c z;  r_l = 1 / sqrt(mean_{c, m of l} zc^2 + eps);
 //   out = zc r_l weight[l, c] + [l = 0] bias[c].

@@ -109,8 +109,9 @@ __device__ __forceinline__ void arrived(float& v) { asm volatile("" : "+v"(v)); 
 
 // ---- sums over a group ------------------------------------------------------
 // Sums of the first `count` of v over a group of T threads, the same in each.
-// Groups of more than a wave use red [2][waves * NV]; `turn` alternates its
-// halves, so one barrier a sum suffices.
+// Groups of more than a wave use red [2][waves * (kMaxDeg + 1)], as
+// group_sums8 does; `turn` alternates its halves, so one barrier a sum
+// suffices.
 template <int T, int NV>
 __device__ __forceinline__ void group_sums(float (&v)[NV], int count, float* red, int& turn) {
 #pragma unroll
@@ -313,7 +314,12 @@ inline int norm_grid(int64_t N) {
   return (int)(want < most ? want : most);
 }
 
-// Calls F(T, NV) for a shape: NV is the next of the built sizes.
+// Calls F(T, NV) for a shape: NV is the next of the built sizes.  Fewer quads than a row may need are built where rows
+// that need no more are common, because quads that stay empty cost registers, and in the gradients LDS and with it
+// workgroups (bf16, us forward / trained, against the largest size alone): 8 threads, 200k x 64: 11.8 / 36 against 13.9 /
+// 43; 16 threads, 200k x 8 x 9: 24 / 65, 29 / 88; 64 threads, 20k x 8 x 49 (two): 14 / 37, 16.6 / 47; 40k x 38 x 16
+// (three): 19.6 / 60, 20.4 / 66; 128 threads, 20k x 33 x 25: 27 / 74, 30 / 99; 512 threads, 4k x 8192 (five): 34 / 104,
+// 57 / 250.  32 and 256 threads meet fewer than three quads at odd K and K = 36 only.
 #define EQTP_NORM_SHAPES(s, F)                                                     \
   ((s).T == 8     ? ((s).NV <= 2 ? F(8, 2) : F(8, 4))                              \
    : (s).T == 16  ? ((s).NV <= 2 ? F(16, 2) : F(16, 4))                            \
