@@ -229,8 +229,9 @@ def attention_plan(src, row_ptr, M: int):
     """(src_ptr [M+1], dst_s [E], perm [E]): the edges grouped by source, what graph_attention's backward pass needs;
     made once, it serves every layer and step over the same graph."""
     rows = _eq.eqtp_edge_rows(row_ptr, src.shape[0])
-    src_ptr, perm, _, dst_s = _eq.eqtp_sort_edges_stable(src, M, src=rows)
-    return src_ptr, dst_s, perm
+    # the grouping could carry the rows along, but takes what it carries for nodes below M: debug mode would refuse them
+    src_ptr, perm, _, _ = _eq.eqtp_sort_edges_stable(src, M)
+    return src_ptr, rows.index_select(0, perm), perm
 
 
 def equivariant_layer_norm(x, lmax: int, weight=None, bias=None, eps: float = 1e-5, out_dtype: int = None):

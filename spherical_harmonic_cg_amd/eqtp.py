@@ -947,7 +947,7 @@ def eqtp_attention_backward(q, k, v, src, row_ptr, lse, grad_out, src_ptr, dst_s
                             need_v: bool = True, need_bias: bool = None, workspace=None, out=None):
     """(grad_q, grad_k, grad_v, grad_bias) of eqtp_attention, each None if not asked for.  ``lse`` is the
     forward call's.  ``src_ptr`` [M+1], ``dst_s`` [E], ``perm`` [E] int32: the edges grouped by source (for grad_k
-    and grad_v; e.g. eqtp_sort_edges_stable on src, carrying eqtp_edge_rows).  ``need_bias`` defaults to whether a
+    and grad_v; e.g. autograd.attention_plan).  ``need_bias`` defaults to whether a
     bias is given.
 
     The forward call's output may stand between ``row_ptr`` and ``lse`` (or be given as ``out``), for programs that

@@ -228,3 +228,48 @@ def test_dropout_under_checkpointing(reentrant):
 
     for a, b in zip(grads(True), grads(False)):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("N,M", [(9, 7), (7, 9), (40, 1)])
+def test_attention_plan_in_debug_mode(N, M):
+    """More rows than sources, and fewer: the checks of debug mode take rows for rows and sources for sources."""
+    eq = _eq()
+    _say("attention plan in debug mode N=%d M=%d" % (N, M))
+    import torch
+
+    from spherical_harmonic_cg_amd import autograd as ag
+
+    c = Case(N, M, [3] * N, 4, 1, 2, 2, seed=34)
+    src, rp = _i32(c.src), _i32(c.row_ptr)
+    was = eq.eqtp_set_debug(True)
+    try:
+        plan = ag.attention_plan(src, rp, M)
+        for a, b in zip(plan, c.plan):
+            assert (a.cpu().numpy() == b).all()
+        leaves = [t[0].clone().requires_grad_() for t in (c.q, c.k, c.v)]
+        ag.graph_attention(*leaves, src, rp, 1, 2, bias=c.bias[0]).backward(c.g[0])
+    finally:
+        eq.eqtp_set_debug(was)
+    _, lse = c.forward(eq)
+    for t, g in zip(leaves, c.backward(eq, lse)):
+        assert torch.equal(t.grad, g)
+
+
+def test_attention_without_rows_or_edges_through_autograd():
+    """No edges, and no rows: zero gradients, from a plan made in the backward pass."""
+    eq = _eq()
+    _say("attention autograd without edges")
+    import torch
+
+    from spherical_harmonic_cg_amd import autograd as ag
+
+    none = torch.empty(0, dtype=torch.int32, device="cuda")
+    for N, M in ((4, 3), (0, 3), (4, 0), (0, 0)):
+        q, k, v = (torch.randn((n, 6, 4), device="cuda", requires_grad=True) for n in (N, M, M))
+        bias = torch.empty((0, 2), device="cuda", requires_grad=True)
+        rp = torch.zeros(N + 1, dtype=torch.int32, device="cuda")
+        out = ag.graph_attention(q, k, v, none, rp, 1, 2, bias=bias)
+        out.backward(torch.ones_like(out))
+        assert out.shape == q.shape and (out == 0).all()
+        for t in (q, k, v, bias):
+            assert t.grad.shape == t.shape and (t.grad == 0).all()
