@@ -656,9 +656,14 @@ typedef struct eqtp_attention_desc {
  *   workspace eqtp_attention_workspace_bytes(d, N, M, E) bytes, 16-byte
  *          aligned (may be NULL when that is 0): partial sums where few long
  *          rows are cut into pieces.
- * Logits, softmax and sums are fp32; out is rounded once.  The order of every
- * sum is fixed: the same bits from call to call.  0 <= N, M, E < 2^31 (E > 0
- * needs N, M > 0).  In debug mode the graph is checked.
+ * Logits, softmax and sums are fp32 (products of bf16 elements are exact and
+ * enter in pairs, with one rounding; a weight is off by 3 half steps and its
+ * logit's error); out is rounded once.  The order of every sum is fixed: the
+ * same bits from call to call.  0 <= N, M, E < 2^31 (E > 0 needs N, M > 0).  In
+ * debug mode the graph is checked.
+ * Rows are shared out by their number and mean length: with 2048 rows or more
+ * (backward: sources, too) a row's edges are one wave's, so a row of very many
+ * edges among short ones takes as long as that wave (100k edges: 4 ms, forward).
  */
 int64_t eqtp_attention_workspace_bytes(const eqtp_attention_desc* d, int64_t N, int64_t M, int64_t E);
 int eqtp_attention(const eqtp_attention_desc* d, int64_t N, int64_t M, int64_t E, const int32_t* src,

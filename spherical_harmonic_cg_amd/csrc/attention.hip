@@ -9,8 +9,9 @@
 // ALUs and the gathers bound the kernels: rows outside an XCD's L2 (4 MiB)
 // arrive at 7.4 to 8.2 TB/s, whatever holds them.  10k atoms, 266k edges,
 // 4 heads of 256 fp32 elements: 2.18 GB a pass, forward 250, by rows 267, by
-// sources 285 us (8.7, 8.2, 7.7 TB/s, a fifth of it L2 hits); 100k atoms,
-// 5.2M edges, bf16, 2 key and value heads of 128: 5.37 GB, 715 us (7.5 TB/s).
+// sources 285 us (8.7, 8.2, 7.7 TB/s, a fifth of it L2 hits; vector ALUs busy
+// 36, 47 and 43% of the time); 100k atoms, 5.2M edges, bf16, 2 key and value
+// heads of 128: 5.37 GB, 718 us (7.5 TB/s).
 //
 // A head's row of D elements is a line of 16-byte units.  G lanes hold it, NU
 // units each (unit lig + G j), beside the q and sums of the same places; dot
@@ -425,15 +426,16 @@ __global__ __launch_bounds__(kJoin) void attn_join_kernel(AttnArgs a, Tiling t, 
 // Row pass: grad_q, and per edge and head the weight w and u = w (a - t),
 // a = g . v, which the source pass reads.  t = sum w a is known only at the
 // row's end, so sum u k is formed as sum w a k - t sum w k, and a waits in u's
-// place until then.  (Where a's share a large part the two sums cancel: 1.25
-// to 1.45 times the error of the direct sum; 3.0e-7 against 2.4e-7 for heads
-// of one element, 20 edges a row.  Where they do not, nothing is lost: 1.4e-7
-// against 1.8e-7 for heads of 16.)  The weights exp(s - lse) are summed and divided by their
-// sum again: it is 1 but for lse's rounding, which counts where the logits are
-// so large that the sum's logarithm is lost in lse (biases of the lowest value).
-// It allows any other factor near 1 too: a moderate lse is taken off as a whole
-// power of two instead of in the difference, which would round (8 half steps of
-// a weight in a row of 4096 edges).
+// place until then.  (Two sums that partly cancel; against fp32 operations with
+// t at hand grad_q is 0.75 to 0.9 times as far off on rows of 20 edges over
+// several lanes, k and v with or without a common mean of up to 16 times their
+// spread, 1.26 times where one lane adds a row, 1.1 on rows of 7000.)  The
+// weights exp(s - lse) are summed and divided by their sum again: it is 1 but
+// for lse's rounding, which counts where the logits are so large that the sum's
+// logarithm is lost in lse (biases of the lowest value).  It allows any other
+// factor near 1 too: a moderate lse is taken off as a whole power of two instead
+// of in the difference, which would round (8 half steps of a weight in a row of
+// 4096 edges).
 //
 // Both lie in tables of E heads numbers, edge by edge, or head by head where
 // heads are dealt to the XCDs: each then writes and reads stretches of its own

@@ -8,9 +8,10 @@
 // makes its own bits.  With K > 1 the stretch touches few channels: the lanes
 // make one block each, once, leave the keep bits in LDS and read them back
 // element by element; made by every thread for itself, the words would take
-// K times the work.  266k x 64 bf16 (K = 1): 16 us (68 MB), 20 us beside a
-// residual (102 MB), the words' multiplications (18 of four passes a block)
-// about as long as the memory; fp32 with K = 49: 5.8 TB/s.
+// K times the work.  266k x 64 bf16 (K = 1): 14 us (68 MB), 18 us beside a
+// residual (102 MB); the vector ALUs, the words' multiplications (18 of four
+// passes a block) above all, are busy 69% of the time; fp32 with K = 49:
+// 5.8 TB/s.
 #include <type_traits>
 
 #include "eqtp_device.hpp"

@@ -4,7 +4,9 @@
 //   zc = z - [l = 0] mean_c z;  r_l = 1 / sqrt(mean_{c, m of l} zc^2 + eps);
 //   out = zc r_l weight[l, c] + [l = 0] bias[c].
 //
-// Bound by HBM: each element is read and written once.  A group of T threads
+// Each element is read and written once: bound by HBM where the tensors are
+// large, by the vector ALUs (a row's fixed work) where they stay in the 256 MB
+// cache or the rows have many degrees and few channels.  A group of T threads
 // (8 to 512) holds a node's row of D = C K elements in registers, NV quads of
 // four consecutive elements a thread, so the row is read once for both the
 // statistics and the result.  Only the first A threads of a group take quads,
@@ -15,8 +17,9 @@
 // Sums by degree are folded over the lanes together (register moves, no LDS),
 // then over a group's waves through LDS.
 // 100k nodes, 32 channels, lmax 3, with dropout and residual: 146 us (819 MB,
-// 5.6 TB/s; a large copy reaches 5.4); 10k x 64 x 16 to bf16: 13 us (61 MB);
-// lmax 4 and 6 with few channels: the vector ALUs (the fixed work of a row).
+// 5.6 TB/s; a large copy reaches 5.4), vector ALUs busy 29% of it; 10k x 64 x
+// 16 to bf16: 13 us (61 MB), 66%; 266k x 64 bf16: 16 us (68 MB), 74%; 5003 x 33
+// x 25 with dropout: 19 us (66 MB), 73%; 66k x 10 x 49 bf16: 54 us (129 MB), 96%.
 #include "norm_device.hpp"
 
 namespace eqtp {

@@ -3,7 +3,7 @@
 //   a = weight g,  zhat = zc r_l,
 //   gz = r_l (a - [l = 0] mean_c a - zhat mean_l(a zhat)) (+ grad_total),
 //   gx = keep gz / (1 - p),  gweight[l, c] = sum g zhat,  gbias[c] = sum g[0].
-// Bound by HBM like the forward pass: z, g (and grad_total) are read once, the
+// Bound as the forward pass is: z, g (and grad_total) are read once, the
 // gradients written once.  Rows lie in groups of threads as there.  The sums
 // over nodes are kept at each thread's own places while its group walks over
 // the rows; at the end a workgroup adds its groups and the components of a
@@ -13,10 +13,11 @@
 // the exact sums (fp32 additions one after the other: 1.9e-7; a pairwise fp32
 // sum: 1.3e-7), in the same time.  A thread's own sum, over the rows of its
 // group, is fp32.
-// 100k nodes, 32 channels, lmax 3, five tensors of 205 MB: 189 us (5.4 TB/s)
-// and 5 for the lines; 266k rows of 64 bf16: 23 and 4.4 us (102 MB).  Dropout
-// makes kernels of its own: its words cost registers, and with them waves
-// (bf16 rows of 64: 34 us with, 24 without).
+// 100k nodes, 32 channels, lmax 3, five tensors of 205 MB: 192 us (5.3 TB/s)
+// and 5 for the lines, vector ALUs busy 26%; 266k rows of 64 bf16: 23 and 4.3
+// us (102 MB), 71%; 66k x 10 x 49 bf16: 70 us (194 MB), 90%.  Dropout makes
+// kernels of its own: its words cost registers, and with them waves (bf16 rows
+// of 64: 34 us with, 24 without).
 #include "norm_device.hpp"
 
 namespace eqtp {
