@@ -440,7 +440,8 @@ __global__ __launch_bounds__(kJoin) void attn_join_kernel(AttnArgs a, Tiling t, 
 // Both lie in tables of E heads numbers, edge by edge, or head by head where
 // heads are dealt to the XCDs: each then writes and reads stretches of its own
 // (edge by edge, four of them wrote to every line: 120 MB written instead of
-// 50, and 8.5 MB of tables beside the gathered rows in each L2 instead of 2).
+// 85, of which the bias's gradient, the caller's and edge by edge, is a part,
+// and 8.5 MB of tables beside the gathered rows in each L2 instead of 2).
 struct EdgeTables {
   float* w;
   float* u;
