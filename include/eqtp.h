@@ -691,6 +691,195 @@ int eqtp_attention_backward(const eqtp_attention_desc* d, int64_t N, int64_t M, 
                             const int32_t* perm, void* grad_q, void* grad_k, void* grad_v, float* grad_bias,
                             void* workspace, int64_t workspace_bytes, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * What stands before and behind the attention.  Rules as for the block above:
+ * any device pointers with the alignment of their elements unless said
+ * otherwise, outputs that overlap nothing unless said otherwise, no atomics
+ * whose order could change a result: the same bits from call to call.
+ * ------------------------------------------------------------------------ */
+
+typedef struct eqtp_bias_desc {
+  int32_t struct_size; /* = sizeof(eqtp_bias_desc) */
+  int32_t heads;       /* H, <= 1024 (more: EQTP_EUNSUPPORTED) */
+  int32_t buckets;     /* B, <= 512 (more: EQTP_EUNSUPPORTED) */
+  float r_cut;         /* edges of this length or more are masked; 0: none is */
+} eqtp_bias_desc;
+
+/*
+ * A learned bias of the attention's logits by distance, one row of a table for
+ * each bucket of edge lengths:
+ *   b(e) = the number of bounds <= |vec_e|,  bias[e, h] = table[b(e), h],
+ *   and -inf (what eqtp_attention takes for a mask) where |vec_e| >= r_cut.
+ * Lengths are compared as squares in 64 bits, so an edge next to a bound falls
+ * where the formula puts it.  A NaN in vec gives NaN.
+ *   vec    [E, 3] fp32;  bounds [B-1] fp32, ascending (else: which bucket is
+ *          unspecified), NULL allowed when B = 1;  table [B, H] fp32.
+ *   bias   [E, H] fp32 out, fully overwritten.  0 <= E < 2^31.
+ * Backward:
+ *   grad_table[b, h] = the sum of grad_bias[e, h] over the edges of bucket b
+ *          (masked edges and NaN lengths take no part, whatever they hold).
+ *   grad_bias [E, H] fp32 (eqtp_attention_backward's);  grad_table [B, H] fp32
+ *          out, fully overwritten (zeros for buckets without edges).
+ *   workspace eqtp_distance_bias_workspace_bytes(d, E) bytes, 16-byte aligned.
+ * Lengths get no gradient: the bias is constant between the bounds.
+ */
+int eqtp_distance_bias(const eqtp_bias_desc* d, int64_t E, const float* vec, const float* bounds, const float* table,
+                       float* bias, void* stream);
+int64_t eqtp_distance_bias_workspace_bytes(const eqtp_bias_desc* d, int64_t E);
+int eqtp_distance_bias_backward(const eqtp_bias_desc* d, int64_t E, const float* vec, const float* bounds,
+                                const float* grad_bias, float* grad_table, void* workspace, int64_t workspace_bytes,
+                                void* stream);
+
+typedef struct eqtp_qk_norm_desc {
+  int32_t struct_size; /* = sizeof(eqtp_qk_norm_desc) */
+  int32_t lmax;        /* 0..6 */
+  int32_t C;           /* channels of q: heads times the width of a head */
+  int32_t heads;       /* divides C; <= 1024, (C / heads) K <= 2048 (more: EQTP_EUNSUPPORTED) */
+  int32_t kv_heads;    /* heads of k, of the same width; <= 1024 */
+  int32_t x_dtype;     /* EQTP_F32 or EQTP_BF16: q, k, the outputs and their gradients */
+  int32_t axes;        /* coordinates of a position, 0..3; 0: no rotation */
+  int32_t pairs;       /* rotated pairs of channels, 1 .. width / 2 with axes > 0 (width even), else 0 */
+  float eps;           /* > 0, finite */
+} eqtp_qk_norm_desc;
+
+/*
+ * Norm of queries and keys by head and degree, and the rotation of their
+ * channels by position, in one pass.  For each node and head of w channels:
+ *   r_l = 1 / sqrt(mean over the w (2l+1) values of x^2 + eps),
+ *   y[c, l m] = x[c, l m] r_l weight[l, c],
+ *   theta[j] = sum_a pos[n, a] freq[a, j]                      (radians),
+ *   out[j] = y[j] cos theta[j] - y[j + w/2] sin theta[j],
+ *   out[j + w/2] = y[j] sin theta[j] + y[j + w/2] cos theta[j]  for j < pairs;
+ * the other channels are y.  All components of a channel turn by one angle, so
+ * the result turns with space as q and k do, and a logit between two nodes
+ * depends on the difference of their positions.  In a periodic cell,
+ * frequencies from its reciprocal lattice make it periodic; along a chain
+ * (axes = 1) this is the usual rotation by place.  Angles are summed and
+ * reduced in 64 bits (good to 1e-6 of a turn up to 10^9 turns).
+ *   q, out_q [N, C, K];  k, out_k [M, C kv_heads / heads, K] (x_dtype); an
+ *   output may be its own input.  N or M may be 0.
+ *   weight_q, weight_k [lmax+1, C / heads] fp32, shared by the heads, or NULL.
+ *   pos_q [N, axes], pos_k [M, axes], freq [axes, pairs] fp32 (axes > 0).
+ * Sums are fp32; an output is rounded once.  0 <= N, M < 2^31.
+ * Backward (u: the gradient turned back, a = weight u, xhat = x r_l):
+ *   grad_x = r_l (a - xhat mean_l(a xhat)),
+ *   grad_weight[l, c] = sum over nodes, heads and m of u xhat,
+ *   grad_pos[n, a] = sum_j freq[a, j] sum over heads and m of (y[j] u[j + w/2] - y[j + w/2] u[j]).
+ *   grad_q, grad_k (x_dtype), grad_weight_q, grad_weight_k [lmax+1, C / heads]
+ *   fp32, grad_pos_q [N, axes], grad_pos_k [M, axes] fp32 out: each may be
+ *   NULL; fully overwritten.  freq gets no gradient.
+ *   workspace eqtp_qk_norm_workspace_bytes(d, N, M) bytes, 16-byte aligned
+ *   (may be NULL when no gradient of a weight is asked for).
+ */
+int eqtp_qk_norm(const eqtp_qk_norm_desc* d, int64_t N, int64_t M, const void* q, const void* k, const float* weight_q,
+                 const float* weight_k, const float* pos_q, const float* pos_k, const float* freq, void* out_q,
+                 void* out_k, void* stream);
+int64_t eqtp_qk_norm_workspace_bytes(const eqtp_qk_norm_desc* d, int64_t N, int64_t M);
+int eqtp_qk_norm_backward(const eqtp_qk_norm_desc* d, int64_t N, int64_t M, const void* q, const void* k,
+                          const float* weight_q, const float* weight_k, const float* pos_q, const float* pos_k,
+                          const float* freq, const void* grad_out_q, const void* grad_out_k, void* grad_q, void* grad_k,
+                          float* grad_weight_q, float* grad_weight_k, float* grad_pos_q, float* grad_pos_k,
+                          void* workspace, int64_t workspace_bytes, void* stream);
+
+#define EQTP_SCORE_SOFTMAX 0
+#define EQTP_SCORE_SIGMOID 1
+
+typedef struct eqtp_route_desc {
+  int32_t struct_size; /* = sizeof(eqtp_route_desc) */
+  int32_t experts;     /* X, <= 256 (more: EQTP_EUNSUPPORTED) */
+  int32_t top_k;       /* experts of a node, <= X; <= 16 (more: EQTP_EUNSUPPORTED) */
+  int32_t groups;      /* divides X; consecutive experts form a group */
+  int32_t top_groups;  /* groups that stay open, <= groups */
+  int32_t score;       /* EQTP_SCORE_* */
+  int32_t renormalise; /* 1: weights divided by their sum, 0: not */
+  int32_t x_dtype;     /* EQTP_F32 or EQTP_BF16: logits and their gradient */
+  float scale;         /* factor of the weights, finite */
+} eqtp_route_desc;
+
+/*
+ * Routing of nodes to experts.  With t the logits of a node:
+ *   s[x] = exp(t[x]) / sum exp(t), or 1 / (1 + exp(-t[x]));
+ *   v = s + bias (the bias balances the experts' load: it steers the choice
+ *       only).  Without a bias, groups = 1: v = t, the same order;
+ *   of the groups, the top_groups with the largest sums of their two largest v
+ *       stay open, and the top_k largest v of their experts are taken, in
+ *       descending order; where values are equal the lower index goes first;
+ *   weight[n, j] = scale s / sum of s over those taken (renormalise), or scale s.
+ * v is compared in 64 bits.  An expert whose logit is -inf, or whose v is -inf
+ * or NaN, is never taken; places that stay empty have idx = -1 and weight 0.  A
+ * NaN among a node's logits gives idx = -1 and weight NaN.
+ *   logits [N, X] (x_dtype);  bias [X] fp32 or NULL;
+ *   idx [N, top_k] int32, weight [N, top_k] fp32 out.  0 <= N < 2^31.
+ * Backward (idx is held fixed and the bias gets no gradient):
+ *   grad_logits [N, X] (x_dtype) out, fully overwritten, from grad_weight
+ *   [N, top_k] fp32 and the forward call's idx.
+ */
+int eqtp_route(const eqtp_route_desc* d, int64_t N, const void* logits, const float* bias, int32_t* idx, float* weight,
+               void* stream);
+int eqtp_route_backward(const eqtp_route_desc* d, int64_t N, const void* logits, const int32_t* idx,
+                        const float* grad_weight, void* grad_logits, void* stream);
+
+/*
+ * Groups a routing: idx [N, top_k] int32, each an expert in [0, experts) or
+ * anything else for none.
+ *   slots [N top_k] int32 out: n top_k + j, grouped by expert, in input order
+ *         within one; places without an expert last.
+ *   ptr   [experts + 1] int32 out: where each expert's places begin in slots
+ *         (differences are the experts' loads).
+ *   order [N] int32 out, or NULL: the nodes, those with the same two lowest
+ *         experts together (with top_k = 1, slots serves as order).
+ *   workspace eqtp_expert_plan_workspace_bytes bytes, 16-byte aligned.
+ * experts <= 256, top_k <= 16 (more: EQTP_EUNSUPPORTED), N top_k < 2^31.
+ */
+int64_t eqtp_expert_plan_workspace_bytes(int64_t N, int top_k, int experts);
+int eqtp_expert_plan(int64_t N, int top_k, int experts, const int32_t* idx, int32_t* order, int32_t* slots, int32_t* ptr,
+                     void* workspace, int64_t workspace_bytes, void* stream);
+
+typedef struct eqtp_expert_desc {
+  int32_t struct_size; /* = sizeof(eqtp_expert_desc) */
+  int32_t lmax;        /* 0..6 */
+  int32_t C;           /* 8, 16, 32, 64 or 128, as for eqtp_linear */
+  int32_t experts;     /* X, <= 256 */
+  int32_t top_k;       /* experts of a node, <= 16 */
+  int32_t x_dtype;     /* EQTP_F32 (fp32 products) or EQTP_BF16 (bf16 products, fp32 sums): h, W, grad_out, grad_h */
+  int32_t out_dtype;   /* EQTP_F32 or EQTP_BF16: out */
+} eqtp_expert_desc;
+
+/*
+ * Per-degree channel linears by expert, a mixture of eqtp_linear:
+ *   out[n, c', l m] = sum_j weight[n, j] sum_c W[idx[n, j], l, c', c] h[n, c, l m].
+ * With top_k = 1 and no weight it is the linear whose weights go by a node's
+ * kind (its element).
+ *   h      [N, C, K];  W [X, lmax+1, C, C] (output channel major) (x_dtype);
+ *   idx    [N, top_k] int32: an index outside [0, X) adds nothing (a node
+ *          without any gets zeros); the same expert twice adds its weights.
+ *   weight [N, top_k] fp32, or NULL (ones).
+ *   order  [N] int32, or NULL: eqtp_expert_plan's.  Any permutation of the
+ *          nodes gives the same bits (an index that is missing leaves its
+ *          node's rows as they were); one that keeps nodes of the same experts
+ *          together is faster.
+ *   out    [N, C, K] (out_dtype), fully overwritten.
+ * h, W, out, grad_out, grad_h and grad_W are 16-byte aligned.  A node's sum
+ * goes over its experts in ascending order, in fp32, and is rounded once.
+ * Backward, each output may be NULL, fully overwritten:
+ *   grad_h      [N, C, K] (x_dtype) = sum_j weight W^T grad_out;
+ *   grad_weight [N, top_k] fp32 = <grad_out, W h> (0 at places without an expert);
+ *   grad_W      [X, lmax+1, C, C] fp32, summed over slots in a fixed order
+ *               (needs slots and ptr; zeros for experts without places).  With
+ *               bf16 operands weight * grad_out enters in two bf16 parts: 2^-16
+ *               of a term at most is lost.
+ *   grad_out    [N, C, K] (x_dtype).
+ *   workspace   eqtp_expert_linear_backward_workspace_bytes(d, N) bytes,
+ *               16-byte aligned.
+ */
+int eqtp_expert_linear(const eqtp_expert_desc* d, int64_t N, const void* h, const void* W, const int32_t* idx,
+                       const float* weight, const int32_t* order, void* out, void* stream);
+int64_t eqtp_expert_linear_backward_workspace_bytes(const eqtp_expert_desc* d, int64_t N);
+int eqtp_expert_linear_backward(const eqtp_expert_desc* d, int64_t N, const void* h, const void* W, const int32_t* idx,
+                                const float* weight, const int32_t* order, const int32_t* slots, const int32_t* ptr,
+                                const void* grad_out, void* grad_h, float* grad_W, float* grad_weight, void* workspace,
+                                int64_t workspace_bytes, void* stream);
+
 /*
  * Test-only: walks the dst-sorted edges with exactly the row -> wave ->
  * lane -> step schedule that eqtp_conv_fused uses for the given (C, lmax,

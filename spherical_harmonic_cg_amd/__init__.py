@@ -13,6 +13,11 @@ from .eqtp import (EQTP_ALGO_AUTO, EQTP_ALGO_EDGE_SO2, EQTP_ALGO_EDGE_VALU, EQTP
                    eqtp_conv_workspace_bytes, eqtp_edge_rows, eqtp_interaction, eqtp_interaction_workspace_bytes, eqtp_linear,
                    eqtp_attention, eqtp_attention_backward, eqtp_attention_backward_workspace_bytes,
                    eqtp_attention_workspace_bytes, eqtp_dropout, eqtp_dropout_add_norm, eqtp_layer_norm, eqtp_layer_norm_backward,
-                   eqtp_layer_norm_workspace_bytes, eqtp_num_paths, eqtp_path_table, eqtp_set_debug, eqtp_sh, eqtp_sort_edges, eqtp_sort_edges_stable, eqtp_sort_workspace_bytes,
+                   eqtp_layer_norm_workspace_bytes,
+                   EQTP_SCORE_SIGMOID, EQTP_SCORE_SOFTMAX, eqtp_distance_bias, eqtp_distance_bias_backward,
+                   eqtp_distance_bias_workspace_bytes, eqtp_expert_linear, eqtp_expert_linear_backward,
+                   eqtp_expert_linear_backward_workspace_bytes, eqtp_expert_plan, eqtp_expert_plan_workspace_bytes,
+                   eqtp_qk_norm, eqtp_qk_norm_backward, eqtp_qk_norm_workspace_bytes, eqtp_route, eqtp_route_backward,
+                   eqtp_num_paths, eqtp_path_table, eqtp_set_debug, eqtp_sh, eqtp_sort_edges, eqtp_sort_edges_stable, eqtp_sort_workspace_bytes,
                    eqtp_status_string,
                    eqtp_test_segment_probe, load_library)

@@ -18,7 +18,8 @@ LIB = os.path.join(HERE, "libeqtp.so")
 ROOT = os.path.dirname(HERE)
 
 SOURCES = ["abi.hip", "sh.hip", "sort.hip", "conv_node.hip", "conv_edge.hip", "conv_bwd.hip", "conv_so2.hip", "conv_bwd_so2.hip", "linear.hip", "interaction.hip", "check.hip", "norm.hip", "norm_grad.hip",
-           "dropout.hip", "attention.hip"]
+           "dropout.hip", "attention.hip", "abi_block.hip", "distance_bias.hip", "head_norm.hip", "route.hip",
+           "expert_plan.hip", "expert.hip", "expert_grad.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [

@@ -9,6 +9,7 @@
 #include <mutex>
 
 #include "../../include/eqtp.h"
+#include "abi_checks.hpp"
 #include "eqtp_device.hpp"
 #include "eqtp_kernels.hpp"
 #include "generated/so2_tables.inc"
@@ -26,10 +27,6 @@ static __device__ __align__(256) unsigned char scratch[kScratchBytes];
 static __device__ __align__(16) int32_t debug_report[2 * eqtp::kCheckWords];
 
 namespace {
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
-bool valid_c(int C) { return C == 8 || C == 16 || C == 32 || C == 64 || C == 128; }
 
 static_assert(offsetof(eqtp_conv_desc, x_dtype) == EQTP_CONV_DESC_SIZE_V1, "descriptor layout");
 static_assert(offsetof(eqtp_conv_desc, out_dtype) == EQTP_CONV_DESC_SIZE_V2, "descriptor layout");
@@ -50,8 +47,6 @@ int out_f32_only(const eqtp_conv_desc* d) {
   const int o = desc_out_dtype(d);
   return o == EQTP_F32 ? EQTP_OK : (o == EQTP_BF16 ? EQTP_EUNSUPPORTED : EQTP_EINVAL);
 }
-constexpr int64_t kMaxIndex = (int64_t(1) << 31) - 1;
-
 // path counts and lists for lmax 0..6 (the same canonical order in both
 // generated tables; lmax <= 3 also has the coupling-form tables)
 int num_paths_host(int lmax, int path_set) {
@@ -82,8 +77,6 @@ const eqtp_gen::PathLs* path_list(int lmax, int path_set) {
                                            eqtp_gen::kSo2Paths_L6_so3};
   return path_set == EQTP_PATHS_PARITY ? parity[lmax] : so3[lmax];
 }
-
-int status_of(hipError_t e) { return e == hipSuccess ? EQTP_OK : EQTP_EHIP; }
 
 // ---- debug mode: graph checks before each launch (see eqtp_set_debug) ----
 int debug_from_env() {
@@ -759,10 +752,6 @@ namespace {
 
 constexpr int kMaxNormRow = 16384;  // elements of a node that the norm's kernels hold in registers
 
-bool dtype_ok(int t) { return t == EQTP_F32 || t == EQTP_BF16; }
-bool aligned_as(const void* p, int dtype) {
-  return (reinterpret_cast<uintptr_t>(p) & (dtype == EQTP_BF16 ? 1u : 3u)) == 0;
-}
 bool aligned8(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
 bool prob_ok(double p) { return p >= 0.0 && p < 1.0; }  // false for NaN
 uint32_t drop_threshold(double p) { return (uint32_t)(p * 4294967296.0); }

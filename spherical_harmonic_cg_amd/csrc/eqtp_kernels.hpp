@@ -156,6 +156,106 @@ struct AttnGradArgs {
   hipStream_t stream;
 };
 
+// bias of the attention's logits by distance buckets (and its gradient: gbias, part)
+struct BiasArgs {
+  int64_t E;
+  int H, B;
+  int first_step;         // largest power of two below B (0 for B = 1)
+  double cut2;            // square of the cut-off, NaN for none
+  const float* vec;
+  const float* bounds;    // [B - 1]
+  const float* table;
+  float* bias;
+  const float* gbias;
+  float* part;            // bias_workspace_floats floats
+  hipStream_t stream;
+};
+int64_t bias_workspace_floats(int64_t E, int B, int H);
+hipError_t launch_distance_bias(const BiasArgs& a);
+hipError_t launch_distance_bias_grad(const BiasArgs& a, float* grad_table);
+
+// norm of queries (side 0) and keys (side 1) by head and degree, with the rotation by position (and the gradients)
+struct HeadSide {
+  int64_t rows;
+  int heads;
+  int stretch, stretches; // heads that a group of threads takes of a node, and how many such stretches a node has
+  const void* x;
+  const float* weight;    // or nullptr
+  const float* pos;       // with axes > 0
+  void* out;
+  const void* gout;
+  void* gx;               // or nullptr
+  float* gpos;            // or nullptr
+  float* part;            // head_norm_workspace_floats floats, or nullptr
+};
+struct HeadNormArgs {
+  int d, K, lmax;         // channels of a head
+  bool bf16;
+  float eps;
+  int axes, R;            // axes of positions (0: no rotation), rotated pairs
+  const float* freq;
+  HeadSide side[2];
+  int blocks_q, blocks_k;
+  hipStream_t stream;
+};
+int64_t head_norm_workspace_floats(int64_t rows, int heads, int d, int lmax);
+hipError_t launch_head_norm(const HeadNormArgs& a);
+hipError_t launch_head_norm_grad(const HeadNormArgs& a, float* const (&gw)[2]);
+
+// routing
+constexpr int kMaxExperts = 256, kMaxTopK = 16;
+struct RouteArgs {
+  int64_t N;
+  int X, k, groups, top_groups;
+  bool bf16, sigmoid, renormalise;
+  float scale;
+  const void* logits;
+  const float* bias;      // or nullptr
+  int32_t* idx;           // (read by the gradient)
+  float* weight;
+  const float* gweight;
+  void* glogits;
+  hipStream_t stream;
+};
+hipError_t launch_route(const RouteArgs& a);
+hipError_t launch_route_grad(const RouteArgs& a);
+
+// the experts' per-degree linears
+struct ExpertArgs {
+  int64_t N;
+  int C, lmax, X, k;
+  bool bf16, out_bf16;
+  const void* h;          // forward: features; backward: the output's gradient
+  const void* W;          // [X, lmax+1, out channel, in channel] as the products take it
+  const int32_t* idx;
+  const float* weight;    // or nullptr
+  const int32_t* order;   // or nullptr
+  void* out;              // backward: h's gradient, or nullptr
+  const void* dot_with;   // backward: h, for the gates' gradient
+  float* gweight;         // or nullptr
+  hipStream_t stream;
+};
+hipError_t launch_expert(const ExpertArgs& a);
+hipError_t launch_transpose_weights(int64_t matrices, int C, bool bf16, const void* W, void* WT, hipStream_t stream);
+struct ExpertGradArgs {
+  int64_t N;
+  int C, lmax, X, k;
+  bool bf16;
+  const void* h;
+  const void* gout;
+  const float* weight;    // or nullptr
+  const int32_t* slots;   // [N k] places n k + j by expert
+  const int32_t* ptr;     // [X + 1]
+  float* gW;
+  float* part;            // expert_grad_floats floats
+  hipStream_t stream;
+};
+int64_t expert_grad_floats(int64_t N, int C, int lmax, int X, int k, bool bf16);
+hipError_t launch_expert_grad(const ExpertGradArgs& a);
+int64_t expert_plan_ints(int64_t N, int k, int X);
+hipError_t launch_expert_plan(int64_t N, int k, int X, const int32_t* idx, int32_t* order, int32_t* slots, int32_t* ptr,
+                              int32_t* ws, hipStream_t stream);
+
 int64_t attn_workspace_bytes(int64_t N, int64_t M, int64_t E, int D, int heads, int kv_heads);
 hipError_t launch_attention(const AttnArgs& a);
 int64_t attn_grad_workspace_bytes(int64_t N, int64_t M, int64_t E, int D, int heads, int kv_heads);
@@ -163,6 +263,8 @@ hipError_t launch_attention_grad(const AttnGradArgs& a);
 hipError_t launch_norm(const NormArgs& a);
 int64_t norm_workspace_floats(int64_t N, int C, int lmax);
 hipError_t launch_norm_grad(const NormGradArgs& a);
+// out[cols] = the sums of the columns of part [parts][cols], in 64 bits and a fixed order
+hipError_t launch_line_sums(int cols, int parts, const float* part, float* out, hipStream_t stream);
 hipError_t launch_dropout(const DropArgs& a);
 hipError_t launch_sh(const float* vec, int64_t E, int lmax, float* Y, hipStream_t stream);
 hipError_t launch_conv_node(const ConvArgs& a);   // sorted edges, fixed weights, matrix cores

@@ -197,6 +197,12 @@ __global__ __launch_bounds__(1024) void norm_weight_sum_kernel(int cols, int wco
   }
 }
 
+hipError_t launch_line_sums(int cols, int parts, const float* part, float* out, hipStream_t stream) {
+  hipLaunchKernelGGL(norm_weight_sum_kernel, dim3((cols + 15) / 16), dim3(1024), 0, stream, cols, cols, parts, part, out,
+                     (float*)nullptr);
+  return hipGetLastError();
+}
+
 constexpr int kMaxParts = 2048;
 
 int64_t norm_workspace_floats(int64_t N, int C, int lmax) {

@@ -25,6 +25,7 @@ EQTP_W_FIXED, EQTP_W_RADIAL = 0, 1
 EQTP_EDGES_DST_SORTED, EQTP_EDGES_UNSORTED = 0, 1
 EQTP_ALGO_AUTO, EQTP_ALGO_NODE_MFMA, EQTP_ALGO_EDGE_VALU, EQTP_ALGO_EDGE_SO2 = 0, 1, 2, 3
 EQTP_F32, EQTP_BF16, EQTP_F32_BF16 = 0, 1, 2
+EQTP_SCORE_SOFTMAX, EQTP_SCORE_SIGMOID = 0, 1
 
 EXPORTED = ("eqtp_num_paths", "eqtp_path_table", "eqtp_sh", "eqtp_conv_fused", "eqtp_conv_workspace_bytes",
             "eqtp_conv_fused_ws", "eqtp_conv_fused_noalloc", "eqtp_conv_messages",
@@ -35,6 +36,10 @@ EXPORTED = ("eqtp_num_paths", "eqtp_path_table", "eqtp_sh", "eqtp_conv_fused", "
             "eqtp_layer_norm_backward", "eqtp_dropout",
             "eqtp_attention_workspace_bytes", "eqtp_attention", "eqtp_attention_backward_workspace_bytes",
             "eqtp_attention_backward",
+            "eqtp_distance_bias", "eqtp_distance_bias_workspace_bytes", "eqtp_distance_bias_backward",
+            "eqtp_qk_norm", "eqtp_qk_norm_workspace_bytes", "eqtp_qk_norm_backward",
+            "eqtp_route", "eqtp_route_backward", "eqtp_expert_plan_workspace_bytes", "eqtp_expert_plan",
+            "eqtp_expert_linear", "eqtp_expert_linear_backward_workspace_bytes", "eqtp_expert_linear_backward",
             "eqtp_status_string", "eqtp_check_graph", "eqtp_set_debug", "eqtp_test_segment_probe")
 
 
@@ -67,6 +72,29 @@ class _AttentionDesc(ctypes.Structure):
     _fields_ = [("struct_size", ctypes.c_int32), ("lmax", ctypes.c_int32), ("C", ctypes.c_int32),
                 ("heads", ctypes.c_int32), ("kv_heads", ctypes.c_int32), ("x_dtype", ctypes.c_int32),
                 ("scale", ctypes.c_float)]
+
+
+class _BiasDesc(ctypes.Structure):
+    _fields_ = [("struct_size", ctypes.c_int32), ("heads", ctypes.c_int32), ("buckets", ctypes.c_int32),
+                ("r_cut", ctypes.c_float)]
+
+
+class _QkNormDesc(ctypes.Structure):
+    _fields_ = [("struct_size", ctypes.c_int32), ("lmax", ctypes.c_int32), ("C", ctypes.c_int32),
+                ("heads", ctypes.c_int32), ("kv_heads", ctypes.c_int32), ("x_dtype", ctypes.c_int32),
+                ("axes", ctypes.c_int32), ("pairs", ctypes.c_int32), ("eps", ctypes.c_float)]
+
+
+class _RouteDesc(ctypes.Structure):
+    _fields_ = [("struct_size", ctypes.c_int32), ("experts", ctypes.c_int32), ("top_k", ctypes.c_int32),
+                ("groups", ctypes.c_int32), ("top_groups", ctypes.c_int32), ("score", ctypes.c_int32),
+                ("renormalise", ctypes.c_int32), ("x_dtype", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+class _ExpertDesc(ctypes.Structure):
+    _fields_ = [("struct_size", ctypes.c_int32), ("lmax", ctypes.c_int32), ("C", ctypes.c_int32),
+                ("experts", ctypes.c_int32), ("top_k", ctypes.c_int32), ("x_dtype", ctypes.c_int32),
+                ("out_dtype", ctypes.c_int32)]
 
 
 _lib = None
@@ -137,6 +165,23 @@ def load_library(path: str = LIB_PATH):
             lib.eqtp_attention_backward_workspace_bytes.restype = i64
             lib.eqtp_attention_backward.argtypes = [ap, i64, i64, i64] + [vp] * 16 + [i64, vp]
             lib.eqtp_attention_backward.restype = i32
+            bp, qp, rp, xp = (ctypes.POINTER(t) for t in (_BiasDesc, _QkNormDesc, _RouteDesc, _ExpertDesc))
+            for name, args, res in (
+                    ("eqtp_distance_bias", [bp, i64] + [vp] * 5, i32),
+                    ("eqtp_distance_bias_workspace_bytes", [bp, i64], i64),
+                    ("eqtp_distance_bias_backward", [bp, i64] + [vp] * 5 + [i64, vp], i32),
+                    ("eqtp_qk_norm", [qp, i64, i64] + [vp] * 10, i32),
+                    ("eqtp_qk_norm_workspace_bytes", [qp, i64, i64], i64),
+                    ("eqtp_qk_norm_backward", [qp, i64, i64] + [vp] * 16 + [i64, vp], i32),
+                    ("eqtp_route", [rp, i64] + [vp] * 5, i32),
+                    ("eqtp_route_backward", [rp, i64] + [vp] * 5, i32),
+                    ("eqtp_expert_plan_workspace_bytes", [i64, i32, i32], i64),
+                    ("eqtp_expert_plan", [i64, i32, i32] + [vp] * 5 + [i64, vp], i32),
+                    ("eqtp_expert_linear", [xp, i64] + [vp] * 7, i32),
+                    ("eqtp_expert_linear_backward_workspace_bytes", [xp, i64], i64),
+                    ("eqtp_expert_linear_backward", [xp, i64] + [vp] * 12 + [i64, vp], i32)):
+                getattr(lib, name).argtypes = args
+                getattr(lib, name).restype = res
             lib.eqtp_status_string.argtypes = [i32]
             lib.eqtp_status_string.restype = ctypes.c_char_p
             lib.eqtp_check_graph.argtypes = [i64, i64] + [vp] * 6
@@ -977,6 +1022,357 @@ def eqtp_attention_backward(q, k, v, src, row_ptr, lse, grad_out, src_ptr, dst_s
                                      workspace.numel() if workspace is not None else 0, _stream())
     _raise(rc, "eqtp_attention_backward")
     return gq, gk, gv, gb
+
+
+@functools.lru_cache(maxsize=256)
+def _bias_desc(heads, buckets, r_cut):
+    # read by the library during a call only, so one instance per distinct descriptor is shared
+    d = _BiasDesc(ctypes.sizeof(_BiasDesc), heads, buckets, r_cut)
+    need = load_library().eqtp_distance_bias_workspace_bytes(ctypes.byref(d), 0)  # checks the descriptor
+    if need < 0:
+        raise EqtpError(int(-need), "eqtp_bias_desc")
+    return ctypes.byref(d), d
+
+
+def _bias_args(vec, bounds, r_cut, heads):
+    torch = _torch()
+    _check(vec, "vec", torch.float32)
+    if vec.dim() != 2 or vec.shape[1] != 3:
+        raise ValueError("vec must be [E, 3]")
+    _check(bounds, "bounds", torch.float32)
+    if bounds.dim() != 1:
+        raise ValueError("bounds must be [B - 1]")
+    return _bias_desc(int(heads), bounds.shape[0] + 1, float(r_cut))[0], vec.shape[0], bounds.shape[0] + 1
+
+
+def eqtp_distance_bias(vec, bounds, table, r_cut: float = 0.0, out=None):
+    """out [E, H] = the row of ``table`` [B, H] that each edge's length |vec_e| falls into (see include/eqtp.h): the
+    number of ``bounds`` [B-1] (ascending) that are at most the length; -inf from ``r_cut`` on (0: no mask).  All
+    float32; the result is eqtp_attention's ``bias``."""
+    torch = _torch()
+    _check(table, "table", torch.float32)
+    if table.dim() != 2:
+        raise ValueError("table must be [B, H]")
+    d, E, B = _bias_args(vec, bounds, r_cut, table.shape[1])
+    if table.shape[0] != B:
+        raise ValueError("table has %d rows, %d bounds need %d" % (table.shape[0], B - 1, B))
+    if out is None:
+        out = torch.empty((E, table.shape[1]), dtype=torch.float32, device=vec.device)
+    else:
+        _check(out, "out", torch.float32, (E, table.shape[1]))
+    _raise(load_library().eqtp_distance_bias(d, E, _ptr(vec), _ptr(bounds), _ptr(table), _ptr(out), _stream()),
+           "eqtp_distance_bias")
+    return out
+
+
+def eqtp_distance_bias_workspace_bytes(E: int, heads: int, buckets: int) -> int:
+    """Device workspace eqtp_distance_bias_backward needs (bytes)."""
+    n = load_library().eqtp_distance_bias_workspace_bytes(_bias_desc(int(heads), int(buckets), 0.0)[0], E)
+    if n < 0:
+        raise EqtpError(int(-n), "eqtp_distance_bias_workspace_bytes")
+    return int(n)
+
+
+def eqtp_distance_bias_backward(vec, bounds, grad_bias, r_cut: float = 0.0, workspace=None):
+    """grad_table [B, H] of eqtp_distance_bias from grad_bias [E, H] float32.  ``workspace``: a uint8 tensor of at
+    least eqtp_distance_bias_workspace_bytes bytes, or None to allocate one."""
+    torch = _torch()
+    _check(grad_bias, "grad_bias", torch.float32)
+    if grad_bias.dim() != 2:
+        raise ValueError("grad_bias must be [E, H]")
+    heads = grad_bias.shape[1]
+    d, E, B = _bias_args(vec, bounds, r_cut, heads)
+    _check(grad_bias, "grad_bias", torch.float32, (E, heads))
+    grad_table = torch.empty((B, heads), dtype=torch.float32, device=vec.device)
+    lib = load_library()
+    workspace = _workspace(workspace, lib.eqtp_distance_bias_workspace_bytes(d, E), vec.device)
+    rc = lib.eqtp_distance_bias_backward(d, E, _ptr(vec), _ptr(bounds), _ptr(grad_bias), _ptr(grad_table),
+                                         _ptr(workspace), workspace.numel(), _stream())
+    _raise(rc, "eqtp_distance_bias_backward")
+    return grad_table
+
+
+@functools.lru_cache(maxsize=256)
+def _qk_norm_desc(lmax, C, heads, kv_heads, x_dtype, axes, pairs, eps):
+    # read by the library during a call only, so one instance per distinct descriptor is shared
+    d = _QkNormDesc(ctypes.sizeof(_QkNormDesc), lmax, C, heads, kv_heads, x_dtype, axes, pairs, eps)
+    need = load_library().eqtp_qk_norm_workspace_bytes(ctypes.byref(d), 0, 0)  # checks the descriptor
+    if need < 0:
+        raise EqtpError(int(-need), "eqtp_qk_norm_desc")
+    return ctypes.byref(d), d
+
+
+def _qk_norm_args(q, k, lmax, heads, weight_q, weight_k, pos_q, pos_k, freq, eps):
+    """Checks the tensors; returns (descriptor, N, M, positions of k)."""
+    torch = _torch()
+    code, N, C = _rows(q, "q", lmax)
+    kcode, M, Ck = _rows(k, "k", lmax)
+    if kcode != code:
+        raise TypeError("q and k must have the same type")
+    if heads <= 0 or C % heads != 0 or C == 0:
+        raise ValueError("heads must divide the %d channels of q" % C)
+    width = C // heads
+    if Ck == 0 or Ck % width != 0:
+        raise ValueError("k has %d channels: it needs heads of %d channels" % (Ck, width))
+    for w, name in ((weight_q, "weight_q"), (weight_k, "weight_k")):
+        if w is not None:
+            _check(w, name, torch.float32, (lmax + 1, width))
+    axes = pairs = 0
+    if freq is not None:
+        _check(freq, "freq", torch.float32)
+        if freq.dim() != 2:
+            raise ValueError("freq must be [axes, pairs]")
+        axes, pairs = freq.shape
+        if pos_k is None and M == N:
+            pos_k = pos_q
+        _check(pos_q, "pos_q", torch.float32, (N, axes))
+        _check(pos_k, "pos_k", torch.float32, (M, axes))
+    elif pos_q is not None or pos_k is not None:
+        raise ValueError("positions need freq")
+    return _qk_norm_desc(lmax, C, heads, Ck // width, code, axes, pairs, float(eps))[0], N, M, pos_k
+
+
+def eqtp_qk_norm(q, k, lmax: int, heads: int, weight_q=None, weight_k=None, pos_q=None, pos_k=None, freq=None,
+                 eps: float = 1e-5, out_q=None, out_k=None):
+    """(out_q, out_k): queries and keys normed by head and degree and turned by position, in one pass (see
+    include/eqtp.h).
+
+    q [N, C, K], k [M, Ck, K] float32 or bfloat16 ([N, C] and [M, Ck] at lmax 0); Ck is a number of heads of q's
+    width.  ``weight_q``, ``weight_k`` [lmax+1, C/heads] float32.  ``freq`` [axes, pairs] float32 with ``pos_q``
+    [N, axes] and ``pos_k`` [M, axes] (pos_q by default where M = N), or None: no rotation.  ``out_q`` and ``out_k``
+    may be q and k."""
+    torch = _torch()
+    d, N, M, pos_k = _qk_norm_args(q, k, lmax, heads, weight_q, weight_k, pos_q, pos_k, freq, eps)
+    if out_q is None:
+        out_q = torch.empty_like(q)
+    else:
+        _check(out_q, "out_q", q.dtype, q.shape)
+    if out_k is None:
+        out_k = torch.empty_like(k)
+    else:
+        _check(out_k, "out_k", k.dtype, k.shape)
+    rc = load_library().eqtp_qk_norm(d, N, M, _ptr(q), _ptr(k), _ptr(weight_q), _ptr(weight_k), _ptr(pos_q), _ptr(pos_k),
+                                     _ptr(freq), _ptr(out_q), _ptr(out_k), _stream())
+    _raise(rc, "eqtp_qk_norm")
+    return out_q, out_k
+
+
+def eqtp_qk_norm_workspace_bytes(N: int, M: int, lmax: int, C: int, heads: int, kv_heads: int = None) -> int:
+    """Device workspace eqtp_qk_norm_backward needs for the gradients of the weights (bytes)."""
+    d = _qk_norm_desc(lmax, C, heads, heads if kv_heads is None else kv_heads, EQTP_F32, 0, 0, 1e-5)[0]
+    n = load_library().eqtp_qk_norm_workspace_bytes(d, N, M)
+    if n < 0:
+        raise EqtpError(int(-n), "eqtp_qk_norm_workspace_bytes")
+    return int(n)
+
+
+def eqtp_qk_norm_backward(q, k, grad_out_q, grad_out_k, lmax: int, heads: int, weight_q=None, weight_k=None, pos_q=None,
+                          pos_k=None, freq=None, eps: float = 1e-5, need_q: bool = True, need_k: bool = True,
+                          need_weight_q: bool = True, need_weight_k: bool = True, need_pos: bool = False,
+                          workspace=None):
+    """(grad_q, grad_k, grad_weight_q, grad_weight_k, grad_pos_q, grad_pos_k) of eqtp_qk_norm, each None if not asked
+    for.  A gradient of an output may be None: then nothing of its side is computed (its gradients are None).  ``workspace``: a uint8 tensor of at least
+    eqtp_qk_norm_workspace_bytes bytes, or None to allocate one if it is needed."""
+    torch = _torch()
+    d, N, M, pos_k = _qk_norm_args(q, k, lmax, heads, weight_q, weight_k, pos_q, pos_k, freq, eps)
+    if need_pos and freq is None:
+        raise ValueError("gradients of positions need freq")
+    sides = []
+    for x, g, name, need, need_w, pos in ((q, grad_out_q, "grad_out_q", need_q, need_weight_q, pos_q),
+                                          (k, grad_out_k, "grad_out_k", need_k, need_weight_k, pos_k)):
+        if g is None:
+            sides.append((None, None, None))
+            continue
+        _check(g, name, x.dtype, x.shape)
+        sides.append((torch.empty_like(x) if need else None,
+                      torch.empty((lmax + 1, q.shape[1] // heads), dtype=torch.float32, device=q.device) if need_w else None,
+                      torch.empty_like(pos) if need_pos else None))
+    (gq, gwq, gpq), (gk, gwk, gpk) = sides
+    lib = load_library()
+    if gwq is not None or gwk is not None:
+        workspace = _workspace(workspace, max(16, lib.eqtp_qk_norm_workspace_bytes(d, N, M)), q.device)
+    rc = lib.eqtp_qk_norm_backward(d, N, M, _ptr(q), _ptr(k), _ptr(weight_q), _ptr(weight_k), _ptr(pos_q), _ptr(pos_k),
+                                   _ptr(freq), _ptr(grad_out_q), _ptr(grad_out_k), _ptr(gq), _ptr(gk), _ptr(gwq),
+                                   _ptr(gwk), _ptr(gpq), _ptr(gpk), _ptr(workspace),
+                                   workspace.numel() if workspace is not None else 0, _stream())
+    _raise(rc, "eqtp_qk_norm_backward")
+    return gq, gk, gwq, gwk, gpq, gpk
+
+
+@functools.lru_cache(maxsize=256)
+def _route_desc(experts, top_k, groups, top_groups, score, renormalise, x_dtype, scale):
+    # read by the library during a call only, so one instance per distinct descriptor is shared
+    d = _RouteDesc(ctypes.sizeof(_RouteDesc), experts, top_k, groups, top_groups, score, renormalise, x_dtype, scale)
+    _raise(load_library().eqtp_route(ctypes.byref(d), 0, None, None, None, None, None), "eqtp_route_desc")  # checks it
+    return ctypes.byref(d), d
+
+
+def _logits(logits):
+    torch = _torch()
+    code = EQTP_BF16 if logits.dtype is torch.bfloat16 else EQTP_F32
+    _check(logits, "logits", torch.bfloat16 if code == EQTP_BF16 else torch.float32)
+    if logits.dim() != 2:
+        raise ValueError("logits must be [N, X]")
+    return code, logits.shape[0], logits.shape[1]
+
+
+def eqtp_route(logits, top_k: int, score: int = EQTP_SCORE_SOFTMAX, bias=None, groups: int = 1, top_groups: int = None,
+               renormalise: bool = True, scale: float = 1.0, idx=None, weight=None):
+    """(idx [N, top_k] int32, weight [N, top_k] float32): each node's experts in descending order and their weights
+    (see include/eqtp.h).  ``logits`` [N, X] float32 or bfloat16; ``bias`` [X] float32 steers the choice only;
+    ``top_groups`` of ``groups`` groups of consecutive experts stay open (all by default)."""
+    torch = _torch()
+    code, N, X = _logits(logits)
+    if bias is not None:
+        _check(bias, "bias", torch.float32, (X,))
+    d, _ = _route_desc(X, int(top_k), int(groups), int(groups if top_groups is None else top_groups), int(score),
+                       int(bool(renormalise)), code, float(scale))
+    if idx is None:
+        idx = torch.empty((N, top_k), dtype=torch.int32, device=logits.device)
+    else:
+        _check(idx, "idx", torch.int32, (N, top_k))
+    if weight is None:
+        weight = torch.empty((N, top_k), dtype=torch.float32, device=logits.device)
+    else:
+        _check(weight, "weight", torch.float32, (N, top_k))
+    _raise(load_library().eqtp_route(d, N, _ptr(logits), _ptr(bias), _ptr(idx), _ptr(weight), _stream()), "eqtp_route")
+    return idx, weight
+
+
+def eqtp_route_backward(logits, idx, grad_weight, score: int = EQTP_SCORE_SOFTMAX, renormalise: bool = True,
+                        scale: float = 1.0):
+    """grad_logits [N, X] (logits' type) of eqtp_route's weights, its choice ``idx`` [N, top_k] held fixed."""
+    torch = _torch()
+    code, N, X = _logits(logits)
+    if idx.dim() != 2:
+        raise ValueError("idx must be [N, top_k]")
+    top_k = idx.shape[1]
+    _check(idx, "idx", torch.int32, (N, top_k))
+    _check(grad_weight, "grad_weight", torch.float32, (N, top_k))
+    d, _ = _route_desc(X, top_k, 1, 1, int(score), int(bool(renormalise)), code, float(scale))
+    out = torch.empty_like(logits)
+    _raise(load_library().eqtp_route_backward(d, N, _ptr(logits), _ptr(idx), _ptr(grad_weight), _ptr(out), _stream()),
+           "eqtp_route_backward")
+    return out
+
+
+def _choice(idx):
+    _check(idx, "idx", _torch().int32)
+    if idx.dim() != 2:
+        raise ValueError("idx must be [N, top_k]")
+    return idx.shape
+
+
+def eqtp_expert_plan_workspace_bytes(N: int, top_k: int, experts: int) -> int:
+    """Device workspace eqtp_expert_plan needs (bytes)."""
+    n = load_library().eqtp_expert_plan_workspace_bytes(N, top_k, experts)
+    if n < 0:
+        raise EqtpError(int(-n), "eqtp_expert_plan_workspace_bytes")
+    return int(n)
+
+
+def eqtp_expert_plan(idx, experts: int, workspace=None):
+    """(order [N], slots [N top_k], ptr [experts+1]) int32: a routing grouped by expert (see include/eqtp.h), for
+    eqtp_expert_linear and its backward call; made once, it serves every layer that uses the routing.  Differences of
+    ptr are the experts' loads.  With top_k = 1, order is slots."""
+    torch = _torch()
+    N, top_k = _choice(idx)
+    need = eqtp_expert_plan_workspace_bytes(N, top_k, experts)
+    slots = torch.empty(N * top_k, dtype=torch.int32, device=idx.device)
+    order = slots if top_k == 1 else torch.empty(N, dtype=torch.int32, device=idx.device)
+    ptr = torch.empty(experts + 1, dtype=torch.int32, device=idx.device)
+    workspace = _workspace(workspace, need, idx.device)
+    rc = load_library().eqtp_expert_plan(N, top_k, experts, _ptr(idx), None if top_k == 1 else _ptr(order), _ptr(slots),
+                                         _ptr(ptr), _ptr(workspace), workspace.numel(), _stream())
+    _raise(rc, "eqtp_expert_plan")
+    return order, slots, ptr
+
+
+@functools.lru_cache(maxsize=256)
+def _expert_desc(lmax, C, experts, top_k, x_dtype, out_dtype):
+    # read by the library during a call only, so one instance per distinct descriptor is shared
+    d = _ExpertDesc(ctypes.sizeof(_ExpertDesc), lmax, C, experts, top_k, x_dtype, out_dtype)
+    need = load_library().eqtp_expert_linear_backward_workspace_bytes(ctypes.byref(d), 0)  # checks the descriptor
+    if need < 0:
+        raise EqtpError(int(-need), "eqtp_expert_desc")
+    return ctypes.byref(d), d
+
+
+def _expert_args(h, W, idx, lmax, weight, plan, out_dtype):
+    """Checks the tensors; returns (descriptor, N, order, slots, ptr)."""
+    torch = _torch()
+    code, N, C = _rows(h, "h", lmax)
+    _check(W, "W", h.dtype)
+    if W.dim() != 4 or W.shape[1:] != (lmax + 1, C, C):
+        raise ValueError("W must be [experts, %d, %d, %d]" % (lmax + 1, C, C))
+    X = W.shape[0]
+    rows, top_k = _choice(idx)
+    if rows != N:
+        raise ValueError("idx has %d rows, h %d" % (rows, N))
+    if weight is not None:
+        _check(weight, "weight", torch.float32, (N, top_k))
+    order = slots = ptr = None
+    if plan is not None:
+        order, slots, ptr = plan
+        _check(order, "order", torch.int32, (N,))
+        _check(slots, "slots", torch.int32, (N * top_k,))
+        _check(ptr, "ptr", torch.int32, (X + 1,))
+    ocode = code if out_dtype is None else out_dtype
+    _torch_dtype(ocode)
+    return _expert_desc(lmax, C, X, top_k, code, ocode)[0], N, order, slots, ptr
+
+
+def eqtp_expert_linear(h, W, idx, lmax: int, weight=None, plan=None, out_dtype: int = None, out=None):
+    """out [N, C, K]: per-degree channel linears by expert, each node's summed under ``weight`` (see include/eqtp.h).
+
+    h [N, C, K], W [X, lmax+1, C, C] float32 or bfloat16 (C = 8, 16, 32, 64 or 128); ``idx`` [N, top_k] int32, outside
+    [0, X) for none; ``weight`` [N, top_k] float32 or None (ones).  ``plan``: eqtp_expert_plan's result, which only
+    makes it faster, or None.  ``out_dtype``: EQTP_F32 or EQTP_BF16 (h's by default)."""
+    torch = _torch()
+    d, N, order, _, _ = _expert_args(h, W, idx, lmax, weight, plan, out_dtype)
+    odt = h.dtype if out_dtype is None else _torch_dtype(out_dtype)
+    if out is None:
+        out = torch.empty_like(h, dtype=odt)
+    else:
+        _check(out, "out", odt, h.shape)
+    _raise(load_library().eqtp_expert_linear(d, N, _ptr(h), _ptr(W), _ptr(idx), _ptr(weight), _ptr(order), _ptr(out),
+                                             _stream()), "eqtp_expert_linear")
+    return out
+
+
+def eqtp_expert_linear_backward_workspace_bytes(N: int, lmax: int, C: int, experts: int, top_k: int,
+                                                x_dtype: int = EQTP_F32) -> int:
+    """Device workspace eqtp_expert_linear_backward needs (bytes)."""
+    n = load_library().eqtp_expert_linear_backward_workspace_bytes(
+        _expert_desc(lmax, C, experts, top_k, x_dtype, x_dtype)[0], N)
+    if n < 0:
+        raise EqtpError(int(-n), "eqtp_expert_linear_backward_workspace_bytes")
+    return int(n)
+
+
+def eqtp_expert_linear_backward(h, W, idx, grad_out, lmax: int, weight=None, plan=None, need_h: bool = True,
+                                need_W: bool = True, need_weight: bool = None, workspace=None):
+    """(grad_h, grad_W float32, grad_weight) of eqtp_expert_linear, each None if not asked for; ``grad_out`` [N, C, K]
+    in h's type.  ``need_weight`` defaults to whether a weight is given.  ``plan``: eqtp_expert_plan's result, made
+    here if it is None and grad_W is asked for.  ``workspace``: a uint8 tensor of at least
+    eqtp_expert_linear_backward_workspace_bytes bytes, or None to allocate one."""
+    torch = _torch()
+    if plan is None and need_W:
+        plan = eqtp_expert_plan(idx, W.shape[0])
+    d, N, order, slots, ptr = _expert_args(h, W, idx, lmax, weight, plan, None)
+    _check(grad_out, "grad_out", h.dtype, h.shape)
+    if need_weight is None:
+        need_weight = weight is not None
+    gh = torch.empty_like(h) if need_h else None
+    gW = torch.empty(W.shape, dtype=torch.float32, device=h.device) if need_W else None
+    gw = torch.empty(idx.shape, dtype=torch.float32, device=h.device) if need_weight else None
+    lib = load_library()
+    workspace = _workspace(workspace, lib.eqtp_expert_linear_backward_workspace_bytes(d, N), h.device)
+    rc = lib.eqtp_expert_linear_backward(d, N, _ptr(h), _ptr(W), _ptr(idx), _ptr(weight), _ptr(order), _ptr(slots),
+                                         _ptr(ptr), _ptr(grad_out), _ptr(gh), _ptr(gW), _ptr(gw), _ptr(workspace),
+                                         workspace.numel(), _stream())
+    _raise(rc, "eqtp_expert_linear_backward")
+    return gh, gW, gw
 
 
 def eqtp_test_segment_probe(row_ptr, src, C: int, lmax: int, algo: int = EQTP_ALGO_NODE_MFMA):

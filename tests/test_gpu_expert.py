@@ -1,0 +1,171 @@
+"""The experts' per-degree linears on the GPU, and the plan of a routing, against
+the 64-bit statements, within bounds derived in mix_reference."""
+import numpy as np
+import pytest
+
+import mix_reference as ref
+from test_gpu_norm import _code, _get, _put, _within
+from test_gpu_parity import _eq, _say
+
+pytestmark = pytest.mark.gpu
+
+
+class Mix:
+    def __init__(self, N, C, lmax, X, k, x="f32", gates=True, seed=0, holes=True):
+        import torch
+
+        r = np.random.default_rng(seed)
+        K = (lmax + 1) ** 2
+        self.N, self.C, self.lmax, self.X, self.k, self.x, self.gates = N, C, lmax, X, k, x, gates
+        self.h, self.g = (_put(r.standard_normal((N, C, K)), x) for _ in range(2))
+        self.W = _put(r.standard_normal((X, lmax + 1, C, C)) / np.sqrt(C), x)
+        self.idx = r.integers(-1 if holes else 0, X + (1 if holes else 0), (N, k)).astype(np.int32)  # some outside
+        if X > 2:
+            self.idx[self.idx == 1] = 2  # an expert that nobody has
+        self.w = _put(r.uniform(0.1, 1.0, (N, k))) if gates else (None, None)
+        self.ti = torch.from_numpy(self.idx).cuda()
+
+    def check(self, eq, plan, out="f32"):
+        o = eq.eqtp_expert_linear(self.h[0], self.W[0], self.ti, self.lmax, weight=self.w[0], plan=plan, out_dtype=_code(eq, out))
+        want, size = ref.expert(self.h[1], self.W[1], self.idx, self.lmax, self.w[1])
+        half = ref.U16 if out == "bf16" else ref.U32
+        _within(_get(o), want, ref.expert_bound(want, size, self.C, self.k, half), "out")
+        grads = self.grads(eq, plan)
+        wants, bounds = ref.expert_backward(self.h[1], self.W[1], self.idx, self.g[1], self.lmax, self.w[1], self.x == "bf16")
+        for t, w, b, name in zip(grads, wants, bounds, ("grad_h", "grad_W", "grad_weight")):
+            _within(_get(t), w, b, name)
+        return o, grads
+
+    def grads(self, eq, plan, **kw):
+        return eq.eqtp_expert_linear_backward(self.h[0], self.W[0], self.ti, self.g[0], self.lmax, weight=self.w[0], plan=plan,
+                                              **dict(dict(need_weight=True), **kw))
+
+
+@pytest.mark.parametrize("x", ["f32", "bf16"])
+@pytest.mark.parametrize("N,C,lmax,X,k,gates", [
+    (1, 64, 3, 8, 2, True), (1, 8, 0, 1, 1, False), (16, 16, 1, 3, 1, False), (17, 32, 2, 4, 2, True), (50, 64, 3, 10, 1, False),
+    (33, 128, 3, 5, 2, True), (40, 32, 3, 8, 4, True), (12, 8, 4, 6, 3, True), (9, 16, 6, 3, 2, True), (5, 128, 6, 2, 2, True),
+    (7, 64, 5, 40, 3, True), (300, 16, 0, 256, 4, True), (100, 128, 0, 2, 1, True), (64, 32, 1, 33, 16, True),
+    (70, 8, 3, 4, 2, False)])
+def test_expert_linear(N, C, lmax, X, k, gates, x):
+    eq = _eq()
+    _say("experts N=%d C=%d lmax=%d X=%d k=%d %s" % (N, C, lmax, X, k, x))
+    import torch
+
+    m = Mix(N, C, lmax, X, k, x, gates, seed=N + C)
+    plan = eq.eqtp_expert_plan(m.ti, X)
+    o, grads = m.check(eq, plan, out="bf16" if x == "bf16" and lmax == 3 else "f32")
+    # without a plan, and in another order: the same bits
+    p = eq.eqtp_expert_linear(m.h[0], m.W[0], m.ti, lmax, weight=m.w[0], out=torch.empty_like(o),
+                              out_dtype=_code(eq, "bf16" if o.dtype == torch.bfloat16 else "f32"))
+    assert torch.equal(o, p)
+    back = (torch.arange(N - 1, -1, -1, dtype=torch.int32, device="cuda"),) + plan[1:]
+    for a, b in zip(grads, m.grads(eq, back)):
+        assert torch.equal(a, b)
+
+
+def _plan_want(idx, X):
+    flat = np.where((idx >= 0) & (idx < X), idx, X).reshape(-1)
+    slots = np.argsort(flat, kind="stable")
+    return slots, np.searchsorted(flat[slots], np.arange(X + 1))
+
+
+@pytest.mark.parametrize("N,k,X", [(0, 2, 4), (1, 1, 1), (1, 16, 256), (255, 1, 7), (256, 2, 8), (1000, 2, 31), (3000, 3, 32),
+                                   (20011, 2, 64), (50000, 1, 256), (5, 4, 2)])
+def test_expert_plan(N, k, X):
+    eq = _eq()
+    _say("expert plan N=%d k=%d X=%d" % (N, k, X))
+    import torch
+
+    idx = np.random.default_rng(N + k).integers(-2, X + 2, (N, k)).astype(np.int32)
+    order, slots, ptr = (t.cpu().numpy() for t in eq.eqtp_expert_plan(torch.from_numpy(idx).cuda(), X))
+    want, ends = _plan_want(idx, X)
+    np.testing.assert_array_equal(slots, want)
+    np.testing.assert_array_equal(ptr, ends)
+    np.testing.assert_array_equal(np.sort(order), np.arange(N))
+    if k > 1 and N:  # nodes by their lowest expert, and by the next one where the bins tell them apart
+        e = np.sort(np.where((idx >= 0) & (idx < X), idx, X), axis=1)[order]
+        assert (np.diff(e[:, 0]) >= 0).all()
+        if (X + 1) ** 2 <= 1024:
+            second = np.array([min([v for v in row if v > row[0]], default=X) for row in e])
+            same = np.diff(e[:, 0]) == 0
+            assert (np.diff(second)[same] >= 0).all()
+
+
+@pytest.mark.parametrize("x", ["f32", "bf16"])
+def test_expert_same_index_twice(x):
+    """The same expert twice in a node's list adds its weights; both places get their gradient."""
+    eq = _eq()
+    _say("experts, the same twice, %s" % x)
+    m = Mix(20, 32, 2, 3, 3, x, True, seed=2)
+    import torch
+
+    m.idx[:] = np.array([2, 2, 0])
+    m.idx[5] = [1, 1, 1]
+    m.ti = torch.from_numpy(m.idx).cuda()
+    m.check(eq, eq.eqtp_expert_plan(m.ti, 3))
+
+
+def test_expert_nobody():
+    """Nodes without an expert: zeros, whatever the features hold; a NaN stays in its own node."""
+    eq = _eq()
+    _say("experts, nobody")
+    import torch
+
+    m = Mix(40, 16, 3, 4, 2, "f32", True, seed=4, holes=False)
+    m.ti[::2] = -1
+    m.ti[1::4] = 9
+    h = m.h[0].clone()
+    h[0], h[3] = float("nan"), float("inf")
+    m.ti[3] = 1
+    plan = eq.eqtp_expert_plan(m.ti, 4)
+    out = eq.eqtp_expert_linear(h, m.W[0], m.ti, 3, weight=m.w[0], plan=plan)
+    assert (out[::2] == 0).all() and (out[1::4] == 0).all() and not torch.isfinite(out[3]).any()
+    assert torch.isfinite(out[4:]).all() and torch.isfinite(out[:3]).all()
+    m.ti[:] = -1
+    gh, gW, gw = m.grads(eq, eq.eqtp_expert_plan(m.ti, 4))
+    assert (gh == 0).all() and (gW == 0).all() and (gw == 0).all()
+
+
+@pytest.mark.parametrize("x", ["f32", "bf16"])
+def test_expert_many_places(x):
+    """Several chunks of an expert's places, summed in a fixed order."""
+    eq = _eq()
+    _say("experts, many places, %s" % x)
+    import torch
+
+    m = Mix(1500, 8, 1, 3, 2, x, True, seed=6)
+    plan = eq.eqtp_expert_plan(m.ti, 3)
+    _, grads = m.check(eq, plan)
+    for a, b in zip(grads, m.grads(eq, plan)):
+        assert torch.equal(a, b)
+    few = m.grads(eq, None, need_h=False)
+    assert few[0] is None and torch.equal(few[1], grads[1]) and torch.equal(few[2], grads[2])
+    few = m.grads(eq, None, need_W=False, need_weight=False)
+    assert few[1] is None and few[2] is None and torch.equal(few[0], grads[0])
+
+
+@pytest.mark.parametrize("x", ["f32", "bf16"])
+def test_expert_is_the_linear(x):
+    """One expert without weights is the per-degree linear."""
+    eq = _eq()
+    _say("experts as the linear, %s" % x)
+    import torch
+
+    r = np.random.default_rng(5)
+    h, W = _put(r.standard_normal((45, 64, 16)), x), _put(r.standard_normal((1, 4, 64, 64)) / 8, x)
+    idx = torch.zeros((45, 1), dtype=torch.int32, device="cuda")
+    a = eq.eqtp_expert_linear(h[0], W[0], idx, 3, out_dtype=eq.EQTP_F32)
+    b = eq.eqtp_linear(h[0], W[0][0].contiguous(), 3, _code(eq, x))
+    want, size = ref.expert(h[1], W[1], np.zeros((45, 1), int), 3)
+    _within(_get(a), _get(b), 2 * ref.expert_bound(want, size, 64, 1, ref.U32), "out")
+
+
+def test_expert_empty():
+    eq = _eq()
+    _say("experts, no nodes")
+    m = Mix(0, 16, 1, 3, 2, "f32", True)
+    plan = eq.eqtp_expert_plan(m.ti, 3)
+    assert eq.eqtp_expert_linear(m.h[0], m.W[0], m.ti, 1, weight=m.w[0], plan=plan).shape == (0, 16, 4)
+    gh, gW, gw = m.grads(eq, plan)
+    assert gh.shape == (0, 16, 4) and (gW == 0).all() and gw.shape == (0, 2)
