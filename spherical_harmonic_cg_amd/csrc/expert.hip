@@ -5,46 +5,31 @@
 //   grad_weight[n, j] = sum_{c, l m} (W^T g)[n, c, l m] h[n, c, l m].
 //
 // Bytes per node: its features once in, once out; flops 2 k C^2 K.  A workgroup
-// takes 16 nodes, stages their features in LDS as planes [component][node][channel] and goes over the experts
-// that any of the 16 has: for each, 16x16 products D[c'][node] on the matrix
-// cores (bf16 operands, or fp32), then total += gate D in the lanes of the
-// nodes that have it.  Nodes in an order in which neighbours share experts
-// (expert_plan.hip) keep that list short; the results do not depend on the
-// order: a node adds its experts in ascending order whatever the others have.
-// A wave keeps a tile of 16 output channels, so each weight is read once a
-// workgroup, from the L2, straight into the operand's registers.  Totals leave
-// through LDS in the features' layout.
+// takes 16 nodes, a wave of it a group of NP components (16 bytes of a channel)
+// and a share of the output channels.  A 16x16 product D[c'][node] of one
+// component wants, in lane (node i, k), the component's values of 4 (fp32) or
+// 8 (bf16) input channels.  The lane reads those channels' 16-byte runs of
+// components, so its registers hold the operands of NP products, in fp32 as
+// they are, in bf16 after a transposition within the lane; D holds NP
+// components of four output channels of the lane's node, which leave as runs.
+// No LDS, no barriers: waves are on their own.
+//
+// The wave goes over the experts that any of the 16 nodes has, in ascending order: total += gate D in the
+// lanes of the nodes that have it.  Nodes in an order in which neighbours share
+// experts (expert_plan.hip) keep that list short; the results do not depend on
+// it.  Weights come from the L2, each once a wave and expert.
 #include <type_traits>
 
 #include "expert_device.hpp"
 
 namespace eqtp {
 
-template <class S, int C>
-struct ExpertCfg {
-  static constexpr bool BF16 = std::is_same<S, __bf16>::value;
-  static constexpr int PAD = BF16 ? 8 : 4;
-  static constexpr int RS = C + PAD;                       // row stride of a plane (elements)
-  static constexpr int ES = (int)sizeof(S);
-  static constexpr int PLANE = kTile * RS + 16 / ES;       // 16 rows and 16 bytes, which spread the planes over the banks
-  static constexpr int WAVES = expert_threads(C) / 64;
-  static constexpr int CT = (C + 15) / 16;                 // tiles of output channels
-  static constexpr int PG = WAVES / CT > 0 ? WAVES / CT : 1;  // waves that share a tile of channels: parts of the planes
-  static constexpr int PPW = kMaxPlanes / PG;              // planes of a wave at most
-  static constexpr int KS = BF16 ? (C + 31) / 32 : (C + 15) / 16;  // steps over the input channels
-  static size_t lds_bytes(int planes) {
-    const size_t in = (size_t)planes * PLANE * ES, out = (size_t)kTile * (C * planes + 4) * 4;
-    return in > out ? in : out;
-  }
-};
-
 template <class S>
 struct Operand;
 template <>
 struct Operand<__bf16> {
   typedef bf16x8 V;
-  static constexpr int N = 8;
-  static __device__ __forceinline__ V zero() { return V{}; }
+  static constexpr int N = 8;  // input channels of a lane and step
   static __device__ __forceinline__ f4 mul(const V& a, const V& b, const f4& c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
   }
@@ -53,7 +38,6 @@ template <>
 struct Operand<float> {
   typedef f4 V;
   static constexpr int N = 4;
-  static __device__ __forceinline__ V zero() { return V{0.f, 0.f, 0.f, 0.f}; }
   static __device__ __forceinline__ f4 mul(const V& a, const V& b, f4 c) {
 #pragma unroll
     for (int s = 0; s < 4; ++s) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[s], b[s], c, 0, 0, 0);
@@ -61,159 +45,182 @@ struct Operand<float> {
   }
 };
 
-template <class S, int C, bool DOT>
-__global__ __launch_bounds__(expert_threads(C)) void expert_kernel(ExpertArgs a) {
-  using Cfg = ExpertCfg<S, C>;
+// smallest of v over the wave
+__device__ __forceinline__ int wave_min(int v) {
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) v = min(v, __shfl_xor(v, o, 64));
+  return __builtin_amdgcn_readfirstlane(v);
+}
+
+constexpr int kListed = kMaxTopK / 4;  // places of a node's list that a lane holds (lane (i, k): k, k + 4, ..)
+
+template <class S, int C, int NP, int CTW, bool DOT>
+__global__ __launch_bounds__(256) void expert_kernel(ExpertArgs a, int groups) {
   using Op = Operand<S>;
   typedef typename Op::V V;
-  constexpr int TH = 64 * Cfg::WAVES;
-  extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
-  __shared__ int node[kTile];
-  __shared__ int expert[kTile][kMaxTopK];
-  __shared__ float gate[kTile][kMaxTopK];
-  __shared__ unsigned met[kMaxExperts / 32];
-  __shared__ float dots[DOT ? Cfg::WAVES : 1][kTile][kMaxTopK];
-  S* hT = reinterpret_cast<S*>(lds);
-  float* ot = reinterpret_cast<float*>(lds);
-  const int tid = threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6);
+  typedef Run<S, NP> In;
+  constexpr int CT = (C + 15) / 16, CS = CT / CTW;
+  constexpr int STEP = 4 * Op::N;                       // input channels of a step
+  constexpr int NS = (C + STEP - 1) / STEP;
+  __shared__ float dots[DOT ? 4 : 1][kTile][kMaxTopK];
+  const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
   const int i16 = lane & 15, kq = lane >> 4;
-  const int ct = wv % Cfg::CT, pg = wv / Cfg::CT;
   const int K = num_comp(a.lmax);
   const int64_t p0 = (int64_t)blockIdx.x * kTile;
   const int nv = (int)min((int64_t)kTile, a.N - p0);
-
-  // the nodes of the tile, their experts and gates, and the experts that any of them has
-  if (tid < kTile) {
-    const int64_t p = p0 + tid;
-    node[tid] = tid < nv ? (a.order ? clamp_index(a.order[p], (int)a.N) : (int)p) : -1;
-  }
-  if (tid < kMaxExperts / 32) met[tid] = 0u;
-  if constexpr (DOT)
-    for (int i = tid; i < Cfg::WAVES * kTile * kMaxTopK; i += TH) (&dots[0][0][0])[i] = 0.0f;
-  __syncthreads();
-  for (int i = tid; i < kTile * a.k; i += TH) {
-    const int r = i / a.k, j = i - r * a.k;
-    int e = -1;
-    float w = 0.0f;
-    if (r < nv) {
-      const int64_t s = (int64_t)node[r] * a.k + j;
-      e = a.idx[s];
-      if (e < 0 || e >= a.X) e = -1;
-      w = a.weight ? a.weight[s] : 1.0f;
-      if (e >= 0) atomicOr(&met[e >> 5], 1u << (e & 31));
+  const int64_t p = p0 + min(i16, nv - 1);
+  const int64_t node = a.order ? clamp_index(a.order[p], (int)a.N) : p;
+  int ex[kListed];
+  float gate[kListed];
+#pragma unroll
+  for (int i = 0; i < kListed; ++i) {
+    const int j = kq + 4 * i;
+    ex[i] = kMaxExperts;
+    gate[i] = 0.0f;
+    if (j < a.k && i16 < nv) {
+      const int e = a.idx[node * a.k + j];
+      ex[i] = e >= 0 && e < a.X ? e : kMaxExperts;
+      gate[i] = a.weight ? a.weight[node * a.k + j] : 1.0f;
     }
-    expert[r][j] = e;
-    gate[r][j] = w;
+  }
+  if constexpr (DOT) {
+    for (int i = lane; i < kTile * kMaxTopK; i += 64) (&dots[wv][0][0])[i] = 0.0f;
+    wave_lds_sync();
   }
 
-  for (int st = 0; st < stretches_of(a.lmax); ++st) {
-    const int m0 = stretch_first(st), np = stretch_planes(st, a.lmax);
-    __syncthreads();
-    // stage the features: (node, channel) rows of np components
-    for (int i = tid; i < kTile * C; i += TH) {
-      const int r = i / C, c = i - r * C;
-      const S* src = static_cast<const S*>(a.h) + ((int64_t)(r < nv ? node[r] : 0) * C + c) * K + m0;
-      for (int m = 0; m < np; ++m) hT[m * Cfg::PLANE + r * Cfg::RS + c] = r < nv ? src[m] : (S)0.0f;
-    }
-    __syncthreads();
-    const int share = (np + Cfg::PG - 1) / Cfg::PG;
-    const int first = pg * share, mine = min(share, np - first);  // this wave's planes
-    f4 total[Cfg::PPW];
-    float held[DOT ? Cfg::PPW : 1][4];
+  for (int task = wv; task < groups * CS; task += waves) {
+    const int g = task / CS, ct0 = (task - g * CS) * CTW;
+    const int m0 = group_first(g, K, NP), dup = g * NP - m0;  // components below dup are the group before's, too
+    // operands: B[s][p] holds this node's component m0 + p of the lane's channels of step s
+    V B[NS][NP];
+    const S* row = static_cast<const S*>(a.h) + node * C * K + m0;
 #pragma unroll
-    for (int i = 0; i < Cfg::PPW; ++i) {
-      total[i] = f4{0.f, 0.f, 0.f, 0.f};
-      if constexpr (DOT) {
+    for (int s = 0; s < NS; ++s) {
+      const int c = s * STEP + kq * Op::N;
+      if constexpr (NP == 1) {
+        B[s][0] = V{};
+        if (c < C) B[s][0] = *reinterpret_cast<const V*>(row + c);
+      } else {
+        typename In::R r[Op::N];
 #pragma unroll
-        for (int v = 0; v < 4; ++v) {
-          const int c = ct * 16 + 4 * kq + v;
-          held[i][v] = 0.0f;
-          if (i < mine && c < C && node[i16] >= 0)
-            held[i][v] = (float)static_cast<const S*>(a.dot_with)[((int64_t)node[i16] * C + c) * K + m0 + first + i];
-        }
+        for (int i = 0; i < Op::N; ++i) r[i] = In::load(row + (c < C ? c + i : 0) * K);
+#pragma unroll
+        for (int q = 0; q < NP; ++q)
+#pragma unroll
+          for (int i = 0; i < Op::N; ++i) B[s][q][i] = c < C ? r[i][q] : (S)0.0f;
       }
     }
-    const int co = ct * 16 + i16;
-    for (int word = 0; word < (a.X + 31) / 32; ++word) {
-      unsigned bits = __builtin_amdgcn_readfirstlane(met[word]);
-      while (bits) {
-        const int e = word * 32 + __builtin_ctz(bits);
-        bits &= bits - 1;
-        float g = 0.0f;
-        bool has = false;
-        for (int j = 0; j < a.k; ++j)
-          if (expert[i16][j] == e) {
-            g += gate[i16][j];
-            has = true;
-          }
-        const S* We = static_cast<const S*>(a.W) + ((int64_t)e * (a.lmax + 1)) * C * C;
-        V wf[Cfg::KS];
-        float dot = 0.0f;
+    f4 total[CTW][NP];
+#pragma unroll
+    for (int t = 0; t < CTW; ++t)
+#pragma unroll
+      for (int q = 0; q < NP; ++q) total[t][q] = f4{0.f, 0.f, 0.f, 0.f};
+    int e = -1;
+    while (true) {
+      int next = kMaxExperts;
+#pragma unroll
+      for (int i = 0; i < kListed; ++i) next = ex[i] > e ? min(next, ex[i]) : next;
+      e = wave_min(next);
+      if (e >= kMaxExperts) break;
+      float w = 0.0f;
+      int has = 0;
+#pragma unroll
+      for (int i = 0; i < kListed; ++i)
+        if (ex[i] == e) {
+          w += gate[i];
+          has = 1;
+        }
+      w += __shfl_xor(w, 16, 64);
+      w += __shfl_xor(w, 32, 64);
+      has |= __shfl_xor(has, 16, 64);
+      has |= __shfl_xor(has, 32, 64);
+      const S* We = static_cast<const S*>(a.W) + (int64_t)e * (a.lmax + 1) * C * C;
+      float dot = 0.0f;
+#pragma unroll
+      for (int t = 0; t < CTW; ++t) {
+        const int co = (ct0 + t) * 16 + i16;
+        typename Run<S, NP>::R held[DOT ? 4 : 1];
+        if constexpr (DOT) {
+          const S* with = static_cast<const S*>(a.dot_with) + node * C * K + m0;
+          const int c = (ct0 + t) * 16 + 4 * kq;
+#pragma unroll
+          for (int v = 0; v < 4; ++v) held[v] = In::load(with + (c + v < C ? c + v : 0) * K);
+        }
+        V wf[NS];
         int have = -1;
 #pragma unroll
-        for (int i = 0; i < Cfg::PPW; ++i) {
-          if (i >= mine) break;
-          const int l = degree_of_plane(m0 + first + i);
+        for (int q = 0; q < NP; ++q) {
+          const int l = degree_of_plane(m0 + q);
           if (l != have) {
             have = l;
+            const S* wr = We + ((int64_t)l * C + (co < C ? co : 0)) * C;
 #pragma unroll
-            for (int s = 0; s < Cfg::KS; ++s) {
-              const int c = (s * 4 + kq) * Op::N;
-              wf[s] = c < C && co < C ? *reinterpret_cast<const V*>(We + ((int64_t)l * C + co) * C + c) : Op::zero();
+            for (int s = 0; s < NS; ++s) {
+              const int c = s * STEP + kq * Op::N;
+              wf[s] = *reinterpret_cast<const V*>(wr + (c < C ? c : 0));
+              if constexpr (C % STEP != 0) wf[s] = c < C ? wf[s] : V{};
             }
           }
-          const S* row = hT + (first + i) * Cfg::PLANE + i16 * Cfg::RS;
           f4 acc = f4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int s = 0; s < Cfg::KS; ++s) {
-            const int c = (s * 4 + kq) * Op::N;
-            const V b = c < C ? *reinterpret_cast<const V*>(row + c) : Op::zero();
-            acc = Op::mul(wf[s], b, acc);
-          }
+          for (int s = 0; s < NS; ++s) acc = Op::mul(wf[s], B[s][q], acc);
 #pragma unroll
           for (int v = 0; v < 4; ++v) {
-            total[i][v] = has ? fmaf(g, acc[v], total[i][v]) : total[i][v];
-            if constexpr (DOT) dot = fmaf(acc[v], held[i][v], dot);
+            total[t][q][v] = has ? fmaf(w, acc[v], total[t][q][v]) : total[t][q][v];
+            if constexpr (DOT)
+              if (q >= dup && (ct0 + t) * 16 + 4 * kq + v < C) dot = fmaf(acc[v], (float)held[v][q], dot);
           }
         }
-        if constexpr (DOT) {
-          dot += __shfl_xor(dot, 16, 64);
-          dot += __shfl_xor(dot, 32, 64);
-          if (kq == 0 && has)
-            for (int j = 0; j < a.k; ++j)
-              if (expert[i16][j] == e) dots[wv][i16][j] += dot;
+      }
+      if constexpr (DOT) {
+        dot += __shfl_xor(dot, 16, 64);
+        dot += __shfl_xor(dot, 32, 64);
+#pragma unroll
+        for (int i = 0; i < kListed; ++i)
+          if (ex[i] == e) dots[wv][i16][kq + 4 * i] += dot;
+      }
+    }
+    if (a.out == nullptr || i16 >= nv) continue;
+#pragma unroll
+    for (int t = 0; t < CTW; ++t) {
+      const int c = (ct0 + t) * 16 + 4 * kq;
+      if (c >= C) continue;
+      const int64_t at = (node * C + c) * K + m0;
+      if constexpr (NP == 1) {
+        if (a.out_bf16) {
+          Run<__bf16, 4>::R o;
+#pragma unroll
+          for (int v = 0; v < 4; ++v) o[v] = (__bf16)total[t][0][v];
+          Run<__bf16, 4>::store(static_cast<__bf16*>(a.out) + at, o);
+        } else {
+          Run<float, 4>::store(static_cast<float*>(a.out) + at, total[t][0]);
+        }
+      } else {
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          if (a.out_bf16) {
+            typename Run<__bf16, NP>::R o;
+#pragma unroll
+            for (int q = 0; q < NP; ++q) o[q] = (__bf16)total[t][q][v];
+            Run<__bf16, NP>::store(static_cast<__bf16*>(a.out) + at + v * K, o);
+          } else {
+#pragma unroll
+            for (int q = 0; q < NP; q += 4)
+              Run<float, 4>::store(static_cast<float*>(a.out) + at + v * K + q,
+                                   f4{total[t][q][v], total[t][q + 1][v], total[t][q + 2][v], total[t][q + 3][v]});
+          }
         }
       }
-    }
-    if (a.out == nullptr) continue;
-    __syncthreads();  // the features are dead: the place holds the output [node][channel][plane] (stride of a node padded)
-    const int NS = C * np + 4;
-#pragma unroll
-    for (int i = 0; i < Cfg::PPW; ++i) {
-      if (i >= mine) break;
-#pragma unroll
-      for (int v = 0; v < 4; ++v) {
-        const int c = ct * 16 + 4 * kq + v;
-        if (c < C) ot[i16 * NS + c * np + first + i] = total[i][v];
-      }
-    }
-    __syncthreads();
-    for (int i = tid; i < nv * C * np; i += TH) {
-      const int r = i / (C * np), at = i - r * (C * np), c = at / np, m = at - c * np;
-      const int64_t o = ((int64_t)node[r] * C + c) * K + m0 + m;
-      const float v = ot[r * NS + at];
-      if (a.out_bf16) static_cast<__bf16*>(a.out)[o] = (__bf16)v;
-      else static_cast<float*>(a.out)[o] = v;
     }
   }
   if constexpr (DOT) {
     __syncthreads();
-    for (int i = tid; i < nv * a.k; i += TH) {
+    for (int i = threadIdx.x; i < nv * a.k; i += blockDim.x) {
       const int r = i / a.k, j = i - r * a.k;
       float v = 0.0f;
-#pragma unroll
-      for (int w = 0; w < Cfg::WAVES; ++w) v += dots[w][r][j];
-      a.gweight[(int64_t)node[r] * a.k + j] = v;
+      for (int w = 0; w < waves; ++w) v += dots[w][r][j];
+      const int64_t n = a.order ? clamp_index(a.order[p0 + r], (int)a.N) : p0 + r;
+      a.gweight[n * a.k + j] = v;
     }
   }
 }
@@ -245,34 +252,44 @@ hipError_t launch_transpose_weights(int64_t matrices, int C, bool bf16, const vo
   return hipGetLastError();
 }
 
-template <class S, int C, bool DOT>
+template <class S, int C, int NP, int CTW, bool DOT>
 static hipError_t expert_launch(const ExpertArgs& a) {
-  using Cfg = ExpertCfg<S, C>;
-  const size_t bytes = Cfg::lds_bytes(a.lmax <= 3 ? num_comp(a.lmax) : kMaxPlanes);
-  static const hipError_t allowed =  // more than 64 KB of LDS has to be asked for, once a kernel
-      hipFuncSetAttribute(reinterpret_cast<const void*>(expert_kernel<S, C, DOT>),
-                          hipFuncAttributeMaxDynamicSharedMemorySize, (int)Cfg::lds_bytes(kMaxPlanes));
-  if (allowed != hipSuccess) return allowed;
-  expert_kernel<S, C, DOT><<<dim3((unsigned)((a.N + kTile - 1) / kTile)), dim3(64 * Cfg::WAVES), bytes, a.stream>>>(a);
+  const int groups = plane_groups(num_comp(a.lmax), NP), tasks = groups * ((C + 15) / 16 / CTW);
+  expert_kernel<S, C, NP, CTW, DOT><<<dim3((unsigned)((a.N + kTile - 1) / kTile)), dim3(64 * (tasks < 4 ? tasks : 4)), 0,
+                                      a.stream>>>(a, groups);
   return hipGetLastError();
 }
 
-template <class S, bool DOT>
+// Output tiles of a wave: all of them up to C = 64, so that a tile's features are read once; fewer where the totals
+// would not leave two waves' registers.
+template <class S, int C, int NP, bool DOT>
+static hipError_t expert_ctw(const ExpertArgs& a) {
+  constexpr int CT = (C + 15) / 16, MOST = NP == 8 ? 2 : 4;
+  return expert_launch<S, C, NP, (CT < MOST ? CT : MOST), DOT>(a);
+}
+
+template <class S, int NP, bool DOT>
 static hipError_t expert_c(const ExpertArgs& a) {
   switch (a.C) {
-    case 8: return expert_launch<S, 8, DOT>(a);
-    case 16: return expert_launch<S, 16, DOT>(a);
-    case 32: return expert_launch<S, 32, DOT>(a);
-    case 64: return expert_launch<S, 64, DOT>(a);
-    case 128: return expert_launch<S, 128, DOT>(a);
+    case 8: return expert_ctw<S, 8, NP, DOT>(a);
+    case 16: return expert_ctw<S, 16, NP, DOT>(a);
+    case 32: return expert_ctw<S, 32, NP, DOT>(a);
+    case 64: return expert_ctw<S, 64, NP, DOT>(a);
+    case 128: return expert_ctw<S, 128, NP, DOT>(a);
     default: return hipErrorInvalidValue;
   }
 }
 
+template <bool DOT>
+static hipError_t expert_np(const ExpertArgs& a) {
+  const int np = planes_at_once(a.bf16, a.lmax);
+  if (a.bf16) return np == 1 ? expert_c<__bf16, 1, DOT>(a) : (np == 4 ? expert_c<__bf16, 4, DOT>(a) : expert_c<__bf16, 8, DOT>(a));
+  return np == 1 ? expert_c<float, 1, DOT>(a) : expert_c<float, 4, DOT>(a);
+}
+
 hipError_t launch_expert(const ExpertArgs& a) {
   if (a.N == 0) return hipSuccess;
-  if (a.gweight) return a.bf16 ? expert_c<__bf16, true>(a) : expert_c<float, true>(a);
-  return a.bf16 ? expert_c<__bf16, false>(a) : expert_c<float, false>(a);
+  return a.gweight ? expert_np<true>(a) : expert_np<false>(a);
 }
 
 }  // namespace eqtp

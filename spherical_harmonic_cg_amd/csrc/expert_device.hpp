@@ -1,5 +1,5 @@
 // expert_device.hpp -- what the experts' linear and its weight gradient share:
-// operand types, and the stretches of components that a pass holds at once.
+// operands of the matrix-core products and how they are read from features.
 #pragma once
 
 #include "eqtp_device.hpp"
@@ -7,20 +7,26 @@
 
 namespace eqtp {
 
-constexpr int kTile = 16;  // nodes (or places) of a tile: the columns of a matrix-core product
-constexpr int kMaxPlanes = 16;
-constexpr int expert_threads(int C) { return C >= 128 ? 512 : 256; }  // a workgroup's
+constexpr int kTile = 16;  // nodes of a tile: the columns of a matrix-core product
 
 __device__ __forceinline__ int degree_of_plane(int m) {
   return m >= 9 ? (m >= 25 ? (m >= 36 ? 6 : 5) : (m >= 16 ? 4 : 3)) : (m >= 4 ? 2 : (m >= 1 ? 1 : 0));
 }
 
-// Components are worked on in stretches of whole degrees with at most 16 of them: degrees 0 to 3 together (or up to
-// lmax), then 4, 5 and 6 one at a time.
-__host__ __device__ constexpr int stretches_of(int lmax) { return lmax <= 3 ? 1 : lmax - 2; }
-__host__ __device__ constexpr int stretch_first(int s) { return s == 0 ? 0 : (s + 3) * (s + 3); }
-__host__ __device__ constexpr int stretch_planes(int s, int lmax) {
-  return s == 0 ? num_comp(lmax < 3 ? lmax : 3) : 2 * (s + 3) + 1;
-}
+// NP consecutive elements, aligned as one element only
+template <class S, int NP>
+struct Run {
+  typedef S V __attribute__((ext_vector_type(NP), aligned(sizeof(S))));
+  typedef S R __attribute__((ext_vector_type(NP)));
+  static __device__ __forceinline__ R load(const S* p) { return *reinterpret_cast<const V*>(p); }
+  static __device__ __forceinline__ void store(S* p, const R& v) { *reinterpret_cast<V*>(p) = v; }
+};
+
+// Components that a wave takes of a channel: 16 bytes of them where a channel has as many (fp32: 4; bf16: 8, or 4 at
+// lmax 1), one at lmax 0.
+constexpr int planes_at_once(bool bf16, int lmax) { return lmax == 0 ? 1 : (bf16 && lmax > 1 ? 8 : 4); }
+constexpr int plane_groups(int K, int np) { return (K + np - 1) / np; }
+// first component of a group: the last one ends with the channel, and takes some that the one before has, too
+__device__ __forceinline__ int group_first(int g, int K, int np) { return min(g * np, K - np); }
 
 }  // namespace eqtp
