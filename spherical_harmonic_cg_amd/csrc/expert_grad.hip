@@ -2,11 +2,16 @@
 //   grad_W[x, l, c', c] = sum over the places (n, j) of expert x of
 //                         weight[n, j] sum_m grad_out[n, c', l m] h[n, c, l m].
 //
-// Places come grouped by expert (expert_plan.hip); a workgroup takes a chunk of
-// one expert's places and keeps all of its C x C matrices in registers: 16x16
-// tiles of outer products over 16 places at a time on the matrix cores.  fp32:
-// the products' operands are fp32.  bf16: a gate's product with the gradient is
-// held in two bf16 parts, both multiplied: 2^-16 of a term at most is lost.  Chunks go to lines of part, which a second kernel adds in a fixed
+// Places come grouped by expert (expert_plan.hip).  A wave takes a chunk of one
+// expert's places and RT x CTC tiles of 16x16 channels, of degrees 0 to 3
+// together or of one degree above, and goes over the chunk four places at a
+// time: lane (channel i, k) reads all of those components of channel i of place
+// k, of the gradient and of h.  In fp32 a component of each is the operand of
+// one product over the four places; in bf16 a degree's components are packed as
+// they lie in memory, so one product sums 4 places and up to 8 components.  No LDS, no barriers.
+// fp32: the products' operands are fp32.  bf16: a gate's product with the
+// gradient is held in two bf16 parts, both multiplied: 2^-16 of a term at most
+// is lost.  Chunks go to lines of part, which a second kernel adds in a fixed
 // order: no atomics, the same bits from call to call.
 #include <type_traits>
 
@@ -14,162 +19,260 @@
 
 namespace eqtp {
 
-template <class S, int C, bool GATES>
-struct ExpertGradCfg {
-  static constexpr bool BF16 = std::is_same<S, __bf16>::value;
-  static constexpr int ES = (int)sizeof(S);
-  // fp32: planes [place][channel], bf16: [channel][place], as the operands are read
-  static constexpr int TS = BF16 ? 16 : (C >= 128 ? 8 : 16);  // places at a time (LDS)
-  static constexpr int RS = BF16 ? 16 + 4 : C + 16;
-  static constexpr int PLANE = BF16 ? C * RS : TS * RS;
-  static constexpr int WAVES = expert_threads(C) / 64;
-  static constexpr int CT = (C + 15) / 16;
-  static constexpr int PG = WAVES / CT > 0 ? WAVES / CT : 1;  // waves that share a tile of output channels: parts of the degrees
-  static constexpr int LPW = (4 + PG - 1) / PG;               // degrees of a wave
-  static constexpr int SETS = BF16 && GATES ? 3 : 2;          // gradient (in two parts) and features
-  static constexpr int PP = 8;                                // planes at a time (LDS)
-  static size_t lds_bytes(int planes) { return (size_t)SETS * (planes < PP ? planes : PP) * PLANE * ES; }
-};
+// Stretches of components that a wave holds at once: degrees 0 to 3 (or up to lmax), then 4, 5 and 6 one at a time.
+__host__ __device__ constexpr int stretches_of(int lmax) { return lmax <= 3 ? 1 : lmax - 2; }
 
 struct ChunkOf {
   int x;            // expert, or -1
   int64_t s0, s1;   // its places
 };
-// chunk b of the experts' places, `per` places at most each
+// Chunk b of the experts' places, `per` places at most each; a whole wave calls it.
 __device__ __forceinline__ ChunkOf chunk_of(const int32_t* ptr, int X, int64_t places, int per, int b) {
+  const int lane = threadIdx.x & 63;
   ChunkOf r = {-1, 0, 0};
-  int at = 0;
-  for (int x = 0; x < X; ++x) {
-    const int64_t lo = min(max((int64_t)ptr[x], (int64_t)0), places), hi = min(max((int64_t)ptr[x + 1], lo), places);
-    const int n = (int)((hi - lo + per - 1) / per);
-    if (b < at + n) {
-      r.x = x;
-      r.s0 = lo + (int64_t)(b - at) * per;
-      r.s1 = min(r.s0 + per, hi);
-      return r;
+  int before = 0;
+  for (int x0 = 0; x0 < X && r.x < 0; x0 += 64) {
+    const int x = x0 + lane;
+    int64_t lo = 0, hi = 0;
+    if (x < X) {
+      lo = min(max((int64_t)ptr[x], (int64_t)0), places);
+      hi = min(max((int64_t)ptr[x + 1], lo), places);
     }
-    at += n;
+    const int n = (int)((hi - lo + per - 1) / per);
+    int incl = n;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const int u = __shfl_up(incl, o, 64);
+      if (lane >= o) incl += u;
+    }
+    const uint64_t past = __ballot(before + incl > b);
+    if (past) {
+      const int src = __builtin_ctzll(past);
+      const int first = before + __shfl(incl - n, src, 64);
+      r.x = __builtin_amdgcn_readfirstlane(x0 + src);
+      r.s0 = __shfl((long long)lo, src, 64) + (int64_t)(b - first) * per;
+      r.s1 = min(r.s0 + per, (int64_t)__shfl((long long)hi, src, 64));
+    }
+    before += __shfl(incl, 63, 64);
   }
   return r;
 }
 
-typedef short bf16x4s __attribute__((ext_vector_type(4)));
+// Up to 16 components of a channel in registers, and products of them by degree.
+template <class S, bool GATES>
+struct Comps;
 
-template <class S, int C, bool GATES>
-__global__ __launch_bounds__(expert_threads(C)) void expert_grad_kernel(ExpertGradArgs a, int per) {
-  using Cfg = ExpertGradCfg<S, C, GATES>;
-  constexpr int TH = 64 * Cfg::WAVES, TS = Cfg::TS;
-  extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
-  __shared__ int node[TS];
-  __shared__ float gate[TS];
-  const int st = blockIdx.y;
-  const int K = num_comp(a.lmax), m0 = stretch_first(st), np = stretch_planes(st, a.lmax);
-  const int l0 = st == 0 ? 0 : st + 3, ln = st == 0 ? min(a.lmax, 3) + 1 : 1;
-  constexpr int PP = Cfg::PP;
-  const int held = min(np, PP);
-  S* gT = reinterpret_cast<S*>(lds);
-  S* gL = gT + held * Cfg::PLANE;  // bf16: what the first part leaves
-  S* hT = gT + (Cfg::SETS - 1) * held * Cfg::PLANE;
-  const int tid = threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int i16 = lane & 15, kq = lane >> 4, ct = wv % Cfg::CT, pg = wv / Cfg::CT;
-  const ChunkOf ch = chunk_of(a.ptr, a.X, a.N * a.k, per, blockIdx.x);
-  if (ch.x < 0) return;
-  f4 acc[Cfg::LPW][Cfg::CT];
+template <bool GATES>
+struct Comps<float, GATES> {
+  float x[16];
+  __device__ __forceinline__ void load(const float* p, int np) {
 #pragma unroll
-  for (int i = 0; i < Cfg::LPW; ++i)
+    for (int w = 0; w < 4; ++w) {
+      if (4 * w + 4 <= np) {
+        const f4 t = Run<float, 4>::load(p + 4 * w);
 #pragma unroll
-    for (int t = 0; t < Cfg::CT; ++t) acc[i][t] = f4{0.f, 0.f, 0.f, 0.f};
-  for (int64_t s = ch.s0; s < ch.s1; s += TS) {
-    const int nv = (int)min((int64_t)TS, ch.s1 - s);
-    __syncthreads();
-    if (tid < TS) {
-      const int64_t slot = tid < nv ? (int64_t)clamp_index(a.slots[s + tid], (int)min(a.N * a.k, (int64_t)0x7fffffff)) : 0;
-      node[tid] = (int)(slot / a.k);
-      gate[tid] = GATES ? a.weight[slot] : 1.0f;
-    }
-    for (int pm = 0; pm < np; pm += PP) {
-      const int pn = min(PP, np - pm);
-      __syncthreads();
-      for (int i = tid; i < TS * C; i += TH) {
-        const int r = i / C, c = i - r * C;
-        const int64_t at = ((int64_t)node[r] * C + c) * K + m0 + pm;
-        const float w = gate[r];
-        for (int m = 0; m < pn; ++m) {
-          const S g = r < nv ? static_cast<const S*>(a.gout)[at + m] : (S)0.0f;
-          const S h = r < nv ? static_cast<const S*>(a.h)[at + m] : (S)0.0f;
-          const int to = m * Cfg::PLANE + (Cfg::BF16 ? c * Cfg::RS + r : r * Cfg::RS + c);
-          hT[to] = h;
-          const float wg = GATES && r < nv ? w * (float)g : (float)g;
-          gT[to] = (S)wg;
-          if constexpr (Cfg::BF16 && GATES) gL[to] = (S)(wg - (float)(S)wg);
-        }
+        for (int q = 0; q < 4; ++q) x[4 * w + q] = t[q];
+      } else {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) x[4 * w + q] = 4 * w + q < np ? p[4 * w + q] : 0.0f;
       }
-      __syncthreads();
+    }
+  }
+  __device__ __forceinline__ void gate(float w, bool live) {
 #pragma unroll
-      for (int i = 0; i < Cfg::LPW; ++i) {
-        const int dl = pg + i * Cfg::PG;
-        if (dl >= ln) break;
-        const int l = l0 + dl;
-        const int ma = max(l * l - m0 - pm, 0), mb = min((l + 1) * (l + 1) - m0 - pm, pn);
-        for (int m = ma; m < mb; ++m) {
-          const int row = ct * 16 + i16 < C ? ct * 16 + i16 : 0;
-          if constexpr (Cfg::BF16) {
-            const int at = m * Cfg::PLANE + row * Cfg::RS + 4 * kq;
-            const bf16x4s ga = *reinterpret_cast<const bf16x4s*>(gT + at);
-            bf16x4s gb = {};
-            if constexpr (GATES) gb = *reinterpret_cast<const bf16x4s*>(gL + at);
+    for (int q = 0; q < 16; ++q) x[q] = live ? (GATES ? x[q] * w : x[q]) : 0.0f;
+  }
+  // acc += this (rows) times b (columns) over components first .. first + n - 1 (constants once unrolled)
+  __device__ __forceinline__ void add(const Comps& b, int first, int n, f4& acc) const {
 #pragma unroll
-            for (int t = 0; t < Cfg::CT; ++t) {
-              const int col = t * 16 + i16 < C ? t * 16 + i16 : 0;
-              const bf16x4s hb = *reinterpret_cast<const bf16x4s*>(hT + m * Cfg::PLANE + col * Cfg::RS + 4 * kq);
-              acc[i][t] = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(ga, hb, acc[i][t], 0, 0, 0);
-              if constexpr (GATES) acc[i][t] = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(gb, hb, acc[i][t], 0, 0, 0);
-            }
-          } else {
+    for (int q = 0; q < 16; ++q)
+      if (q >= first && q < first + n) acc = __builtin_amdgcn_mfma_f32_16x16x4f32(x[q], b.x[q], acc, 0, 0, 0);
+  }
+};
+
+template <bool GATES>
+struct Comps<__bf16, GATES> {
+  uint32_t x[8], lo[GATES ? 8 : 1];  // pairs of components; what the first part of a product leaves
+  __device__ __forceinline__ void load(const __bf16* p, int np) {
+    const uint16_t* h = reinterpret_cast<const uint16_t*>(p);
 #pragma unroll
-            for (int q = 0; q < TS; q += 4) {
-              const int base = m * Cfg::PLANE + (q + kq) * Cfg::RS;
-              const float ga = gT[base + row];
+    for (int w = 0; w < 2; ++w) {
+      if (8 * w + 8 <= np) {
+        const uint4 t = __builtin_bit_cast(uint4, Run<__bf16, 8>::load(p + 8 * w));
+        x[4 * w] = t.x;
+        x[4 * w + 1] = t.y;
+        x[4 * w + 2] = t.z;
+        x[4 * w + 3] = t.w;
+      } else {
 #pragma unroll
-              for (int t = 0; t < Cfg::CT; ++t) {
-                const int col = t * 16 + i16 < C ? t * 16 + i16 : 0;
-                acc[i][t] = __builtin_amdgcn_mfma_f32_16x16x4f32(ga, hT[base + col], acc[i][t], 0, 0, 0);
-              }
-            }
-          }
+        for (int q = 0; q < 4; ++q) {
+          const int m = 8 * w + 2 * q;
+          x[4 * w + q] = (m < np ? (uint32_t)h[m] : 0u) | (m + 1 < np ? (uint32_t)h[m + 1] << 16 : 0u);
         }
       }
     }
   }
-  // lane (i16, kq) holds D[c' = 16 ct + 4 kq + v][c = 16 t + i16]
-  float* line = a.part + (int64_t)blockIdx.x * (a.lmax + 1) * C * C;
+  __device__ __forceinline__ void gate(float w, bool live) {
 #pragma unroll
-  for (int i = 0; i < Cfg::LPW; ++i) {
-    const int dl = pg + i * Cfg::PG;
-    if (dl >= ln) break;
-#pragma unroll
-    for (int t = 0; t < Cfg::CT; ++t)
-#pragma unroll
-      for (int v = 0; v < 4; ++v) {
-        const int r = ct * 16 + 4 * kq + v, c = t * 16 + i16;
-        if (r < C && c < C) line[((int64_t)(l0 + dl) * C + r) * C + c] = acc[i][t][v];
+    for (int q = 0; q < 8; ++q) {
+      if constexpr (GATES) {
+        const float a = w * __uint_as_float(x[q] << 16), b = w * __uint_as_float(x[q] & 0xffff0000u);
+        typedef __bf16 b2 __attribute__((ext_vector_type(2)));
+        const uint32_t hi = __builtin_bit_cast(uint32_t, b2{(__bf16)a, (__bf16)b});
+        const float ra = a - __uint_as_float(hi << 16), rb = b - __uint_as_float(hi & 0xffff0000u);
+        x[q] = live ? hi : 0u;
+        lo[q] = live ? __builtin_bit_cast(uint32_t, b2{(__bf16)ra, (__bf16)rb}) : 0u;
+      } else {
+        x[q] = live ? x[q] : 0u;
       }
+    }
+  }
+  // the words that hold components first .. first + n - 1, eight components from word `at` on, others cleared
+  static __device__ __forceinline__ bf16x8 part(const uint32_t (&v)[8], int at, int first, int n) {
+    uint32_t o[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int m = 2 * (at + q);
+      const uint32_t keep = (m >= first && m < first + n ? 0xffffu : 0u) | (m + 1 >= first && m + 1 < first + n ? 0xffff0000u : 0u);
+      o[q] = at + q < 8 ? v[(at + q) & 7] & keep : 0u;
+    }
+    return __builtin_bit_cast(bf16x8, uint4{o[0], o[1], o[2], o[3]});
+  }
+  __device__ __forceinline__ void add(const Comps& b, int first, int n, f4& acc) const {
+#pragma unroll
+    for (int at = first / 2; 2 * at < first + n; at += 4) {
+      const bf16x8 bv = part(b.x, at, first, n);
+      acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(part(x, at, first, n), bv, acc, 0, 0, 0);
+      if constexpr (GATES) acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(part(lo, at, first, n), bv, acc, 0, 0, 0);
+    }
+  }
+};
+
+template <int C>
+struct ExpertGradCfg {
+  static constexpr int CT = (C + 15) / 16;
+  static constexpr int RT = CT < 2 ? CT : 2, CTC = CT < 2 ? CT : 2;  // tiles of a wave: rows, columns
+  static constexpr int SPLITS = (CT / RT) * (CT / CTC);
+};
+
+// LMAX: 0 to 3, the degrees of the first stretch; 4 to 6, one degree
+template <class S, int C, bool GATES, int LMAX>
+__device__ __forceinline__ void expert_grad_walk(const ExpertGradArgs& a, const ChunkOf& ch, int split, float* line) {
+  using Cfg = ExpertGradCfg<C>;
+  constexpr int RT = Cfg::RT, CTC = Cfg::CTC;
+  constexpr int L0 = LMAX <= 3 ? 0 : LMAX, LN = LMAX - L0 + 1, NPL = LMAX <= 3 ? (LMAX + 1) * (LMAX + 1) : 2 * LMAX + 1;
+  const int K = num_comp(a.lmax), lane = threadIdx.x & 63, i16 = lane & 15, kq = lane >> 4;
+  const int rt = split / (Cfg::CT / CTC) * RT, cc = split % (Cfg::CT / CTC) * CTC;
+  f4 acc[LN][RT][CTC];
+#pragma unroll
+  for (int l = 0; l < LN; ++l)
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+#pragma unroll
+      for (int t = 0; t < CTC; ++t) acc[l][r][t] = f4{0.f, 0.f, 0.f, 0.f};
+  const int last = (int)min(a.N * a.k, (int64_t)0x7fffffff);
+  for (int64_t s0 = ch.s0; s0 < ch.s1; s0 += 64) {
+    // 64 places, one a lane: node and gate
+    const int64_t mine = min(s0 + lane, ch.s1 - 1);
+    const int slot = clamp_index(a.slots[mine], last);
+    const int my_node = slot / a.k;
+    const float my_gate = GATES ? a.weight[slot] : 1.0f;
+    const int steps = (int)min((int64_t)16, (ch.s1 - s0 + 3) / 4);
+    for (int st = 0; st < steps; ++st) {
+      const int from = 4 * st + kq;
+      const int64_t node = __shfl(my_node, from, 64);
+      const float w = __shfl(my_gate, from, 64);
+      const bool live = s0 + from < ch.s1;
+      Comps<S, GATES> g[RT], h[CTC];
+      const int64_t base = node * C * K + L0 * L0;
+#pragma unroll
+      for (int r = 0; r < RT; ++r) {
+        const int c = (rt + r) * 16 + i16;
+        g[r].load(static_cast<const S*>(a.gout) + base + (c < C ? c : 0) * K, NPL);
+      }
+#pragma unroll
+      for (int t = 0; t < CTC; ++t) {
+        const int c = (cc + t) * 16 + i16;
+        h[t].load(static_cast<const S*>(a.h) + base + (c < C ? c : 0) * K, NPL);
+      }
+#pragma unroll
+      for (int r = 0; r < RT; ++r) g[r].gate(w, live);
+#pragma unroll
+      for (int l = 0; l < LN; ++l)
+#pragma unroll
+        for (int r = 0; r < RT; ++r)
+#pragma unroll
+          for (int t = 0; t < CTC; ++t) {
+            if constexpr (LMAX <= 3) g[r].add(h[t], l * l, 2 * l + 1, acc[l][r][t]);
+            else g[r].add(h[t], 0, NPL, acc[l][r][t]);
+          }
+    }
+  }
+  // lane (i16, kq) holds D[c' = 4 kq + v][c = i16] of each tile
+#pragma unroll
+  for (int l = 0; l < LN; ++l)
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+#pragma unroll
+      for (int t = 0; t < CTC; ++t)
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          const int row = (rt + r) * 16 + 4 * kq + v, col = (cc + t) * 16 + i16;
+          if (row < C && col < C) line[((int64_t)(L0 + l) * C + row) * C + col] = acc[l][r][t][v];
+        }
+}
+
+// a wave a workgroup: the splits of a chunk beside each other, on one XCD (workgroups go round the eight)
+template <class S, int C, bool GATES>
+__global__ __launch_bounds__(64) void expert_grad_kernel(ExpertGradArgs a, int per, int lines) {
+  constexpr int SPLITS = ExpertGradCfg<C>::SPLITS;
+  const int round = blockIdx.x / (8 * SPLITS), in = blockIdx.x % (8 * SPLITS);
+  const int chunk = round * 8 + in % 8, split = in / 8;
+  if (chunk >= lines) return;
+  const ChunkOf ch = chunk_of(a.ptr, a.X, a.N * a.k, per, chunk);
+  if (ch.x < 0) return;
+  float* line = a.part + (int64_t)chunk * (a.lmax + 1) * C * C;
+  switch (blockIdx.y == 0 ? min(a.lmax, 3) : blockIdx.y + 3) {
+    case 0: expert_grad_walk<S, C, GATES, 0>(a, ch, split, line); break;
+    case 1: expert_grad_walk<S, C, GATES, 1>(a, ch, split, line); break;
+    case 2: expert_grad_walk<S, C, GATES, 2>(a, ch, split, line); break;
+    case 3: expert_grad_walk<S, C, GATES, 3>(a, ch, split, line); break;
+    case 4: expert_grad_walk<S, C, GATES, 4>(a, ch, split, line); break;
+    case 5: expert_grad_walk<S, C, GATES, 5>(a, ch, split, line); break;
+    default: expert_grad_walk<S, C, GATES, 6>(a, ch, split, line); break;
   }
 }
 
 // grad_W[x] = the sum of its chunks' lines, in order, in 64 bits (zeros without one); blockIdx.y: the expert
 __global__ __launch_bounds__(256) void expert_grad_sum_kernel(ExpertGradArgs a, int per, int64_t size, int lines) {
-  int at = 0, n = 0;
-  for (int x = 0; x <= (int)blockIdx.y; ++x) {
-    at += n;
+  __shared__ int begin, count;
+  if (threadIdx.x < 64) {
+    // chunks of the experts before this one, and its own
     const int64_t places = a.N * a.k;
-    const int64_t lo = min(max((int64_t)a.ptr[x], (int64_t)0), places), hi = min(max((int64_t)a.ptr[x + 1], lo), places);
-    n = (int)((hi - lo + per - 1) / per);
+    int before = 0, own = 0;
+    for (int x = threadIdx.x; x <= (int)blockIdx.y; x += 64) {
+      const int64_t lo = min(max((int64_t)a.ptr[x], (int64_t)0), places), hi = min(max((int64_t)a.ptr[x + 1], lo), places);
+      const int n = (int)((hi - lo + per - 1) / per);
+      if (x < (int)blockIdx.y) before += n;
+      else own = n;
+    }
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      before += __shfl_xor(before, o, 64);
+      own += __shfl_xor(own, o, 64);
+    }
+    if (threadIdx.x == 0) {
+      begin = min(before, lines);
+      count = min(own, lines - begin);
+    }
   }
+  __syncthreads();
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (i >= size) return;
+  const float* p = a.part + begin * size + i;
   double s = 0.0;
-  for (int j = 0; j < n && at + j < lines; ++j) s += a.part[(at + j) * size + i];
+#pragma unroll 8
+  for (int j = 0; j < count; ++j) s += p[j * size];
   a.gW[blockIdx.y * size + i] = (float)s;
 }
 
@@ -193,16 +296,11 @@ int64_t expert_grad_floats(int64_t N, int C, int lmax, int X, int k, bool bf16) 
 
 template <class S, int C, bool GATES>
 static hipError_t expert_grad_launch(const ExpertGradArgs& a) {
-  using Cfg = ExpertGradCfg<S, C, GATES>;
   const int per = chunk_places(a.N, a.C, a.lmax, a.k, a.bf16);
   const int64_t chunks = chunks_at_most(a.N, a.C, a.lmax, a.X, a.k, a.bf16), size = (int64_t)(a.lmax + 1) * C * C;
-  static const hipError_t allowed =
-      hipFuncSetAttribute(reinterpret_cast<const void*>(expert_grad_kernel<S, C, GATES>),
-                          hipFuncAttributeMaxDynamicSharedMemorySize, (int)Cfg::lds_bytes(kMaxPlanes));
-  if (allowed != hipSuccess) return allowed;
   if (chunks > 0)
-    expert_grad_kernel<S, C, GATES><<<dim3((unsigned)chunks, stretches_of(a.lmax)), dim3(64 * Cfg::WAVES),
-                                      Cfg::lds_bytes(a.lmax <= 3 ? num_comp(a.lmax) : kMaxPlanes), a.stream>>>(a, per);
+    expert_grad_kernel<S, C, GATES><<<dim3((unsigned)((chunks + 7) / 8 * 8 * ExpertGradCfg<C>::SPLITS), stretches_of(a.lmax)),
+                                      dim3(64), 0, a.stream>>>(a, per, (int)chunks);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   expert_grad_sum_kernel<<<dim3((unsigned)((size + 255) / 256), a.X), dim3(256), 0, a.stream>>>(a, per, size, (int)chunks);
