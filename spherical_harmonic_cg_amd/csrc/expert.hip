@@ -55,14 +55,14 @@ __device__ __forceinline__ int wave_min(int v) {
 constexpr int kListed = kMaxTopK / 4;  // places of a node's list that a lane holds (lane (i, k): k, k + 4, ..)
 
 template <class S, int C, int NP, int CTW, bool DOT>
-__global__ __launch_bounds__(256) void expert_kernel(ExpertArgs a, int groups) {
+__global__ __launch_bounds__(512) void expert_kernel(ExpertArgs a, int groups) {
   using Op = Operand<S>;
   typedef typename Op::V V;
   typedef Run<S, NP> In;
   constexpr int CT = (C + 15) / 16, CS = CT / CTW;
   constexpr int STEP = 4 * Op::N;                       // input channels of a step
   constexpr int NS = (C + STEP - 1) / STEP;
-  __shared__ float dots[DOT ? 4 : 1][kTile][kMaxTopK];
+  __shared__ float dots[DOT ? 8 : 1][kTile][kMaxTopK];
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
   const int i16 = lane & 15, kq = lane >> 4;
   const int K = num_comp(a.lmax);
@@ -115,13 +115,41 @@ __global__ __launch_bounds__(256) void expert_kernel(ExpertArgs a, int groups) {
     for (int t = 0; t < CTW; ++t)
 #pragma unroll
       for (int q = 0; q < NP; ++q) total[t][q] = f4{0.f, 0.f, 0.f, 0.f};
-    int e = -1;
-    while (true) {
+    // (the gates' gradient: what the lane's results meet)
+    typename In::R held[DOT ? CTW : 1][4];
+    if constexpr (DOT) {
+      const S* with = static_cast<const S*>(a.dot_with) + node * C * K + m0;
+#pragma unroll
+      for (int t = 0; t < CTW; ++t)
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          const int c = (ct0 + t) * 16 + 4 * kq + v;
+          held[t][v] = In::load(with + (c < C ? c : 0) * K);
+        }
+    }
+    const int lf = degree_of_plane(m0), ll = degree_of_plane(m0 + NP - 1);
+    // a tile's weights of one expert and degree
+    auto weights = [&](V(&wf)[NS], int e, int t, int l) {
+      const int co = (ct0 + t) * 16 + i16;
+      const S* wr = static_cast<const S*>(a.W) + (((int64_t)e * (a.lmax + 1) + l) * C + (co < C ? co : 0)) * C;
+#pragma unroll
+      for (int s = 0; s < NS; ++s) {
+        const int c = s * STEP + kq * Op::N;
+        wf[s] = *reinterpret_cast<const V*>(wr + (c < C ? c : 0));
+        if constexpr (C % STEP != 0) wf[s] = c < C ? wf[s] : V{};
+      }
+    };
+    auto after = [&](int e) {  // the next expert of the tile
       int next = kMaxExperts;
 #pragma unroll
       for (int i = 0; i < kListed; ++i) next = ex[i] > e ? min(next, ex[i]) : next;
-      e = wave_min(next);
-      if (e >= kMaxExperts) break;
+      return wave_min(next);
+    };
+    int e = after(-1);
+    V wf[NS];
+    weights(wf, min(e, a.X - 1), 0, lf);
+    while (e < kMaxExperts) {
+      const int then = after(e);
       float w = 0.0f;
       int has = 0;
 #pragma unroll
@@ -134,42 +162,29 @@ __global__ __launch_bounds__(256) void expert_kernel(ExpertArgs a, int groups) {
       w += __shfl_xor(w, 32, 64);
       has |= __shfl_xor(has, 16, 64);
       has |= __shfl_xor(has, 32, 64);
-      const S* We = static_cast<const S*>(a.W) + (int64_t)e * (a.lmax + 1) * C * C;
       float dot = 0.0f;
 #pragma unroll
       for (int t = 0; t < CTW; ++t) {
-        const int co = (ct0 + t) * 16 + i16;
-        typename Run<S, NP>::R held[DOT ? 4 : 1];
-        if constexpr (DOT) {
-          const S* with = static_cast<const S*>(a.dot_with) + node * C * K + m0;
-          const int c = (ct0 + t) * 16 + 4 * kq;
+        for (int l = lf; l <= ll; ++l) {
+          // the weights after these are on their way while these are multiplied
+          const bool same = l < ll;
+          V wn[NS];
+          weights(wn, same || t + 1 < CTW ? e : min(then, a.X - 1), same ? t : (t + 1 < CTW ? t + 1 : 0), same ? l + 1 : lf);
 #pragma unroll
-          for (int v = 0; v < 4; ++v) held[v] = In::load(with + (c + v < C ? c + v : 0) * K);
-        }
-        V wf[NS];
-        int have = -1;
+          for (int q = 0; q < NP; ++q) {
+            if (degree_of_plane(m0 + q) != l) continue;
+            f4 acc = f4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int q = 0; q < NP; ++q) {
-          const int l = degree_of_plane(m0 + q);
-          if (l != have) {
-            have = l;
-            const S* wr = We + ((int64_t)l * C + (co < C ? co : 0)) * C;
+            for (int s = 0; s < NS; ++s) acc = Op::mul(wf[s], B[s][q], acc);
 #pragma unroll
-            for (int s = 0; s < NS; ++s) {
-              const int c = s * STEP + kq * Op::N;
-              wf[s] = *reinterpret_cast<const V*>(wr + (c < C ? c : 0));
-              if constexpr (C % STEP != 0) wf[s] = c < C ? wf[s] : V{};
+            for (int v = 0; v < 4; ++v) {
+              total[t][q][v] = has ? fmaf(w, acc[v], total[t][q][v]) : total[t][q][v];
+              if constexpr (DOT)
+                if (q >= dup && (ct0 + t) * 16 + 4 * kq + v < C) dot = fmaf(acc[v], (float)held[t][v][q], dot);
             }
           }
-          f4 acc = f4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int s = 0; s < NS; ++s) acc = Op::mul(wf[s], B[s][q], acc);
-#pragma unroll
-          for (int v = 0; v < 4; ++v) {
-            total[t][q][v] = has ? fmaf(w, acc[v], total[t][q][v]) : total[t][q][v];
-            if constexpr (DOT)
-              if (q >= dup && (ct0 + t) * 16 + 4 * kq + v < C) dot = fmaf(acc[v], (float)held[v][q], dot);
-          }
+          for (int s = 0; s < NS; ++s) wf[s] = wn[s];
         }
       }
       if constexpr (DOT) {
@@ -179,6 +194,7 @@ __global__ __launch_bounds__(256) void expert_kernel(ExpertArgs a, int groups) {
         for (int i = 0; i < kListed; ++i)
           if (ex[i] == e) dots[wv][i16][kq + 4 * i] += dot;
       }
+      e = then;
     }
     if (a.out == nullptr || i16 >= nv) continue;
 #pragma unroll
@@ -255,7 +271,7 @@ hipError_t launch_transpose_weights(int64_t matrices, int C, bool bf16, const vo
 template <class S, int C, int NP, int CTW, bool DOT>
 static hipError_t expert_launch(const ExpertArgs& a) {
   const int groups = plane_groups(num_comp(a.lmax), NP), tasks = groups * ((C + 15) / 16 / CTW);
-  expert_kernel<S, C, NP, CTW, DOT><<<dim3((unsigned)((a.N + kTile - 1) / kTile)), dim3(64 * (tasks < 4 ? tasks : 4)), 0,
+  expert_kernel<S, C, NP, CTW, DOT><<<dim3((unsigned)((a.N + kTile - 1) / kTile)), dim3(64 * (tasks < 8 ? tasks : 8)), 0,
                                       a.stream>>>(a, groups);
   return hipGetLastError();
 }
@@ -264,7 +280,7 @@ static hipError_t expert_launch(const ExpertArgs& a) {
 // would not leave two waves' registers.
 template <class S, int C, int NP, bool DOT>
 static hipError_t expert_ctw(const ExpertArgs& a) {
-  constexpr int CT = (C + 15) / 16, MOST = NP == 8 ? 2 : 4;
+  constexpr int CT = (C + 15) / 16, MOST = 2;
   return expert_launch<S, C, NP, (CT < MOST ? CT : MOST), DOT>(a);
 }
 
