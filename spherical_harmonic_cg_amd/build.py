@@ -36,9 +36,12 @@ FLAGS = [
 
 # per-source additions: the radial edge-aligned kernel and the grad_vec kernel
 # consume their matrix-core results on the vector ALUs, so they are produced in
-# VGPRs (no copies out of the accumulation registers)
+# VGPRs (no copies out of the accumulation registers); the experts' kernels, too,
+# whose other values would spill while the accumulation half stays unused
 EXTRA_FLAGS = {"conv_so2.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
-               "conv_bwd.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
+               "conv_bwd.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
+               "expert.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
+               "expert_grad.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
 
 
 def _compile(src: str) -> str:

@@ -18,9 +18,11 @@
 // lanes of the nodes that have it.  Nodes in an order in which neighbours share
 // experts (expert_plan.hip) keep that list short; the results do not depend on
 // it.  Weights come from the L2, each once a wave and expert.
+#include <atomic>
 #include <type_traits>
 
 #include "expert_device.hpp"
+#include "lane_ops.hpp"
 
 namespace eqtp {
 
@@ -45,189 +47,267 @@ struct Operand<float> {
   }
 };
 
-// smallest of v over the wave
+typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
+
+// Smallest of v over the wave; sum over the lanes with the same i16 (both by register moves).
+template <int CTRL>
+__device__ __forceinline__ int dpp_min(int v) {
+  return min(v, __builtin_amdgcn_update_dpp(v, v, CTRL, 0xf, 0xf, false));
+}
 __device__ __forceinline__ int wave_min(int v) {
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) v = min(v, __shfl_xor(v, o, 64));
-  return __builtin_amdgcn_readfirstlane(v);
+  v = dpp_min<0x140>(dpp_min<0x141>(dpp_min<0x4E>(dpp_min<0xB1>(v))));
+  const auto a = __builtin_amdgcn_permlane16_swap((unsigned)v, (unsigned)v, false, false);
+  v = min((int)a[0], (int)a[1]);
+  const auto b = __builtin_amdgcn_permlane32_swap((unsigned)v, (unsigned)v, false, false);
+  return __builtin_amdgcn_readfirstlane(min((int)b[0], (int)b[1]));
+}
+__device__ __forceinline__ float rows_sum(float v) {
+  const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = __uint_as_float(a[0]) + __uint_as_float(a[1]);
+  const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(b[0]) + __uint_as_float(b[1]);
 }
 
 constexpr int kListed = kMaxTopK / 4;  // places of a node's list that a lane holds (lane (i, k): k, k + 4, ..)
 
-template <class S, int C, int NP, int CTW, bool DOT>
-__global__ __launch_bounds__(512) void expert_kernel(ExpertArgs a, int groups) {
-  using Op = Operand<S>;
-  typedef typename Op::V V;
-  typedef Run<S, NP> In;
-  constexpr int CT = (C + 15) / 16, CS = CT / CTW;
-  constexpr int STEP = 4 * Op::N;                       // input channels of a step
-  constexpr int NS = (C + STEP - 1) / STEP;
-  __shared__ float dots[DOT ? 8 : 1][kTile][kMaxTopK];
-  const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
-  const int i16 = lane & 15, kq = lane >> 4;
-  const int K = num_comp(a.lmax);
-  const int64_t p0 = (int64_t)blockIdx.x * kTile;
-  const int nv = (int)min((int64_t)kTile, a.N - p0);
-  const int64_t p = p0 + min(i16, nv - 1);
-  const int64_t node = a.order ? clamp_index(a.order[p], (int)a.N) : p;
+// The experts and gates of the lane's node (kMaxExperts: none).
+struct Listed {
   int ex[kListed];
   float gate[kListed];
+  __device__ __forceinline__ void load(const ExpertArgs& a, int64_t node, bool live, int kq) {
 #pragma unroll
-  for (int i = 0; i < kListed; ++i) {
-    const int j = kq + 4 * i;
-    ex[i] = kMaxExperts;
-    gate[i] = 0.0f;
-    if (j < a.k && i16 < nv) {
-      const int e = a.idx[node * a.k + j];
-      ex[i] = e >= 0 && e < a.X ? e : kMaxExperts;
-      gate[i] = a.weight ? a.weight[node * a.k + j] : 1.0f;
+    for (int i = 0; i < kListed; ++i) {
+      const int j = kq + 4 * i;
+      ex[i] = kMaxExperts;
+      gate[i] = 0.0f;
+      if (j < a.k && live) {
+        const int e = a.idx[node * a.k + j];
+        ex[i] = e >= 0 && e < a.X ? e : kMaxExperts;
+        gate[i] = a.weight ? a.weight[node * a.k + j] : 1.0f;
+      }
     }
   }
+  // the tile's lowest expert above e (whole waves)
+  __device__ __forceinline__ int after(int e) const {
+    int next = kMaxExperts;
+#pragma unroll
+    for (int i = 0; i < kListed; ++i) next = ex[i] > e ? min(next, ex[i]) : next;
+    return wave_min(next);
+  }
+  // whether the lane's node has e, and its gate
+  __device__ __forceinline__ bool has(int e, int i16, float& w) const {
+    bool mine = false;
+    w = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kListed; ++i)
+      if (ex[i] == e) {
+        w += gate[i];
+        mine = true;
+      }
+    w = rows_sum(w);
+    const uint64_t b = __ballot(mine);
+    return (unsigned)((b | b >> 16 | b >> 32 | b >> 48) >> i16) & 1u;
+  }
+};
+
+__host__ __device__ constexpr int staged_row(int C, int K, int es) { return C * K * es + 16; }  // bytes, 16 spread the banks
+constexpr int kStagedMost = 144 << 10;  // bytes of LDS for whole rows
+
+template <class S, int C, int L>
+struct ExpertCfg {
+  using Op = Operand<S>;
+  static constexpr bool BF16 = std::is_same<S, __bf16>::value;
+  static constexpr int K = num_comp(L), NP = planes_at_once(BF16, L), GROUPS = plane_groups(K, NP);
+  static constexpr int CT = (C + 15) / 16;                  // tiles of output channels
+  static constexpr int CTW = CT < 2 ? CT : (C == 128 && NP == 4 ? 4 : 2), CS = CT / CTW;  // of a wave; shares of waves
+  static constexpr int TASKS = GROUPS * CS, WAVES = TASKS < 8 ? TASKS : 8;
+  static constexpr int STEP = 4 * Op::N;                    // input channels of a step
+  static constexpr int NS = (C + STEP - 1) / STEP;
+  static constexpr int ROW = staged_row(C, K, sizeof(S));
+  // rows go through LDS where there is a wave for each task and they fit (in fp32, as the output may be)
+  static constexpr bool STAGED = TASKS <= 8 && kTile * staged_row(C, K, 4) <= kStagedMost;
+  static constexpr bool ALIGNED = K % NP == 0;
+  static constexpr int UNITS = C * K * (int)sizeof(S) / 16;  // 16-byte units of a row
+  static constexpr int U = (kTile * UNITS + 64 * WAVES - 1) / (64 * WAVES);  // of a tile, for a thread
+  typedef typename Op::V B[NS][NP];
+  typedef typename Run<S, NP>::R Held[CTW][4];
+  typedef f4 Total[CTW][NP];
+};
+
+// A wave's operands: B[s][q] holds component q of the group of this node's channels of step s.  row: the node's
+// features from the group's first component on.
+template <class S, int C, int L, bool ALIGNED>
+__device__ __forceinline__ void take_operands(const S* row, int kq, typename ExpertCfg<S, C, L>::B& B) {
+  using Cfg = ExpertCfg<S, C, L>;
+  using Op = Operand<S>;
+  constexpr int K = Cfg::K, NP = Cfg::NP;
+  typedef Run<S, NP, ALIGNED> In;
+#pragma unroll
+  for (int s = 0; s < Cfg::NS; ++s) {
+    const int c = s * Cfg::STEP + kq * Op::N;
+    if constexpr (NP == 1) {
+      B[s][0] = typename Op::V{};
+      if (c < C) B[s][0] = *reinterpret_cast<const typename Op::V*>(row + c);  // (rows are 16-byte aligned)
+    } else {
+      typename In::R r[Op::N];
+#pragma unroll
+      for (int i = 0; i < Op::N; ++i) r[i] = In::load(row + (c < C ? c + i : 0) * K);
+#pragma unroll
+      for (int q = 0; q < NP; ++q)
+#pragma unroll
+        for (int i = 0; i < Op::N; ++i) B[s][q][i] = c < C ? r[i][q] : (S)0.0f;
+    }
+  }
+}
+
+// The wave's products: total[t][q] = the sum over the tile's experts of the gate times D of output tile ct0 + t and
+// component m0 + q.  DOT: also the sums of D times what lies at the same places of `with`, by place of the node's
+// list, into dots [kTile][kMaxTopK]; components below dup are another wave's.
+template <class S, int C, int L, bool DOT>
+__device__ __forceinline__ void multiply(const ExpertArgs& a, const Listed& list, int m0, int dup, int ct0, int i16, int kq,
+                                         const typename ExpertCfg<S, C, L>::B& B, const typename ExpertCfg<S, C, L>::Held& held,
+                                         typename ExpertCfg<S, C, L>::Total& total, float (*dots)[kMaxTopK]) {
+  using Cfg = ExpertCfg<S, C, L>;
+  using Op = Operand<S>;
+  typedef typename Op::V V;
+  constexpr int NP = Cfg::NP, CTW = Cfg::CTW;
+#pragma unroll
+  for (int t = 0; t < CTW; ++t)
+#pragma unroll
+    for (int q = 0; q < NP; ++q) total[t][q] = f4{0.f, 0.f, 0.f, 0.f};
+  const int lf = degree_of_plane(m0), ll = degree_of_plane(m0 + NP - 1);
+  // a tile's weights of one expert and degree
+  auto weights = [&](V(&wf)[Cfg::NS], int e, int t, int l) {
+    const int co = (ct0 + t) * 16 + i16;
+    const S* wr = static_cast<const S*>(a.W) + (int64_t)(e * (L + 1) + l) * (C * C) + (co < C ? co : 0) * C;
+#pragma unroll
+    for (int s = 0; s < Cfg::NS; ++s) {
+      const int c = s * Cfg::STEP + kq * Op::N;
+      wf[s] = *reinterpret_cast<const V*>(wr + (c < C ? c : 0));
+      if constexpr (C % Cfg::STEP != 0) wf[s] = c < C ? wf[s] : V{};
+    }
+  };
+  int e = list.after(-1);
+  V wf[Cfg::NS];
+  weights(wf, min(e, a.X - 1), 0, lf);
+  while (e < kMaxExperts) {
+    const int then = list.after(e);
+    float w;
+    const bool has = list.has(e, i16, w);
+    float dot = 0.0f;
+#pragma unroll
+    for (int t = 0; t < CTW; ++t) {
+      for (int l = lf; l <= ll; ++l) {
+        // the weights after these are on their way while these are multiplied
+        const bool same = l < ll;
+        V wn[Cfg::NS];
+        weights(wn, same || t + 1 < CTW ? e : min(then, a.X - 1), same ? t : (t + 1 < CTW ? t + 1 : 0), same ? l + 1 : lf);
+#pragma unroll
+        for (int q = 0; q < NP; ++q) {
+          if (degree_of_plane(m0 + q) != l) continue;
+          f4 acc = f4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int s = 0; s < Cfg::NS; ++s) acc = Op::mul(wf[s], B[s][q], acc);
+#pragma unroll
+          for (int v = 0; v < 4; ++v) {
+            total[t][q][v] = has ? fmaf(w, acc[v], total[t][q][v]) : total[t][q][v];
+            if constexpr (DOT)
+              if (q >= dup && (ct0 + t) * 16 + 4 * kq + v < C) dot = fmaf(acc[v], (float)held[t][v][q], dot);
+          }
+        }
+#pragma unroll
+        for (int s = 0; s < Cfg::NS; ++s) wf[s] = wn[s];
+      }
+    }
+    if constexpr (DOT) {
+      dot = rows_sum(dot);
+#pragma unroll
+      for (int i = 0; i < kListed; ++i)
+        if (list.ex[i] == e) dots[i16][kq + 4 * i] += dot;
+    }
+    e = then;
+  }
+}
+
+// What the lane's results meet in the gates' gradient.
+template <class S, int C, int L>
+__device__ __forceinline__ void take_held(const S* row, int ct0, int kq, typename ExpertCfg<S, C, L>::Held& held) {
+  constexpr int K = ExpertCfg<S, C, L>::K, NP = ExpertCfg<S, C, L>::NP, CTW = ExpertCfg<S, C, L>::CTW;
+#pragma unroll
+  for (int t = 0; t < CTW; ++t)
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      const int c = (ct0 + t) * 16 + 4 * kq + v;
+      held[t][v] = Run<S, NP>::load(row + (c < C ? c : 0) * K);
+    }
+}
+
+// A lane's results of a tile: NP components (K = 1: one) of four channels.
+template <class O, int K, int NP, bool ALIGNED>
+__device__ __forceinline__ void put_runs(O* o, const f4 (&total)[NP]) {
+  if constexpr (NP == 1) {
+    typename Run<O, 4, ALIGNED>::R r;
+#pragma unroll
+    for (int v = 0; v < 4; ++v) r[v] = (O)total[0][v];
+    Run<O, 4, ALIGNED>::store(o, r);
+  } else {
+    constexpr int W = NP * (int)sizeof(O) > 16 ? 16 / (int)sizeof(O) : NP;
+#pragma unroll
+    for (int v = 0; v < 4; ++v)
+#pragma unroll
+      for (int q = 0; q < NP; q += W) {
+        typename Run<O, W, ALIGNED>::R r;
+#pragma unroll
+        for (int i = 0; i < W; ++i) r[i] = (O)total[q + i][v];
+        Run<O, W, ALIGNED>::store(o + v * K + q, r);
+      }
+  }
+}
+
+template <class S, int C, int L, bool ALIGNED>
+__device__ __forceinline__ void put_tiles(const ExpertArgs& a, unsigned char* row, int m0, int ct0, int kq,
+                                          const typename ExpertCfg<S, C, L>::Total& total) {
+  constexpr int K = ExpertCfg<S, C, L>::K, NP = ExpertCfg<S, C, L>::NP, CTW = ExpertCfg<S, C, L>::CTW;
+#pragma unroll
+  for (int t = 0; t < CTW; ++t) {
+    const int c = (ct0 + t) * 16 + 4 * kq;
+    if (c >= C) continue;
+    if (a.out_bf16) put_runs<__bf16, K, NP, ALIGNED>(reinterpret_cast<__bf16*>(row) + c * K + m0, total[t]);
+    else put_runs<float, K, NP, ALIGNED>(reinterpret_cast<float*>(row) + c * K + m0, total[t]);
+  }
+}
+
+__device__ __forceinline__ int64_t node_at(const ExpertArgs& a, int64_t p) {
+  return a.order ? clamp_index(a.order[p], (int)a.N) : p;
+}
+
+// Runs from and to memory: one tile a workgroup, its tasks (group of components, share of the channels) dealt to its waves.
+template <class S, int C, int L, bool DOT>
+__global__ __launch_bounds__(512) void expert_kernel(ExpertArgs a) {
+  using Cfg = ExpertCfg<S, C, L>;
+  constexpr int K = Cfg::K, NP = Cfg::NP, CTW = Cfg::CTW, waves = Cfg::WAVES;
+  __shared__ float dots[DOT ? 8 : 1][kTile][kMaxTopK];
+  const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int i16 = lane & 15, kq = lane >> 4;
+  const int64_t p0 = (int64_t)blockIdx.x * kTile;
+  const int nv = (int)min((int64_t)kTile, a.N - p0);
+  const int64_t node = node_at(a, p0 + min(i16, nv - 1));
+  Listed list;
+  list.load(a, node, i16 < nv, kq);
   if constexpr (DOT) {
     for (int i = lane; i < kTile * kMaxTopK; i += 64) (&dots[wv][0][0])[i] = 0.0f;
     wave_lds_sync();
   }
-
-  for (int task = wv; task < groups * CS; task += waves) {
-    const int g = task / CS, ct0 = (task - g * CS) * CTW;
-    const int m0 = group_first(g, K, NP), dup = g * NP - m0;  // components below dup are the group before's, too
-    // operands: B[s][p] holds this node's component m0 + p of the lane's channels of step s
-    V B[NS][NP];
-    const S* row = static_cast<const S*>(a.h) + node * C * K + m0;
-#pragma unroll
-    for (int s = 0; s < NS; ++s) {
-      const int c = s * STEP + kq * Op::N;
-      if constexpr (NP == 1) {
-        B[s][0] = V{};
-        if (c < C) B[s][0] = *reinterpret_cast<const V*>(row + c);
-      } else {
-        typename In::R r[Op::N];
-#pragma unroll
-        for (int i = 0; i < Op::N; ++i) r[i] = In::load(row + (c < C ? c + i : 0) * K);
-#pragma unroll
-        for (int q = 0; q < NP; ++q)
-#pragma unroll
-          for (int i = 0; i < Op::N; ++i) B[s][q][i] = c < C ? r[i][q] : (S)0.0f;
-      }
-    }
-    f4 total[CTW][NP];
-#pragma unroll
-    for (int t = 0; t < CTW; ++t)
-#pragma unroll
-      for (int q = 0; q < NP; ++q) total[t][q] = f4{0.f, 0.f, 0.f, 0.f};
-    // (the gates' gradient: what the lane's results meet)
-    typename In::R held[DOT ? CTW : 1][4];
-    if constexpr (DOT) {
-      const S* with = static_cast<const S*>(a.dot_with) + node * C * K + m0;
-#pragma unroll
-      for (int t = 0; t < CTW; ++t)
-#pragma unroll
-        for (int v = 0; v < 4; ++v) {
-          const int c = (ct0 + t) * 16 + 4 * kq + v;
-          held[t][v] = In::load(with + (c < C ? c : 0) * K);
-        }
-    }
-    const int lf = degree_of_plane(m0), ll = degree_of_plane(m0 + NP - 1);
-    // a tile's weights of one expert and degree
-    auto weights = [&](V(&wf)[NS], int e, int t, int l) {
-      const int co = (ct0 + t) * 16 + i16;
-      const S* wr = static_cast<const S*>(a.W) + (((int64_t)e * (a.lmax + 1) + l) * C + (co < C ? co : 0)) * C;
-#pragma unroll
-      for (int s = 0; s < NS; ++s) {
-        const int c = s * STEP + kq * Op::N;
-        wf[s] = *reinterpret_cast<const V*>(wr + (c < C ? c : 0));
-        if constexpr (C % STEP != 0) wf[s] = c < C ? wf[s] : V{};
-      }
-    };
-    auto after = [&](int e) {  // the next expert of the tile
-      int next = kMaxExperts;
-#pragma unroll
-      for (int i = 0; i < kListed; ++i) next = ex[i] > e ? min(next, ex[i]) : next;
-      return wave_min(next);
-    };
-    int e = after(-1);
-    V wf[NS];
-    weights(wf, min(e, a.X - 1), 0, lf);
-    while (e < kMaxExperts) {
-      const int then = after(e);
-      float w = 0.0f;
-      int has = 0;
-#pragma unroll
-      for (int i = 0; i < kListed; ++i)
-        if (ex[i] == e) {
-          w += gate[i];
-          has = 1;
-        }
-      w += __shfl_xor(w, 16, 64);
-      w += __shfl_xor(w, 32, 64);
-      has |= __shfl_xor(has, 16, 64);
-      has |= __shfl_xor(has, 32, 64);
-      float dot = 0.0f;
-#pragma unroll
-      for (int t = 0; t < CTW; ++t) {
-        for (int l = lf; l <= ll; ++l) {
-          // the weights after these are on their way while these are multiplied
-          const bool same = l < ll;
-          V wn[NS];
-          weights(wn, same || t + 1 < CTW ? e : min(then, a.X - 1), same ? t : (t + 1 < CTW ? t + 1 : 0), same ? l + 1 : lf);
-#pragma unroll
-          for (int q = 0; q < NP; ++q) {
-            if (degree_of_plane(m0 + q) != l) continue;
-            f4 acc = f4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int s = 0; s < NS; ++s) acc = Op::mul(wf[s], B[s][q], acc);
-#pragma unroll
-            for (int v = 0; v < 4; ++v) {
-              total[t][q][v] = has ? fmaf(w, acc[v], total[t][q][v]) : total[t][q][v];
-              if constexpr (DOT)
-                if (q >= dup && (ct0 + t) * 16 + 4 * kq + v < C) dot = fmaf(acc[v], (float)held[t][v][q], dot);
-            }
-          }
-#pragma unroll
-          for (int s = 0; s < NS; ++s) wf[s] = wn[s];
-        }
-      }
-      if constexpr (DOT) {
-        dot += __shfl_xor(dot, 16, 64);
-        dot += __shfl_xor(dot, 32, 64);
-#pragma unroll
-        for (int i = 0; i < kListed; ++i)
-          if (ex[i] == e) dots[wv][i16][kq + 4 * i] += dot;
-      }
-      e = then;
-    }
-    if (a.out == nullptr || i16 >= nv) continue;
-#pragma unroll
-    for (int t = 0; t < CTW; ++t) {
-      const int c = (ct0 + t) * 16 + 4 * kq;
-      if (c >= C) continue;
-      const int64_t at = (node * C + c) * K + m0;
-      if constexpr (NP == 1) {
-        if (a.out_bf16) {
-          Run<__bf16, 4>::R o;
-#pragma unroll
-          for (int v = 0; v < 4; ++v) o[v] = (__bf16)total[t][0][v];
-          Run<__bf16, 4>::store(static_cast<__bf16*>(a.out) + at, o);
-        } else {
-          Run<float, 4>::store(static_cast<float*>(a.out) + at, total[t][0]);
-        }
-      } else {
-#pragma unroll
-        for (int v = 0; v < 4; ++v) {
-          if (a.out_bf16) {
-            typename Run<__bf16, NP>::R o;
-#pragma unroll
-            for (int q = 0; q < NP; ++q) o[q] = (__bf16)total[t][q][v];
-            Run<__bf16, NP>::store(static_cast<__bf16*>(a.out) + at + v * K, o);
-          } else {
-#pragma unroll
-            for (int q = 0; q < NP; q += 4)
-              Run<float, 4>::store(static_cast<float*>(a.out) + at + v * K + q,
-                                   f4{total[t][q][v], total[t][q + 1][v], total[t][q + 2][v], total[t][q + 3][v]});
-          }
-        }
-      }
-    }
+  for (int task = wv; task < Cfg::TASKS; task += waves) {
+    const int g = task / Cfg::CS, ct0 = (task - g * Cfg::CS) * CTW, m0 = group_first(g, K, NP);
+    typename Cfg::B B;
+    typename Cfg::Held held;
+    typename Cfg::Total total;
+    take_operands<S, C, L, false>(static_cast<const S*>(a.h) + node * (C * K) + m0, kq, B);
+    if constexpr (DOT) take_held<S, C, L>(static_cast<const S*>(a.dot_with) + node * (C * K) + m0, ct0, kq, held);
+    multiply<S, C, L, DOT>(a, list, m0, g * NP - m0, ct0, i16, kq, B, held, total, dots[DOT ? wv : 0]);
+    if (a.out != nullptr && i16 < nv)
+      put_tiles<S, C, L, false>(a, static_cast<unsigned char*>(a.out) + node * (C * K * (a.out_bf16 ? 2 : 4)), m0, ct0, kq, total);
   }
   if constexpr (DOT) {
     __syncthreads();
@@ -235,9 +315,89 @@ __global__ __launch_bounds__(512) void expert_kernel(ExpertArgs a, int groups) {
       const int r = i / a.k, j = i - r * a.k;
       float v = 0.0f;
       for (int w = 0; w < waves; ++w) v += dots[w][r][j];
-      const int64_t n = a.order ? clamp_index(a.order[p0 + r], (int)a.N) : p0 + r;
-      a.gweight[n * a.k + j] = v;
+      a.gweight[node_at(a, p0 + r) * a.k + j] = v;
     }
+  }
+}
+
+// Runs from and to LDS, through which a workgroup moves its nodes' whole rows: a task a wave, tile after tile.  While a
+// tile is worked on, the next one's rows and lists are on their way into registers, and the order of the one after.
+template <class S, int C, int L, bool DOT>
+__global__ __launch_bounds__(512, 2) void expert_staged_kernel(ExpertArgs a, int64_t tiles) {
+  using Cfg = ExpertCfg<S, C, L>;
+  constexpr int K = Cfg::K, NP = Cfg::NP, CTW = Cfg::CTW, waves = Cfg::WAVES, U = Cfg::U, row_in = Cfg::ROW;
+  extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
+  __shared__ float dots[DOT ? waves : 1][kTile][kMaxTopK];
+  __shared__ int nid[2][kTile];
+  const int tid = threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int i16 = lane & 15, kq = lane >> 4;
+  const int row_out = staged_row(C, K, a.out_bf16 ? 2 : 4);
+  const int g = wv / Cfg::CS, ct0 = (wv - g * Cfg::CS) * CTW, m0 = group_first(g, K, NP);
+  u32x4 rows[U];
+  Listed list;
+  int ahead = 0;
+  auto ask_order = [&](int64_t tile) {  // nodes of a tile (its first one for places past the last)
+    if (tid < kTile && tile < tiles) {
+      const int64_t p = tile * kTile + tid;
+      ahead = (int)node_at(a, p < a.N ? p : tile * kTile);
+    }
+  };
+  auto ask_rows = [&](int64_t tile, const int* n) {
+    if (tile >= tiles) return;
+    const int nv = (int)min((int64_t)kTile, a.N - tile * kTile);
+#pragma unroll
+    for (int j = 0; j < U; ++j) {
+      const int i = tid + j * (64 * waves), r = i / Cfg::UNITS;
+      rows[j] = reinterpret_cast<const u32x4*>(a.h)[(int64_t)n[r < nv ? r : 0] * Cfg::UNITS + (i - r * Cfg::UNITS)];
+    }
+    list.load(a, n[i16], i16 < nv, kq);
+  };
+  int64_t tile = blockIdx.x;
+  ask_order(tile);
+  if (tid < kTile) nid[0][tid] = ahead;
+  __syncthreads();
+  ask_rows(tile, nid[0]);
+  ask_order(tile + gridDim.x);
+  for (int turn = 0; tile < tiles; tile += gridDim.x, turn ^= 1) {
+    const int nv = (int)min((int64_t)kTile, a.N - tile * kTile);
+#pragma unroll
+    for (int j = 0; j < U; ++j) {
+      const int i = tid + j * (64 * waves), r = i / Cfg::UNITS;
+      if (r < kTile) *reinterpret_cast<u32x4*>(lds + r * row_in + (i - r * Cfg::UNITS) * 16) = rows[j];
+    }
+    if (tid < kTile) nid[turn ^ 1][tid] = ahead;
+    if constexpr (DOT)
+      for (int i = lane; i < kTile * kMaxTopK; i += 64) (&dots[wv][0][0])[i] = 0.0f;
+    __syncthreads();
+    typename Cfg::B B;
+    typename Cfg::Held held;
+    typename Cfg::Total total;
+    if constexpr (DOT) take_held<S, C, L>(static_cast<const S*>(a.dot_with) + (int64_t)nid[turn][i16] * (C * K) + m0, ct0, kq, held);
+    take_operands<S, C, L, Cfg::ALIGNED>(reinterpret_cast<const S*>(lds + i16 * row_in) + m0, kq, B);
+    const Listed now = list;
+    ask_rows(tile + gridDim.x, nid[turn ^ 1]);
+    ask_order(tile + 2 * gridDim.x);
+    multiply<S, C, L, DOT>(a, now, m0, g * NP - m0, ct0, i16, kq, B, held, total, dots[DOT ? wv : 0]);
+    __syncthreads();  // every wave has its operands: the place takes the results
+    if (a.out != nullptr) put_tiles<S, C, L, Cfg::ALIGNED>(a, lds + i16 * row_out, m0, ct0, kq, total);
+    __syncthreads();
+    if (a.out != nullptr) {
+      const int out_units = row_out / 16 - 1;
+      for (int r = wv; r < nv; r += waves) {
+        u32x4* to = reinterpret_cast<u32x4*>(static_cast<unsigned char*>(a.out) + (int64_t)nid[turn][r] * (row_out - 16));
+        const u32x4* from = reinterpret_cast<const u32x4*>(lds + r * row_out);
+#pragma unroll 4
+        for (int i = lane; i < out_units; i += 64) to[i] = from[i];
+      }
+    }
+    if constexpr (DOT)
+      for (int i = tid; i < nv * a.k; i += blockDim.x) {
+        const int r = i / a.k, j = i - r * a.k;
+        float v = 0.0f;
+        for (int w = 0; w < waves; ++w) v += dots[w][r][j];
+        a.gweight[(int64_t)nid[turn][r] * a.k + j] = v;
+      }
+    __syncthreads();  // the next tile's rows come into the same place
   }
 }
 
@@ -268,44 +428,61 @@ hipError_t launch_transpose_weights(int64_t matrices, int C, bool bf16, const vo
   return hipGetLastError();
 }
 
-template <class S, int C, int NP, int CTW, bool DOT>
+template <class S, int C, int L, bool DOT>
 static hipError_t expert_launch(const ExpertArgs& a) {
-  const int groups = plane_groups(num_comp(a.lmax), NP), tasks = groups * ((C + 15) / 16 / CTW);
-  expert_kernel<S, C, NP, CTW, DOT><<<dim3((unsigned)((a.N + kTile - 1) / kTile)), dim3(64 * (tasks < 8 ? tasks : 8)), 0,
-                                      a.stream>>>(a, groups);
+  using Cfg = ExpertCfg<S, C, L>;
+  const int64_t tiles = (a.N + kTile - 1) / kTile;
+  if constexpr (Cfg::STAGED) {
+    const int bytes = kTile * (a.out && !a.out_bf16 ? staged_row(C, Cfg::K, 4) : Cfg::ROW);
+    static std::atomic<int> known[2];  // workgroups that a compute unit holds
+    std::atomic<int>& held = known[a.out && !a.out_bf16];
+    int n = held.load(std::memory_order_relaxed);
+    if (n == 0) {
+      if (hipOccupancyMaxActiveBlocksPerMultiprocessor(&n, expert_staged_kernel<S, C, L, DOT>, 64 * Cfg::WAVES, bytes) != hipSuccess ||
+          n < 1)
+        n = 1;
+      held.store(n, std::memory_order_relaxed);
+    }
+    // as many workgroups as the card holds, all with the same number of tiles
+    const int64_t most = (int64_t)num_cus() * n, each = (tiles + most - 1) / most;
+    expert_staged_kernel<S, C, L, DOT>
+        <<<dim3((unsigned)((tiles + each - 1) / each)), dim3(64 * Cfg::WAVES), bytes, a.stream>>>(a, tiles);
+  } else {
+    expert_kernel<S, C, L, DOT><<<dim3((unsigned)tiles), dim3(64 * Cfg::WAVES), 0, a.stream>>>(a);
+  }
   return hipGetLastError();
 }
 
-// Output tiles of a wave: all of them up to C = 64, so that a tile's features are read once; fewer where the totals
-// would not leave two waves' registers.
-template <class S, int C, int NP, bool DOT>
-static hipError_t expert_ctw(const ExpertArgs& a) {
-  constexpr int CT = (C + 15) / 16, MOST = 2;
-  return expert_launch<S, C, NP, (CT < MOST ? CT : MOST), DOT>(a);
-}
-
-template <class S, int NP, bool DOT>
+template <class S, int L, bool DOT>
 static hipError_t expert_c(const ExpertArgs& a) {
   switch (a.C) {
-    case 8: return expert_ctw<S, 8, NP, DOT>(a);
-    case 16: return expert_ctw<S, 16, NP, DOT>(a);
-    case 32: return expert_ctw<S, 32, NP, DOT>(a);
-    case 64: return expert_ctw<S, 64, NP, DOT>(a);
-    case 128: return expert_ctw<S, 128, NP, DOT>(a);
+    case 8: return expert_launch<S, 8, L, DOT>(a);
+    case 16: return expert_launch<S, 16, L, DOT>(a);
+    case 32: return expert_launch<S, 32, L, DOT>(a);
+    case 64: return expert_launch<S, 64, L, DOT>(a);
+    case 128: return expert_launch<S, 128, L, DOT>(a);
     default: return hipErrorInvalidValue;
   }
 }
 
-template <bool DOT>
-static hipError_t expert_np(const ExpertArgs& a) {
-  const int np = planes_at_once(a.bf16, a.lmax);
-  if (a.bf16) return np == 1 ? expert_c<__bf16, 1, DOT>(a) : (np == 4 ? expert_c<__bf16, 4, DOT>(a) : expert_c<__bf16, 8, DOT>(a));
-  return np == 1 ? expert_c<float, 1, DOT>(a) : expert_c<float, 4, DOT>(a);
+template <class S, bool DOT>
+static hipError_t expert_l(const ExpertArgs& a) {
+  switch (a.lmax) {
+    case 0: return expert_c<S, 0, DOT>(a);
+    case 1: return expert_c<S, 1, DOT>(a);
+    case 2: return expert_c<S, 2, DOT>(a);
+    case 3: return expert_c<S, 3, DOT>(a);
+    case 4: return expert_c<S, 4, DOT>(a);
+    case 5: return expert_c<S, 5, DOT>(a);
+    case 6: return expert_c<S, 6, DOT>(a);
+    default: return hipErrorInvalidValue;
+  }
 }
 
 hipError_t launch_expert(const ExpertArgs& a) {
   if (a.N == 0) return hipSuccess;
-  return a.gweight ? expert_np<true>(a) : expert_np<false>(a);
+  if (a.gweight) return a.bf16 ? expert_l<__bf16, true>(a) : expert_l<float, true>(a);
+  return a.bf16 ? expert_l<__bf16, false>(a) : expert_l<float, false>(a);
 }
 
 }  // namespace eqtp

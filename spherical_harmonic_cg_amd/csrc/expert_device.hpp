@@ -13,10 +13,10 @@ __device__ __forceinline__ int degree_of_plane(int m) {
   return m >= 9 ? (m >= 25 ? (m >= 36 ? 6 : 5) : (m >= 16 ? 4 : 3)) : (m >= 4 ? 2 : (m >= 1 ? 1 : 0));
 }
 
-// NP consecutive elements, aligned as one element only
-template <class S, int NP>
+// NP consecutive elements, aligned as a whole, or as one element only
+template <class S, int NP, bool ALIGNED = false>
 struct Run {
-  typedef S V __attribute__((ext_vector_type(NP), aligned(sizeof(S))));
+  typedef S V __attribute__((ext_vector_type(NP), aligned(ALIGNED ? NP * sizeof(S) : sizeof(S))));
   typedef S R __attribute__((ext_vector_type(NP)));
   static __device__ __forceinline__ R load(const S* p) { return *reinterpret_cast<const V*>(p); }
   static __device__ __forceinline__ void store(S* p, const R& v) { *reinterpret_cast<V*>(p) = v; }
