@@ -176,38 +176,41 @@ __device__ __forceinline__ void multiply(const ExpertArgs& a, const Listed& list
 #pragma unroll
     for (int q = 0; q < NP; ++q) total[t][q] = f4{0.f, 0.f, 0.f, 0.f};
   const int lf = degree_of_plane(m0), ll = degree_of_plane(m0 + NP - 1);
-  // a tile's weights of one expert and degree
-  auto weights = [&](V(&wf)[Cfg::NS], int e, int t, int l) {
-    const int co = (ct0 + t) * 16 + i16;
-    const S* wr = static_cast<const S*>(a.W) + (int64_t)(e * (L + 1) + l) * (C * C) + (co < C ? co : 0) * C;
+  // the wave's weights of one expert and degree
+  typedef V Weights[CTW][Cfg::NS];
+  auto weights = [&](Weights& wf, int e, int l) {
+    const S* We = static_cast<const S*>(a.W) + (int64_t)(e * (L + 1) + l) * (C * C);
 #pragma unroll
-    for (int s = 0; s < Cfg::NS; ++s) {
-      const int c = s * Cfg::STEP + kq * Op::N;
-      wf[s] = *reinterpret_cast<const V*>(wr + (c < C ? c : 0));
-      if constexpr (C % Cfg::STEP != 0) wf[s] = c < C ? wf[s] : V{};
+    for (int t = 0; t < CTW; ++t) {
+      const int co = (ct0 + t) * 16 + i16;
+#pragma unroll
+      for (int s = 0; s < Cfg::NS; ++s) {
+        const int c = s * Cfg::STEP + kq * Op::N;
+        wf[t][s] = *reinterpret_cast<const V*>(We + (co < C ? co : 0) * C + (c < C ? c : 0));
+        if constexpr (C % Cfg::STEP != 0) wf[t][s] = c < C ? wf[t][s] : V{};
+      }
     }
   };
   int e = list.after(-1);
-  V wf[Cfg::NS];
-  weights(wf, min(e, a.X - 1), 0, lf);
+  Weights wf;
+  weights(wf, min(e, a.X - 1), lf);
   while (e < kMaxExperts) {
     const int then = list.after(e);
     float w;
     const bool has = list.has(e, i16, w);
     float dot = 0.0f;
+    for (int l = lf; l <= ll; ++l) {
+      // the weights after these are on their way while these are multiplied
+      Weights wn;
+      weights(wn, l < ll ? e : min(then, a.X - 1), l < ll ? l + 1 : lf);
 #pragma unroll
-    for (int t = 0; t < CTW; ++t) {
-      for (int l = lf; l <= ll; ++l) {
-        // the weights after these are on their way while these are multiplied
-        const bool same = l < ll;
-        V wn[Cfg::NS];
-        weights(wn, same || t + 1 < CTW ? e : min(then, a.X - 1), same ? t : (t + 1 < CTW ? t + 1 : 0), same ? l + 1 : lf);
+      for (int q = 0; q < NP; ++q) {
+        if (degree_of_plane(m0 + q) != l) continue;
 #pragma unroll
-        for (int q = 0; q < NP; ++q) {
-          if (degree_of_plane(m0 + q) != l) continue;
+        for (int t = 0; t < CTW; ++t) {
           f4 acc = f4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int s = 0; s < Cfg::NS; ++s) acc = Op::mul(wf[s], B[s][q], acc);
+          for (int s = 0; s < Cfg::NS; ++s) acc = Op::mul(wf[t][s], B[s][q], acc);
 #pragma unroll
           for (int v = 0; v < 4; ++v) {
             total[t][q][v] = has ? fmaf(w, acc[v], total[t][q][v]) : total[t][q][v];
@@ -215,9 +218,11 @@ __device__ __forceinline__ void multiply(const ExpertArgs& a, const Listed& list
               if (q >= dup && (ct0 + t) * 16 + 4 * kq + v < C) dot = fmaf(acc[v], (float)held[t][v][q], dot);
           }
         }
-#pragma unroll
-        for (int s = 0; s < Cfg::NS; ++s) wf[s] = wn[s];
       }
+#pragma unroll
+      for (int t = 0; t < CTW; ++t)
+#pragma unroll
+        for (int s = 0; s < Cfg::NS; ++s) wf[t][s] = wn[t][s];
     }
     if constexpr (DOT) {
       dot = rows_sum(dot);
@@ -401,6 +406,172 @@ __global__ __launch_bounds__(512, 2) void expert_staged_kernel(ExpertArgs a, int
   }
 }
 
+// fp32: a tile a workgroup, its rows in LDS; a wave reads its operands from there 16 input channels at a time, just
+// before their products.
+// ONE: a node has one expert at most and no gate, and the products go straight into the totals (the same bits).
+template <int C, int L, bool DOT, bool ONE>
+__device__ __forceinline__ void multiply_steps(const ExpertArgs& a, const Listed& list, const float* row, int m0, int dup, int ct0,
+                                               int i16, int kq, const typename ExpertCfg<float, C, L>::Held& held,
+                                               typename ExpertCfg<float, C, L>::Total& total, float (*dots)[kMaxTopK]) {
+  using Cfg = ExpertCfg<float, C, L>;
+  typedef Run<float, Cfg::NP, Cfg::ALIGNED> In;
+  constexpr int K = Cfg::K, NP = Cfg::NP, CTW = Cfg::CTW, NL = NP == 1 ? 1 : 2;  // (four components: two degrees at most)
+  const int lf = degree_of_plane(m0), ll = degree_of_plane(m0 + NP - 1);
+  typedef f4 Weights[NL][CTW];
+  auto weights = [&](Weights& wf, int e, int s) {
+    const int c = s * 16 + kq * 4;
+#pragma unroll
+    for (int d = 0; d < NL; ++d) {
+      const float* We = static_cast<const float*>(a.W) + (int64_t)(e * (L + 1) + (d == 0 ? lf : ll)) * (C * C) + (c < C ? c : 0);
+#pragma unroll
+      for (int t = 0; t < CTW; ++t) {
+        const int co = (ct0 + t) * 16 + i16;
+        wf[d][t] = *reinterpret_cast<const f4*>(We + (co < C ? co : 0) * C);
+        if constexpr (C % 16 != 0) wf[d][t] = c < C ? wf[d][t] : f4{0.f, 0.f, 0.f, 0.f};
+      }
+    }
+  };
+#pragma unroll
+  for (int t = 0; t < CTW; ++t)
+#pragma unroll
+    for (int q = 0; q < NP; ++q) total[t][q] = f4{0.f, 0.f, 0.f, 0.f};
+  int e = list.after(-1);
+  Weights wf;
+  weights(wf, min(e, a.X - 1), 0);
+  while (e < kMaxExperts) {
+    const int then = list.after(e);
+    float w;
+    const bool has = list.has(e, i16, w);
+    typename Cfg::Total apart;
+    if constexpr (!ONE) {
+#pragma unroll
+      for (int t = 0; t < CTW; ++t)
+#pragma unroll
+        for (int q = 0; q < NP; ++q) apart[t][q] = f4{0.f, 0.f, 0.f, 0.f};
+    }
+    typename Cfg::Total& into = ONE ? total : apart;
+#pragma unroll 2
+    for (int s = 0; s < Cfg::NS; ++s) {
+      Weights wn;  // on their way while these are multiplied
+      weights(wn, s + 1 < Cfg::NS ? e : min(then, a.X - 1), s + 1 < Cfg::NS ? s + 1 : 0);
+      const int c = s * 16 + kq * 4;
+      float x[4][NP];
+      if constexpr (NP == 1) {
+        const f4 r = *reinterpret_cast<const f4*>(row + (c < C ? c : 0));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i][0] = r[i];
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const typename In::R r = In::load(row + (c < C ? c + i : 0) * K);
+#pragma unroll
+          for (int q = 0; q < NP; ++q) x[i][q] = r[q];
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int q = 0; q < NP; ++q) {
+          if constexpr (ONE) x[i][q] = has ? x[i][q] : 0.0f;
+          if constexpr (C % 16 != 0) x[i][q] = c < C ? x[i][q] : 0.0f;
+        }
+#pragma unroll
+      for (int q = 0; q < NP; ++q) {
+        if (NL == 1 || degree_of_plane(m0 + q) == lf) {
+#pragma unroll
+          for (int t = 0; t < CTW; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) into[t][q] = __builtin_amdgcn_mfma_f32_16x16x4f32(wf[0][t][i], x[i][q], into[t][q], 0, 0, 0);
+        } else {
+#pragma unroll
+          for (int t = 0; t < CTW; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              into[t][q] = __builtin_amdgcn_mfma_f32_16x16x4f32(wf[NL - 1][t][i], x[i][q], into[t][q], 0, 0, 0);
+        }
+      }
+#pragma unroll
+      for (int d = 0; d < NL; ++d)
+#pragma unroll
+        for (int t = 0; t < CTW; ++t) wf[d][t] = wn[d][t];
+    }
+    float dot = 0.0f;
+#pragma unroll
+    for (int t = 0; t < CTW; ++t)
+#pragma unroll
+      for (int q = 0; q < NP; ++q)
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          if constexpr (!ONE) total[t][q][v] = has ? fmaf(w, apart[t][q][v], total[t][q][v]) : total[t][q][v];
+          if constexpr (DOT)
+            if (q >= dup && (ct0 + t) * 16 + 4 * kq + v < C) dot = fmaf(apart[t][q][v], held[t][v][q], dot);
+        }
+    if constexpr (DOT) {
+      dot = rows_sum(dot);
+#pragma unroll
+      for (int i = 0; i < kListed; ++i)
+        if (list.ex[i] == e) dots[i16][kq + 4 * i] += dot;
+    }
+    e = then;
+  }
+}
+
+template <int C, int L, bool DOT, bool ONE>
+__global__ __launch_bounds__(512) void expert_f32_kernel(ExpertArgs a) {
+  using Cfg = ExpertCfg<float, C, L>;
+  constexpr int K = Cfg::K, NP = Cfg::NP, CTW = Cfg::CTW, waves = Cfg::WAVES, U = Cfg::U, row_in = Cfg::ROW;
+  extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
+  __shared__ float dots[DOT ? waves : 1][kTile][kMaxTopK];
+  const int tid = threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int i16 = lane & 15, kq = lane >> 4;
+  const int g = wv / Cfg::CS, ct0 = (wv - g * Cfg::CS) * CTW, m0 = group_first(g, K, NP);
+  const int64_t p0 = (int64_t)blockIdx.x * kTile;
+  const int nv = (int)min((int64_t)kTile, a.N - p0);
+  {
+    u32x4 rows[U];
+#pragma unroll
+    for (int j = 0; j < U; ++j) {
+      const int i = tid + j * (64 * waves), r = i / Cfg::UNITS;
+      rows[j] = reinterpret_cast<const u32x4*>(a.h)[node_at(a, p0 + (r < nv ? r : 0)) * Cfg::UNITS + (i - r * Cfg::UNITS)];
+    }
+#pragma unroll
+    for (int j = 0; j < U; ++j) {
+      const int i = tid + j * (64 * waves), r = i / Cfg::UNITS;
+      if (r < kTile) *reinterpret_cast<u32x4*>(lds + r * row_in + (i - r * Cfg::UNITS) * 16) = rows[j];
+    }
+  }
+  const int64_t node = node_at(a, p0 + min(i16, nv - 1));
+  Listed list;
+  list.load(a, node, i16 < nv, kq);
+  if constexpr (DOT)
+    for (int i = lane; i < kTile * kMaxTopK; i += 64) (&dots[wv][0][0])[i] = 0.0f;
+  typename Cfg::Held held;
+  typename Cfg::Total total;
+  if constexpr (DOT) take_held<float, C, L>(static_cast<const float*>(a.dot_with) + node * (C * K) + m0, ct0, kq, held);
+  __syncthreads();
+  multiply_steps<C, L, DOT, ONE>(a, list, reinterpret_cast<const float*>(lds + i16 * row_in) + m0, m0, g * NP - m0, ct0, i16, kq, held,
+                            total, dots[DOT ? wv : 0]);
+  __syncthreads();  // every wave has read its operands: the place takes the results
+  if (a.out != nullptr) {
+    const int row_out = staged_row(C, K, a.out_bf16 ? 2 : 4), units = row_out / 16 - 1;
+    put_tiles<float, C, L, Cfg::ALIGNED>(a, lds + i16 * row_out, m0, ct0, kq, total);
+    __syncthreads();
+    for (int r = wv; r < nv; r += waves) {
+      u32x4* to = reinterpret_cast<u32x4*>(static_cast<unsigned char*>(a.out) + node_at(a, p0 + r) * (row_out - 16));
+      const u32x4* from = reinterpret_cast<const u32x4*>(lds + r * row_out);
+#pragma unroll 4
+      for (int i = lane; i < units; i += 64) to[i] = from[i];
+    }
+  }
+  if constexpr (DOT)
+    for (int i = tid; i < nv * a.k; i += blockDim.x) {
+      const int r = i / a.k, j = i - r * a.k;
+      float v = 0.0f;
+      for (int w = 0; w < waves; ++w) v += dots[w][r][j];
+      a.gweight[node_at(a, p0 + r) * a.k + j] = v;
+    }
+}
+
 // WT[i][c][c'] = W[i][c'][c] for each of `matrices` C x C matrices
 template <class S>
 __global__ __launch_bounds__(256) void transpose_weights_kernel(int64_t matrices, int C, const S* __restrict__ W,
@@ -432,7 +603,16 @@ template <class S, int C, int L, bool DOT>
 static hipError_t expert_launch(const ExpertArgs& a) {
   using Cfg = ExpertCfg<S, C, L>;
   const int64_t tiles = (a.N + kTile - 1) / kTile;
-  if constexpr (Cfg::STAGED) {
+  if constexpr (Cfg::STAGED && !Cfg::BF16) {
+    const dim3 grid((unsigned)tiles), block(64 * Cfg::WAVES);
+    if constexpr (!DOT) {
+      if (a.k == 1 && a.weight == nullptr) {
+        expert_f32_kernel<C, L, DOT, true><<<grid, block, kTile * Cfg::ROW, a.stream>>>(a);
+        return hipGetLastError();
+      }
+    }
+    expert_f32_kernel<C, L, DOT, false><<<grid, block, kTile * Cfg::ROW, a.stream>>>(a);
+  } else if constexpr (Cfg::STAGED && !DOT) {
     const int bytes = kTile * (a.out && !a.out_bf16 ? staged_row(C, Cfg::K, 4) : Cfg::ROW);
     static std::atomic<int> known[2];  // workgroups that a compute unit holds
     std::atomic<int>& held = known[a.out && !a.out_bf16];

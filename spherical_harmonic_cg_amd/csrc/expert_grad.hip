@@ -155,13 +155,15 @@ struct ExpertGradCfg {
   static constexpr int SPLITS = (CT / RT) * (CT / CTC);
 };
 
+constexpr int kGradWaves = 4;  // of a workgroup: they share a chunk
+
 // LMAX: 0 to 3, the degrees of the first stretch; 4 to 6, one degree
 template <class S, int C, bool GATES, int LMAX>
-__device__ __forceinline__ void expert_grad_walk(const ExpertGradArgs& a, const ChunkOf& ch, int split, float* line) {
+__device__ __forceinline__ void expert_grad_walk(const ExpertGradArgs& a, const ChunkOf& ch, int split, float* line, float* lds) {
   using Cfg = ExpertGradCfg<C>;
   constexpr int RT = Cfg::RT, CTC = Cfg::CTC;
   constexpr int L0 = LMAX <= 3 ? 0 : LMAX, LN = LMAX - L0 + 1, NPL = LMAX <= 3 ? (LMAX + 1) * (LMAX + 1) : 2 * LMAX + 1;
-  const int K = num_comp(a.lmax), lane = threadIdx.x & 63, i16 = lane & 15, kq = lane >> 4;
+  const int K = num_comp(a.lmax), lane = threadIdx.x & 63, wv = threadIdx.x >> 6, i16 = lane & 15, kq = lane >> 4;
   const int rt = split / (Cfg::CT / CTC) * RT, cc = split % (Cfg::CT / CTC) * CTC;
   f4 acc[LN][RT][CTC];
 #pragma unroll
@@ -172,13 +174,13 @@ __device__ __forceinline__ void expert_grad_walk(const ExpertGradArgs& a, const 
       for (int t = 0; t < CTC; ++t) acc[l][r][t] = f4{0.f, 0.f, 0.f, 0.f};
   const int last = (int)min(a.N * a.k, (int64_t)0x7fffffff);
   for (int64_t s0 = ch.s0; s0 < ch.s1; s0 += 64) {
-    // 64 places, one a lane: node and gate
+    // 64 places, one a lane: node and gate; the waves take turns with the fours of them
     const int64_t mine = min(s0 + lane, ch.s1 - 1);
     const int slot = clamp_index(a.slots[mine], last);
     const int my_node = slot / a.k;
     const float my_gate = GATES ? a.weight[slot] : 1.0f;
     const int steps = (int)min((int64_t)16, (ch.s1 - s0 + 3) / 4);
-    for (int st = 0; st < steps; ++st) {
+    for (int st = wv; st < steps; st += kGradWaves) {
       const int from = 4 * st + kq;
       const int64_t node = __shfl(my_node, from, 64);
       const float w = __shfl(my_gate, from, 64);
@@ -208,6 +210,30 @@ __device__ __forceinline__ void expert_grad_walk(const ExpertGradArgs& a, const 
           }
     }
   }
+  // the waves' sums, one wave after the other (in order) into the first one's, a degree at a time
+#pragma unroll
+  for (int l = 0; l < LN; ++l) {
+    constexpr int REGS = RT * CTC * 4;
+    __syncthreads();
+    if (wv > 0)
+#pragma unroll
+      for (int r = 0; r < RT; ++r)
+#pragma unroll
+        for (int t = 0; t < CTC; ++t)
+#pragma unroll
+          for (int v = 0; v < 4; ++v) lds[((wv - 1) * REGS + (r * CTC + t) * 4 + v) * 64 + lane] = acc[l][r][t][v];
+    __syncthreads();
+    if (wv == 0)
+#pragma unroll
+      for (int w = 0; w < kGradWaves - 1; ++w)
+#pragma unroll
+        for (int r = 0; r < RT; ++r)
+#pragma unroll
+          for (int t = 0; t < CTC; ++t)
+#pragma unroll
+            for (int v = 0; v < 4; ++v) acc[l][r][t][v] += lds[(w * REGS + (r * CTC + t) * 4 + v) * 64 + lane];
+  }
+  if (wv > 0) return;
   // lane (i16, kq) holds D[c' = 4 kq + v][c = i16] of each tile
 #pragma unroll
   for (int l = 0; l < LN; ++l)
@@ -222,10 +248,11 @@ __device__ __forceinline__ void expert_grad_walk(const ExpertGradArgs& a, const 
         }
 }
 
-// a wave a workgroup: the splits of a chunk beside each other, on one XCD (workgroups go round the eight)
+// The splits of a chunk beside each other, on one XCD (workgroups go round the eight).
 template <class S, int C, bool GATES>
-__global__ __launch_bounds__(64) void expert_grad_kernel(ExpertGradArgs a, int per, int lines) {
+__global__ __launch_bounds__(64 * kGradWaves) void expert_grad_kernel(ExpertGradArgs a, int per, int lines) {
   constexpr int SPLITS = ExpertGradCfg<C>::SPLITS;
+  __shared__ float lds[(kGradWaves - 1) * ExpertGradCfg<C>::RT * ExpertGradCfg<C>::CTC * 4 * 64];
   const int round = blockIdx.x / (8 * SPLITS), in = blockIdx.x % (8 * SPLITS);
   const int chunk = round * 8 + in % 8, split = in / 8;
   if (chunk >= lines) return;
@@ -233,13 +260,13 @@ __global__ __launch_bounds__(64) void expert_grad_kernel(ExpertGradArgs a, int p
   if (ch.x < 0) return;
   float* line = a.part + (int64_t)chunk * (a.lmax + 1) * C * C;
   switch (blockIdx.y == 0 ? min(a.lmax, 3) : blockIdx.y + 3) {
-    case 0: expert_grad_walk<S, C, GATES, 0>(a, ch, split, line); break;
-    case 1: expert_grad_walk<S, C, GATES, 1>(a, ch, split, line); break;
-    case 2: expert_grad_walk<S, C, GATES, 2>(a, ch, split, line); break;
-    case 3: expert_grad_walk<S, C, GATES, 3>(a, ch, split, line); break;
-    case 4: expert_grad_walk<S, C, GATES, 4>(a, ch, split, line); break;
-    case 5: expert_grad_walk<S, C, GATES, 5>(a, ch, split, line); break;
-    default: expert_grad_walk<S, C, GATES, 6>(a, ch, split, line); break;
+    case 0: expert_grad_walk<S, C, GATES, 0>(a, ch, split, line, lds); break;
+    case 1: expert_grad_walk<S, C, GATES, 1>(a, ch, split, line, lds); break;
+    case 2: expert_grad_walk<S, C, GATES, 2>(a, ch, split, line, lds); break;
+    case 3: expert_grad_walk<S, C, GATES, 3>(a, ch, split, line, lds); break;
+    case 4: expert_grad_walk<S, C, GATES, 4>(a, ch, split, line, lds); break;
+    case 5: expert_grad_walk<S, C, GATES, 5>(a, ch, split, line, lds); break;
+    default: expert_grad_walk<S, C, GATES, 6>(a, ch, split, line, lds); break;
   }
 }
 
@@ -267,13 +294,17 @@ __global__ __launch_bounds__(256) void expert_grad_sum_kernel(ExpertGradArgs a, 
     }
   }
   __syncthreads();
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= size) return;
+  // 64 columns and four stretches of lines a workgroup
+  __shared__ double part[4][64];
+  const int c = threadIdx.x & 63, k = threadIdx.x >> 6;
+  const int64_t i = (int64_t)blockIdx.x * 64 + c;  // (the lines' length is a multiple of 64)
   const float* p = a.part + begin * size + i;
   double s = 0.0;
 #pragma unroll 8
-  for (int j = 0; j < count; ++j) s += p[j * size];
-  a.gW[blockIdx.y * size + i] = (float)s;
+  for (int j = k; j < count; j += 4) s += p[j * size];
+  part[k][c] = s;
+  __syncthreads();
+  if (k == 0) a.gW[blockIdx.y * size + i] = (float)((part[0][c] + part[1][c]) + (part[2][c] + part[3][c]));
 }
 
 // Places of a chunk: enough that a chunk's line is a small part of what it reads, and about 1024 chunks at most.
@@ -300,10 +331,10 @@ static hipError_t expert_grad_launch(const ExpertGradArgs& a) {
   const int64_t chunks = chunks_at_most(a.N, a.C, a.lmax, a.X, a.k, a.bf16), size = (int64_t)(a.lmax + 1) * C * C;
   if (chunks > 0)
     expert_grad_kernel<S, C, GATES><<<dim3((unsigned)((chunks + 7) / 8 * 8 * ExpertGradCfg<C>::SPLITS), stretches_of(a.lmax)),
-                                      dim3(64), 0, a.stream>>>(a, per, (int)chunks);
+                                      dim3(64 * kGradWaves), 0, a.stream>>>(a, per, (int)chunks);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  expert_grad_sum_kernel<<<dim3((unsigned)((size + 255) / 256), a.X), dim3(256), 0, a.stream>>>(a, per, size, (int)chunks);
+  expert_grad_sum_kernel<<<dim3((unsigned)(size / 64), a.X), dim3(256), 0, a.stream>>>(a, per, size, (int)chunks);
   return hipGetLastError();
 }
 
