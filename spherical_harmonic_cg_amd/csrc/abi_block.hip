@@ -26,7 +26,7 @@ eqtp::BiasArgs bias_args(const eqtp_bias_desc* d, int64_t E, const float* vec, c
   a.E = E;
   a.H = d->heads;
   a.B = d->buckets;
-  for (int s = 1; s < d->buckets; s *= 2) a.first_step = s;
+  for (int s = 1; s < d->buckets; s *= 4) a.first_step = s;
   a.cut2 = d->r_cut > 0.0f ? (double)d->r_cut * (double)d->r_cut : NAN;
   a.vec = vec;
   a.bounds = bounds;

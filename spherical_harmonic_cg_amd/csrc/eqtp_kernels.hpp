@@ -160,7 +160,7 @@ struct AttnGradArgs {
 struct BiasArgs {
   int64_t E;
   int H, B;
-  int first_step;         // largest power of two below B (0 for B = 1)
+  int first_step;         // largest power of four below B (0 for B = 1)
   double cut2;            // square of the cut-off, NaN for none
   const float* vec;
   const float* bounds;    // [B - 1]
