@@ -8,194 +8,279 @@
 // practice by the choice's instructions.  A node's experts lie eight by eight
 // in G lanes (G = 1 for up to 8 experts, 32 for 256), so a wave works on 64 / G
 // nodes and a round of the choice costs each lane eight comparisons and log2 G
-// exchanges.  v is held in 64 bits: an expert that leads by a hair leads here
-// as in the formula.
+// exchanges.
+//
+// An expert that leads by a hair has to lead as in the formula, whatever fp32
+// makes of it.  The choice is made in fp32 and looked at: an fp32 v is off by
+// 2^-20 (1 + the largest |bias|) at most (the hardware's exponential and
+// reciprocal, a step each, their arguments, the sum and the bias), so where every one taken leads the next by more than
+// twice that, and open groups the closed ones by four times, it is the
+// formula's.  Where not -- one node in some thousands, or equal scores -- the
+// wave chooses again in 64 bits, with the index beside the value.
 #include "norm_device.hpp"
 
 namespace eqtp {
 
 constexpr int kPer = 8;  // experts of a lane
 
+// values of consecutive elements from index x on: `have` of them (0 to 8), the others `none`
 template <class T>
-__device__ __forceinline__ float logit(const void* p, int64_t i) { return (float)static_cast<const T*>(p)[i]; }
-
-// s of one expert in 64 bits; for softmax `top` and `total` are the row's
-__device__ __forceinline__ double score64(double t, bool sigmoid, double top, double total) {
-  return sigmoid ? 1.0 / (1.0 + exp(-t)) : exp(t - top) / total;
+__device__ __forceinline__ void load8(const T* p, int have, float none, float (&t)[kPer]) {
+  if (have >= kPer) {
+    const typename Quad<T>::Raw a = Quad<T>::load(p), b = Quad<T>::load(p + 4);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      t[i] = (float)a[i];
+      t[4 + i] = (float)b[i];
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) t[i] = i < have ? (float)p[i] : none;
+  }
 }
 
+template <int CTRL>
+__device__ __forceinline__ float dpp_max(float v) {
+  return fmaxf(v, __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xf, 0xf, false)));
+}
+// largest of v over groups of G lanes (up to 32)
 template <int G>
-__device__ __forceinline__ double group_sum64(double v) {
+__device__ __forceinline__ float lane_max(float v) {
+  if constexpr (G >= 2) v = dpp_max<0xB1>(v);
+  if constexpr (G >= 4) v = dpp_max<0x4E>(v);
+  if constexpr (G >= 8) v = dpp_max<0x141>(v);
+  if constexpr (G >= 16) v = dpp_max<0x140>(v);
+  if constexpr (G >= 32) {
+    const unsigned a = __builtin_bit_cast(unsigned, v);
+    const auto r = __builtin_amdgcn_permlane16_swap(a, a, false, false);
+    v = fmaxf(__builtin_bit_cast(float, (unsigned)r[0]), __builtin_bit_cast(float, (unsigned)r[1]));
+  }
+  return v;
+}
+template <int G>
+__device__ __forceinline__ double lane_sum64(double v) {
 #pragma unroll
   for (int o = 1; o < G; o <<= 1) v += __shfl_xor(v, o, G);
   return v;
 }
-template <int G>
-__device__ __forceinline__ float group_sum32(float v) {
-#pragma unroll
-  for (int o = 1; o < G; o <<= 1) v += __shfl_xor(v, o, G);
-  return v;
-}
-template <int G>
-__device__ __forceinline__ float group_max(float v) {
-#pragma unroll
-  for (int o = 1; o < G; o <<= 1) v = fmaxf(v, __shfl_xor(v, o, G));
-  return v;
-}
 
+// exp(t) by the hardware's power of two: 2 steps and t's rounding off
+__device__ __forceinline__ float fast_exp(float t) { return __builtin_amdgcn_exp2f(t * 1.44269504088896340736f); }
+
+constexpr float kNone = -__builtin_inff();
 // takes part: not -inf and not NaN
-__device__ __forceinline__ bool open_to(double v) { return v > -__builtin_inf(); }
+template <class F>
+__device__ __forceinline__ bool open_to(F v) { return v > -__builtin_inf(); }
 
-// Groups of experts: closes (v = -inf) the experts of all but the best groups.
-// vals [X] and sums [groups] of the row in LDS (one wave's own).
-template <int G>
-__device__ __forceinline__ void close_groups(const RouteArgs& a, int lane, double (&v)[kPer], double* vals, double* sums) {
-  const int size = a.X / a.groups;
+// Groups of experts: closes (v = -inf) the experts of all but the best groups.  Returns by how much the worst open
+// group leads the best closed one (the same in all lanes).  of: the experts' groups, of `size` each; vals [X] and sums [groups] of the row in LDS.
+template <int G, class F>
+__device__ __forceinline__ F close_groups(const RouteArgs& a, int lane, int size, const int (&of)[kPer], F (&v)[kPer], F* vals, F* sums) {
+  const F low = (F)-__builtin_inf();
 #pragma unroll
   for (int i = 0; i < kPer; ++i)
     if (lane * kPer + i < a.X) vals[lane * kPer + i] = v[i];
   wave_lds_sync();
   for (int g = lane; g < a.groups; g += G) {
-    double first = -__builtin_inf(), second = first;
+    F first = low, second = low;
     for (int i = 0; i < size; ++i) {
-      const double t = vals[g * size + i];
-      if (t > first) {
-        second = first;
-        first = t;
-      } else if (t > second) {
-        second = t;
-      }
+      const F t = vals[g * size + i];
+      second = t > first ? first : (t > second ? t : second);
+      first = t > first ? t : first;
     }
     sums[g] = open_to(second) ? first + second : first;
+  }
+  wave_lds_sync();
+  // lane's groups: whether each is among the best, marked in vals; and the border
+  F worst = (F)__builtin_inf(), best = low;
+  for (int g = lane; g < a.groups; g += G) {
+    const F mine = sums[g];
+    int ahead = 0;
+    for (int o = 0; o < a.groups; ++o) {
+      const F other = sums[o];
+      ahead += other > mine || (other == mine && o < g);
+    }
+    const bool kept = ahead < a.top_groups;
+    vals[g] = kept ? (F)1 : (F)0;  // (a group has at least one expert: g < X)
+    if (kept) worst = mine < worst ? mine : worst;
+    else best = mine > best ? mine : best;
   }
   wave_lds_sync();
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
     const int x = lane * kPer + i;
-    if (x >= a.X) continue;
-    const int g = x / size;
-    const double mine = sums[g];
-    int ahead = 0;
-    for (int o = 0; o < a.groups; ++o) ahead += sums[o] > mine || (sums[o] == mine && o < g);
-    if (ahead >= a.top_groups) v[i] = -__builtin_inf();
+    if (x < a.X && vals[of[i]] == (F)0) v[i] = low;
   }
-  wave_lds_sync();  // the next row's values come into the same place
+#pragma unroll
+  for (int o = 1; o < G; o <<= 1) {
+    const F w = __shfl_xor(worst, o, G), b = __shfl_xor(best, o, G);
+    worst = w < worst ? w : worst;
+    best = b > best ? b : best;
+  }
+  wave_lds_sync();  // the next values come into the same place
+  return open_to(best) ? worst - best : (F)__builtin_inf();
+}
+
+// The choice in 64 bits: taken[r] is the expert of place lane + r G.
+template <int G, int P>
+__device__ __forceinline__ void choose_wide(const RouteArgs& a, int lane, const float (&t)[kPer], const float (&bias)[kPer],
+                                            float top, bool direct, int size, const int (&of)[kPer], double* vals, int (&taken)[P]) {
+  double v[kPer];
+  if (direct) {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) v[i] = (double)t[i];
+  } else if (a.sigmoid) {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) v[i] = 1.0 / (1.0 + exp(-(double)t[i])) + (double)bias[i];
+  } else {
+    double total = 0.0;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      v[i] = exp((double)t[i] - (double)top);
+      total += v[i];  // (0 past the last expert)
+    }
+    total = lane_sum64<G>(total);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) v[i] = v[i] / total + (double)bias[i];
+  }
+#pragma unroll
+  for (int i = 0; i < kPer; ++i)
+    if (!(t[i] > kNone) || !open_to(v[i])) v[i] = -__builtin_inf();
+  if (a.groups > 1) close_groups<G, double>(a, lane, size, of, v, vals, vals + a.X);
+  for (int j = 0; j < a.k; ++j) {
+    double best = -__builtin_inf();
+    int at = -1;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      if (v[i] > best) {
+        best = v[i];
+        at = lane * kPer + i;
+      }
+#pragma unroll
+    for (int o = 1; o < G; o <<= 1) {
+      const double ob = __shfl_xor(best, o, G);
+      const int oa = __shfl_xor(at, o, G);
+      if (ob > best || (ob == best && oa >= 0 && (at < 0 || oa < at))) {
+        best = ob;
+        at = oa;
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < P; ++r)
+      if (j == lane + r * G) taken[r] = at;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      if (at == lane * kPer + i) v[i] = -__builtin_inf();
+  }
 }
 
 template <class T, int G>
 __global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
-  constexpr int R = 256 / G;
+  constexpr int R = 256 / G, P = (kMaxTopK + G - 1) / G;  // rows of a workgroup; places of a lane
   extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
-  const int lane = threadIdx.x % G, row = threadIdx.x / G;
+  const int lane = threadIdx.x % G, row = threadIdx.x / G, shift = (threadIdx.x & 63) / G * G;
+  const uint64_t group = (G == 64 ? ~0ull : (1ull << (G & 63)) - 1) << shift;
   double* vals = reinterpret_cast<double*>(lds) + row * (a.X + a.groups);
-  float bias[kPer];
+  const int have = min(max(a.X - lane * kPer, 0), kPer);
+  const int size = a.X / a.groups;
+  int of[kPer];
+  float bias[kPer], most = 0.0f;
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) bias[i] = a.bias && lane * kPer + i < a.X ? a.bias[lane * kPer + i] : 0.0f;
+  for (int i = 0; i < kPer; ++i) {
+    of[i] = (lane * kPer + i) / size;
+    bias[i] = a.bias && i < have ? a.bias[lane * kPer + i] : 0.0f;
+    const float b = fabsf(bias[i]);
+    most = fmaxf(most, b < __builtin_inff() ? b : 0.0f);
+  }
+  const bool direct = a.bias == nullptr && a.groups == 1;  // the logits' order is the scores'
+  const float off = direct ? 0.0f : 0x1p-20f * (1.0f + lane_max<G>(most));  // of a v, at most
   for (int64_t n = (int64_t)blockIdx.x * R + row; n < a.N; n += (int64_t)gridDim.x * R) {
-    float t[kPer];
-    float top = -__builtin_inff();
-    int spoilt = 0;
+    float t[kPer], v[kPer], top = kNone, all = 0.0f;
+    load8(static_cast<const T*>(a.logits) + n * a.X + (have ? lane * kPer : 0), have, kNone, t);
+    bool nan = false;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-      const int x = lane * kPer + i;
-      t[i] = x < a.X ? logit<T>(a.logits, n * a.X + x) : -__builtin_inff();
       top = fmaxf(top, t[i]);
-      spoilt |= t[i] != t[i];
+      nan |= t[i] != t[i];
     }
-#pragma unroll
-    for (int o = 1; o < G; o <<= 1) spoilt |= __shfl_xor(spoilt, o, G);
-    const bool plain = a.bias == nullptr && a.groups == 1;  // the logits' order is the scores'
-    double v[kPer];
-    float all = 0.0f;  // sum of exp(t - top)
+    const bool spoilt = (__ballot(nan) & group) != 0;
     if (!a.sigmoid) {
-      top = group_max<G>(top);
-      if (!plain) {
-        double total = 0.0;
+      top = lane_max<G>(top);
+      if (!direct || !a.renormalise) {
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
-          v[i] = exp((double)t[i] - (double)top);
-          total += lane * kPer + i < a.X ? v[i] : 0.0;
+          v[i] = fast_exp(t[i] - top);  // (0 past the last expert)
+          all += v[i];
         }
-        total = group_sum64<G>(total);
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) v[i] = v[i] / total + (double)bias[i];
-        all = (float)total;
-      } else if (!a.renormalise) {
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) all += lane * kPer + i < a.X ? expf(t[i] - top) : 0.0f;
-        all = group_sum32<G>(all);
+        all = lane_sum<G>(all);
       }
-    } else if (!plain) {
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) v[i] = 1.0 / (1.0 + exp(-(double)t[i])) + (double)bias[i];
     }
+    if (direct) {
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      if (plain) v[i] = (double)t[i];
-      // a masked expert (logit -inf) is never taken, whatever its bias
-      if (!(t[i] > -__builtin_inff()) || !open_to(v[i])) v[i] = -__builtin_inf();
+      for (int i = 0; i < kPer; ++i) v[i] = t[i] > kNone ? t[i] : kNone;
+    } else {
+      const float inv = a.sigmoid ? 1.0f : __builtin_amdgcn_rcpf(all);
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        v[i] = (a.sigmoid ? __builtin_amdgcn_rcpf(1.0f + fast_exp(-t[i])) : v[i] * inv) + bias[i];
+        if (!(t[i] > kNone) || !open_to(v[i])) v[i] = kNone;
+      }
     }
-    if (a.groups > 1) close_groups<G>(a, lane, v, vals, vals + a.X);
-    // k rounds: the largest v, the lower index where equal; lane j of the row keeps the one of round j (j + G, ..)
-    float logit_of[kMaxTopK];
-    int taken[kMaxTopK];
+    bool close = false;
+    if (a.groups > 1) {
+      float* f = reinterpret_cast<float*>(vals);
+      close = !(close_groups<G, float>(a, lane, size, of, v, f, f + a.X) > 4.0f * off);
+    }
+    // k rounds, and one for who comes next: the largest v; lane j of the row keeps the expert of place j (j + G, ..)
+    int taken[P];
 #pragma unroll
-    for (int j = 0; j < kMaxTopK; ++j) {
-      if (j >= a.k) break;
-      double best = -__builtin_inf();
+    for (int r = 0; r < P; ++r) taken[r] = -1;
+    float last = __builtin_inff();
+    for (int j = 0; j <= a.k; ++j) {
+      float best = fmaxf(fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3])), fmaxf(fmaxf(v[4], v[5]), fmaxf(v[6], v[7])));
+      best = lane_max<G>(best);
+      close |= open_to(best) && !(last - best > 2.0f * off);  // (an infinite v: looked at again, too)
+      last = best;
+      if (j == a.k) break;
       int at = -1;
-      float mine = -__builtin_inff();
 #pragma unroll
-      for (int i = 0; i < kPer; ++i)
-        if (v[i] > best) {
-          best = v[i];
-          at = lane * kPer + i;
-          mine = t[i];
-        }
+      for (int i = kPer - 1; i >= 0; --i) at = v[i] == best ? i : at;
+      const bool mine = at >= 0 && open_to(best);
+      const uint64_t who = __ballot(mine) & group;
+      close |= (who & (who - 1)) != 0;  // equal ones in two lanes (in one lane: the next round's)
+      const int owner = who ? __builtin_ctzll(who) - shift : 0;
+      const int expert = who ? owner * kPer + __shfl(at, owner, G) : -1;
 #pragma unroll
-      for (int o = 1; o < G; o <<= 1) {
-        const double ob = __shfl_xor(best, o, G);
-        const int oa = __shfl_xor(at, o, G);
-        const float om = __shfl_xor(mine, o, G);
-        if (ob > best || (ob == best && oa >= 0 && (at < 0 || oa < at))) {
-          best = ob;
-          at = oa;
-          mine = om;
-        }
-      }
-      taken[j] = spoilt ? -1 : at;
-      logit_of[j] = mine;
+      for (int r = 0; r < P; ++r)
+        if (j == lane + r * G) taken[r] = expert;
 #pragma unroll
-      for (int i = 0; i < kPer; ++i)
-        if (at == lane * kPer + i) v[i] = -__builtin_inf();
+      for (int i = 0; i < kPer; ++i) v[i] = mine && i == at ? kNone : v[i];
     }
+    if (__any(close)) choose_wide<G, P>(a, lane, t, bias, top, direct, size, of, vals, taken);
     // weights: s = exp(min(t, 0)) / (1 + exp(-|t|)), or exp(t - top) / all; renormalised ones from
     // exp(.. - the largest exponent among those taken), which neither under- nor overflows
-    float ref = 0.0f;
-    if (a.renormalise) {
-      ref = -__builtin_inff();
+    float w[P], lt[P], ref = a.renormalise ? kNone : (a.sigmoid ? 0.0f : top), sum = 0.0f;
 #pragma unroll
-      for (int j = 0; j < kMaxTopK; ++j)
-        if (j < a.k && taken[j] >= 0) ref = fmaxf(ref, a.sigmoid ? fminf(logit_of[j], 0.0f) : logit_of[j]);
-    } else if (!a.sigmoid) {
-      ref = top;
+    for (int r = 0; r < P; ++r) {
+      if (spoilt) taken[r] = -1;
+      lt[r] = taken[r] >= 0 ? (float)static_cast<const T*>(a.logits)[n * a.X + taken[r]] : 0.0f;
+      if (a.renormalise && taken[r] >= 0) ref = fmaxf(ref, a.sigmoid ? fminf(lt[r], 0.0f) : lt[r]);
     }
-    float w[kMaxTopK], sum = 0.0f;
+    if (a.renormalise) ref = lane_max<G>(ref);
 #pragma unroll
-    for (int j = 0; j < kMaxTopK; ++j) {
-      if (j >= a.k) break;
-      w[j] = 0.0f;
-      if (taken[j] >= 0)
-        w[j] = a.sigmoid ? expf(fminf(logit_of[j], 0.0f) - ref) / (1.0f + expf(-fabsf(logit_of[j]))) : expf(logit_of[j] - ref);
-      sum += w[j];
+    for (int r = 0; r < P; ++r) {
+      w[r] = 0.0f;
+      if (taken[r] >= 0)
+        w[r] = a.sigmoid ? expf(fminf(lt[r], 0.0f) - ref) / (1.0f + expf(-fabsf(lt[r]))) : expf(lt[r] - ref);
+      sum += w[r];
     }
-    if (!a.renormalise) sum = a.sigmoid ? 1.0f : all;
+    sum = a.renormalise ? lane_sum<G>(sum) : (a.sigmoid ? 1.0f : all);
 #pragma unroll
-    for (int j = 0; j < kMaxTopK; ++j) {
-      if (j >= a.k) break;
-      if (j % G == lane) {
-        a.idx[n * a.k + j] = taken[j];
-        a.weight[n * a.k + j] = taken[j] >= 0 ? w[j] / sum * a.scale : (spoilt ? __builtin_nanf("") : 0.0f);
+    for (int r = 0; r < P; ++r) {
+      const int j = lane + r * G;
+      if (j < a.k) {
+        a.idx[n * a.k + j] = taken[r];
+        a.weight[n * a.k + j] = taken[r] >= 0 ? w[r] / sum * a.scale : (spoilt ? __builtin_nanf("") : 0.0f);
       }
     }
   }
@@ -204,74 +289,78 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
 // Gradient: only those taken get one where the weights are renormalised or the scores are the logits' own.
 //   p = s / sum (or s), g = scale gweight, dot = sum over those taken of g p:
 //   renormalised: p (g - dot) [(1 - s) for sigmoid];  else s (1 - s) g, or p (g - dot) for every expert (g = 0 where not taken).
+// Lane j of a row works on place j; the row goes through LDS, where the places' gradients are put among the others'.
 template <class T, int G>
 __global__ __launch_bounds__(256) void route_grad_kernel(RouteArgs a) {
-  constexpr int R = 256 / G;
+  constexpr int R = 256 / G, P = (kMaxTopK + G - 1) / G;
+  __shared__ float rows[R][G * kPer];
   const int lane = threadIdx.x % G, row = threadIdx.x / G;
+  const int have = min(max(a.X - lane * kPer, 0), kPer);
+  const bool whole = !a.sigmoid && !a.renormalise;
   for (int64_t n = (int64_t)blockIdx.x * R + row; n < a.N; n += (int64_t)gridDim.x * R) {
-    const bool whole = !a.sigmoid && !a.renormalise;
-    float t[kPer], top = -__builtin_inff(), all = 0.0f;
+    float t[kPer], top = kNone, all = 0.0f;
     if (whole) {
+      load8(static_cast<const T*>(a.logits) + n * a.X + (have ? lane * kPer : 0), have, kNone, t);
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) top = fmaxf(top, t[i]);
+      top = lane_max<G>(top);
+      if (top == kNone) top = 0.0f;  // (every expert is masked)
 #pragma unroll
       for (int i = 0; i < kPer; ++i) {
-        const int x = lane * kPer + i;
-        t[i] = x < a.X ? logit<T>(a.logits, n * a.X + x) : -__builtin_inff();
-        top = fmaxf(top, t[i]);
-      }
-      top = group_max<G>(top);
-      if (top == -__builtin_inff()) top = 0.0f;  // (every expert is masked)
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        t[i] = lane * kPer + i < a.X ? expf(t[i] - top) : 0.0f;
+        t[i] = expf(t[i] - top);
         all += t[i];
       }
-      all = group_sum32<G>(all);
+      all = lane_sum<G>(all);
       if (all == 0.0f) all = 1.0f;
     }
-    int taken[kMaxTopK];
-    float lt[kMaxTopK], p[kMaxTopK], g[kMaxTopK], ref = -__builtin_inff(), sum = 0.0f, dot = 0.0f;
+    int taken[P];
+    float lt[P], p[P], g[P], ref = a.renormalise ? kNone : (a.sigmoid ? 0.0f : top), sum = 0.0f, dot = 0.0f;
 #pragma unroll
-    for (int j = 0; j < kMaxTopK; ++j) {
-      if (j >= a.k) break;
-      taken[j] = a.idx[n * a.k + j];
-      if (taken[j] < 0 || taken[j] >= a.X) taken[j] = -1;
-      g[j] = a.gweight[n * a.k + j] * a.scale;
-      lt[j] = taken[j] >= 0 ? logit<T>(a.logits, n * a.X + taken[j]) : 0.0f;
-      if (taken[j] >= 0) ref = fmaxf(ref, a.sigmoid ? fminf(lt[j], 0.0f) : lt[j]);
+    for (int r = 0; r < P; ++r) {
+      const int j = lane + r * G;
+      taken[r] = j < a.k ? a.idx[n * a.k + j] : -1;
+      g[r] = j < a.k ? a.gweight[n * a.k + j] * a.scale : 0.0f;
+      if (taken[r] >= a.X) taken[r] = -1;
+      lt[r] = taken[r] >= 0 ? (float)static_cast<const T*>(a.logits)[n * a.X + taken[r]] : 0.0f;
+      if (a.renormalise && taken[r] >= 0) ref = fmaxf(ref, a.sigmoid ? fminf(lt[r], 0.0f) : lt[r]);
     }
-    if (!a.renormalise) ref = a.sigmoid ? 0.0f : top;
+    if (a.renormalise) ref = lane_max<G>(ref);
 #pragma unroll
-    for (int j = 0; j < kMaxTopK; ++j) {
-      if (j >= a.k) break;
-      p[j] = 0.0f;
-      if (taken[j] >= 0)
-        p[j] = a.sigmoid ? expf(fminf(lt[j], 0.0f) - ref) / (1.0f + expf(-fabsf(lt[j]))) : expf(lt[j] - ref);
-      sum += p[j];
+    for (int r = 0; r < P; ++r) {
+      p[r] = 0.0f;
+      if (taken[r] >= 0)
+        p[r] = a.sigmoid ? expf(fminf(lt[r], 0.0f) - ref) / (1.0f + expf(-fabsf(lt[r]))) : expf(lt[r] - ref);
+      sum += p[r];
     }
-    if (!a.renormalise) sum = a.sigmoid ? 1.0f : all;
+    sum = a.renormalise ? lane_sum<G>(sum) : (a.sigmoid ? 1.0f : all);
 #pragma unroll
-    for (int j = 0; j < kMaxTopK; ++j) {
-      if (j >= a.k) break;
-      p[j] = taken[j] >= 0 ? p[j] / sum : 0.0f;
-      dot = taken[j] >= 0 ? fmaf(g[j], p[j], dot) : dot;
+    for (int r = 0; r < P; ++r) {
+      p[r] = taken[r] >= 0 ? p[r] / sum : 0.0f;
+      dot = taken[r] >= 0 ? fmaf(g[r], p[r], dot) : dot;
     }
-    if (a.sigmoid && !a.renormalise) dot = 0.0f;
-    float out[kPer];
+    dot = a.sigmoid && !a.renormalise ? 0.0f : lane_sum<G>(dot);
+    float* mine = rows[row];
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) out[i] = whole ? 0.0f - t[i] / all * dot : 0.0f;
+    for (int i = 0; i < kPer; i += 4)
+      *reinterpret_cast<f4*>(mine + lane * kPer + i) =
+          whole ? f4{0.0f - t[i] / all * dot, 0.0f - t[i + 1] / all * dot, 0.0f - t[i + 2] / all * dot, 0.0f - t[i + 3] / all * dot}
+                : f4{0.0f, 0.0f, 0.0f, 0.0f};
+    wave_lds_sync();
 #pragma unroll
-    for (int j = 0; j < kMaxTopK; ++j) {
-      if (j >= a.k) break;
-      float v = p[j] * (g[j] - dot);
-      if (a.sigmoid) v /= 1.0f + expf(lt[j]);  // 1 - s
-#pragma unroll
-      for (int i = 0; i < kPer; ++i)
-        if (taken[j] >= 0 && taken[j] == lane * kPer + i) out[i] = v;
+    for (int r = 0; r < P; ++r) {
+      float v = p[r] * (g[r] - dot);
+      if (a.sigmoid) v /= 1.0f + expf(lt[r]);  // 1 - s
+      if (taken[r] >= 0) mine[taken[r]] = v;
     }
-    T* o = static_cast<T*>(a.glogits) + n * a.X;
+    wave_lds_sync();
+    T* o = static_cast<T*>(a.glogits) + n * a.X + lane * kPer;
 #pragma unroll
-    for (int i = 0; i < kPer; ++i)
-      if (lane * kPer + i < a.X) o[lane * kPer + i] = (T)out[i];
+    for (int i = 0; i < kPer; i += 4) {
+      const f4 q = *reinterpret_cast<const f4*>(mine + lane * kPer + i);
+      const float v[4] = {q[0], q[1], q[2], q[3]};
+      store4(o + i, have - i, true, v);
+    }
+    wave_lds_sync();  // the next row comes into the same place
   }
 }
 
