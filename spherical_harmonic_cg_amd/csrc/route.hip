@@ -7,16 +7,17 @@
 // Reads 4 N X bytes and writes 8 N k: bound by HBM where N is large, in
 // practice by the choice's instructions.  A node's experts lie eight by eight
 // in G lanes (G = 1 for up to 8 experts, 32 for 256), so a wave works on 64 / G
-// nodes and a round of the choice costs each lane eight comparisons and log2 G
-// exchanges.
+// nodes.  Each lane sorts its eight once; a round of the choice then compares
+// the lanes' first ones, and the lane that had the best moves on.
 //
 // An expert that leads by a hair has to lead as in the formula, whatever fp32
 // makes of it.  The choice is made in fp32 and looked at: an fp32 v is off by
-// 2^-20 (1 + the largest |bias|) at most (the hardware's exponential and
-// reciprocal, a step each, their arguments, the sum and the bias), so where every one taken leads the next by more than
-// twice that, and open groups the closed ones by four times, it is the
-// formula's.  Where not -- one node in some thousands, or equal scores -- the
-// wave chooses again in 64 bits, with the index beside the value.
+// 2^-19 (1 + the largest |bias|) at most (the hardware's exponential and
+// reciprocal, a step each, their arguments, the sum, the bias, and the three
+// bits of its key that say where it lies), so where every one taken leads the
+// next by more than twice that, and open groups the closed ones by four times,
+// it is the formula's.  Where not -- one node in some hundreds, or equal scores
+// -- the wave chooses again in 64 bits, with the index beside the value.
 #include "norm_device.hpp"
 
 namespace eqtp {
@@ -83,10 +84,16 @@ __device__ __forceinline__ F close_groups(const RouteArgs& a, int lane, int size
   wave_lds_sync();
   for (int g = lane; g < a.groups; g += G) {
     F first = low, second = low;
-    for (int i = 0; i < size; ++i) {
-      const F t = vals[g * size + i];
-      second = t > first ? first : (t > second ? t : second);
-      first = t > first ? t : first;
+    for (int i0 = 0; i0 < size; i0 += 8) {  // (eight reads beside each other, not one after the other's wait)
+      F t[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) t[i] = vals[g * size + min(i0 + i, size - 1)];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (i0 + i >= size) t[i] = low;
+        second = t[i] > first ? first : (t[i] > second ? t[i] : second);
+        first = t[i] > first ? t[i] : first;
+      }
     }
     sums[g] = open_to(second) ? first + second : first;
   }
@@ -96,9 +103,13 @@ __device__ __forceinline__ F close_groups(const RouteArgs& a, int lane, int size
   for (int g = lane; g < a.groups; g += G) {
     const F mine = sums[g];
     int ahead = 0;
-    for (int o = 0; o < a.groups; ++o) {
-      const F other = sums[o];
-      ahead += other > mine || (other == mine && o < g);
+    for (int o0 = 0; o0 < a.groups; o0 += 8) {
+      F other[8];
+#pragma unroll
+      for (int o = 0; o < 8; ++o) other[o] = sums[min(o0 + o, a.groups - 1)];
+#pragma unroll
+      for (int o = 0; o < 8; ++o)
+        ahead += o0 + o < a.groups && (other[o] > mine || (other[o] == mine && o0 + o < g));
     }
     const bool kept = ahead < a.top_groups;
     vals[g] = kept ? (F)1 : (F)0;  // (a group has at least one expert: g < X)
@@ -119,6 +130,91 @@ __device__ __forceinline__ F close_groups(const RouteArgs& a, int lane, int size
   }
   wave_lds_sync();  // the next values come into the same place
   return open_to(best) ? worst - best : (F)__builtin_inf();
+}
+
+// Keys: whole numbers in the order of the values, their lowest three bits the place in the lane (the lower index the
+// larger key), so that a lane's eight are all different; values lose 2^-20 of themselves at most.
+__device__ __forceinline__ int key_of(float v, int i) {
+  const int s = __builtin_bit_cast(int, v);
+  return ((s ^ (s >> 31 & 0x7fffffff)) & ~7) | (7 - i);
+}
+__device__ __forceinline__ float key_value(int key) {
+  const int s = key & ~7;
+  return __builtin_bit_cast(float, s ^ (s >> 31 & 0x7fffffff));
+}
+constexpr int kNoKey = (int)0x807fffff;  // -inf's, and those below: closed
+
+__device__ __forceinline__ void order_two(int& a, int& b) {
+  const int hi = max(a, b), lo = min(a, b);
+  a = hi;
+  b = lo;
+}
+// descending; 19 exchanges (odd-even merge sort)
+__device__ __forceinline__ void sort8(int (&k)[kPer]) {
+#pragma unroll
+  for (int i = 0; i < 8; i += 2) order_two(k[i], k[i + 1]);
+#pragma unroll
+  for (int i = 0; i < 8; i += 4) {
+    order_two(k[i], k[i + 2]);
+    order_two(k[i + 1], k[i + 3]);
+    order_two(k[i + 1], k[i + 2]);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) order_two(k[i], k[i + 4]);
+  order_two(k[2], k[4]);
+  order_two(k[3], k[5]);
+  order_two(k[1], k[2]);
+  order_two(k[3], k[4]);
+  order_two(k[5], k[6]);
+}
+
+template <int CTRL>
+__device__ __forceinline__ int dpp_maxi(int v) {
+  return max(v, __builtin_amdgcn_update_dpp(v, v, CTRL, 0xf, 0xf, false));
+}
+template <int G>
+__device__ __forceinline__ int lane_maxi(int v) {
+  if constexpr (G >= 2) v = dpp_maxi<0xB1>(v);
+  if constexpr (G >= 4) v = dpp_maxi<0x4E>(v);
+  if constexpr (G >= 8) v = dpp_maxi<0x141>(v);
+  if constexpr (G >= 16) v = dpp_maxi<0x140>(v);
+  if constexpr (G >= 32) {
+    const auto r = __builtin_amdgcn_permlane16_swap((unsigned)v, (unsigned)v, false, false);
+    v = max((int)r[0], (int)r[1]);
+  }
+  return v;
+}
+
+// close_groups for groups of 8, 16, 32, .. experts -- whole lanes -- from the lanes' sorted keys.
+template <int G>
+__device__ __forceinline__ float close_lanes(const RouteArgs& a, int lane, int size, int (&key)[kPer], float* sums) {
+  float first = key[0] > kNoKey ? key_value(key[0]) : kNone, second = key[1] > kNoKey ? key_value(key[1]) : kNone;
+  const int span = size / kPer;
+  for (int o = 1; o < span; o <<= 1) {
+    const float f = __shfl_xor(first, o, G), s = __shfl_xor(second, o, G);
+    second = fmaxf(fminf(first, f), fmaxf(second, s));
+    first = fmaxf(first, f);
+  }
+  const float mine = open_to(second) ? first + second : first;
+  const int g = lane / span;
+  if (g < a.groups && lane == g * span) sums[g] = mine;
+  wave_lds_sync();
+  int ahead = 0;
+  for (int o0 = 0; o0 < a.groups; o0 += 8) {
+    float other[8];
+#pragma unroll
+    for (int o = 0; o < 8; ++o) other[o] = sums[min(o0 + o, a.groups - 1)];
+#pragma unroll
+    for (int o = 0; o < 8; ++o) ahead += o0 + o < a.groups && (other[o] > mine || (other[o] == mine && o0 + o < g));
+  }
+  wave_lds_sync();  // the next row's sums come into the same place
+  const bool kept = ahead < a.top_groups, is = g < a.groups;
+  const float best = lane_max<G>(is && !kept ? mine : kNone);
+  const float worst = -lane_max<G>(is && kept ? -mine : kNone);
+  if (!kept)
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) key[i] = kNoKey;
+  return open_to(best) ? worst - best : __builtin_inff();
 }
 
 // The choice in 64 bits: taken[r] is the expert of place lane + r G.
@@ -178,11 +274,11 @@ template <class T, int G>
 __global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
   constexpr int R = 256 / G, P = (kMaxTopK + G - 1) / G;  // rows of a workgroup; places of a lane
   extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
-  const int lane = threadIdx.x % G, row = threadIdx.x / G, shift = (threadIdx.x & 63) / G * G;
-  const uint64_t group = (G == 64 ? ~0ull : (1ull << (G & 63)) - 1) << shift;
+  const int lane = threadIdx.x % G, row = threadIdx.x / G;
   double* vals = reinterpret_cast<double*>(lds) + row * (a.X + a.groups);
   const int have = min(max(a.X - lane * kPer, 0), kPer);
   const int size = a.X / a.groups;
+  const bool whole_lanes = size % kPer == 0 && (size & (size - 1)) == 0;
   int of[kPer];
   float bias[kPer], most = 0.0f;
 #pragma unroll
@@ -193,7 +289,7 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
     most = fmaxf(most, b < __builtin_inff() ? b : 0.0f);
   }
   const bool direct = a.bias == nullptr && a.groups == 1;  // the logits' order is the scores'
-  const float off = direct ? 0.0f : 0x1p-20f * (1.0f + lane_max<G>(most));  // of a v, at most
+  const float off = direct ? 0.0f : 0x1p-19f * (1.0f + lane_max<G>(most));  // of a v, at most (keys' part included)
   for (int64_t n = (int64_t)blockIdx.x * R + row; n < a.N; n += (int64_t)gridDim.x * R) {
     float t[kPer], v[kPer], top = kNone, all = 0.0f;
     load8(static_cast<const T*>(a.logits) + n * a.X + (have ? lane * kPer : 0), have, kNone, t);
@@ -203,7 +299,7 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
       top = fmaxf(top, t[i]);
       nan |= t[i] != t[i];
     }
-    const bool spoilt = (__ballot(nan) & group) != 0;
+    const bool spoilt = lane_maxi<G>(nan) != 0;
     if (!a.sigmoid) {
       top = lane_max<G>(top);
       if (!direct || !a.renormalise) {
@@ -227,34 +323,38 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
       }
     }
     bool close = false;
-    if (a.groups > 1) {
+    if (a.groups > 1 && !whole_lanes) {
       float* f = reinterpret_cast<float*>(vals);
       close = !(close_groups<G, float>(a, lane, size, of, v, f, f + a.X) > 4.0f * off);
     }
-    // k rounds, and one for who comes next: the largest v; lane j of the row keeps the expert of place j (j + G, ..)
+    int key[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) key[i] = key_of(v[i], i);
+    sort8(key);
+    if (a.groups > 1 && whole_lanes) close = !(close_lanes<G>(a, lane, size, key, reinterpret_cast<float*>(vals)) > 4.0f * off);
+    // k rounds, and one for who comes next: the largest of the lanes' first keys; lane j of the row keeps the expert of
+    // place j (j + G, ..).  Equal keys of two lanes: the one with the higher index goes, the next round meets the other.
     int taken[P];
 #pragma unroll
     for (int r = 0; r < P; ++r) taken[r] = -1;
     float last = __builtin_inff();
     for (int j = 0; j <= a.k; ++j) {
-      float best = fmaxf(fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3])), fmaxf(fmaxf(v[4], v[5]), fmaxf(v[6], v[7])));
-      best = lane_max<G>(best);
-      close |= open_to(best) && !(last - best > 2.0f * off);  // (an infinite v: looked at again, too)
-      last = best;
+      const int best = lane_maxi<G>(key[0]);
+      const float value = key_value(best);
+      // (an infinite v: looked at again, too)
+      close |= best > kNoKey && !(last - value > fmaf(0x1p-20f, fmaxf(fabsf(value), last < __builtin_inff() ? fabsf(last) : 0.0f), 2.0f * off));
+      last = value;
       if (j == a.k) break;
-      int at = -1;
-#pragma unroll
-      for (int i = kPer - 1; i >= 0; --i) at = v[i] == best ? i : at;
-      const bool mine = at >= 0 && open_to(best);
-      const uint64_t who = __ballot(mine) & group;
-      close |= (who & (who - 1)) != 0;  // equal ones in two lanes (in one lane: the next round's)
-      const int owner = who ? __builtin_ctzll(who) - shift : 0;
-      const int expert = who ? owner * kPer + __shfl(at, owner, G) : -1;
+      const bool mine = key[0] == best && best > kNoKey;
+      const int expert = lane_maxi<G>(mine ? lane * kPer + 7 - (best & 7) : -1);
 #pragma unroll
       for (int r = 0; r < P; ++r)
         if (j == lane + r * G) taken[r] = expert;
+      if (expert >> 3 == lane) {
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) v[i] = mine && i == at ? kNone : v[i];
+        for (int i = 0; i < kPer - 1; ++i) key[i] = key[i + 1];
+        key[kPer - 1] = kNoKey;
+      }
     }
     if (__any(close)) choose_wide<G, P>(a, lane, t, bias, top, direct, size, of, vals, taken);
     // weights: s = exp(min(t, 0)) / (1 + exp(-|t|)), or exp(t - top) / all; renormalised ones from
