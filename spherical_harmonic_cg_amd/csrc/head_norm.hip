@@ -146,7 +146,7 @@ __global__ __launch_bounds__(256) void head_norm_kernel(HeadNormArgs a, int A) {
   Turns<T, NV, KT> tr;
   tr.none();
   for (; p.item < p.items; p.item += p.step) {
-    const int64_t n = p.item / s.stretches;
+    const int64_t n = s.stretches == 1 ? p.item : (p.items < 0x80000000 ? (int64_t)((uint32_t)p.item / (uint32_t)s.stretches) : p.item / s.stretches);
     const int h0 = (int)(p.item - n * s.stretches) * s.stretch;
     if (a.axes) tr.make(sl, s.pos + n * a.axes, a.freq, a.axes, a.R);
     const int hn = min(s.stretch, s.heads - h0);
@@ -204,7 +204,7 @@ __global__ __launch_bounds__(256) void head_norm_grad_kernel(HeadNormArgs a, int
   Turns<T, NV, KT> tr;
   tr.none();
   for (; p.item < p.items; p.item += p.step) {
-    const int64_t n = p.item / s.stretches;
+    const int64_t n = s.stretches == 1 ? p.item : (p.items < 0x80000000 ? (int64_t)((uint32_t)p.item / (uint32_t)s.stretches) : p.item / s.stretches);
     const int h0 = (int)(p.item - n * s.stretches) * s.stretch;
     if (a.axes) tr.make(sl, s.pos + n * a.axes, a.freq, a.axes, a.R);
     const int hn = min(s.stretch, s.heads - h0);
@@ -328,16 +328,19 @@ static HeadShape head_shape(int d, int K) {
 
 constexpr int kHeadParts = 2048;  // workgroups of the gradient kernel at most
 
-// How the items of both sides are dealt: whole nodes where there are plenty, single heads where there are few.
+// How the items of both sides are dealt: as many heads of a node to an item as leave an item to each group that the card
+// holds (a node's angles are made once an item).
 static void head_deal(HeadNormArgs& a, int T, int held) {
   const int R = 256 / T;
   const int64_t most = (int64_t)num_cus() * held;
+  const int64_t all = a.side[0].rows * a.side[0].heads + a.side[1].rows * a.side[1].heads;
   int64_t want[2];
   for (int i = 0; i < 2; ++i) {
     HeadSide& s = a.side[i];
-    const bool whole = s.gpos != nullptr || (a.side[0].rows + a.side[1].rows) >= most * R;
-    s.stretch = whole ? s.heads : 1;
-    s.stretches = whole ? 1 : s.heads;
+    int64_t stretch = s.gpos != nullptr ? s.heads : all / (most * R);
+    stretch = stretch < 1 ? 1 : (stretch > s.heads ? s.heads : stretch);
+    s.stretches = (int)((s.heads + stretch - 1) / stretch);
+    s.stretch = (s.heads + s.stretches - 1) / s.stretches;
     want[i] = (s.rows * s.stretches + R - 1) / R;
   }
   // workgroups in the ratio of the sides' elements, at most what the card holds at once

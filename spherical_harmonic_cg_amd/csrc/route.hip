@@ -270,8 +270,9 @@ __device__ __forceinline__ void choose_wide(const RouteArgs& a, int lane, const 
   }
 }
 
+// (four waves a SIMD: the choice in 64 bits would take registers from the ordinary one, 35 us with three)
 template <class T, int G>
-__global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
+__global__ __launch_bounds__(256, 4) void route_kernel(RouteArgs a) {
   constexpr int R = 256 / G, P = (kMaxTopK + G - 1) / G;  // rows of a workgroup; places of a lane
   extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
   const int lane = threadIdx.x % G, row = threadIdx.x / G;
