@@ -178,7 +178,7 @@ hipError_t launch_distance_bias_grad(const BiasArgs& a, float* grad_table);
 struct HeadSide {
   int64_t rows;
   int heads;
-  int stretch, stretches; // heads that a group of threads takes of a node, and how many such stretches a node has
+  bool whole;             // a group of threads takes all heads of a node
   const void* x;
   const float* weight;    // or nullptr
   const float* pos;       // with axes > 0
@@ -193,6 +193,7 @@ struct HeadNormArgs {
   bool bf16;
   float eps;
   int axes, R;            // axes of positions (0: no rotation), rotated pairs
+  int turns;              // angles that a workgroup holds at a time, at most
   const float* freq;
   HeadSide side[2];
   int blocks_q, blocks_k;

@@ -16,8 +16,8 @@
 // holds a head's row in registers as pairs: quad i of the row's first half
 // beside quad i of its second half, NV pairs of quads a thread, so both ends of
 // a rotation are in one thread.  As in the layer norm, A threads of a group take quads and a
-// thread's slots keep their components, weights and angles from row to row; a
-// group stays with a node for several heads, and its angles are made once.
+// thread's slots keep their components and weights from row to row.  A workgroup
+// makes the angles of its rows' nodes together, once for all heads of a node.
 // Angles are summed and reduced to a fraction of a turn in 64 bits (a position
 // of 10^5 times a frequency of 1 loses 4e-3 rad in fp32), their sine and cosine
 // are fp32.
@@ -32,6 +32,15 @@ constexpr int kTrig = KT == 0 ? 4 : (KT == 1 ? 1 : 2);  // channels of a quad
 struct HeadShape {
   int T, NV, A;
 };
+
+// cosine and sine of a node's angle j
+__device__ __forceinline__ void turn_of(const float* pos, const float* freq, int axes, int R, int j, float& c, float& s) {
+  double t = 0.0;
+  for (int a = 0; a < axes; ++a) t = fma((double)pos[a], (double)freq[a * R + j], t);
+  t *= 0.15915494309189533577;  // turns
+  t -= rint(t);
+  sincospif(2.0f * (float)t, &s, &c);
+}
 
 template <int T, int NV, int KT>
 struct Turns {
@@ -56,13 +65,20 @@ struct Turns {
         const int ch = channel(sl, j, q);
         c[j][q] = 1.0f;
         s[j][q] = 0.0f;
-        if (sl.on && ch < R) {
-          double t = 0.0;
-          for (int a = 0; a < axes; ++a) t = fma((double)pos[a], (double)freq[a * R + ch], t);
-          t *= 0.15915494309189533577;
-          t -= rint(t);
-          sincospif(2.0f * (float)t, &s[j][q], &c[j][q]);
-        }
+        if (sl.on && ch < R) turn_of(pos, freq, axes, R, ch, c[j][q], s[j][q]);
+      }
+  }
+  // from a table of a node's angles [R]
+  template <class S>
+  __device__ __forceinline__ void read(const S& sl, const float2* table, int R) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int q = 0; q < NC; ++q) {
+        const int ch = channel(sl, j, q);
+        const float2 t = table[min(ch, R - 1)];
+        c[j][q] = ch < R ? t.x : 1.0f;
+        s[j][q] = ch < R ? t.y : 0.0f;
       }
   }
   // of slot q
@@ -76,20 +92,43 @@ struct Turns {
   }
 };
 
-// A workgroup's side (queries or keys) and its first item: items are (node, stretch of heads).
+// A workgroup's side (queries or keys) and the first of its groups' items: heads of nodes one after the other, or,
+// where a group takes whole nodes, nodes.
 struct HeadPlace {
-  int64_t item, step, items;
+  int64_t first, step, items;
   int side;
 };
-__device__ __forceinline__ HeadPlace head_place(const HeadNormArgs& a, int R, int g) {
+__device__ __forceinline__ HeadPlace head_place(const HeadNormArgs& a, int R) {
   HeadPlace p;
   p.side = (int)blockIdx.x >= a.blocks_q;
   const int b = blockIdx.x - (p.side ? a.blocks_q : 0);
   const int blocks = p.side ? gridDim.x - a.blocks_q : a.blocks_q;
-  p.item = (int64_t)b * R + g;
+  p.first = (int64_t)b * R;
   p.step = (int64_t)blocks * R;
-  p.items = a.side[p.side].rows * a.side[p.side].stretches;
+  p.items = a.side[p.side].rows * (a.side[p.side].whole ? 1 : a.side[p.side].heads);
   return p;
+}
+__device__ __forceinline__ int64_t node_of(int64_t item, int64_t items, int heads) {
+  return items < 0x80000000 ? (int64_t)((uint32_t)item / (uint32_t)heads) : item / heads;
+}
+
+// The angles of the nodes that a workgroup's R items from `first` on belong to, made together: each once for all the
+// heads of a node.  tables: two, used in turn.
+template <int R>
+__device__ __forceinline__ const float2* head_turns(const HeadNormArgs& a, const HeadSide& s, const HeadPlace& p, int64_t first,
+                                                    int64_t n0, float2* tables, int size, int& turn) {
+  float2* tab = tables + turn * size;
+  turn ^= 1;
+  const int64_t last = min(first + R, p.items) - 1;
+  const int count = (int)(node_of(last, p.items, s.heads) - n0 + 1) * a.R;
+  for (int i = threadIdx.x; i < count; i += 256) {
+    const int n = i / a.R;
+    float2 t;
+    turn_of(s.pos + (n0 + n) * a.axes, a.freq, a.axes, a.R, i - n * a.R, t.x, t.y);
+    tab[i] = t;
+  }
+  __syncthreads();
+  return tab;
 }
 
 template <int T, int NV, int KT>
@@ -137,7 +176,8 @@ __global__ __launch_bounds__(256) void head_norm_kernel(HeadNormArgs a, int A) {
   constexpr int R = 256 / T;
   const int d = a.d, K = a.K, half = (d + 1) / 2, D0 = half * K, D1 = (d - half) * K, deg = KT == 0 ? 1 : a.lmax + 1;
   Slots<T, KT> sl(K, A);
-  HeadPlace p = head_place(a, R, threadIdx.x / T);
+  const int g = threadIdx.x / T;
+  const HeadPlace p = head_place(a, R);
   const HeadSide s = a.side[p.side];
   const bool tail0 = (D0 & 3) != 0, tail1 = (D1 & 3) != 0;
   const float inv_mine = 1.0f / (float)(d * (KT == 0 ? 1 : 2 * (int)sum8_index<(T < 8 ? 8 : T)>() + 1));
@@ -145,11 +185,22 @@ __global__ __launch_bounds__(256) void head_norm_kernel(HeadNormArgs a, int A) {
   head_weights(s, sl, d, half, w0, w1);
   Turns<T, NV, KT> tr;
   tr.none();
-  for (; p.item < p.items; p.item += p.step) {
-    const int64_t n = s.stretches == 1 ? p.item : (p.items < 0x80000000 ? (int64_t)((uint32_t)p.item / (uint32_t)s.stretches) : p.item / s.stretches);
-    const int h0 = (int)(p.item - n * s.stretches) * s.stretch;
-    if (a.axes) tr.make(sl, s.pos + n * a.axes, a.freq, a.axes, a.R);
-    const int hn = min(s.stretch, s.heads - h0);
+  extern __shared__ __attribute__((aligned(8))) float2 tables[];
+  int turn = 0;
+  for (int64_t first = p.first; first < p.items; first += p.step) {
+    const int64_t item = first + g;
+    const bool live = item < p.items;
+    int64_t n = min(item, p.items - 1);
+    int h0 = 0;
+    if (!s.whole) {
+      const int64_t n0 = node_of(first, p.items, s.heads), head = n;
+      n = node_of(head, p.items, s.heads);
+      h0 = (int)(head - n * s.heads);
+      if (a.axes) tr.read(sl, head_turns<R>(a, s, p, first, n0, tables, a.turns, turn) + (n - n0) * a.R, a.R);
+    } else if (a.axes) {
+      tr.make(sl, s.pos + n * a.axes, a.freq, a.axes, a.R);
+    }
+    const int hn = !live ? 0 : (s.whole ? s.heads : 1);
     for (int h = 0; h < hn; ++h) {
       sl.row();
       const int64_t at = (n * s.heads + h0 + h) * (int64_t)(D0 + D1);
@@ -195,7 +246,7 @@ __global__ __launch_bounds__(256) void head_norm_grad_kernel(HeadNormArgs a, int
   const int d = a.d, K = a.K, half = (d + 1) / 2, D0 = half * K, D1 = (d - half) * K, deg = KT == 0 ? 1 : a.lmax + 1;
   Slots<T, KT> sl(K, A);
   const int g = threadIdx.x / T;
-  HeadPlace p = head_place(a, R, g);
+  const HeadPlace p = head_place(a, R);
   const HeadSide s = a.side[p.side];
   const bool tail0 = (D0 & 3) != 0, tail1 = (D1 & 3) != 0;
   const float inv_mine = 1.0f / (float)(d * (KT == 0 ? 1 : 2 * (int)sum8_index<(T < 8 ? 8 : T)>() + 1));
@@ -203,11 +254,22 @@ __global__ __launch_bounds__(256) void head_norm_grad_kernel(HeadNormArgs a, int
   head_weights(s, sl, d, half, w0, w1);
   Turns<T, NV, KT> tr;
   tr.none();
-  for (; p.item < p.items; p.item += p.step) {
-    const int64_t n = s.stretches == 1 ? p.item : (p.items < 0x80000000 ? (int64_t)((uint32_t)p.item / (uint32_t)s.stretches) : p.item / s.stretches);
-    const int h0 = (int)(p.item - n * s.stretches) * s.stretch;
-    if (a.axes) tr.make(sl, s.pos + n * a.axes, a.freq, a.axes, a.R);
-    const int hn = min(s.stretch, s.heads - h0);
+  extern __shared__ __attribute__((aligned(8))) float2 tables[];
+  int turn = 0;
+  for (int64_t first = p.first; first < p.items; first += p.step) {
+    const int64_t item = first + g;
+    const bool live = item < p.items;
+    int64_t n = min(item, p.items - 1);
+    int h0 = 0;
+    if (!s.whole) {
+      const int64_t n0 = node_of(first, p.items, s.heads), head = n;
+      n = node_of(head, p.items, s.heads);
+      h0 = (int)(head - n * s.heads);
+      if (a.axes) tr.read(sl, head_turns<R>(a, s, p, first, n0, tables, a.turns, turn) + (n - n0) * a.R, a.R);
+    } else if (a.axes) {
+      tr.make(sl, s.pos + n * a.axes, a.freq, a.axes, a.R);
+    }
+    const int hn = !live ? 0 : (s.whole ? s.heads : 1);
     float gt[NV][Turns<T, NV, KT>::NC] = {};
     for (int h = 0; h < hn; ++h) {
       sl.row();
@@ -270,7 +332,7 @@ __global__ __launch_bounds__(256) void head_norm_grad_kernel(HeadNormArgs a, int
         }
       }
     }
-    if (s.gpos) {  // (a stretch is then all heads)
+    if (s.gpos && live) {  // (the group has had all heads then)
       for (int ax = 0; ax < a.axes; ++ax) {
         float v = 0.0f;
 #pragma unroll
@@ -328,22 +390,22 @@ static HeadShape head_shape(int d, int K) {
 
 constexpr int kHeadParts = 2048;  // workgroups of the gradient kernel at most
 
-// How the items of both sides are dealt: as many heads of a node to an item as leave an item to each group that the card
-// holds (a node's angles are made once an item).
+// How the items of both sides are dealt: workgroups in the ratio of the sides' elements, at most what the card holds.
+// A group takes one head at a time, its neighbours the next ones, so that a workgroup reads rows in a stretch; whole
+// nodes only for the gradient of positions, which sums over heads.
 static void head_deal(HeadNormArgs& a, int T, int held) {
   const int R = 256 / T;
   const int64_t most = (int64_t)num_cus() * held;
-  const int64_t all = a.side[0].rows * a.side[0].heads + a.side[1].rows * a.side[1].heads;
   int64_t want[2];
+  a.turns = 0;
   for (int i = 0; i < 2; ++i) {
     HeadSide& s = a.side[i];
-    int64_t stretch = s.gpos != nullptr ? s.heads : all / (most * R);
-    stretch = stretch < 1 ? 1 : (stretch > s.heads ? s.heads : stretch);
-    s.stretches = (int)((s.heads + stretch - 1) / stretch);
-    s.stretch = (s.heads + s.stretches - 1) / s.stretches;
-    want[i] = (s.rows * s.stretches + R - 1) / R;
+    s.whole = s.gpos != nullptr;
+    want[i] = (s.rows * (s.whole ? 1 : s.heads) + R - 1) / R;
+    // R heads in a row belong to as many nodes at most
+    const int nodes = R / s.heads + 2 < R ? R / s.heads + 2 : R;
+    if (!s.whole && nodes * a.R > a.turns) a.turns = nodes * a.R;
   }
-  // workgroups in the ratio of the sides' elements, at most what the card holds at once
   const int64_t e0 = a.side[0].rows * a.side[0].heads, e1 = a.side[1].rows * a.side[1].heads;
   int64_t b0 = e0 + e1 > 0 ? (int64_t)((double)most * e0 / (e0 + e1) + 0.5) : 0, b1 = most - b0;
   if (e0 > 0 && b0 < 1) b0 = 1;
@@ -370,7 +432,7 @@ static hipError_t head_launch(HeadNormArgs a, int A, bool grad, int* blocks) {
     blocks[1] = a.blocks_k;
   }
   if (a.blocks_q + a.blocks_k == 0) return hipSuccess;
-  kernel<<<dim3(a.blocks_q + a.blocks_k), dim3(256), 0, a.stream>>>(a, A);
+  kernel<<<dim3(a.blocks_q + a.blocks_k), dim3(256), 2 * sizeof(float2) * a.turns, a.stream>>>(a, A);
   return hipGetLastError();
 }
 
