@@ -29,6 +29,8 @@ namespace eqtp {
 template <int KT>
 constexpr int kTrig = KT == 0 ? 4 : (KT == 1 ? 1 : 2);  // channels of a quad
 
+constexpr int kMaxAxes = 3;
+
 struct HeadShape {
   int T, NV, A;
 };
@@ -187,27 +189,28 @@ __global__ __launch_bounds__(256) void head_norm_kernel(HeadNormArgs a, int A) {
   tr.none();
   extern __shared__ __attribute__((aligned(8))) float2 tables[];
   int turn = 0;
+  RowQuads<E, NV> r0, r1;
+  auto ask = [&](int64_t at) {
+    r0.load((const E*)s.x + at, sl, A, D0);
+    r1.load((const E*)s.x + at + D0, sl, A, D1);
+  };
   for (int64_t first = p.first; first < p.items; first += p.step) {
     const int64_t item = first + g;
     const bool live = item < p.items;
     int64_t n = min(item, p.items - 1);
-    int h0 = 0;
+    int64_t at = n * (s.whole ? s.heads : 1) * (int64_t)(D0 + D1);
+    ask(at);  // (before the angles, which take their time)
     if (!s.whole) {
-      const int64_t n0 = node_of(first, p.items, s.heads), head = n;
-      n = node_of(head, p.items, s.heads);
-      h0 = (int)(head - n * s.heads);
+      const int64_t n0 = node_of(first, p.items, s.heads);
+      n = node_of(n, p.items, s.heads);
       if (a.axes) tr.read(sl, head_turns<R>(a, s, p, first, n0, tables, a.turns, turn) + (n - n0) * a.R, a.R);
     } else if (a.axes) {
       tr.make(sl, s.pos + n * a.axes, a.freq, a.axes, a.R);
     }
     const int hn = !live ? 0 : (s.whole ? s.heads : 1);
-    for (int h = 0; h < hn; ++h) {
+    for (int h = 0; h < hn; ++h, at += D0 + D1) {
       sl.row();
-      const int64_t at = (n * s.heads + h0 + h) * (int64_t)(D0 + D1);
-      const E* x = (const E*)s.x + at;
-      RowQuads<E, NV> r0, r1;
-      r0.load(x, sl, A, D0);
-      r1.load(x + D0, sl, A, D1);
+      if (h > 0) ask(at);
       float x0[NV][4], x1[NV][4], sq[4] = {}, m[4];
       r0.values(sl, A, D0, false, tail0, x0);
       r1.values(sl, A, D1, false, tail1, x1);
@@ -243,6 +246,7 @@ template <class E, int T, int NV, int KT>
 __global__ __launch_bounds__(256) void head_norm_grad_kernel(HeadNormArgs a, int A) {
   constexpr int R = 256 / T;
   __shared__ float pos[R * T * NV * 4];  // per group: a value for each place of a half
+  __shared__ float head_sums[2][R * kMaxAxes];
   const int d = a.d, K = a.K, half = (d + 1) / 2, D0 = half * K, D1 = (d - half) * K, deg = KT == 0 ? 1 : a.lmax + 1;
   Slots<T, KT> sl(K, A);
   const int g = threadIdx.x / T;
@@ -256,29 +260,30 @@ __global__ __launch_bounds__(256) void head_norm_grad_kernel(HeadNormArgs a, int
   tr.none();
   extern __shared__ __attribute__((aligned(8))) float2 tables[];
   int turn = 0;
+  RowQuads<E, NV> r0, r1, q0, q1;
+  auto ask = [&](int64_t at) {
+    r0.load((const E*)s.x + at, sl, A, D0);
+    r1.load((const E*)s.x + at + D0, sl, A, D1);
+    q0.load((const E*)s.gout + at, sl, A, D0);
+    q1.load((const E*)s.gout + at + D0, sl, A, D1);
+  };
   for (int64_t first = p.first; first < p.items; first += p.step) {
     const int64_t item = first + g;
     const bool live = item < p.items;
     int64_t n = min(item, p.items - 1);
-    int h0 = 0;
+    int64_t at = n * (s.whole ? s.heads : 1) * (int64_t)(D0 + D1);
     if (!s.whole) {
-      const int64_t n0 = node_of(first, p.items, s.heads), head = n;
-      n = node_of(head, p.items, s.heads);
-      h0 = (int)(head - n * s.heads);
+      const int64_t n0 = node_of(first, p.items, s.heads);
+      n = node_of(n, p.items, s.heads);
       if (a.axes) tr.read(sl, head_turns<R>(a, s, p, first, n0, tables, a.turns, turn) + (n - n0) * a.R, a.R);
     } else if (a.axes) {
       tr.make(sl, s.pos + n * a.axes, a.freq, a.axes, a.R);
     }
     const int hn = !live ? 0 : (s.whole ? s.heads : 1);
     float gt[NV][Turns<T, NV, KT>::NC] = {};
-    for (int h = 0; h < hn; ++h) {
+    for (int h = 0; h < hn; ++h, at += D0 + D1) {
       sl.row();
-      const int64_t at = (n * s.heads + h0 + h) * (int64_t)(D0 + D1);
-      RowQuads<E, NV> r0, r1, q0, q1;
-      r0.load((const E*)s.x + at, sl, A, D0);
-      r1.load((const E*)s.x + at + D0, sl, A, D1);
-      q0.load((const E*)s.gout + at, sl, A, D0);
-      q1.load((const E*)s.gout + at + D0, sl, A, D1);
+      ask(at);
       float x0[NV][4], x1[NV][4], u0[NV][4], u1[NV][4], sq[4] = {}, sa[4] = {}, m[4], ma[4];
       r0.values(sl, A, D0, false, tail0, x0);
       r1.values(sl, A, D1, false, tail1, x1);
@@ -332,7 +337,8 @@ __global__ __launch_bounds__(256) void head_norm_grad_kernel(HeadNormArgs a, int
         }
       }
     }
-    if (s.gpos && live) {  // (the group has had all heads then)
+    if (s.gpos) {  // over the heads: the group's own, or groups beside each other
+      float* sums = head_sums[turn] + g * kMaxAxes;
       for (int ax = 0; ax < a.axes; ++ax) {
         float v = 0.0f;
 #pragma unroll
@@ -343,7 +349,21 @@ __global__ __launch_bounds__(256) void head_norm_grad_kernel(HeadNormArgs a, int
             if (sl.on && ch < a.R) v = fmaf(a.freq[ax * a.R + ch], gt[j][q], v);
           }
         v = lane_sum<T>(v);
-        if (sl.t == 0) s.gpos[n * a.axes + ax] = v;
+        if (sl.t == 0 && live) {
+          if (s.whole) s.gpos[n * a.axes + ax] = v;
+          else sums[ax] = v;
+        }
+      }
+      if (!s.whole) {
+        __syncthreads();
+        const int64_t n0 = node_of(first, p.items, s.heads);
+        for (int i = threadIdx.x; i < R / s.heads * a.axes; i += 256) {
+          const int k = i / a.axes, ax = i - k * a.axes;
+          if (n0 + k >= s.rows) continue;
+          float v = 0.0f;
+          for (int h = 0; h < s.heads; ++h) v += head_sums[turn][(k * s.heads + h) * kMaxAxes + ax];
+          s.gpos[(n0 + k) * a.axes + ax] = v;
+        }
       }
     }
   }
@@ -372,14 +392,14 @@ __global__ __launch_bounds__(256) void head_norm_grad_kernel(HeadNormArgs a, int
 
 // The smallest group whose threads hold half a head's row in two quads or fewer; beyond 64 threads' worth, four or six
 // (a head's row has up to 2048 elements).
-static HeadShape head_shape(int d, int K) {
+static HeadShape head_shape(int d, int K, bool grad) {
   const int D0 = (d + 1) / 2 * K, Q = (D0 + 3) / 4;
   const int P = K % 4 == 0 ? K / 4 : K;
   HeadShape s = {64, 0, 64 / P * P};
-  for (int T : {2, 4, 8, 16, 32}) {
-    if (K > 1 && T < 8) continue;
+  for (int T : {1, 2, 4, 8, 16, 32}) {
+    if (T < (K > 1 ? 8 : (grad ? 2 : 1))) continue;
     const int A = T / P * P;
-    if (A > 0 && (Q + A - 1) / A <= 2) {
+    if (A > 0 && (Q + A - 1) / A <= (grad ? 1 : 2)) {
       s = {T, 0, A};
       break;
     }
@@ -392,7 +412,7 @@ constexpr int kHeadParts = 2048;  // workgroups of the gradient kernel at most
 
 // How the items of both sides are dealt: workgroups in the ratio of the sides' elements, at most what the card holds.
 // A group takes one head at a time, its neighbours the next ones, so that a workgroup reads rows in a stretch; whole
-// nodes only for the gradient of positions, which sums over heads.
+// nodes only for the gradient of positions where a workgroup's groups are no whole number of nodes: it sums over heads.
 static void head_deal(HeadNormArgs& a, int T, int held) {
   const int R = 256 / T;
   const int64_t most = (int64_t)num_cus() * held;
@@ -400,7 +420,7 @@ static void head_deal(HeadNormArgs& a, int T, int held) {
   a.turns = 0;
   for (int i = 0; i < 2; ++i) {
     HeadSide& s = a.side[i];
-    s.whole = s.gpos != nullptr;
+    s.whole = s.gpos != nullptr && R % s.heads != 0;
     want[i] = (s.rows * (s.whole ? 1 : s.heads) + R - 1) / R;
     // R heads in a row belong to as many nodes at most
     const int nodes = R / s.heads + 2 < R ? R / s.heads + 2 : R;
@@ -438,7 +458,8 @@ static hipError_t head_launch(HeadNormArgs a, int A, bool grad, int* blocks) {
 
 // Calls F(T, NV): the next of the built sizes.
 #define EQTP_HEAD_SHAPES0(s, F)                                                              \
-  ((s).T == 2    ? ((s).NV <= 1 ? F(2, 1) : F(2, 2))                                         \
+  ((s).T == 1    ? ((s).NV <= 1 ? F(1, 1) : F(1, 2))                                         \
+   : (s).T == 2  ? ((s).NV <= 1 ? F(2, 1) : F(2, 2))                                                                   \
    : (s).T == 4  ? F(4, 2)                                                                   \
    : (s).T == 8  ? F(8, 2)                                                                   \
    : (s).T == 16 ? F(16, 2)                                                                  \
@@ -450,9 +471,23 @@ static hipError_t head_launch(HeadNormArgs a, int A, bool grad, int* blocks) {
    : (s).T == 32 ? ((s).NV <= 1 ? F(32, 1) : F(32, 2))                                       \
                  : ((s).NV <= 2 ? F(64, 2) : ((s).NV <= 4 ? F(64, 4) : F(64, 6))))
 
+#define EQTP_HEAD_GRAD_SHAPES0(s, F)                                                         \
+  ((s).T == 2    ? F(2, 1)                                                                   \
+   : (s).T == 4  ? F(4, 1)                                                                   \
+   : (s).T == 8  ? F(8, 1)                                                                   \
+   : (s).T == 16 ? F(16, 1)                                                                  \
+   : (s).T == 32 ? F(32, 1)                                                                  \
+                 : ((s).NV <= 1 ? F(64, 1) : ((s).NV <= 2 ? F(64, 2) : F(64, 4))))
+#define EQTP_HEAD_GRAD_SHAPES1(s, F)                                                         \
+  ((s).T == 8    ? F(8, 1)                                                                   \
+   : (s).T == 16 ? F(16, 1)                                                                  \
+   : (s).T == 32 ? F(32, 1)                                                                  \
+                 : ((s).NV <= 1 ? F(64, 1)                                                   \
+                                : ((s).NV <= 2 ? F(64, 2) : ((s).NV <= 4 ? F(64, 4) : F(64, 6)))))
+
 template <class E, int KT>
 static hipError_t head_norm_t(const HeadNormArgs& a) {
-  const HeadShape s = head_shape(a.d, a.K);
+  const HeadShape s = head_shape(a.d, a.K, false);
 #define EQTP_HEAD(T_, NV_) head_launch<head_norm_kernel<E, T_, NV_, KT>, T_>(a, s.A, false, nullptr)
   if constexpr (KT == 0) return EQTP_HEAD_SHAPES0(s, EQTP_HEAD);
   else return EQTP_HEAD_SHAPES1(s, EQTP_HEAD);
@@ -461,10 +496,10 @@ static hipError_t head_norm_t(const HeadNormArgs& a) {
 
 template <class E, int KT>
 static hipError_t head_norm_grad_t(const HeadNormArgs& a, int* blocks) {
-  const HeadShape s = head_shape(a.d, a.K);
+  const HeadShape s = head_shape(a.d, a.K, true);
 #define EQTP_HEAD(T_, NV_) head_launch<head_norm_grad_kernel<E, T_, NV_, KT>, T_>(a, s.A, true, blocks)
-  if constexpr (KT == 0) return EQTP_HEAD_SHAPES0(s, EQTP_HEAD);
-  else return EQTP_HEAD_SHAPES1(s, EQTP_HEAD);
+  if constexpr (KT == 0) return EQTP_HEAD_GRAD_SHAPES0(s, EQTP_HEAD);
+  else return EQTP_HEAD_GRAD_SHAPES1(s, EQTP_HEAD);
 #undef EQTP_HEAD
 }
 
