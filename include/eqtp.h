@@ -860,7 +860,7 @@ typedef struct eqtp_expert_desc {
  *          together is faster.
  *   out    [N, C, K] (out_dtype), fully overwritten.
  * h, W, out, grad_out, grad_h and grad_W are 16-byte aligned.  A node's sum
- * goes over its experts in ascending order, in fp32, and is rounded once.
+ * goes over its experts in a fixed order, in fp32, and is rounded once.
  * Backward, each output may be NULL, fully overwritten:
  *   grad_h      [N, C, K] (x_dtype) = sum_j weight W^T grad_out;
  *   grad_weight [N, top_k] fp32 = <grad_out, W h> (0 at places without an expert);

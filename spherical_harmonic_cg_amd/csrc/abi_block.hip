@@ -122,8 +122,19 @@ int expert_check(const eqtp_expert_desc* d, int64_t N) {
 }
 
 int64_t expert_weights(const eqtp_expert_desc* d) { return (int64_t)d->experts * (d->lmax + 1) * d->C * d->C; }
-int64_t transposed_bytes(const eqtp_expert_desc* d) {
-  return (expert_weights(d) * (d->x_dtype == EQTP_BF16 ? 2 : 4) + 255) / 256 * 256;
+// the workspace of the backward pass: transposed weights, parts of the gates' gradient, the weight gradient's lines
+struct ExpertWs {
+  int64_t gates, lines, total;
+};
+ExpertWs expert_ws(const eqtp_expert_desc* d, int64_t N) {
+  auto al = [](int64_t b) { return (b + 255) / 256 * 256; };
+  const bool bf16 = d->x_dtype == EQTP_BF16;
+  ExpertWs w;
+  w.gates = eqtp::expert_as_is(N) ? 0 : al(expert_weights(d) * (bf16 ? 2 : 4));
+  w.lines = w.gates + al(4 * eqtp::expert_gate_floats(N, d->C, d->lmax, d->top_k));
+  w.total = w.lines + 4 * eqtp::expert_grad_floats(N, d->C, d->lmax, d->experts, d->top_k, bf16);
+  if (w.total < 16) w.total = 16;
+  return w;
 }
 
 }  // namespace
@@ -298,7 +309,7 @@ int eqtp_expert_linear(const eqtp_expert_desc* d, int64_t N, const void* h, cons
 int64_t eqtp_expert_linear_backward_workspace_bytes(const eqtp_expert_desc* d, int64_t N) {
   const int rc = expert_check(d, N);
   if (rc != EQTP_OK) return -rc;
-  return transposed_bytes(d) + 4 * eqtp::expert_grad_floats(N, d->C, d->lmax, d->experts, d->top_k, d->x_dtype == EQTP_BF16);
+  return expert_ws(d, N).total;
 }
 
 int eqtp_expert_linear_backward(const eqtp_expert_desc* d, int64_t N, const void* h, const void* W, const int32_t* idx,
@@ -314,14 +325,16 @@ int eqtp_expert_linear_backward(const eqtp_expert_desc* d, int64_t N, const void
   if (N > 0 && !grad_h && !grad_W && !grad_weight) return EQTP_EINVAL;
   if (N > 0 && (!grad_out || (rows && (!W || !idx)) || ((grad_W || grad_weight) && !h))) return EQTP_EINVAL;
   if (grad_W && (!ptr || (N > 0 && !slots))) return EQTP_EINVAL;
-  const int64_t part = transposed_bytes(d);
-  if (!workspace || !aligned16(workspace) ||
-      workspace_bytes < part + 4 * eqtp::expert_grad_floats(N, d->C, d->lmax, d->experts, d->top_k, bf16))
-    return EQTP_EINVAL;
+  const ExpertWs ws = expert_ws(d, N);
+  if (!workspace || !aligned16(workspace) || workspace_bytes < ws.total) return EQTP_EINVAL;
+  unsigned char* base = static_cast<unsigned char*>(workspace);
   const hipStream_t st = (hipStream_t)stream;
   if (rows && N > 0) {
-    const int rt = status_of(eqtp::launch_transpose_weights((int64_t)d->experts * (d->lmax + 1), d->C, bf16, W, workspace, st));
-    if (rt != EQTP_OK) return rt;
+    const bool as_is = eqtp::expert_as_is(N);
+    if (!as_is) {
+      const int rt = status_of(eqtp::launch_transpose_weights((int64_t)d->experts * (d->lmax + 1), d->C, bf16, W, workspace, st));
+      if (rt != EQTP_OK) return rt;
+    }
     eqtp::ExpertArgs a = {};
     a.N = N;
     a.C = d->C;
@@ -331,13 +344,15 @@ int eqtp_expert_linear_backward(const eqtp_expert_desc* d, int64_t N, const void
     a.bf16 = bf16;
     a.out_bf16 = bf16;
     a.h = grad_out;
-    a.W = workspace;
+    a.W = as_is ? W : workspace;
+    a.as_is = as_is;
     a.idx = idx;
     a.weight = weight;
     a.order = order;
     a.out = grad_h;
     a.dot_with = h;
     a.gweight = grad_weight;
+    a.part = reinterpret_cast<float*>(base + ws.gates);
     a.stream = st;
     const int rg = status_of(eqtp::launch_expert(a));
     if (rg != EQTP_OK) return rg;
@@ -356,7 +371,7 @@ int eqtp_expert_linear_backward(const eqtp_expert_desc* d, int64_t N, const void
   g.slots = slots;
   g.ptr = ptr;
   g.gW = grad_W;
-  g.part = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + part);
+  g.part = reinterpret_cast<float*>(base + ws.lines);
   g.stream = st;
   return status_of(eqtp::launch_expert_grad(g));
 }

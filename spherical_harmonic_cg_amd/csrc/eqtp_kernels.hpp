@@ -228,15 +228,19 @@ struct ExpertArgs {
   bool bf16, out_bf16;
   const void* h;          // forward: features; backward: the output's gradient
   const void* W;          // [X, lmax+1, out channel, in channel] as the products take it
+  bool as_is;             // very few nodes, backward: the weights as they are, the other way round
   const int32_t* idx;
   const float* weight;    // or nullptr
   const int32_t* order;   // or nullptr
   void* out;              // backward: h's gradient, or nullptr
   const void* dot_with;   // backward: h, for the gates' gradient
   float* gweight;         // or nullptr
+  float* part;            // few nodes, with gweight: expert_gate_floats floats
   hipStream_t stream;
 };
+int64_t expert_gate_floats(int64_t N, int C, int lmax, int k);
 hipError_t launch_expert(const ExpertArgs& a);
+bool expert_as_is(int64_t N);  // so few nodes that the backward pass takes the weights as they are
 hipError_t launch_transpose_weights(int64_t matrices, int C, bool bf16, const void* W, void* WT, hipStream_t stream);
 struct ExpertGradArgs {
   int64_t N;

@@ -651,8 +651,103 @@ static hipError_t expert_l(const ExpertArgs& a) {
   }
 }
 
+// ---------------------------------------------------------------------------
+// Few nodes: a tile of 16 columns would multiply mostly nothing, and one wave
+// after the other would wait for weights.  A workgroup takes CB output channels of one node, its features in
+// LDS; a thread one output component at a time, with vector-ALU products.
+// For very few nodes the backward pass reads the weights as they are (no transposed copy).
+// ---------------------------------------------------------------------------
+constexpr int kFewThreads = 256;
+
+template <class S, bool DOT, bool TRANS>
+__global__ __launch_bounds__(kFewThreads) void expert_few_kernel(ExpertArgs a, int CB) {
+  extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
+  __shared__ float sums[kFewThreads / 64][kMaxTopK];
+  float* h = reinterpret_cast<float*>(lds);  // [C][K]
+  const int C = a.C, K = num_comp(a.lmax), tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
+  const int64_t n = blockIdx.x;
+  const int c0 = blockIdx.y * CB;
+  const S* src = static_cast<const S*>(a.h) + n * C * K;
+  for (int i = tid; i < C * K; i += kFewThreads) h[i] = (float)src[i];
+  if constexpr (DOT)
+    for (int i = tid; i < kFewThreads / 64 * kMaxTopK; i += kFewThreads) (&sums[0][0])[i] = 0.0f;
+  __syncthreads();
+  for (int o0 = 0; o0 < CB * K; o0 += kFewThreads) {
+    const bool on = o0 + tid < CB * K;
+    const int o = on ? o0 + tid : 0, co = c0 + o / K, m = o - o / K * K, l = degree_of_plane(m);
+    float total = 0.0f;
+    const float with = DOT && on ? (float)static_cast<const S*>(a.dot_with)[(n * C + co) * K + m] : 0.0f;
+    for (int j = 0; j < a.k; ++j) {
+      const int e = a.idx[n * a.k + j];
+      if (e < 0 || e >= a.X) continue;
+      const S* W = static_cast<const S*>(a.W) + (int64_t)(e * (a.lmax + 1) + l) * C * C + (TRANS ? co : co * C);
+      float acc = 0.0f;
+#pragma unroll 8
+      for (int c = 0; c < C; ++c) acc = fmaf((float)W[TRANS ? c * C : c], h[c * K + m], acc);
+      total = fmaf(a.weight ? a.weight[n * a.k + j] : 1.0f, acc, total);
+      if constexpr (DOT) {
+        const float d = lane_sum<64>(acc * with);
+        if (lane == 0) sums[wv][j] += d;
+      }
+    }
+    if (on && a.out != nullptr) {
+      const int64_t at = (n * C + co) * K + m;
+      if (a.out_bf16) static_cast<__bf16*>(a.out)[at] = (__bf16)total;
+      else static_cast<float*>(a.out)[at] = total;
+    }
+  }
+  if constexpr (DOT) {
+    __syncthreads();
+    if (tid < a.k) a.part[(n * a.k + tid) * gridDim.y + blockIdx.y] = (sums[0][tid] + sums[1][tid]) + (sums[2][tid] + sums[3][tid]);
+  }
+}
+// the workgroups' sums of each place, in order
+__global__ __launch_bounds__(256) void expert_few_gates_kernel(int64_t places, int parts, const float* __restrict__ part,
+                                                               float* __restrict__ gweight) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= places) return;
+  float v = 0.0f;
+  for (int j = 0; j < parts; ++j) v += part[i * parts + j];
+  gweight[i] = v;
+}
+
+// Up to 512 nodes (us, fp32, 8 experts, 2 of a node, against the tiles: 64 channels at lmax 3, 256 nodes 10 / 38, 512 nodes
+// 15 / 28, 1024 nodes 28 / 28; 128 channels at lmax 0, 512 nodes 12 / 15, 1024 nodes 21 / 15; bf16, 128 channels at lmax
+// 3, 512 nodes 38 / 37).
+static bool expert_few(int64_t N) { return N <= 512; }
+// The other way round the weights are read an element at a time (us, gradients of 128 channels at lmax 3: 32 nodes 27, with
+// the transposed copy 20; one node 17, 20).
+bool expert_as_is(int64_t N) { return N <= 16; }
+// a workgroup's outputs: a thread each
+static int few_channels(int C, int K) {
+  int CB = kFewThreads / K < C ? kFewThreads / K : C;
+  while (C % CB != 0) --CB;
+  return CB;
+}
+int64_t expert_gate_floats(int64_t N, int C, int lmax, int k) {
+  return expert_few(N) ? N * k * (C / few_channels(C, num_comp(lmax))) : 0;
+}
+
+template <class S>
+static hipError_t few_launch(const ExpertArgs& a) {
+  const int K = num_comp(a.lmax), bytes = a.C * K * 4, CB = few_channels(a.C, K);
+  const dim3 grid((unsigned)a.N, a.C / CB);
+  if (a.gweight) {
+    if (a.as_is) expert_few_kernel<S, true, true><<<grid, dim3(kFewThreads), bytes, a.stream>>>(a, CB);
+    else expert_few_kernel<S, true, false><<<grid, dim3(kFewThreads), bytes, a.stream>>>(a, CB);
+    expert_few_gates_kernel<<<dim3((unsigned)((a.N * a.k + 255) / 256)), dim3(256), 0, a.stream>>>(a.N * a.k, a.C / CB, a.part,
+                                                                                                 a.gweight);
+  } else if (a.as_is) {
+    expert_few_kernel<S, false, true><<<grid, dim3(kFewThreads), bytes, a.stream>>>(a, CB);
+  } else {
+    expert_few_kernel<S, false, false><<<grid, dim3(kFewThreads), bytes, a.stream>>>(a, CB);
+  }
+  return hipGetLastError();
+}
+
 hipError_t launch_expert(const ExpertArgs& a) {
   if (a.N == 0) return hipSuccess;
+  if (expert_few(a.N)) return a.bf16 ? few_launch<__bf16>(a) : few_launch<float>(a);
   if (a.gweight) return a.bf16 ? expert_l<__bf16, true>(a) : expert_l<float, true>(a);
   return a.bf16 ? expert_l<__bf16, false>(a) : expert_l<float, false>(a);
 }

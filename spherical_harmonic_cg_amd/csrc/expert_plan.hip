@@ -5,7 +5,7 @@
 //   ptr [X+1]:   where each expert's places begin;
 //   order [N]:   the nodes by their two lowest experts.
 // Stable counting sorts of both at once: counts of a tile of nodes in LDS, one
-// scan, ranks from wave ballots; three launches.  With many experts the nodes'
+// scan, ranks from wave ballots; three launches, or one for few places.  With many experts the nodes'
 // second key is coarsened to 1024 bins in all: order only has to be a good
 // one, the linear's results do not depend on it.
 #include "eqtp_device.hpp"
@@ -176,9 +176,61 @@ __global__ __launch_bounds__(256) void plan_place_kernel(PlanShape p, const int3
   }
 }
 
+// Few places: all three steps by one workgroup (256 places a round, two groupings).
+constexpr int kFewPlaces = 1024;
+__global__ __launch_bounds__(256) void plan_few_kernel(PlanShape p, const int32_t* __restrict__ idx, int32_t* __restrict__ slots,
+                                                       int32_t* __restrict__ order, int32_t* __restrict__ ptr) {
+  __shared__ int toff[kPlanBins], wcnt[4 * kPlanBins], wsum[4];
+  const int t = threadIdx.x, lane = t & 63, wv = t >> 6;
+  for (int nodes = 0; nodes < (order ? 2 : 1); ++nodes) {
+    const int bins = nodes ? p.bins2 : p.X + 1, count = (int)(nodes ? p.N : p.N * p.k);
+    for (int b = t; b < kPlanBins; b += 256) toff[b] = 0;
+    for (int b = t; b < 4 * bins; b += 256) wcnt[b] = 0;
+    __syncthreads();
+    for (int i = t; i < count; i += 256) atomicAdd(&toff[nodes ? node_key(p, idx, i) : expert_of(idx[i], p.X)], 1);
+    __syncthreads();
+    // exclusive scan of the 1024 bins, four a thread
+    int v[4], sum = 0;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      v[q] = toff[4 * t + q];
+      sum += v[q];
+    }
+    int incl = sum;
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+      const int u = __shfl_up(incl, off, 64);
+      if (lane >= off) incl += u;
+    }
+    if (lane == 63) wsum[wv] = incl;
+    __syncthreads();
+    int run = incl - sum;
+    for (int w = 0; w < wv; ++w) run += wsum[w];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      toff[4 * t + q] = run;
+      if (!nodes && 4 * t + q <= p.X) ptr[4 * t + q] = run;
+      run += v[q];
+    }
+    __syncthreads();
+    const int bits = bits_for(bins);
+    for (int i = 0; i < count; i += 256) {
+      const bool valid = i + t < count;
+      const int key = !valid ? 0 : (nodes ? node_key(p, idx, i + t) : expert_of(idx[i + t], p.X));
+      const int pos = take_places(key, valid, bits, bins, toff, wcnt);
+      if (valid) (nodes ? order : slots)[pos] = i + t;
+    }
+    __syncthreads();
+  }
+}
+
 hipError_t launch_expert_plan(int64_t N, int k, int X, const int32_t* idx, int32_t* order, int32_t* slots, int32_t* ptr,
                               int32_t* ws, hipStream_t stream) {
   const PlanShape p = plan_shape(N, k, X);
+  if (N * k <= kFewPlaces) {
+    hipLaunchKernelGGL(plan_few_kernel, dim3(1), dim3(256), 0, stream, p, idx, slots, order, ptr);
+    return hipGetLastError();
+  }
   int* hist1 = ws;
   int* hist2 = order ? ws + (int64_t)(X + 1) * p.tiles : nullptr;
   hipLaunchKernelGGL(plan_count_kernel, dim3(p.tiles), dim3(256), 0, stream, p, idx, hist1, hist2);

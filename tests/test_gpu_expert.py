@@ -46,7 +46,13 @@ class Mix:
     (1, 64, 3, 8, 2, True), (1, 8, 0, 1, 1, False), (16, 16, 1, 3, 1, False), (17, 32, 2, 4, 2, True), (50, 64, 3, 10, 1, False),
     (33, 128, 3, 5, 2, True), (40, 32, 3, 8, 4, True), (12, 8, 4, 6, 3, True), (9, 16, 6, 3, 2, True), (5, 128, 6, 2, 2, True),
     (7, 64, 5, 40, 3, True), (300, 16, 0, 256, 4, True), (100, 128, 0, 2, 1, True), (64, 32, 1, 33, 16, True),
-    (70, 8, 3, 4, 2, False)])
+    (70, 8, 3, 4, 2, False),
+    # more than 512 nodes: tiles of 16 on the matrix cores, every width and stretch of degrees
+    (520, 64, 3, 10, 1, False), (530, 64, 3, 8, 2, True), (515, 128, 3, 3, 2, True), (529, 32, 3, 8, 4, True),
+    (521, 16, 3, 5, 2, True), (600, 8, 3, 6, 2, True), (517, 128, 0, 4, 2, True), (700, 64, 0, 9, 1, False),
+    (540, 32, 1, 33, 5, True), (523, 64, 1, 7, 2, True), (531, 128, 1, 2, 1, False), (513, 32, 2, 4, 2, True),
+    (518, 64, 2, 3, 1, True), (514, 16, 2, 256, 2, True), (519, 32, 4, 3, 2, True), (516, 64, 4, 4, 1, False),
+    (513, 16, 5, 3, 2, True), (515, 8, 6, 4, 3, True), (514, 64, 6, 2, 2, True)])
 def test_expert_linear(N, C, lmax, X, k, gates, x):
     eq = _eq()
     _say("experts N=%d C=%d lmax=%d X=%d k=%d %s" % (N, C, lmax, X, k, x))
