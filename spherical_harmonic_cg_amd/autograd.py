@@ -1,5 +1,6 @@
 """PyTorch autograd wrappers of the fused convolution and of the parts of a
-transformer block around it (norm, dropout, attention).
+transformer block around it (norm, dropout, attention with its distance bias
+and the norm of queries and keys, routing and the experts' linears).
 
 The forward calls eqtp_conv_fused.  The backward groups the edges by source
 node on the GPU (eqtp_edge_rows, eqtp_sort_edges) so that grad_x is summed per
@@ -225,6 +226,90 @@ class GraphAttentionFunction(torch.autograd.Function):
         return gq, gk, gv, gb, None, None, None, None, None, None
 
 
+class DistanceBiasFunction(torch.autograd.Function):
+    """out = the table's rows by edge length."""
+
+    @staticmethod
+    def forward(ctx, table, vec, bounds, r_cut):
+        ctx.save_for_backward(vec, bounds)
+        ctx.r_cut = r_cut
+        return _eq.eqtp_distance_bias(vec, bounds, table, r_cut=r_cut)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, grad_out):
+        if not ctx.needs_input_grad[0]:
+            return (None,) * 4
+        vec, bounds = ctx.saved_tensors
+        return _eq.eqtp_distance_bias_backward(vec, bounds, _dense(grad_out), r_cut=ctx.r_cut), None, None, None
+
+
+class QkNormFunction(torch.autograd.Function):
+    """(q, k) normed by head and degree and turned by position."""
+
+    @staticmethod
+    def forward(ctx, q, k, weight_q, weight_k, pos_q, pos_k, freq, lmax, heads, eps):
+        ctx.save_for_backward(q, k, weight_q, weight_k, pos_q, pos_k, freq)
+        ctx.lmax, ctx.heads, ctx.eps = lmax, heads, eps
+        ctx.set_materialize_grads(False)
+        return _eq.eqtp_qk_norm(q, k, lmax, heads, weight_q, weight_k, pos_q, pos_k, freq, eps)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, grad_q, grad_k):
+        q, k, weight_q, weight_k, pos_q, pos_k, freq = ctx.saved_tensors
+        need = ctx.needs_input_grad
+        if (grad_q is None and grad_k is None) or not any(need[:6]):
+            return (None,) * 10
+        gq, gk, gwq, gwk, gpq, gpk = _eq.eqtp_qk_norm_backward(
+            q, k, _dense(grad_q), _dense(grad_k), ctx.lmax, ctx.heads, weight_q, weight_k, pos_q, pos_k, freq, ctx.eps,
+            need_q=need[0], need_k=need[1], need_weight_q=need[2], need_weight_k=need[3], need_pos=need[4] or need[5])
+        return gq, gk, gwq, gwk, gpq if need[4] else None, gpk if need[5] else None, None, None, None, None
+
+
+class RouteFunction(torch.autograd.Function):
+    """(idx, weight) of a routing."""
+
+    @staticmethod
+    def forward(ctx, logits, bias, top_k, score, groups, top_groups, renormalise, scale):
+        idx, weight = _eq.eqtp_route(logits, top_k, score, bias, groups, top_groups, renormalise, scale)
+        ctx.save_for_backward(logits, idx)
+        ctx.how = score, renormalise, scale
+        ctx.mark_non_differentiable(idx)
+        return idx, weight
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, _, grad_weight):
+        if not ctx.needs_input_grad[0]:
+            return (None,) * 8
+        logits, idx = ctx.saved_tensors
+        return (_eq.eqtp_route_backward(logits, idx, _dense(grad_weight), *ctx.how),) + (None,) * 7
+
+
+class ExpertLinearFunction(torch.autograd.Function):
+    """out = the experts' per-degree linears of h, summed under their weights."""
+
+    @staticmethod
+    def forward(ctx, h, W, weight, idx, lmax, out_dtype, plan):
+        ctx.save_for_backward(h, W, weight, idx, *(plan if plan is not None else ()))
+        ctx.lmax = lmax
+        return _eq.eqtp_expert_linear(h, W, idx, lmax, weight=weight, plan=plan, out_dtype=out_dtype)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, grad_out):
+        h, W, weight, idx = ctx.saved_tensors[:4]
+        plan = ctx.saved_tensors[4:]
+        need_h, need_W, need_weight = ctx.needs_input_grad[:3]
+        if not (need_h or need_W or need_weight):
+            return (None,) * 7
+        gh, gW, gw = _eq.eqtp_expert_linear_backward(h, W, idx, _dense(grad_out.to(h.dtype)), ctx.lmax, weight=weight,
+                                                     plan=plan if len(plan) == 3 else None, need_h=need_h, need_W=need_W,
+                                                     need_weight=need_weight)
+        return gh, gW.to(W.dtype) if gW is not None else None, gw, None, None, None, None
+
+
 def attention_plan(src, row_ptr, M: int):
     """(src_ptr [M+1], dst_s [E], perm [E]): the edges grouped by source, what graph_attention's backward pass needs;
     made once, it serves every layer and step over the same graph."""
@@ -257,3 +342,31 @@ def graph_attention(q, k, v, src, row_ptr, lmax: int, heads: int, scale: float =
     """Differentiable attention over a graph (see eqtp_attention).  ``plan``: attention_plan's result, or None to
     group the edges in each backward pass.  ``scale`` is a number and gets no gradient (scale q to learn one)."""
     return GraphAttentionFunction.apply(q, k, v, bias, src, row_ptr, lmax, heads, scale, plan)
+
+
+def distance_bias(vec, bounds, table, r_cut: float = 0.0):
+    """Differentiable (in ``table``) bias of graph_attention's logits by edge length (see eqtp_distance_bias); vec gets
+    no gradient."""
+    return DistanceBiasFunction.apply(table, vec, bounds, float(r_cut))
+
+
+def qk_norm(q, k, lmax: int, heads: int, weight_q=None, weight_k=None, pos_q=None, pos_k=None, freq=None,
+            eps: float = 1e-5):
+    """Differentiable (q, k) for graph_attention, normed by head and degree and turned by position (see eqtp_qk_norm);
+    ``freq`` gets no gradient."""
+    if pos_k is None and freq is not None and q.shape[0] == k.shape[0]:
+        pos_k = pos_q  # both sides' gradients then reach it
+    return QkNormFunction.apply(q, k, weight_q, weight_k, pos_q, pos_k, freq, lmax, heads, float(eps))
+
+
+def route(logits, top_k: int, score: int = _eq.EQTP_SCORE_SOFTMAX, bias=None, groups: int = 1, top_groups: int = None,
+          renormalise: bool = True, scale: float = 1.0):
+    """Differentiable (in ``logits``, through the weights) (idx, weight) (see eqtp_route); ``bias`` steers the choice and
+    gets no gradient."""
+    return RouteFunction.apply(logits, bias, top_k, score, groups, top_groups, renormalise, float(scale))
+
+
+def expert_linear(h, W, idx, lmax: int, weight=None, plan=None, out_dtype: int = None):
+    """Differentiable per-degree linears by expert (see eqtp_expert_linear).  ``plan``: eqtp_expert_plan's result, which
+    serves every layer over the same routing, or None to make it in each backward pass."""
+    return ExpertLinearFunction.apply(h, W, weight, idx, lmax, out_dtype, plan)

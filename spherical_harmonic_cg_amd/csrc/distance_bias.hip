@@ -222,7 +222,7 @@ hipError_t launch_distance_bias_grad(const BiasArgs& a, float* grad_table) {
       if (e != hipSuccess) return e;
     }
   }
-  return launch_line_sums(a.B * a.H, a.E > 0 ? s.blocks : 0, a.part, grad_table, a.stream);
+  return launch_line_sums({a.B * a.H, a.E > 0 ? s.blocks : 0, a.part, grad_table}, {}, a.stream);
 }
 
 }  // namespace eqtp

@@ -269,7 +269,12 @@ hipError_t launch_norm(const NormArgs& a);
 int64_t norm_workspace_floats(int64_t N, int C, int lmax);
 hipError_t launch_norm_grad(const NormGradArgs& a);
 // out[cols] = the sums of the columns of part [parts][cols], in 64 bits and a fixed order
-hipError_t launch_line_sums(int cols, int parts, const float* part, float* out, hipStream_t stream);
+struct LineSums {
+  int cols, parts;  // cols 0: none
+  const float* part;
+  float* out;
+};
+hipError_t launch_line_sums(const LineSums& a, const LineSums& b, hipStream_t stream);
 hipError_t launch_dropout(const DropArgs& a);
 hipError_t launch_sh(const float* vec, int64_t E, int lmax, float* Y, hipStream_t stream);
 hipError_t launch_conv_node(const ConvArgs& a);   // sorted edges, fixed weights, matrix cores

@@ -14,7 +14,7 @@
 namespace eqtp {
 
 constexpr int kPlanBins = 1024;
-constexpr int kPlanTiles = 64;  // tiles at most
+constexpr int kPlanTiles = 256, kPlanCounts = 1 << 16;  // tiles, and counts of the nodes' keys, at most (one workgroup adds them)
 
 struct PlanShape {
   int X, k, b_bins, bins2, rounds, tiles;
@@ -27,7 +27,8 @@ static PlanShape plan_shape(int64_t N, int k, int X) {
   p.k = k;
   p.b_bins = X + 1 < kPlanBins / (X + 1) ? X + 1 : kPlanBins / (X + 1);
   p.bins2 = (X + 1) * p.b_bins;
-  const int64_t r = (N + 256 * kPlanTiles - 1) / (256 * kPlanTiles);
+  const int64_t most = 256 * (int64_t)(kPlanCounts / p.bins2 < kPlanTiles ? kPlanCounts / p.bins2 : kPlanTiles);
+  const int64_t r = (N + most - 1) / most;
   p.rounds = r < 1 ? 1 : (int)r;
   p.tiles = (int)((N + 256 * (int64_t)p.rounds - 1) / (256 * (int64_t)p.rounds));
   if (p.tiles < 1) p.tiles = 1;

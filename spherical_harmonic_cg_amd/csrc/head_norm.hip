@@ -522,12 +522,11 @@ hipError_t launch_head_norm_grad(const HeadNormArgs& a, float* const (&gw)[2]) {
     else e = a.K == 1 ? head_norm_grad_t<float, 0>(a, blocks) : (a.K % 4 == 0 ? head_norm_grad_t<float, 1>(a, blocks) : head_norm_grad_t<float, 2>(a, blocks));
     if (e != hipSuccess) return e;
   }
+  LineSums l[2] = {};
+  int n = 0;
   for (int i = 0; i < 2; ++i)
-    if (gw[i]) {
-      const hipError_t e = launch_line_sums((a.lmax + 1) * a.d, blocks[i], a.side[i].part, gw[i], a.stream);
-      if (e != hipSuccess) return e;
-    }
-  return hipSuccess;
+    if (gw[i]) l[n++] = {(a.lmax + 1) * a.d, blocks[i], a.side[i].part, gw[i]};
+  return launch_line_sums(l[0], l[1], a.stream);
 }
 
 }  // namespace eqtp

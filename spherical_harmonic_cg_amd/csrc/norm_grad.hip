@@ -197,9 +197,31 @@ __global__ __launch_bounds__(1024) void norm_weight_sum_kernel(int cols, int wco
   }
 }
 
-hipError_t launch_line_sums(int cols, int parts, const float* part, float* out, hipStream_t stream) {
-  hipLaunchKernelGGL(norm_weight_sum_kernel, dim3((cols + 15) / 16), dim3(1024), 0, stream, cols, cols, parts, part, out,
-                     (float*)nullptr);
+// The same for one or two sets of lines at once (blockIdx.y).
+__global__ __launch_bounds__(1024) void line_sums_kernel(LineSums a, LineSums b) {
+  const LineSums& l = blockIdx.y ? b : a;
+  __shared__ double red[64][17];
+  const int cc = threadIdx.x & 15, k = threadIdx.x >> 4, col = blockIdx.x * 16 + cc;
+  if (blockIdx.x * 16 >= (unsigned)l.cols) return;
+  double s = 0.0;
+  if (col < l.cols) {
+#pragma unroll 8
+    for (int p = k; p < l.parts; p += 64) s += l.part[(int64_t)p * l.cols + col];
+  }
+  red[k][cc] = s;
+  __syncthreads();
+  if (k == 0 && col < l.cols) {
+    s = 0.0;
+#pragma unroll
+    for (int i = 0; i < 64; ++i) s += red[i][cc];
+    l.out[col] = (float)s;
+  }
+}
+
+hipError_t launch_line_sums(const LineSums& a, const LineSums& b, hipStream_t stream) {
+  const int cols = a.cols > b.cols ? a.cols : b.cols;
+  if (cols == 0) return hipSuccess;
+  hipLaunchKernelGGL(line_sums_kernel, dim3((cols + 15) / 16, b.cols > 0 ? 2 : 1), dim3(1024), 0, stream, a, b);
   return hipGetLastError();
 }
 
