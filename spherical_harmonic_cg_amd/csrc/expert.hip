@@ -415,17 +415,20 @@ __device__ __forceinline__ void multiply_steps(const ExpertArgs& a, const Listed
                                                typename ExpertCfg<float, C, L>::Total& total, float (*dots)[kMaxTopK]) {
   using Cfg = ExpertCfg<float, C, L>;
   typedef Run<float, Cfg::NP, Cfg::ALIGNED> In;
-  constexpr int K = Cfg::K, NP = Cfg::NP, CTW = Cfg::CTW;
+  constexpr int K = Cfg::K, NP = Cfg::NP, CTW = Cfg::CTW, NL = NP == 1 ? 1 : 2;  // (four components: two degrees at most)
   const int lf = degree_of_plane(m0), ll = degree_of_plane(m0 + NP - 1);
-  typedef f4 Weights[CTW];
-  auto weights = [&](Weights& wf, int e, int l, int s) {
+  typedef f4 Weights[NL][CTW];
+  auto weights = [&](Weights& wf, int e, int s) {
     const int c = s * 16 + kq * 4;
-    const float* We = static_cast<const float*>(a.W) + (int64_t)(e * (L + 1) + l) * (C * C) + (c < C ? c : 0);
 #pragma unroll
-    for (int t = 0; t < CTW; ++t) {
-      const int co = (ct0 + t) * 16 + i16;
-      wf[t] = *reinterpret_cast<const f4*>(We + (co < C ? co : 0) * C);
-      if constexpr (C % 16 != 0) wf[t] = c < C ? wf[t] : f4{0.f, 0.f, 0.f, 0.f};
+    for (int d = 0; d < NL; ++d) {
+      const float* We = static_cast<const float*>(a.W) + (int64_t)(e * (L + 1) + (d == 0 ? lf : ll)) * (C * C) + (c < C ? c : 0);
+#pragma unroll
+      for (int t = 0; t < CTW; ++t) {
+        const int co = (ct0 + t) * 16 + i16;
+        wf[d][t] = *reinterpret_cast<const f4*>(We + (co < C ? co : 0) * C);
+        if constexpr (C % 16 != 0) wf[d][t] = c < C ? wf[d][t] : f4{0.f, 0.f, 0.f, 0.f};
+      }
     }
   };
 #pragma unroll
@@ -434,7 +437,7 @@ __device__ __forceinline__ void multiply_steps(const ExpertArgs& a, const Listed
     for (int q = 0; q < NP; ++q) total[t][q] = f4{0.f, 0.f, 0.f, 0.f};
   int e = list.after(-1);
   Weights wf;
-  weights(wf, min(e, a.X - 1), lf, 0);
+  weights(wf, min(e, a.X - 1), 0);
   while (e < kMaxExperts) {
     const int then = list.after(e);
     float w;
@@ -447,12 +450,10 @@ __device__ __forceinline__ void multiply_steps(const ExpertArgs& a, const Listed
         for (int q = 0; q < NP; ++q) apart[t][q] = f4{0.f, 0.f, 0.f, 0.f};
     }
     typename Cfg::Total& into = ONE ? total : apart;
-    // (short loops: this code is fetched anew for every launch, and unrolled it took longer to come than to run)
-#pragma unroll 1
-    for (int l = lf, s = 0; l <= ll;) {
-      const int l1 = s + 1 < Cfg::NS ? l : l + 1, s1 = s + 1 < Cfg::NS ? s + 1 : 0;
+#pragma unroll 2
+    for (int s = 0; s < Cfg::NS; ++s) {
       Weights wn;  // on their way while these are multiplied
-      weights(wn, l1 <= ll ? e : min(then, a.X - 1), l1 <= ll ? l1 : lf, s1);
+      weights(wn, s + 1 < Cfg::NS ? e : min(then, a.X - 1), s + 1 < Cfg::NS ? s + 1 : 0);
       const int c = s * 16 + kq * 4;
       float x[4][NP];
       if constexpr (NP == 1) {
@@ -476,16 +477,23 @@ __device__ __forceinline__ void multiply_steps(const ExpertArgs& a, const Listed
         }
 #pragma unroll
       for (int q = 0; q < NP; ++q) {
-        if (NP > 1 && degree_of_plane(m0 + q) != l) continue;
+        if (NL == 1 || degree_of_plane(m0 + q) == lf) {
 #pragma unroll
-        for (int t = 0; t < CTW; ++t)
+          for (int t = 0; t < CTW; ++t)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) into[t][q] = __builtin_amdgcn_mfma_f32_16x16x4f32(wf[t][i], x[i][q], into[t][q], 0, 0, 0);
+            for (int i = 0; i < 4; ++i) into[t][q] = __builtin_amdgcn_mfma_f32_16x16x4f32(wf[0][t][i], x[i][q], into[t][q], 0, 0, 0);
+        } else {
+#pragma unroll
+          for (int t = 0; t < CTW; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              into[t][q] = __builtin_amdgcn_mfma_f32_16x16x4f32(wf[NL - 1][t][i], x[i][q], into[t][q], 0, 0, 0);
+        }
       }
 #pragma unroll
-      for (int t = 0; t < CTW; ++t) wf[t] = wn[t];
-      l = l1;
-      s = s1;
+      for (int d = 0; d < NL; ++d)
+#pragma unroll
+        for (int t = 0; t < CTW; ++t) wf[d][t] = wn[d][t];
     }
     float dot = 0.0f;
 #pragma unroll

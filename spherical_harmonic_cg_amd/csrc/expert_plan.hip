@@ -74,20 +74,29 @@ __global__ __launch_bounds__(256) void plan_count_kernel(PlanShape p, const int3
     for (int b = threadIdx.x; b < p.bins2; b += 256) hist2[b * p.tiles + blockIdx.x] = c2[b];
 }
 
-// Exclusive scans of both counts (a workgroup each) in place; ptr from the first.
+// Exclusive scans of both counts (a workgroup each) in place; ptr from the first.  4096 counts at a time through LDS, so
+// that memory is read and written along the lanes; the next ones are on their way meanwhile.
 __global__ __launch_bounds__(1024) void plan_scan_kernel(PlanShape p, int* __restrict__ hist1, int* __restrict__ hist2,
                                                          int32_t* __restrict__ ptr) {
-  __shared__ int wsum[16];
+  __shared__ int wsum[16], part[4096];
   int* a = blockIdx.x ? hist2 : hist1;
   const int len = (blockIdx.x ? p.bins2 : p.X + 1) * p.tiles;
   const int t = threadIdx.x, lane = t & 63, wv = t >> 6;
-  int carry = 0;
+  int carry = 0, next[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) next[q] = 1024 * q + t < len ? a[1024 * q + t] : 0;
   for (int c0 = 0; c0 < len; c0 += 4096) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      part[1024 * q + t] = next[q];
+      const int i = c0 + 4096 + 1024 * q + t;
+      next[q] = i < len ? a[i] : 0;
+    }
+    __syncthreads();
     int v[4], sum = 0;
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      const int i = c0 + 4 * t + q;
-      v[q] = i < len ? a[i] : 0;
+      v[q] = part[4 * t + q];
       sum += v[q];
     }
     int incl = sum;
@@ -106,16 +115,20 @@ __global__ __launch_bounds__(1024) void plan_scan_kernel(PlanShape p, int* __res
     }
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      const int i = c0 + 4 * t + q;
-      if (i < len) {
-        a[i] = run;
-        if (blockIdx.x == 0 && i % p.tiles == 0) ptr[i / p.tiles] = run;
-      }
+      part[4 * t + q] = run;
       run += v[q];
     }
     carry += all;
-    __syncthreads();  // wsum is written again
+    __syncthreads();
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int i = c0 + 1024 * q + t;
+      if (i < len) a[i] = part[1024 * q + t];
+    }
+    __syncthreads();  // part and wsum are written again
   }
+  if (blockIdx.x == 0)
+    for (int x = t; x <= p.X; x += 1024) ptr[x] = a[x * p.tiles];
 }
 
 // Places of one round's 256 items among those of their keys, in item order: toff [bins] are the keys' next free
