@@ -408,11 +408,14 @@ __global__ __launch_bounds__(512, 2) void expert_staged_kernel(ExpertArgs a, int
 
 // fp32: a tile a workgroup, its rows in LDS; a wave reads its operands from there 16 input channels at a time, just
 // before their products.
-// ONE: a node has one expert at most and no gate, and the products go straight into the totals (the same bits).
+// ONE: a node has one expert at most and no gate, so a tile of one expert needs no totals beside its products.  Where it
+// meets several, each one's products are written to its nodes' rows (row_out; null for none) right away -- a node keeps
+// nothing of the other experts', whatever their weights hold -- and the call returns true.
 template <int C, int L, bool DOT, bool ONE>
-__device__ __forceinline__ void multiply_steps(const ExpertArgs& a, const Listed& list, const float* row, int m0, int dup, int ct0,
+__device__ __forceinline__ bool multiply_steps(const ExpertArgs& a, const Listed& list, const float* row, int m0, int dup, int ct0,
                                                int i16, int kq, const typename ExpertCfg<float, C, L>::Held& held,
-                                               typename ExpertCfg<float, C, L>::Total& total, float (*dots)[kMaxTopK]) {
+                                               typename ExpertCfg<float, C, L>::Total& total, float (*dots)[kMaxTopK],
+                                               unsigned char* row_out) {
   using Cfg = ExpertCfg<float, C, L>;
   typedef Run<float, Cfg::NP, Cfg::ALIGNED> In;
   constexpr int K = Cfg::K, NP = Cfg::NP, CTW = Cfg::CTW, NL = NP == 1 ? 1 : 2;  // (four components: two degrees at most)
@@ -438,8 +441,10 @@ __device__ __forceinline__ void multiply_steps(const ExpertArgs& a, const Listed
   int e = list.after(-1);
   Weights wf;
   weights(wf, min(e, a.X - 1), 0);
+  bool several = false, done = false;
   while (e < kMaxExperts) {
     const int then = list.after(e);
+    several |= then < kMaxExperts;
     float w;
     const bool has = list.has(e, i16, w);
     typename Cfg::Total apart;
@@ -472,7 +477,6 @@ __device__ __forceinline__ void multiply_steps(const ExpertArgs& a, const Listed
       for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int q = 0; q < NP; ++q) {
-          if constexpr (ONE) x[i][q] = has ? x[i][q] : 0.0f;
           if constexpr (C % 16 != 0) x[i][q] = c < C ? x[i][q] : 0.0f;
         }
 #pragma unroll
@@ -495,6 +499,17 @@ __device__ __forceinline__ void multiply_steps(const ExpertArgs& a, const Listed
 #pragma unroll
         for (int t = 0; t < CTW; ++t) wf[d][t] = wn[d][t];
     }
+    if constexpr (ONE) {
+      if (several && has && row_out != nullptr) put_tiles<float, C, L, Cfg::ALIGNED>(a, row_out, m0, ct0, kq, total);
+      done |= has;
+      const bool keep = has && !several;
+#pragma unroll
+      for (int t = 0; t < CTW; ++t)
+#pragma unroll
+        for (int q = 0; q < NP; ++q)
+#pragma unroll
+          for (int v = 0; v < 4; ++v) total[t][q][v] = keep ? total[t][q][v] : 0.0f;
+    }
     float dot = 0.0f;
 #pragma unroll
     for (int t = 0; t < CTW; ++t)
@@ -514,6 +529,8 @@ __device__ __forceinline__ void multiply_steps(const ExpertArgs& a, const Listed
     }
     e = then;
   }
+  if (ONE && several && !done && row_out != nullptr) put_tiles<float, C, L, Cfg::ALIGNED>(a, row_out, m0, ct0, kq, total);  // zeros
+  return ONE && several;
 }
 
 template <int C, int L, bool DOT, bool ONE>
@@ -549,8 +566,11 @@ __global__ __launch_bounds__(512) void expert_f32_kernel(ExpertArgs a) {
   typename Cfg::Total total;
   if constexpr (DOT) take_held<float, C, L>(static_cast<const float*>(a.dot_with) + node * (C * K) + m0, ct0, kq, held);
   __syncthreads();
-  multiply_steps<C, L, DOT, ONE>(a, list, reinterpret_cast<const float*>(lds + i16 * row_in) + m0, m0, g * NP - m0, ct0, i16, kq, held,
-                            total, dots[DOT ? wv : 0]);
+  unsigned char* own = ONE && i16 < nv ? static_cast<unsigned char*>(a.out) + node * (C * K * (a.out_bf16 ? 2 : 4)) : nullptr;
+  // (whether a tile meets several experts is the same in all its waves)
+  if (multiply_steps<C, L, DOT, ONE>(a, list, reinterpret_cast<const float*>(lds + i16 * row_in) + m0, m0, g * NP - m0, ct0, i16, kq,
+                                     held, total, dots[DOT ? wv : 0], own))
+    return;
   __syncthreads();  // every wave has read its operands: the place takes the results
   if (a.out != nullptr) {
     const int row_out = staged_row(C, K, a.out_bf16 ? 2 : 4), units = row_out / 16 - 1;
@@ -694,7 +714,7 @@ __global__ __launch_bounds__(kFewThreads) void expert_few_kernel(ExpertArgs a, i
       for (int c = 0; c < C; ++c) acc = fmaf((float)W[TRANS ? c * C : c], h[c * K + m], acc);
       total = fmaf(a.weight ? a.weight[n * a.k + j] : 1.0f, acc, total);
       if constexpr (DOT) {
-        const float d = lane_sum<64>(acc * with);
+        const float d = lane_sum<64>(on ? acc * with : 0.0f);
         if (lane == 0) sums[wv][j] += d;
       }
     }

@@ -82,6 +82,10 @@ struct Comps<float, GATES> {
 #pragma unroll
     for (int q = 0; q < 16; ++q) x[q] = live ? (GATES ? x[q] * w : x[q]) : 0.0f;
   }
+  __device__ __forceinline__ void clear(bool live) {
+#pragma unroll
+    for (int q = 0; q < 16; ++q) x[q] = live ? x[q] : 0.0f;
+  }
   // acc += this (rows) times b (columns) over components first .. first + n - 1 (constants once unrolled)
   __device__ __forceinline__ void add(const Comps& b, int first, int n, f4& acc) const {
 #pragma unroll
@@ -126,6 +130,10 @@ struct Comps<__bf16, GATES> {
         x[q] = live ? x[q] : 0u;
       }
     }
+  }
+  __device__ __forceinline__ void clear(bool live) {
+#pragma unroll
+    for (int q = 0; q < 8; ++q) x[q] = live ? x[q] : 0u;
   }
   // the words that hold components first .. first + n - 1, eight components from word `at` on, others cleared
   static __device__ __forceinline__ bf16x8 part(const uint32_t (&v)[8], int at, int first, int n) {
@@ -199,6 +207,9 @@ __device__ __forceinline__ void expert_grad_walk(const ExpertGradArgs& a, const 
       }
 #pragma unroll
       for (int r = 0; r < RT; ++r) g[r].gate(w, live);
+      if (s0 + 4 * st + 4 > ch.s1)  // places past the chunk read its last one's rows: an infinity of h times 0 is none of it
+#pragma unroll
+        for (int t = 0; t < CTC; ++t) h[t].clear(live);
 #pragma unroll
       for (int l = 0; l < LN; ++l)
 #pragma unroll

@@ -175,3 +175,58 @@ def test_expert_empty():
     assert eq.eqtp_expert_linear(m.h[0], m.W[0], m.ti, 1, weight=m.w[0], plan=plan).shape == (0, 16, 4)
     gh, gW, gw = m.grads(eq, plan)
     assert gh.shape == (0, 16, 4) and (gW == 0).all() and gw.shape == (0, 2)
+
+
+@pytest.mark.parametrize("x", ["f32", "bf16"])
+@pytest.mark.parametrize("N,C,lmax,k,gates", [(20, 16, 1, 1, False), (600, 64, 3, 1, False), (600, 32, 0, 1, False),
+                                              (530, 8, 2, 1, False), (600, 64, 3, 2, True), (520, 32, 4, 1, False)])
+def test_an_expert_that_is_not_finite(N, C, lmax, k, gates, x):
+    """Its nodes get what it holds, the others' bits are those that they have without it."""
+    import torch
+
+    eq = _eq()
+    _say("an expert that is not finite, N=%d C=%d lmax=%d k=%d %s" % (N, C, lmax, k, x))
+    m = Mix(N, C, lmax, 4, k, x, gates, seed=N + lmax)
+    W = m.W[0]
+    bad = W.clone()
+    bad[2, :, ::2] = float("nan")
+    bad[2, :, 1::2] = float("inf")
+    meets = (m.ti == 2).any(1)
+    none = ((m.ti < 0) | (m.ti >= 4)).all(1)
+    assert meets.any() and not meets.all()
+    for plan in (None, eq.eqtp_expert_plan(m.ti, 4)):
+        outs = []
+        for weights in (W, bad):
+            o = eq.eqtp_expert_linear(m.h[0], weights, m.ti, lmax, weight=m.w[0], plan=plan)
+            gh, _, gw = eq.eqtp_expert_linear_backward(m.h[0], weights, m.ti, m.g[0], lmax, weight=m.w[0], plan=plan, need_W=False)
+            outs.append((o, gh, gw))
+        for clean, spoilt in zip(*outs):
+            if clean is not None:
+                assert torch.equal(clean[~meets], spoilt[~meets])
+        assert not torch.isfinite(outs[1][0][meets]).any()
+        assert not outs[1][0][none].any() and not outs[1][1][none].any()
+
+
+@pytest.mark.parametrize("x", ["f32", "bf16"])
+def test_infinities_are_no_nan(x):
+    """An infinite feature's gradients are infinite where no term of the sum is of the other sign."""
+    import torch
+
+    eq = _eq()
+    _say("infinite features %s" % x)
+    dt = torch.bfloat16 if x == "bf16" else torch.float32
+    N, C, lmax = 5, 8, 1
+    h = torch.ones(N, C, 4, dtype=dt, device="cuda")
+    h[N - 1, 3, 0] = float("inf")
+    g = torch.ones(N, C, 4, dtype=dt, device="cuda")
+    W = torch.ones(1, 2, C, C, dtype=dt, device="cuda")
+    idx = torch.zeros(N, 1, dtype=torch.int32, device="cuda")
+    _, gW, _ = eq.eqtp_expert_linear_backward(h, W, idx, g, lmax)
+    want = torch.full((1, 2, C, C), 5.0, device="cuda")
+    want[:, 1] = 15.0
+    want[0, 0, :, 3] = float("inf")
+    assert torch.equal(gW, want)
+    g[0, 0, 0] = float("inf")
+    w = torch.ones(N, 1, device="cuda")
+    _, _, gw = eq.eqtp_expert_linear_backward(torch.ones_like(h), W, idx, g, lmax, weight=w, need_W=False)
+    assert torch.equal(gw[:, 0], torch.tensor([float("inf")] + [4.0 * C * C] * (N - 1), device="cuda"))
