@@ -409,13 +409,13 @@ __global__ __launch_bounds__(512, 2) void expert_staged_kernel(ExpertArgs a, int
 // fp32: a tile a workgroup, its rows in LDS; a wave reads its operands from there 16 input channels at a time, just
 // before their products.
 // ONE: a node has one expert at most and no gate, so a tile of one expert needs no totals beside its products.  Where it
-// meets several, each one's products are written to its nodes' rows (row_out; null for none) right away -- a node keeps
+// meets several, each one's products are written to its nodes' rows right away -- a node keeps
 // nothing of the other experts', whatever their weights hold -- and the call returns true.
 template <int C, int L, bool DOT, bool ONE>
 __device__ __forceinline__ bool multiply_steps(const ExpertArgs& a, const Listed& list, const float* row, int m0, int dup, int ct0,
                                                int i16, int kq, const typename ExpertCfg<float, C, L>::Held& held,
                                                typename ExpertCfg<float, C, L>::Total& total, float (*dots)[kMaxTopK],
-                                               unsigned char* row_out) {
+                                               int64_t p0, int nv) {
   using Cfg = ExpertCfg<float, C, L>;
   typedef Run<float, Cfg::NP, Cfg::ALIGNED> In;
   constexpr int K = Cfg::K, NP = Cfg::NP, CTW = Cfg::CTW, NL = NP == 1 ? 1 : 2;  // (four components: two degrees at most)
@@ -442,6 +442,10 @@ __device__ __forceinline__ bool multiply_steps(const ExpertArgs& a, const Listed
   Weights wf;
   weights(wf, min(e, a.X - 1), 0);
   bool several = false, done = false;
+  auto put = [&] {  // (the row's place is looked up again: held over the products, it would take their registers)
+    unsigned char* o = static_cast<unsigned char*>(a.out) + node_at(a, p0 + i16) * (C * K * (a.out_bf16 ? 2 : 4));
+    put_tiles<float, C, L, Cfg::ALIGNED>(a, o, m0, ct0, kq, total);
+  };
   while (e < kMaxExperts) {
     const int then = list.after(e);
     several |= then < kMaxExperts;
@@ -500,7 +504,7 @@ __device__ __forceinline__ bool multiply_steps(const ExpertArgs& a, const Listed
         for (int t = 0; t < CTW; ++t) wf[d][t] = wn[d][t];
     }
     if constexpr (ONE) {
-      if (several && has && row_out != nullptr) put_tiles<float, C, L, Cfg::ALIGNED>(a, row_out, m0, ct0, kq, total);
+      if (several && has) put();
       done |= has;
       const bool keep = has && !several;
 #pragma unroll
@@ -529,12 +533,16 @@ __device__ __forceinline__ bool multiply_steps(const ExpertArgs& a, const Listed
     }
     e = then;
   }
-  if (ONE && several && !done && row_out != nullptr) put_tiles<float, C, L, Cfg::ALIGNED>(a, row_out, m0, ct0, kq, total);  // zeros
+  if (ONE && several && !done && i16 < nv) put();  // zeros
   return ONE && several;
 }
 
+// (ONE: registers for two workgroups of eight waves a compute unit where the LDS holds two, 38 us; with eight registers
+// more and one workgroup 42: 10k nodes of 64 x 16)
+constexpr int f32_waves(int C, int L, bool one) { return one && 2 * kTile * staged_row(C, num_comp(L), 4) <= (160 << 10) ? 4 : 2; }
+
 template <int C, int L, bool DOT, bool ONE>
-__global__ __launch_bounds__(512) void expert_f32_kernel(ExpertArgs a) {
+__global__ __launch_bounds__(512, f32_waves(C, L, ONE)) void expert_f32_kernel(ExpertArgs a) {
   using Cfg = ExpertCfg<float, C, L>;
   constexpr int K = Cfg::K, NP = Cfg::NP, CTW = Cfg::CTW, waves = Cfg::WAVES, U = Cfg::U, row_in = Cfg::ROW;
   extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
@@ -566,10 +574,9 @@ __global__ __launch_bounds__(512) void expert_f32_kernel(ExpertArgs a) {
   typename Cfg::Total total;
   if constexpr (DOT) take_held<float, C, L>(static_cast<const float*>(a.dot_with) + node * (C * K) + m0, ct0, kq, held);
   __syncthreads();
-  unsigned char* own = ONE && i16 < nv ? static_cast<unsigned char*>(a.out) + node * (C * K * (a.out_bf16 ? 2 : 4)) : nullptr;
   // (whether a tile meets several experts is the same in all its waves)
   if (multiply_steps<C, L, DOT, ONE>(a, list, reinterpret_cast<const float*>(lds + i16 * row_in) + m0, m0, g * NP - m0, ct0, i16, kq,
-                                     held, total, dots[DOT ? wv : 0], own))
+                                     held, total, dots[DOT ? wv : 0], p0, nv))
     return;
   __syncthreads();  // every wave has read its operands: the place takes the results
   if (a.out != nullptr) {
