@@ -6,7 +6,11 @@
 // Lengths are compared as squares in 64 bits: a component squared is exact
 // there, so the bucket of an edge next to a bound is the formula's.
 //
-// Both passes read 12 bytes an edge and write or read 4 H: bound by HBM.
+// Both passes read 12 bytes an edge and write or read 4 H.  Forward: 5.24M edges
+// x 8 heads, 64 buckets, 41 us, 5.7 TB/s, a copy's rate; 266k x 4, 33 buckets
+// 4.6 us; 20k x 4 3.4 us, a launch.
+// Backward: the same cases 88 us (2.6 TB/s: vector ALUs and LDS) and 12 us, and
+// 4 to 5 us for the lines' sums.
 #include "eqtp_device.hpp"
 #include "eqtp_kernels.hpp"
 
@@ -43,7 +47,8 @@ __device__ __forceinline__ int bucket_of(const BiasArgs& a, const double* b2, co
   return r2 >= a.cut2 ? kBeyond : (r2 == r2 ? pos : kNoLength);
 }
 
-// Forward: a wave finds the buckets of 64 edges, one a lane, and then writes
+// Forward (table in LDS up to 48 KB, so that three workgroups share a compute unit; larger ones are read through the
+// caches): a wave finds the buckets of 64 edges, one a lane, and then writes
 // their 64 H consecutive values together, V a lane and step (V = 4 where H is
 // a multiple of 4), each from its edge's row of the table.
 template <int V, bool LDS>
@@ -89,8 +94,9 @@ __global__ __launch_bounds__(256) void distance_bias_kernel(BiasArgs a) {
 // (heads: up to 64 of H), and each lane adds into a table of its own in LDS,
 // [bucket][lane]: no two lanes share an address, so there are no atomics (64
 // lanes' LDS additions take 190 cycles, a read and a write a few), every bank
-// serves one lane, and the sums are the same from call to call.  A workgroup then adds its lanes and waves in 64 bits into a line of
-// part, and the lines are added by the norm's second kernel.
+// serves one lane, and the sums are the same from call to call.  A workgroup
+// then adds its lanes and waves in 64 bits into a line of part, and the lines
+// are added by a second kernel, in 64 bits too.
 // A wave's next edges, and the first eight steps' values of them, are on their
 // way while it adds: with 8 waves a compute unit (their tables fill the LDS)
 // little else hides the memory.

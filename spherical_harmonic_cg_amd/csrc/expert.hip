@@ -4,20 +4,34 @@
 // gradients of h and of the gates:
 //   grad_weight[n, j] = sum_{c, l m} (W^T g)[n, c, l m] h[n, c, l m].
 //
-// Bytes per node: its features once in, once out; flops 2 k C^2 K.  A workgroup
-// takes 16 nodes, a wave of it a group of NP components (16 bytes of a channel)
-// and a share of the output channels.  A 16x16 product D[c'][node] of one
+// Bytes per node: its features once in, once out; flops 2 k C^2 K.  Tiles: a
+// workgroup takes 16 nodes, a wave of it a group of NP components (16 bytes of a
+// channel) and a share of the output channels.  A 16x16 product D[c'][node] of one
 // component wants, in lane (node i, k), the component's values of 4 (fp32) or
 // 8 (bf16) input channels.  The lane reads those channels' 16-byte runs of
 // components, so its registers hold the operands of NP products, in fp32 as
 // they are, in bf16 after a transposition within the lane; D holds NP
 // components of four output channels of the lane's node, which leave as runs.
-// No LDS, no barriers: waves are on their own.
 //
-// The wave goes over the experts that any of the 16 nodes has, in ascending order: total += gate D in the
-// lanes of the nodes that have it.  Nodes in an order in which neighbours share
-// experts (expert_plan.hip) keep that list short; the results do not depend on
-// it.  Weights come from the L2, each once a wave and expert.
+// The wave goes over the experts that any of the 16 nodes has, in ascending
+// order: total += gate D in the lanes of the nodes that have it.  Nodes in an
+// order in which neighbours share experts (expert_plan.hip) keep that list short;
+// the results do not depend on it.  Weights come from the L2, each once a wave
+// and expert.
+//
+// Four forms:
+//   few nodes (up to 512): a thread an output, on the vector ALUs;
+//   fp32 rows that fit (expert_f32_kernel): rows go through LDS, operands are
+//     read 16 channels at a time.  10k nodes x 64 x 16, one of 10 experts: 38 to
+//     41 us, 34 TFLOP/s (bytes 15 us, products 9): 626 tiles on 512 workgroups
+//     at a time, and LDS reads between a wave's products;
+//   bf16 rows that fit, without the gates' gradient (expert_staged_kernel): rows
+//     through LDS, tiles one after the other.  100k nodes x 32 x 16, 2 of 8: 59
+//     us, 3.5 TB/s, where the direct form took 71;
+//   the rest (expert_kernel: rows that do not fit, lmax 4 and above, and bf16
+//     with the gates' gradient, where the rows of a second tensor leave no
+//     registers for a tile ahead): runs from and to memory, no barriers.  The
+//     gradients of h and of the gates of that case: 96 us, 3.2 TB/s.
 #include <atomic>
 #include <type_traits>
 

@@ -5,7 +5,8 @@
 //   ptr [X+1]:   where each expert's places begin;
 //   order [N]:   the nodes by their two lowest experts.
 // Stable counting sorts of both at once: counts of a tile of nodes in LDS, one
-// scan, ranks from wave ballots; three launches, or one for few places.  With many experts the nodes'
+// scan, ranks from wave ballots; three launches (100k nodes, 2 of 8 experts: 5 + 7
+// + 6 us, each a few dependent steps), or one for few places (one node 5 us).  With many experts the nodes'
 // second key is coarsened to 1024 bins in all: order only has to be a good
 // one, the linear's results do not depend on it.
 #include "eqtp_device.hpp"
@@ -190,7 +191,8 @@ __global__ __launch_bounds__(256) void plan_place_kernel(PlanShape p, const int3
   }
 }
 
-// Few places: all three steps by one workgroup (256 places a round, two groupings).
+// Few places: all three steps by one workgroup, 256 places a round, two groupings.  Up to 1024 of them: 256 nodes of 2
+// take 5 us in one launch, 9 in three; a workgroup's rounds grow with the places.
 constexpr int kFewPlaces = 1024;
 __global__ __launch_bounds__(256) void plan_few_kernel(PlanShape p, const int32_t* __restrict__ idx, int32_t* __restrict__ slots,
                                                        int32_t* __restrict__ order, int32_t* __restrict__ ptr) {

@@ -4,8 +4,9 @@
 //   the k largest v of them are taken, the lower index first where v is equal;
 //   weight = scale s / (sum of s over those taken), or scale s.
 //
-// Reads 4 N X bytes and writes 8 N k: bound by HBM where N is large, in
-// practice by the choice's instructions.  A node's experts lie eight by eight
+// Reads 4 N X bytes and writes 8 N k; bound by the choice's instructions: 100k
+// nodes, 6 of 64 experts, 4 of 8 groups, sigmoid with a bias 31 us, where a copy
+// of the bytes takes 6; its gradient 10 us (its bytes' time is the same).  1000 nodes, 2 of 8: 6 us.  A node's experts lie eight by eight
 // in G lanes (G = 1 for up to 8 experts, 32 for 256), so a wave works on 64 / G
 // nodes.  Each lane sorts its eight once; a round of the choice then compares
 // the lanes' first ones, and the lane that had the best moves on.
