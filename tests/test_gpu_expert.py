@@ -230,3 +230,19 @@ def test_infinities_are_no_nan(x):
     w = torch.ones(N, 1, device="cuda")
     _, _, gw = eq.eqtp_expert_linear_backward(torch.ones_like(h), W, idx, g, lmax, weight=w, need_W=False)
     assert torch.equal(gw[:, 0], torch.tensor([float("inf")] + [4.0 * C * C] * (N - 1), device="cuda"))
+
+
+@pytest.mark.parametrize("x", ["f32", "bf16"])
+@pytest.mark.parametrize("N,C,lmax,k", [(1, 8, 1, 2), (40, 64, 3, 2), (600, 64, 3, 1), (600, 64, 3, 2), (530, 128, 3, 1),
+                                        (520, 8, 2, 1), (700, 16, 0, 1), (515, 32, 5, 2)])
+def test_both_types_of_the_output(N, C, lmax, k, x):
+    """One fp32 sum, rounded once: the bf16 output is the fp32 one's rounding, with and without a plan."""
+    import torch
+
+    eq = _eq()
+    _say("both types of the output, N=%d C=%d lmax=%d k=%d %s" % (N, C, lmax, k, x))
+    m = Mix(N, C, lmax, 5, k, x, k > 1, seed=N + C + lmax)
+    for plan in (None, eq.eqtp_expert_plan(m.ti, 5)):
+        wide, narrow = (eq.eqtp_expert_linear(m.h[0], m.W[0], m.ti, lmax, weight=m.w[0], plan=plan, out_dtype=t)
+                        for t in (eq.EQTP_F32, eq.EQTP_BF16))
+        assert torch.equal(wide.to(torch.bfloat16), narrow)
