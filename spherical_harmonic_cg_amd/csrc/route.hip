@@ -315,7 +315,7 @@ __global__ __launch_bounds__(256, 4) void route_kernel(RouteArgs a) {
     }
     if (direct) {
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) v[i] = t[i] > kNone ? t[i] : kNone;
+      for (int i = 0; i < kPer; ++i) v[i] = t[i] > kNone ? t[i] + 0.0f : kNone;  // (-0 becomes 0: keys tell them apart)
     } else {
       const float inv = a.sigmoid ? 1.0f : __builtin_amdgcn_rcpf(all);
 #pragma unroll

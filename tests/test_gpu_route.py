@@ -103,3 +103,28 @@ def test_route_less_aligned():
     for X in (8, 12, 64, 65):
         _check(eq, r.standard_normal((70, X)), 3, "bf16", shift=1)
         _check(eq, r.standard_normal((70, X)), 3, "f32", shift=3, sigmoid=True)
+
+
+@pytest.mark.parametrize("x", ["f32", "bf16"])
+@pytest.mark.parametrize("sigmoid", [False, True])
+@pytest.mark.parametrize("X", [3, 8, 9, 64, 200])
+def test_route_zeros_of_both_signs(X, sigmoid, x):
+    """0 and -0 are equal: the lower index goes first, within a lane's experts and across lanes.  In rows without other
+    ties, alone and side by side (a tie in a row has its neighbours looked at again, too)."""
+    eq = _eq()
+    _say("route, zeros of both signs, X=%d %s" % (X, x))
+    for at in {(0, 1), (0, X - 1), (X // 2, X - 1), (X // 3, X // 2 + 1)}:
+        for top in (True, False):  # the zeros are the largest, or stand behind another
+            t = -1.0 - np.arange(X) % 100 - 0.25 * (np.arange(X) // 100)
+            t[at[0]], t[at[1]] = -0.0, 0.0
+            if not top:
+                t[[i for i in range(X) if i not in at][-1]] = 2.0
+            for rows in (1, 70):
+                for k in (1, min(2, X), min(3, X)):
+                    idx, _ = _check(eq, np.tile(t, (rows, 1)), k, x, sigmoid=sigmoid)
+                    assert not top or (idx[:, 0] == at[0]).all()
+    t = np.full((1, X), -0.0)
+    t[0, X - 1] = 0.0
+    for groups, bias in ((1, None), (1, np.where(np.arange(X) % 2, 0.0, -0.0)), (X, None)):
+        idx, _ = _check(eq, t, 1, x, bias=bias, groups=groups, sigmoid=sigmoid)
+        assert int(idx[0, 0]) == 0
