@@ -309,7 +309,7 @@ __global__ __launch_bounds__(512) void expert_kernel(ExpertArgs a) {
   __shared__ float dots[DOT ? 8 : 1][kTile][kMaxTopK];
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int i16 = lane & 15, kq = lane >> 4;
-  const int64_t p0 = (int64_t)blockIdx.x * kTile;
+  const int64_t p0 = a.first + (int64_t)blockIdx.x * kTile;
   const int nv = (int)min((int64_t)kTile, a.N - p0);
   const int64_t node = node_at(a, p0 + min(i16, nv - 1));
   Listed list;
@@ -565,7 +565,7 @@ __global__ __launch_bounds__(512, f32_waves(C, L, ONE)) void expert_f32_kernel(E
   const int tid = threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int i16 = lane & 15, kq = lane >> 4;
   const int g = wv / Cfg::CS, ct0 = (wv - g * Cfg::CS) * CTW, m0 = group_first(g, K, NP);
-  const int64_t p0 = (int64_t)blockIdx.x * kTile;
+  const int64_t p0 = a.first + (int64_t)blockIdx.x * kTile;
   const int nv = (int)min((int64_t)kTile, a.N - p0);
   {
     u32x4 rows[U];
@@ -641,19 +641,36 @@ hipError_t launch_transpose_weights(int64_t matrices, int C, bool bf16, const vo
   return hipGetLastError();
 }
 
+// Launches of a tile a workgroup: a launch holds less than 2^32 threads (more wrap round, without an error), so the tiles
+// beyond go to further ones.
+constexpr int64_t kLaunchThreads = int64_t(1) << 31;
+template <class F>
+static hipError_t over_tiles(ExpertArgs a, int64_t tiles, int threads, F launch) {
+  const int64_t most = kLaunchThreads / threads;
+  for (int64_t t = 0; t < tiles; t += most) {
+    a.first = t * kTile;
+    launch(a, dim3((unsigned)(tiles - t < most ? tiles - t : most)), dim3(threads));
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
 template <class S, int C, int L, bool DOT>
 static hipError_t expert_launch(const ExpertArgs& a) {
   using Cfg = ExpertCfg<S, C, L>;
   const int64_t tiles = (a.N + kTile - 1) / kTile;
   if constexpr (Cfg::STAGED && !Cfg::BF16) {
-    const dim3 grid((unsigned)tiles), block(64 * Cfg::WAVES);
+    constexpr int lds = kTile * Cfg::ROW;
     if constexpr (!DOT) {
-      if (a.k == 1 && a.weight == nullptr) {
-        expert_f32_kernel<C, L, DOT, true><<<grid, block, kTile * Cfg::ROW, a.stream>>>(a);
-        return hipGetLastError();
-      }
+      if (a.k == 1 && a.weight == nullptr)
+        return over_tiles(a, tiles, 64 * Cfg::WAVES, [](const ExpertArgs& part, dim3 grid, dim3 block) {
+          expert_f32_kernel<C, L, DOT, true><<<grid, block, lds, part.stream>>>(part);
+        });
     }
-    expert_f32_kernel<C, L, DOT, false><<<grid, block, kTile * Cfg::ROW, a.stream>>>(a);
+    return over_tiles(a, tiles, 64 * Cfg::WAVES, [](const ExpertArgs& part, dim3 grid, dim3 block) {
+      expert_f32_kernel<C, L, DOT, false><<<grid, block, lds, part.stream>>>(part);
+    });
   } else if constexpr (Cfg::STAGED && !DOT) {
     const int bytes = kTile * (a.out && !a.out_bf16 ? staged_row(C, Cfg::K, 4) : Cfg::ROW);
     static std::atomic<int> known[2];  // workgroups that a compute unit holds
@@ -669,10 +686,12 @@ static hipError_t expert_launch(const ExpertArgs& a) {
     const int64_t most = (int64_t)num_cus() * n, each = (tiles + most - 1) / most;
     expert_staged_kernel<S, C, L, DOT>
         <<<dim3((unsigned)((tiles + each - 1) / each)), dim3(64 * Cfg::WAVES), bytes, a.stream>>>(a, tiles);
+    return hipGetLastError();
   } else {
-    expert_kernel<S, C, L, DOT><<<dim3((unsigned)tiles), dim3(64 * Cfg::WAVES), 0, a.stream>>>(a);
+    return over_tiles(a, tiles, 64 * Cfg::WAVES, [](const ExpertArgs& part, dim3 grid, dim3 block) {
+      expert_kernel<S, C, L, DOT><<<grid, block, 0, part.stream>>>(part);
+    });
   }
-  return hipGetLastError();
 }
 
 template <class S, int L, bool DOT>

@@ -93,3 +93,35 @@ def test_experts_far(x, k):
     assert torch.equal(got[1], want[1])
     if k > 1:
         assert torch.equal(last(got[2]), want[2])
+
+
+@pytest.mark.parametrize("x,k,gates", [("f32", 1, False), ("f32", 1, True), ("bf16", 1, True)])
+def test_experts_of_many_nodes(x, k, gates):
+    """More than 2^30 nodes: more threads than a launch holds at one tile a workgroup."""
+    import torch
+
+    eq = _eq()
+    C, X = 8, 3
+    N = 2 ** 30 + TAIL
+    dt = torch.bfloat16 if x == "bf16" else torch.float32
+    _say("experts N=%d C=%d %s gates=%s" % (N, C, x, gates))
+    torch.manual_seed(4)
+    h = torch.zeros(N, C, device="cuda", dtype=dt)
+    W = torch.randn(X, 1, C, C, device="cuda").to(dt)
+    idx = torch.zeros(N, k, device="cuda", dtype=torch.int32)
+    weight = torch.ones(N, k, device="cuda") if gates else None
+    far = [slice(0, TAIL), slice(N // 2, N // 2 + TAIL), slice(N - TAIL, N)]
+    for at in far:
+        h[at] = torch.randn(TAIL, C, device="cuda").to(dt)
+        idx[at] = torch.randint(-1, X, (TAIL, k), device="cuda", dtype=torch.int32)
+        if gates:
+            weight[at] = torch.rand(TAIL, k, device="cuda")
+    cut = lambda t, at: None if t is None else t[at].contiguous()  # noqa: E731
+    out = eq.eqtp_expert_linear(h, W, idx, 0, weight=weight)
+    for at in far:
+        assert torch.equal(out[at], eq.eqtp_expert_linear(cut(h, at), W, cut(idx, at), 0, weight=cut(weight, at)))
+    gh, _, gw = eq.eqtp_expert_linear_backward(h, W, idx, out, 0, weight=weight, need_W=False)
+    for at in far:
+        a, _, b = eq.eqtp_expert_linear_backward(cut(h, at), W, cut(idx, at), cut(out, at), 0, weight=cut(weight, at), need_W=False)
+        assert torch.equal(gh[at], a)
+        assert not gates or torch.equal(gw[at], b)
