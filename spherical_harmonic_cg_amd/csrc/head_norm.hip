@@ -56,11 +56,16 @@ template <int T, int NV, int KT>
 struct Turns {
   static constexpr int NC = kTrig<KT>;
   float c[NV][NC], s[NV][NC];
-  __device__ __forceinline__ void none() {
+  bool turned[NV][4];  // of the slots' channels: the same in every row
+  template <class S>
+  __device__ __forceinline__ void begin(const S& sl, int R) {
 #pragma unroll
-    for (int j = 0; j < NV; ++j)
+    for (int j = 0; j < NV; ++j) {
 #pragma unroll
       for (int q = 0; q < NC; ++q) c[j][q] = 1.0f, s[j][q] = 0.0f;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) turned[j][q] = sl.channel(q, j) < R;
+    }
   }
   template <class S>
   static __device__ __forceinline__ int channel(const S& sl, int j, int q) {
@@ -99,6 +104,16 @@ struct Turns {
   template <class S>
   __device__ __forceinline__ float sn(const S& sl, int j, int q) const {
     return KT == 0 ? s[j][q % NC] : (KT == 1 ? s[j][0] : (q >= sl.wrap ? s[j][NC - 1] : s[j][0]));
+  }
+  // A pair, turned; the other way round where SIGN is -1.  Of channels that are not turned both stay as they are, and
+  // neither meets the other: a product with sine 0 would make NaN of an infinity half a head away.
+  template <int SIGN, class S>
+  __device__ __forceinline__ void turn(const S& sl, int j, int q, float& a, float& b) const {
+    const float co = cs(sl, j, q), si = sn(sl, j, q);
+    const float ta = SIGN > 0 ? fmaf(a, co, -b * si) : fmaf(a, co, b * si);
+    const float tb = SIGN > 0 ? fmaf(a, si, b * co) : fmaf(b, co, -a * si);
+    a = turned[j][q] ? ta : a;
+    b = turned[j][q] ? tb : b;
   }
 };
 
@@ -194,7 +209,7 @@ __global__ __launch_bounds__(256) void head_norm_kernel(HeadNormArgs a, int A) {
   float w0[NV][4], w1[NV][4];
   head_weights(s, sl, d, half, w0, w1);
   Turns<T, NV, KT> tr;
-  tr.none();
+  tr.begin(sl, a.R);
   extern __shared__ __attribute__((aligned(8))) float2 tables[];
   int turn = 0;
   RowQuads<E, NV> r0, r1;
@@ -236,10 +251,9 @@ __global__ __launch_bounds__(256) void head_norm_kernel(HeadNormArgs a, int A) {
         float o0[4], o1[4];
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          const float y0 = x0[j][q] * m[q] * w0[j][q], y1 = x1[j][q] * m[q] * w1[j][q];
-          const float c = tr.cs(sl, j, q), sn = tr.sn(sl, j, q);
-          o0[q] = fmaf(y0, c, -y1 * sn);
-          o1[q] = fmaf(y0, sn, y1 * c);
+          o0[q] = x0[j][q] * m[q] * w0[j][q];
+          o1[q] = x1[j][q] * m[q] * w1[j][q];
+          tr.template turn<1>(sl, j, q, o0[q], o1[q]);
         }
         if (sl.on) {
           store4(o + i, D0 - i, tail0, o0);
@@ -265,7 +279,7 @@ __global__ __launch_bounds__(256) void head_norm_grad_kernel(HeadNormArgs a, int
   float w0[NV][4], w1[NV][4], aw0[NV][4] = {}, aw1[NV][4] = {};
   head_weights(s, sl, d, half, w0, w1);
   Turns<T, NV, KT> tr;
-  tr.none();
+  tr.begin(sl, a.R);
   extern __shared__ __attribute__((aligned(8))) float2 tables[];
   int turn = 0;
   RowQuads<E, NV> r0, r1, q0, q1;
@@ -301,12 +315,9 @@ __global__ __launch_bounds__(256) void head_norm_grad_kernel(HeadNormArgs a, int
       for (int j = 0; j < NV; ++j)
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          const float c = tr.cs(sl, j, q), sn = tr.sn(sl, j, q);
-          const float b0 = fmaf(u0[j][q], c, u1[j][q] * sn), b1 = fmaf(u1[j][q], c, -u0[j][q] * sn);
-          u0[j][q] = b0;
-          u1[j][q] = b1;
+          tr.template turn<-1>(sl, j, q, u0[j][q], u1[j][q]);
           sq[q] = fmaf(x1[j][q], x1[j][q], fmaf(x0[j][q], x0[j][q], sq[q]));
-          sa[q] = fmaf(b1 * w1[j][q], x1[j][q], fmaf(b0 * w0[j][q], x0[j][q], sa[q]));
+          sa[q] = fmaf(u1[j][q] * w1[j][q], x1[j][q], fmaf(u0[j][q] * w0[j][q], x0[j][q], sa[q]));
         }
       degree_means<T, KT>(sl, sq, deg, inv_mine, m);
       degree_means<T, KT>(sl, sa, deg, inv_mine, ma);

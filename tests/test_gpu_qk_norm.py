@@ -139,3 +139,53 @@ def test_qk_norm_spoilt_rows():
     keep = torch.ones(9, dtype=torch.bool)
     keep[[3, 5]] = False
     assert torch.equal(out[keep.cuda()], good[keep.cuda()])
+
+
+@pytest.mark.parametrize("x", ["f32", "bf16"])
+@pytest.mark.parametrize("lmax,w,axes,R", [(0, 16, 0, 0), (0, 16, 1, 3), (0, 7, 0, 0), (1, 8, 0, 0), (1, 8, 3, 2), (2, 6, 2, 1),
+                                           (2, 5, 0, 0), (3, 32, 1, 5), (0, 128, 1, 20)])
+def test_qk_norm_channels_that_are_not_turned(lmax, w, axes, R, x):
+    """A channel that is not turned is its own: what stands half a head further on (or back) does not reach it, infinite
+    or not -- a weight, a feature, a gradient."""
+    eq = _eq()
+    _say("qk norm, channels that are not turned, lmax=%d w=%d R=%d %s" % (lmax, w, R, x))
+    import torch
+
+    s = Sides(6, 5, lmax, 2, 2, w, x, axes, R, seed=w + lmax)
+    half = w // 2
+    outs = eq.eqtp_qk_norm(s.q[0], s.k[0], lmax, 2, **s.how())
+    back = lambda q, g, how: eq.eqtp_qk_norm_backward(q, s.k[0], g, s.gk[0], lmax, 2, need_pos=axes > 0, **how)
+    clean = back(s.q[0], s.gq[0], s.how())
+    for c in (R, half - 1, half + R, w - 1):  # (the first and the last of those not turned, of either half)
+        # an infinite weight: its channel of all nodes and heads, and nothing else
+        how = dict(s.how(), weight_q=s.wq[0].clone())
+        how["weight_q"][lmax, c] = float("inf")
+        got = eq.eqtp_qk_norm(s.q[0], s.k[0], lmax, 2, **how)
+        spoilt = torch.zeros_like(got[0], dtype=torch.bool).reshape(6, 2, w, -1)
+        spoilt[:, :, c, lmax * lmax:] = True
+        spoilt = spoilt.reshape(got[0].shape)
+        assert torch.equal(got[0][~spoilt], outs[0][~spoilt]) and torch.equal(got[1], outs[1])
+        assert not torch.isfinite(got[0][spoilt]).any()
+        # a channel's gradient of infinity: the gradients of its own node's head and degree, and of its own weight
+        g = s.gq[0].clone()
+        g[2, w + c, lmax * lmax] = float("inf")
+        grads = back(s.q[0], g, s.how())
+        spoilt = torch.zeros_like(g, dtype=torch.bool)
+        spoilt[2, w:, lmax * lmax:] = True
+        assert torch.equal(grads[0][~spoilt], clean[0][~spoilt]) and not torch.isfinite(grads[0][spoilt]).any()
+        spoilt = torch.zeros_like(grads[2], dtype=torch.bool)
+        spoilt[lmax, c] = True
+        assert torch.equal(grads[2][~spoilt], clean[2][~spoilt]) and not torch.isfinite(grads[2][spoilt]).any()
+        for i in (1, 3, 4, 5):
+            assert (grads[i] is None and clean[i] is None) or torch.equal(grads[i], clean[i])
+        # an infinite feature: NaN there, zeros in the rest of its degree (the norm is infinite)
+        q = s.q[0].clone()
+        q[2, w + c, lmax * lmax] = float("inf")
+        got = eq.eqtp_qk_norm(q, s.k[0], lmax, 2, **s.how())[0]
+        assert torch.isnan(got[2, w + c, lmax * lmax])
+        rest = got[2, w:, lmax * lmax:].clone()
+        rest[c, 0] = 0.0
+        assert (rest == 0).all()
+        keep = torch.ones_like(got, dtype=torch.bool)
+        keep[2, w:, lmax * lmax:] = False
+        assert torch.equal(got[keep], outs[0][keep])
