@@ -867,7 +867,7 @@ typedef struct eqtp_expert_desc {
  *   grad_W      [X, lmax+1, C, C] fp32, summed over slots in a fixed order
  *               (needs slots and ptr; zeros for experts without places).  With
  *               bf16 operands weight * grad_out enters in two bf16 parts: 2^-16
- *               of a term at most is lost (and an infinite h gives NaN).
+ *               of a term at most is lost.
  *   grad_out    [N, C, K] (x_dtype).
  *   workspace   eqtp_expert_linear_backward_workspace_bytes(d, N) bytes,
  *               16-byte aligned.

@@ -16,7 +16,11 @@
 // 68 us (410 MB, 6.1 TB/s, half of it found in the L2s) and 7.
 // fp32: the products' operands are fp32.  bf16: a gate's product with the
 // gradient is held in two bf16 parts, both multiplied: 2^-16 of a term at most
-// is lost.  Chunks go to lines of part, which a second kernel adds in a fixed
+// is lost.  Where an infinity meets them (inf - inf is the second part of an
+// infinite product, and the two parts of one may have different signs) a sum
+// comes out as NaN: the wave then goes over its places again, carefully, and
+// what is still NaN is one by the formula.
+// Chunks go to lines of part, which a second kernel adds in a fixed
 // order: no atomics, the same bits from call to call.
 #include <type_traits>
 
@@ -83,6 +87,7 @@ struct Comps<float, GATES> {
       }
     }
   }
+  template <bool CAREFUL>
   __device__ __forceinline__ void gate(float w, bool live) {
 #pragma unroll
     for (int q = 0; q < 16; ++q) x[q] = live ? (GATES ? x[q] * w : x[q]) : 0.0f;
@@ -92,12 +97,18 @@ struct Comps<float, GATES> {
     for (int q = 0; q < 16; ++q) x[q] = live ? x[q] : 0.0f;
   }
   // acc += this (rows) times b (columns) over components first .. first + n - 1 (constants once unrolled)
+  template <bool CAREFUL>
   __device__ __forceinline__ void add(const Comps& b, int first, int n, f4& acc) const {
 #pragma unroll
     for (int q = 0; q < 16; ++q)
       if (q >= first && q < first + n) acc = __builtin_amdgcn_mfma_f32_16x16x4f32(x[q], b.x[q], acc, 0, 0, 0);
   }
 };
+
+// where a pair of bf16 is infinite or NaN: the halves' bits set
+__device__ __forceinline__ uint32_t not_finite(uint32_t v) {
+  return ((v & 0x7f80u) == 0x7f80u ? 0xffffu : 0u) | ((v & 0x7f800000u) == 0x7f800000u ? 0xffff0000u : 0u);
+}
 
 template <bool GATES>
 struct Comps<__bf16, GATES> {
@@ -121,16 +132,22 @@ struct Comps<__bf16, GATES> {
       }
     }
   }
+  // CAREFUL: an infinite product has no second part, and a finite one beyond bf16's largest a finite first one
+  template <bool CAREFUL>
   __device__ __forceinline__ void gate(float w, bool live) {
 #pragma unroll
     for (int q = 0; q < 8; ++q) {
       if constexpr (GATES) {
         const float a = w * __uint_as_float(x[q] << 16), b = w * __uint_as_float(x[q] & 0xffff0000u);
         typedef __bf16 b2 __attribute__((ext_vector_type(2)));
-        const uint32_t hi = __builtin_bit_cast(uint32_t, b2{(__bf16)a, (__bf16)b});
+        uint32_t hi = __builtin_bit_cast(uint32_t, b2{(__bf16)a, (__bf16)b});
+        if constexpr (CAREFUL)
+          hi -= (fabsf(a) < __builtin_inff() && (hi & 0x7fffu) == 0x7f80u ? 1u : 0u) +
+                (fabsf(b) < __builtin_inff() && (hi & 0x7fff0000u) == 0x7f800000u ? 0x10000u : 0u);
         const float ra = a - __uint_as_float(hi << 16), rb = b - __uint_as_float(hi & 0xffff0000u);
         x[q] = live ? hi : 0u;
         lo[q] = live ? __builtin_bit_cast(uint32_t, b2{(__bf16)ra, (__bf16)rb}) : 0u;
+        if constexpr (CAREFUL) lo[q] &= ~not_finite(hi);
       } else {
         x[q] = live ? x[q] : 0u;
       }
@@ -151,12 +168,18 @@ struct Comps<__bf16, GATES> {
     }
     return __builtin_bit_cast(bf16x8, uint4{o[0], o[1], o[2], o[3]});
   }
+  // CAREFUL: an infinity of b meets the first parts only
+  template <bool CAREFUL>
   __device__ __forceinline__ void add(const Comps& b, int first, int n, f4& acc) const {
 #pragma unroll
     for (int at = first / 2; 2 * at < first + n; at += 4) {
       const bf16x8 bv = part(b.x, at, first, n);
       acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(part(x, at, first, n), bv, acc, 0, 0, 0);
-      if constexpr (GATES) acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(part(lo, at, first, n), bv, acc, 0, 0, 0);
+      if constexpr (GATES) {
+        uint4 t = __builtin_bit_cast(uint4, bv);
+        if constexpr (CAREFUL) t = {t.x & ~not_finite(t.x), t.y & ~not_finite(t.y), t.z & ~not_finite(t.z), t.w & ~not_finite(t.w)};
+        acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(part(lo, at, first, n), __builtin_bit_cast(bf16x8, t), acc, 0, 0, 0);
+      }
     }
   }
 };
@@ -179,52 +202,68 @@ __device__ __forceinline__ void expert_grad_walk(const ExpertGradArgs& a, const 
   const int K = num_comp(a.lmax), lane = threadIdx.x & 63, wv = threadIdx.x >> 6, i16 = lane & 15, kq = lane >> 4;
   const int rt = split / (Cfg::CT / CTC) * RT, cc = split % (Cfg::CT / CTC) * CTC;
   f4 acc[LN][RT][CTC];
-#pragma unroll
-  for (int l = 0; l < LN; ++l)
-#pragma unroll
-    for (int r = 0; r < RT; ++r)
-#pragma unroll
-      for (int t = 0; t < CTC; ++t) acc[l][r][t] = f4{0.f, 0.f, 0.f, 0.f};
   const int last = (int)min(a.N * a.k, (int64_t)0x7fffffff);
-  for (int64_t s0 = ch.s0; s0 < ch.s1; s0 += 64) {
-    // 64 places, one a lane: node and gate; the waves take turns with the fours of them
-    const int64_t mine = min(s0 + lane, ch.s1 - 1);
-    const int slot = clamp_index(a.slots[mine], last);
-    const int my_node = slot / a.k;
-    const float my_gate = GATES ? a.weight[slot] : 1.0f;
-    const int steps = (int)min((int64_t)16, (ch.s1 - s0 + 3) / 4);
-    for (int st = wv; st < steps; st += kGradWaves) {
-      const int from = 4 * st + kq;
-      const int64_t node = __shfl(my_node, from, 64);
-      const float w = __shfl(my_gate, from, 64);
-      const bool live = s0 + from < ch.s1;
-      Comps<S, GATES> g[RT], h[CTC];
-      const int64_t base = node * C * K + L0 * L0;
+  auto walk = [&](auto careful) {
+    constexpr bool CAREFUL = careful;
 #pragma unroll
-      for (int r = 0; r < RT; ++r) {
-        const int c = (rt + r) * 16 + i16;
-        g[r].load(static_cast<const S*>(a.gout) + base + (c < C ? c : 0) * K, NPL);
+    for (int l = 0; l < LN; ++l)
+#pragma unroll
+      for (int r = 0; r < RT; ++r)
+#pragma unroll
+        for (int t = 0; t < CTC; ++t) acc[l][r][t] = f4{0.f, 0.f, 0.f, 0.f};
+    for (int64_t s0 = ch.s0; s0 < ch.s1; s0 += 64) {
+      // 64 places, one a lane: node and gate; the waves take turns with the fours of them
+      const int64_t mine = min(s0 + lane, ch.s1 - 1);
+      const int slot = clamp_index(a.slots[mine], last);
+      const int my_node = slot / a.k;
+      const float my_gate = GATES ? a.weight[slot] : 1.0f;
+      const int steps = (int)min((int64_t)16, (ch.s1 - s0 + 3) / 4);
+      for (int st = wv; st < steps; st += kGradWaves) {
+        const int from = 4 * st + kq;
+        const int64_t node = __shfl(my_node, from, 64);
+        const float w = __shfl(my_gate, from, 64);
+        const bool live = s0 + from < ch.s1;
+        Comps<S, GATES> g[RT], h[CTC];
+        const int64_t base = node * C * K + L0 * L0;
+#pragma unroll
+        for (int r = 0; r < RT; ++r) {
+          const int c = (rt + r) * 16 + i16;
+          g[r].load(static_cast<const S*>(a.gout) + base + (c < C ? c : 0) * K, NPL);
+        }
+#pragma unroll
+        for (int t = 0; t < CTC; ++t) {
+          const int c = (cc + t) * 16 + i16;
+          h[t].load(static_cast<const S*>(a.h) + base + (c < C ? c : 0) * K, NPL);
+        }
+#pragma unroll
+        for (int r = 0; r < RT; ++r) g[r].template gate<CAREFUL>(w, live);
+        if (s0 + 4 * st + 4 > ch.s1)  // places past the chunk read its last one's rows: an infinity of h times 0 is none of it
+#pragma unroll
+          for (int t = 0; t < CTC; ++t) h[t].clear(live);
+#pragma unroll
+        for (int l = 0; l < LN; ++l)
+#pragma unroll
+          for (int r = 0; r < RT; ++r)
+#pragma unroll
+            for (int t = 0; t < CTC; ++t) {
+              if constexpr (LMAX <= 3) g[r].template add<CAREFUL>(h[t], l * l, 2 * l + 1, acc[l][r][t]);
+              else g[r].template add<CAREFUL>(h[t], 0, NPL, acc[l][r][t]);
+            }
       }
-#pragma unroll
-      for (int t = 0; t < CTC; ++t) {
-        const int c = (cc + t) * 16 + i16;
-        h[t].load(static_cast<const S*>(a.h) + base + (c < C ? c : 0) * K, NPL);
-      }
-#pragma unroll
-      for (int r = 0; r < RT; ++r) g[r].gate(w, live);
-      if (s0 + 4 * st + 4 > ch.s1)  // places past the chunk read its last one's rows: an infinity of h times 0 is none of it
-#pragma unroll
-        for (int t = 0; t < CTC; ++t) h[t].clear(live);
-#pragma unroll
-      for (int l = 0; l < LN; ++l)
-#pragma unroll
-        for (int r = 0; r < RT; ++r)
-#pragma unroll
-          for (int t = 0; t < CTC; ++t) {
-            if constexpr (LMAX <= 3) g[r].add(h[t], l * l, 2 * l + 1, acc[l][r][t]);
-            else g[r].add(h[t], 0, NPL, acc[l][r][t]);
-          }
     }
+  };
+  walk(std::false_type{});
+  if constexpr (GATES && std::is_same<S, __bf16>::value) {
+    bool nan = false;
+#pragma unroll
+    for (int l = 0; l < LN; ++l)
+#pragma unroll
+      for (int r = 0; r < RT; ++r)
+#pragma unroll
+        for (int t = 0; t < CTC; ++t)
+#pragma unroll
+          for (int v = 0; v < 4; ++v) nan |= acc[l][r][t][v] != acc[l][r][t][v];
+    if (__any(nan)) walk(std::true_type{});
   }
   // the waves' sums, one wave after the other (in order) into the first one's, a degree at a time
 #pragma unroll

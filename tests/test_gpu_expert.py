@@ -246,3 +246,61 @@ def test_both_types_of_the_output(N, C, lmax, k, x):
         wide, narrow = (eq.eqtp_expert_linear(m.h[0], m.W[0], m.ti, lmax, weight=m.w[0], plan=plan, out_dtype=t)
                         for t in (eq.EQTP_F32, eq.EQTP_BF16))
         assert torch.equal(wide.to(torch.bfloat16), narrow)
+
+
+@pytest.mark.parametrize("x", ["f32", "bf16"])
+@pytest.mark.parametrize("lmax", [0, 1, 3, 4])
+def test_infinities_under_gates(lmax, x):
+    """Infinite features and gradients under gates whose products with them fill more than one bf16: the weights'
+    gradients are infinite where they enter a sum, as those without gates are, and nowhere else; NaN stays NaN."""
+    import torch
+
+    eq = _eq()
+    _say("infinities under gates, lmax=%d %s" % (lmax, x))
+    dt = torch.bfloat16 if x == "bf16" else torch.float32
+    N, C, K = 9, 16, (lmax + 1) ** 2
+    for gate in (0.3, 1.0 / 3.0, 0.7, 0.5):
+        h, g = (torch.ones(N, C, K, dtype=dt, device="cuda") for _ in range(2))
+        W = torch.ones(2, lmax + 1, C, C, dtype=dt, device="cuda")
+        idx = torch.zeros(N, 1, dtype=torch.int32, device="cuda")
+        idx[6:] = 1
+        w = torch.full((N, 1), gate, device="cuda")
+        back = lambda: eq.eqtp_expert_linear_backward(h, W, idx, g, lmax, weight=w, need_h=False, need_weight=False)[1]
+        clean = back()
+        assert torch.isfinite(clean).all()
+        want = clean.clone()
+        h[4, 3, K - 1] = float("inf")
+        want[0, lmax, :, 3] = float("inf")
+        assert torch.equal(back(), want)
+        g[5, 7, K - 1] = -float("inf")
+        want[0, lmax, 7, :] = -float("inf")
+        got = back()
+        assert torch.isnan(got[0, lmax, 7, 3])  # inf - inf
+        got[0, lmax, 7, 3] = want[0, lmax, 7, 3] = 0.0
+        assert torch.equal(got, want)
+        h[4, 3, K - 1] = float("nan")
+        got = back()
+        assert torch.isnan(got[0, lmax, :, 3]).all()
+        got[0, lmax, :, 3] = want[0, lmax, :, 3] = 0.0
+        assert torch.equal(got, want)
+
+
+def test_products_beyond_the_largest_bf16():
+    """A gate's product with a gradient that fp32 holds and bf16 does not."""
+    import torch
+
+    eq = _eq()
+    _say("products beyond the largest bf16")
+    big = float(torch.finfo(torch.bfloat16).max)
+    N, C = 6, 16
+    h = torch.full((N, C, 1), 2.0 ** -40, dtype=torch.bfloat16, device="cuda")
+    g = torch.ones(N, C, 1, dtype=torch.bfloat16, device="cuda")
+    g[2, 5], g[4, 6] = big, -big
+    W = torch.ones(1, 1, C, C, dtype=torch.bfloat16, device="cuda")
+    idx = torch.zeros(N, 1, dtype=torch.int32, device="cuda")
+    w = torch.full((N, 1), 1.0035, device="cuda")
+    gW = eq.eqtp_expert_linear_backward(h, W, idx, g, 0, weight=w, need_h=False, need_weight=False)[1]
+    want = (w.double()[:, :, None] * g.double()).sum(0) @ h.double()[0].t()
+    assert float((w * big).max()) < float("inf")
+    # a term in two parts: 2^-16 of it; the other five are as nothing, or 1: six additions
+    assert ((gW[0, 0].double() - want).abs() <= (2.0 ** -16 + 8 * 2.0 ** -24) * want.abs()).all()
