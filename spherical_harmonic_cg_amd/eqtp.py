@@ -1028,6 +1028,8 @@ def eqtp_attention_backward(q, k, v, src, row_ptr, lse, grad_out, src_ptr, dst_s
 def _bias_desc(heads, buckets, r_cut):
     # read by the library during a call only, so one instance per distinct descriptor is shared
     d = _BiasDesc(ctypes.sizeof(_BiasDesc), heads, buckets, r_cut)
+    if r_cut != 0.0 and d.r_cut == 0.0:
+        raise ValueError("r_cut = %g is 0 in float32, which would mask nothing" % r_cut)
     need = load_library().eqtp_distance_bias_workspace_bytes(ctypes.byref(d), 0)  # checks the descriptor
     if need < 0:
         raise EqtpError(int(-need), "eqtp_bias_desc")

@@ -184,3 +184,13 @@ def test_binding_refusals():
         e.eqtp_expert_plan(i, 8)
     with pytest.raises(ValueError, match="on the GPU"):
         e.eqtp_expert_linear(x, torch.zeros(2, 2, 8, 8), i, 1)
+
+
+def test_r_cut_that_float32_has_not():
+    """A cut-off too short for float32 is refused: as 0 it would mask no edge where it has to mask all."""
+    e = _lib()
+    for r in (1e-50, -1e-50):
+        with pytest.raises(ValueError, match="float32"):
+            e._bias_desc(4, 8, r)
+    for r in (0.0, 1e-45, 5.0, 1e300):
+        e._bias_desc(4, 8, r)
