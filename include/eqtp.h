@@ -750,12 +750,17 @@ typedef struct eqtp_qk_norm_desc {
  *   theta[j] = sum_a pos[n, a] freq[a, j]                      (radians),
  *   out[j] = y[j] cos theta[j] - y[j + w/2] sin theta[j],
  *   out[j + w/2] = y[j] sin theta[j] + y[j + w/2] cos theta[j]  for j < pairs;
- * the other channels are y.  All components of a channel turn by one angle, so
- * the result turns with space as q and k do, and a logit between two nodes
- * depends on the difference of their positions.  In a periodic cell,
- * frequencies from its reciprocal lattice make it periodic; along a chain
- * (axes = 1) this is the usual rotation by place.  Angles are summed and
- * reduced in 64 bits (good to 1e-6 of a turn up to 10^9 turns).
+ * the other channels are y.  A logit between two nodes depends on the
+ * difference of their positions.  All components of a channel turn by one
+ * angle, so as long as the angles stay, the result turns with space as q and k
+ * do.  Positions in space (axes = 3) turn with it, and their angles stay only
+ * where freq is turned, too, as a cell's reciprocal lattice is with its cell
+ * (which also makes the angles periodic in the cell).  With a freq that stays as
+ * it is, logits and what follows from them depend on the orientation, and
+ * grad_pos_q and grad_pos_k carry a torque.  Along a chain (axes = 1), or by
+ * any coordinate that space does not turn, this is the usual rotation by place.
+ * Angles are summed and reduced in 64 bits (good to 1e-6 of a turn up to 10^9
+ * turns).
  *   q, out_q [N, C, K];  k, out_k [M, C kv_heads / heads, K] (x_dtype); an
  *   output may be its own input.  N or M may be 0.
  *   weight_q, weight_k [lmax+1, C / heads] fp32, shared by the heads, or NULL.

@@ -6,7 +6,8 @@
 //   out[j] = y[j] cos theta[j] - y[j + d/2] sin theta[j]        (j < R),
 //   out[j + d/2] = y[j] sin theta[j] + y[j + d/2] cos theta[j],
 // every component m of a channel by the same angle, so rotations of space
-// commute with it.  Backward, with u the gradient turned back and a = weight u:
+// commute with it where they leave the angles as they are (freq turned with
+// pos, or positions along something that space does not turn).  Backward, with u the gradient turned back and a = weight u:
 //   gx = r_l a - r_l^3 x mean_l(a x),  gweight[l, c] = sum u x r_l,
 //   gtheta[j] = sum_{heads, m} y[j] u[j + d/2] - y[j + d/2] u[j]
 // (the cross product of a pair is the same before and after the turn),

@@ -1141,8 +1141,9 @@ def eqtp_qk_norm(q, k, lmax: int, heads: int, weight_q=None, weight_k=None, pos_
 
     q [N, C, K], k [M, Ck, K] float32 or bfloat16 ([N, C] and [M, Ck] at lmax 0); Ck is a number of heads of q's
     width.  ``weight_q``, ``weight_k`` [lmax+1, C/heads] float32.  ``freq`` [axes, pairs] float32 with ``pos_q``
-    [N, axes] and ``pos_k`` [M, axes] (pos_q by default where M = N), or None: no rotation.  ``out_q`` and ``out_k``
-    may be q and k."""
+    [N, axes] and ``pos_k`` [M, axes] (pos_q by default where M = N), or None: no rotation.  Where space turns the
+    positions, ``freq`` has to be turned, too, or logits depend on the orientation.  ``out_q`` and ``out_k`` may be q
+    and k."""
     torch = _torch()
     d, N, M, pos_k = _qk_norm_args(q, k, lmax, heads, weight_q, weight_k, pos_q, pos_k, freq, eps)
     if out_q is None:

@@ -3,6 +3,7 @@ import numpy as np
 import pytest
 
 import mix_reference as ref
+from test_oracle_conv import _apply_D, _rotation, _wigner_blocks
 
 
 def _differences(f, x, g, eps=1e-6):
@@ -45,6 +46,29 @@ def test_head_norm_gradient(lmax, heads, w, axes):
         at = lambda t, p: ref.head_norm(t, heads, lmax, weight, p, freq)["out"]
         p, o, s = r.standard_normal((3, 1, axes))
         np.testing.assert_allclose((at(q, p) * at(k, o)).sum(), (at(q, p + s) * at(k, o + s)).sum(), rtol=1e-9)
+
+
+@pytest.mark.parametrize("lmax", [0, 1, 3])
+def test_head_norm_in_turned_space(lmax):
+    """With freq turned as the positions are, the result turns with space as the features do and gradients of positions
+    turn with the positions; with freq held fixed, logits depend on the orientation."""
+    r = np.random.default_rng(4)
+    heads, w, K = 2, 6, (lmax + 1) ** 2
+    Q = _rotation(lmax)
+    D = _wigner_blocks(Q, lmax)
+    x, g = r.standard_normal((2, 5, heads * w, K))
+    weight, freq, pos = 1 + 0.2 * r.standard_normal((lmax + 1, w)), r.standard_normal((3, 2)), r.standard_normal((5, 3))
+    at = lambda t, p, f: ref.head_norm(t, heads, lmax, weight, p, f)["out"].reshape(x.shape)  # noqa: E731
+    out, turned = at(x, pos, freq), at(_apply_D(D, x), pos @ Q.T, Q @ freq)
+    np.testing.assert_allclose(turned, _apply_D(D, out), atol=1e-12)
+    (gx, gw, gpos), _ = ref.head_norm_backward(x, g, heads, lmax, weight, pos, freq)
+    (tx, tw, tpos), _ = ref.head_norm_backward(_apply_D(D, x), _apply_D(D, g), heads, lmax, weight, pos @ Q.T, Q @ freq)
+    np.testing.assert_allclose(tx, _apply_D(D, gx), atol=1e-12)
+    np.testing.assert_allclose(tw, gw, atol=1e-12)
+    np.testing.assert_allclose(tpos, gpos @ Q.T, atol=1e-12)
+    logit = lambda y: (y[0] * y[1]).sum()  # noqa: E731
+    np.testing.assert_allclose(logit(turned), logit(out), atol=1e-11)
+    assert abs(logit(at(_apply_D(D, x), pos @ Q.T, freq)) - logit(out)) > 1e-3
 
 
 @pytest.mark.parametrize("sigmoid", [False, True])
