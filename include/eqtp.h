@@ -865,7 +865,9 @@ typedef struct eqtp_expert_desc {
  *          together is faster.
  *   out    [N, C, K] (out_dtype), fully overwritten.
  * h, W, out, grad_out, grad_h and grad_W are 16-byte aligned.  A node's sum
- * goes over its experts in a fixed order, in fp32, and is rounded once.
+ * goes over its experts in a fixed order, in fp32, and is rounded once.  The
+ * order, and that of a product's channels, is another one in calls of up to 512
+ * nodes, so a node's last bits may differ between a small call and a large one.
  * Backward, each output may be NULL, fully overwritten:
  *   grad_h      [N, C, K] (x_dtype) = sum_j weight W^T grad_out;
  *   grad_weight [N, top_k] fp32 = <grad_out, W h> (0 at places without an expert);

@@ -368,5 +368,6 @@ def route(logits, top_k: int, score: int = _eq.EQTP_SCORE_SOFTMAX, bias=None, gr
 
 def expert_linear(h, W, idx, lmax: int, weight=None, plan=None, out_dtype: int = None):
     """Differentiable per-degree linears by expert (see eqtp_expert_linear).  ``plan``: eqtp_expert_plan's result, which
-    serves every layer over the same routing, or None to make it in each backward pass."""
+    serves every layer over the same routing, or None to make it in each backward pass.  A float32 output of bfloat16
+    features has its gradient rounded to bfloat16 before it is used, and W's is rounded to W's type in the end."""
     return ExpertLinearFunction.apply(h, W, weight, idx, lmax, out_dtype, plan)
