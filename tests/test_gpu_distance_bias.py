@@ -78,3 +78,38 @@ def test_distance_bias_long_sums():
     # 1024 workgroups of 4 waves of 16 edges side by side: 8 additions a lane, and one rounding of a line and the result
     _within(got[1], g[1].sum(0), ref.u * 12 * np.abs(g[1]).sum(0), "grad_table")
     assert (got[[0, 2]] == 0).all()
+
+
+@pytest.mark.parametrize("B,H,one", [(512, 1, False), (512, 3, False), (512, 8, False), (512, 65, False), (512, 8, True),
+                                     (512, 65, True), (257, 1, True), (257, 3, False), (257, 65, False), (64, 8, False),
+                                     (64, 65, False), (64, 3, True), (2, 1, False), (2, 8, True)])
+def test_distance_bias_many_rounds(B, H, one):
+    """Every wave goes over many stretches of edges, all with gradients: the sums are those of all edges, in many buckets
+    or all in one, within bounds that count a lane's own additions."""
+    eq = _eq()
+    _say("distance bias, many rounds, B=%d H=%d one=%s" % (B, H, one))
+    import torch
+
+    # a lane's table has B + 1 places of 4 bytes in LDS, beside the bounds: 80 KB of them a workgroup, 160 KB a compute unit
+    waves = min(4, max(1, (80 << 10) // ((B + 1) * 256 + 8 * B)))
+    held = min(32 // waves, max(1, (160 << 10) // (waves * (B + 1) * 256 + 8 * B)))
+    blocks = min(2048, torch.cuda.get_device_properties(0).multi_processor_count * held)
+    rounds = 5
+    E = 64 * waves * blocks * (rounds - 1) + 12345  # some waves have a last round, one of them in part
+    r = np.random.default_rng(H + B)
+    bounds = np.sort(r.uniform(0.2, 5.0, B - 1)).astype(np.float32)
+    away = np.full(E, 0.01, np.float32) if one else r.uniform(0.0, 5.5, E).astype(np.float32)
+    vec = np.zeros((E, 3), dtype=np.float32)
+    vec[np.arange(E), r.integers(0, 3, E)] = away
+    g = _put(1.0 + r.standard_normal((E, H)))
+    got = _get(eq.eqtp_distance_bias_backward(_put(vec)[0], _put(bounds)[0], g[0], r_cut=5.25))
+    bucket = np.where(away < 5.25, np.searchsorted(bounds, away, side="right"), B)
+    rows = np.argsort(bucket, kind="stable")
+    upto = np.searchsorted(bucket[rows], np.arange(B + 1))
+    want, size = np.zeros((B, H)), np.zeros((B, H))
+    for b in range(B):
+        mine = g[1][rows[upto[b]:upto[b + 1]]]
+        want[b], size[b] = mine.sum(0), np.abs(mine).sum(0)
+    # a lane: one edge in 64 / heads places of each stretch; then a line's rounding, and the result's
+    adds = rounds * -(-64 // (64 // min(H, 64)))
+    _within(got, want, ref.u * (adds + 3) * size, "grad_table")

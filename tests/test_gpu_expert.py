@@ -304,3 +304,94 @@ def test_products_beyond_the_largest_bf16():
     assert float((w * big).max()) < float("inf")
     # a term in two parts: 2^-16 of it; the other five are as nothing, or 1: six additions
     assert ((gW[0, 0].double() - want).abs() <= (2.0 ** -16 + 8 * 2.0 ** -24) * want.abs()).all()
+
+
+def _far_reference(m):
+    """The statement of mix_reference, expert by expert: (out, grad_h, grad_W, grad_weight), the sums of their terms'
+    sizes, and each expert's places."""
+    h, W, g = m.h[1], m.W[1], m.g[1]
+    N, C, K = h.shape
+    w = np.ones(m.idx.shape) if m.w[1] is None else m.w[1]
+    vals = [np.zeros_like(h), np.zeros_like(h), np.zeros_like(W), np.zeros(m.idx.shape)]
+    sizes, places = [np.zeros_like(v) for v in vals], np.zeros(m.X)
+    for j in range(m.k):
+        for e in range(m.X):
+            n = np.nonzero(m.idx[:, j] == e)[0]
+            places[e] += len(n)
+            for l in range(m.lmax + 1):
+                s = slice(l * l, (l + 1) ** 2)
+                hl, gl, wl = h[n][:, :, s], g[n][:, :, s], w[n, j][:, None, None]
+                for v, f in ((vals, lambda t: t), (sizes, np.abs)):
+                    A, a, b, c = f(W[e, l]), f(hl), f(gl), f(wl)
+                    y = np.matmul(A, a)
+                    v[0][n, :, s] += c * y
+                    v[1][n, :, s] += c * np.matmul(A.T, b)
+                    v[2][e, l] += np.tensordot(c * b, a, axes=((0, 2), (0, 2)))
+                    v[3][n, j] += (b * y).sum((1, 2))
+    return vals, sizes, places
+
+
+def test_far_reference_is_the_statement():
+    m = Mix(7, 8, 2, 3, 2, seed=1)
+    vals, _, _ = _far_reference(m)
+    np.testing.assert_allclose(vals[0], ref.expert(m.h[1], m.W[1], m.idx, 2, m.w[1])[0], rtol=1e-12, atol=1e-13)
+    for a, b in zip(vals[1:], ref.expert_backward(m.h[1], m.W[1], m.idx, m.g[1], 2, m.w[1])[0]):
+        np.testing.assert_allclose(a, b, rtol=1e-12, atol=1e-13)
+
+
+@pytest.mark.parametrize("x", ["f32", "bf16"])
+@pytest.mark.parametrize("k,gates", [(1, False), (2, True)])
+@pytest.mark.parametrize("N,C,lmax", [(600, 128, 2), (530, 128, 3), (545, 128, 4), (521, 128, 5), (518, 128, 6), (600, 128, 1),
+                                      (533, 64, 4), (520, 64, 5), (517, 32, 6)])
+def test_expert_wide(N, C, lmax, k, gates, x):
+    """The widest rows in the tiles' forms: every degree at 128 channels."""
+    eq = _eq()
+    _say("experts, wide, N=%d C=%d lmax=%d k=%d %s" % (N, C, lmax, k, x))
+    m = Mix(N, C, lmax, 4, k, x, gates, seed=N + lmax)
+    vals, sizes, places = _far_reference(m)
+    K, u = (lmax + 1) ** 2, ref.u
+    half = ref.U16 if x == "bf16" else u
+    plan = eq.eqtp_expert_plan(m.ti, 4)
+    for p in (plan, None):
+        o = eq.eqtp_expert_linear(m.h[0], m.W[0], m.ti, lmax, weight=m.w[0], plan=p, out_dtype=eq.EQTP_F32)
+        _within(_get(o), vals[0], ref.expert_bound(vals[0], sizes[0], C, k, u), "out")
+    gh, gW, gw = m.grads(eq, plan)
+    # (the bounds of mix_reference.expert_backward)
+    _within(_get(gh), vals[1], ref.expert_bound(vals[1], sizes[1], C, k, half), "grad_h")
+    terms = places[:, None, None, None] * (2 * lmax + 1)
+    _within(_get(gW), vals[2], (2 * u * (terms + 4) + (ref.U16 ** 2 if x == "bf16" and gates else 0.0)) * sizes[2], "grad_W")
+    _within(_get(gw), vals[3], 2 * u * (C + 16 * K + 16) * sizes[3], "grad_weight")
+
+
+@pytest.mark.parametrize("x", ["f32", "bf16"])
+@pytest.mark.parametrize("N,C,lmax,k,gates", [(30, 64, 3, 2, True), (600, 64, 3, 1, False), (600, 64, 3, 2, True), (600, 32, 0, 1, False),
+                                              (530, 8, 2, 3, True), (520, 32, 4, 1, False), (520, 32, 5, 2, True),
+                                              (515, 128, 2, 2, True)])
+def test_a_node_that_is_not_finite(N, C, lmax, k, gates, x):
+    """NaN and infinities in a node's features and gradients stay in its own rows and in its experts' weight gradients."""
+    import torch
+
+    eq = _eq()
+    _say("a node that is not finite, N=%d C=%d lmax=%d k=%d %s" % (N, C, lmax, k, x))
+    m = Mix(N, C, lmax, 5, k, x, gates, seed=N + lmax + k)
+    bad = [3, N // 2, N - 1]
+    for i, n in enumerate(bad):
+        m.ti[n] = 2 if i < 2 else 3
+    plan = eq.eqtp_expert_plan(m.ti, 5)
+    h, g = m.h[0].clone(), m.g[0].clone()
+    for n, v in zip(bad, ("nan", "inf", "nan")):
+        h[n] = float(v)
+        g[n] = float(v)
+    keep = torch.ones(N, dtype=torch.bool, device="cuda")
+    keep[bad] = False
+    runs = []
+    for a, b in ((m.h[0], m.g[0]), (h, g)):
+        o = eq.eqtp_expert_linear(a, m.W[0], m.ti, lmax, weight=m.w[0], plan=plan)
+        runs.append((o,) + eq.eqtp_expert_linear_backward(a, m.W[0], m.ti, b, lmax, weight=m.w[0], plan=plan))
+    for i, (clean, spoilt) in enumerate(zip(*runs)):
+        if clean is None:
+            continue
+        if i == 2:  # the weights' gradient, by expert
+            assert torch.equal(clean[[0, 1, 4]], spoilt[[0, 1, 4]]) and not torch.isfinite(spoilt[[2, 3]]).any()
+        else:
+            assert torch.equal(clean[keep], spoilt[keep]) and not torch.isfinite(spoilt[bad]).any()

@@ -189,3 +189,43 @@ def test_qk_norm_channels_that_are_not_turned(lmax, w, axes, R, x):
         keep = torch.ones_like(got, dtype=torch.bool)
         keep[2, w:, lmax * lmax:] = False
         assert torch.equal(got[keep], outs[0][keep])
+
+
+def _group(w, K):
+    """(threads, nodes' heads of a workgroup) of the gradient's groups: a quad of half a head's row a thread."""
+    quads, per = ((w + 1) // 2 * K + 3) // 4, K // 4 if K % 4 == 0 else K
+    for T in (2, 4, 8, 16, 32, 64):
+        if T >= (8 if K > 1 else 2) and T >= per and (quads <= T // per * per or T == 64):
+            return T, 256 // T
+
+
+@pytest.mark.parametrize("N,M,lmax,heads,kv,w,axes,R", [
+    (40001, 20000, 0, 2, 1, 16, 1, 8), (4001, 1000, 3, 4, 2, 8, 3, 4), (9001, 4500, 2, 4, 4, 4, 0, 0),
+    # heads that are no divisor of a workgroup's groups, with gradients of positions: a group takes whole nodes, many of them
+    (30001, 9000, 0, 3, 3, 16, 1, 8), (20003, 20003, 1, 3, 1, 4, 3, 1), (8001, 3000, 3, 6, 3, 8, 3, 4),
+    (6007, 700, 0, 40, 40, 16, 2, 3), (2503, 2503, 2, 40, 10, 4, 3, 2)])
+def test_qk_norm_many_rows_of_a_group(N, M, lmax, heads, kv, w, axes, R):
+    """Many rounds of every group, whole nodes among them; the weights' gradients against bounds that count a thread's
+    own additions, so that a lost row would show."""
+    eq = _eq()
+    _say("qk norm, many rows of a group, N=%d heads=%d" % (N, heads))
+    import torch
+
+    s = Sides(N, M, lmax, heads, kv, w, "f32", axes, R, seed=N)
+    _, grads = s.check(eq)
+    cus = torch.cuda.get_device_properties(0).multi_processor_count
+    rounds = 256 // _group(w, (lmax + 1) ** 2)[0]
+    share = N * heads / (N * heads + M * kv)
+    for i, (x, g, rows, h, pos, part) in enumerate(((s.q[1], s.gq[1], N, heads, s.pq[1], share),
+                                                    (s.k[1], s.gk[1], M, kv, s.pk[1], 1.0 - share))):
+        p = ref.head_norm(x, h, lmax, None, pos, s.f[1])
+        g = g.reshape(p["x"].shape)
+        t, xhat = g * p["c"] - p["other"](g) * p["s"], p["x"] * p["r"]
+        size = (np.abs(g) + np.abs(p["other"](g))) * np.abs(xhat)
+        # workgroups: one a compute unit at least, in the ratio of the sides' elements; a head is one addition a place
+        groups = max(1, int(cus * part)) * rounds
+        adds = -(-rows * h // groups) + h
+        for l in range(lmax + 1):
+            m = slice(l * l, (l + 1) ** 2)
+            _within(_get(grads[2 + i])[l], (t * xhat)[..., m].sum(axis=(0, 1, 3)),
+                    ref.u * (30 + adds) * size[..., m].sum(axis=(0, 1, 3)), "grad_weight %d" % i)
