@@ -342,12 +342,11 @@ __global__ __launch_bounds__(512) void expert_kernel(ExpertArgs a) {
 
 // Runs from and to LDS, through which a workgroup moves its nodes' whole rows: a task a wave, tile after tile.  While a
 // tile is worked on, the next one's rows and lists are on their way into registers, and the order of the one after.
-template <class S, int C, int L, bool DOT>
+template <class S, int C, int L>
 __global__ __launch_bounds__(512, 2) void expert_staged_kernel(ExpertArgs a, int64_t tiles) {
   using Cfg = ExpertCfg<S, C, L>;
   constexpr int K = Cfg::K, NP = Cfg::NP, CTW = Cfg::CTW, waves = Cfg::WAVES, U = Cfg::U, row_in = Cfg::ROW;
   extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
-  __shared__ float dots[DOT ? waves : 1][kTile][kMaxTopK];
   __shared__ int nid[2][kTile];
   const int tid = threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int i16 = lane & 15, kq = lane >> 4;
@@ -386,37 +385,25 @@ __global__ __launch_bounds__(512, 2) void expert_staged_kernel(ExpertArgs a, int
       if (r < kTile) *reinterpret_cast<u32x4*>(lds + r * row_in + (i - r * Cfg::UNITS) * 16) = rows[j];
     }
     if (tid < kTile) nid[turn ^ 1][tid] = ahead;
-    if constexpr (DOT)
-      for (int i = lane; i < kTile * kMaxTopK; i += 64) (&dots[wv][0][0])[i] = 0.0f;
     __syncthreads();
     typename Cfg::B B;
-    typename Cfg::Held held;
+    const typename Cfg::Held held = {};  // (of the form with the gates' gradient)
     typename Cfg::Total total;
-    if constexpr (DOT) take_held<S, C, L>(static_cast<const S*>(a.dot_with) + (int64_t)nid[turn][i16] * (C * K) + m0, ct0, kq, held);
     take_operands<S, C, L, Cfg::ALIGNED>(reinterpret_cast<const S*>(lds + i16 * row_in) + m0, kq, B);
     const Listed now = list;
     ask_rows(tile + gridDim.x, nid[turn ^ 1]);
     ask_order(tile + 2 * gridDim.x);
-    multiply<S, C, L, DOT>(a, now, m0, g * NP - m0, ct0, i16, kq, B, held, total, dots[DOT ? wv : 0]);
+    multiply<S, C, L, false>(a, now, m0, 0, ct0, i16, kq, B, held, total, nullptr);
     __syncthreads();  // every wave has its operands: the place takes the results
-    if (a.out != nullptr) put_tiles<S, C, L, Cfg::ALIGNED>(a, lds + i16 * row_out, m0, ct0, kq, total);
+    put_tiles<S, C, L, Cfg::ALIGNED>(a, lds + i16 * row_out, m0, ct0, kq, total);
     __syncthreads();
-    if (a.out != nullptr) {
-      const int out_units = row_out / 16 - 1;
-      for (int r = wv; r < nv; r += waves) {
-        u32x4* to = reinterpret_cast<u32x4*>(static_cast<unsigned char*>(a.out) + (int64_t)nid[turn][r] * (row_out - 16));
-        const u32x4* from = reinterpret_cast<const u32x4*>(lds + r * row_out);
+    const int out_units = row_out / 16 - 1;
+    for (int r = wv; r < nv; r += waves) {
+      u32x4* to = reinterpret_cast<u32x4*>(static_cast<unsigned char*>(a.out) + (int64_t)nid[turn][r] * (row_out - 16));
+      const u32x4* from = reinterpret_cast<const u32x4*>(lds + r * row_out);
 #pragma unroll 4
-        for (int i = lane; i < out_units; i += 64) to[i] = from[i];
-      }
+      for (int i = lane; i < out_units; i += 64) to[i] = from[i];
     }
-    if constexpr (DOT)
-      for (int i = tid; i < nv * a.k; i += blockDim.x) {
-        const int r = i / a.k, j = i - r * a.k;
-        float v = 0.0f;
-        for (int w = 0; w < waves; ++w) v += dots[w][r][j];
-        a.gweight[(int64_t)nid[turn][r] * a.k + j] = v;
-      }
     __syncthreads();  // the next tile's rows come into the same place
   }
 }
@@ -672,19 +659,19 @@ static hipError_t expert_launch(const ExpertArgs& a) {
       expert_f32_kernel<C, L, DOT, false><<<grid, block, lds, part.stream>>>(part);
     });
   } else if constexpr (Cfg::STAGED && !DOT) {
-    const int bytes = kTile * (a.out && !a.out_bf16 ? staged_row(C, Cfg::K, 4) : Cfg::ROW);
+    const int bytes = kTile * (a.out_bf16 ? Cfg::ROW : staged_row(C, Cfg::K, 4));
     static std::atomic<int> known[2];  // workgroups that a compute unit holds
-    std::atomic<int>& held = known[a.out && !a.out_bf16];
+    std::atomic<int>& held = known[a.out_bf16];
     int n = held.load(std::memory_order_relaxed);
     if (n == 0) {
-      if (hipOccupancyMaxActiveBlocksPerMultiprocessor(&n, expert_staged_kernel<S, C, L, DOT>, 64 * Cfg::WAVES, bytes) != hipSuccess ||
+      if (hipOccupancyMaxActiveBlocksPerMultiprocessor(&n, expert_staged_kernel<S, C, L>, 64 * Cfg::WAVES, bytes) != hipSuccess ||
           n < 1)
         n = 1;
       held.store(n, std::memory_order_relaxed);
     }
     // as many workgroups as the card holds, all with the same number of tiles
     const int64_t most = (int64_t)num_cus() * n, each = (tiles + most - 1) / most;
-    expert_staged_kernel<S, C, L, DOT>
+    expert_staged_kernel<S, C, L>
         <<<dim3((unsigned)((tiles + each - 1) / each)), dim3(64 * Cfg::WAVES), bytes, a.stream>>>(a, tiles);
     return hipGetLastError();
   } else {
