@@ -236,7 +236,7 @@ struct ExpertArgs {
   const void* dot_with;   // backward: h, for the gates' gradient
   float* gweight;         // or nullptr
   float* part;            // few nodes, with gweight: expert_gate_floats floats
-  int64_t first;          // first place of a launch that takes a tile a workgroup
+  int64_t places;         // in the order (or rows) from a launch's first one on, where it takes a tile a workgroup
   hipStream_t stream;
 };
 int64_t expert_gate_floats(int64_t N, int C, int lmax, int k);

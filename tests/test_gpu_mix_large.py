@@ -117,11 +117,14 @@ def test_experts_of_many_nodes(x, k, gates):
         if gates:
             weight[at] = torch.rand(TAIL, k, device="cuda")
     cut = lambda t, at: None if t is None else t[at].contiguous()  # noqa: E731
-    out = eq.eqtp_expert_linear(h, W, idx, 0, weight=weight)
-    for at in far:
-        assert torch.equal(out[at], eq.eqtp_expert_linear(cut(h, at), W, cut(idx, at), 0, weight=cut(weight, at)))
-    gh, _, gw = eq.eqtp_expert_linear_backward(h, W, idx, out, 0, weight=weight, need_W=False)
-    for at in far:
-        a, _, b = eq.eqtp_expert_linear_backward(cut(h, at), W, cut(idx, at), cut(out, at), 0, weight=cut(weight, at), need_W=False)
-        assert torch.equal(gh[at], a)
-        assert not gates or torch.equal(gw[at], b)
+    back = torch.arange(N - 1, -1, -1, device="cuda", dtype=torch.int32)  # an order: the last node first
+    for plan in (None, (back, back, torch.zeros(X + 1, device="cuda", dtype=torch.int32))):
+        out = eq.eqtp_expert_linear(h, W, idx, 0, weight=weight, plan=plan)
+        for at in far:
+            assert torch.equal(out[at], eq.eqtp_expert_linear(cut(h, at), W, cut(idx, at), 0, weight=cut(weight, at)))
+        gh, _, gw = eq.eqtp_expert_linear_backward(h, W, idx, out, 0, weight=weight, plan=plan, need_W=False)
+        for at in far:
+            a, _, b = eq.eqtp_expert_linear_backward(cut(h, at), W, cut(idx, at), cut(out, at), 0, weight=cut(weight, at), need_W=False)
+            assert torch.equal(gh[at], a)
+            assert not gates or torch.equal(gw[at], b)
+        del out, gh, gw
