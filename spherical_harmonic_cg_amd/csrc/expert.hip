@@ -539,9 +539,12 @@ __device__ __forceinline__ bool multiply_steps(const ExpertArgs& a, const Listed
   return ONE && several;
 }
 
-// (ONE: registers for two workgroups of eight waves a compute unit where the LDS holds two, 38 us; with eight registers
-// more and one workgroup 42: 10k nodes of 64 x 16)
-constexpr int f32_waves(int C, int L, bool one) { return one && 2 * kTile * staged_row(C, num_comp(L), 4) <= (160 << 10) ? 4 : 2; }
+// (ONE: registers for two workgroups of eight waves a compute unit where the LDS holds two, 37 us; with eight registers
+// more and one workgroup 42: 10k nodes of 64 x 16.  With 128 channels a wave has twice the products, which half of the
+// registers do not hold: 10k nodes at lmax 1 and 2, 48 and 176 us against 39 and 95.)
+constexpr int f32_waves(int C, int L, bool one) {
+  return one && C < 128 && 2 * kTile * staged_row(C, num_comp(L), 4) <= (160 << 10) ? 4 : 2;
+}
 
 template <int C, int L, bool DOT, bool ONE>
 __global__ __launch_bounds__(512, f32_waves(C, L, ONE)) void expert_f32_kernel(ExpertArgs a) {
@@ -782,9 +785,12 @@ __global__ __launch_bounds__(256) void expert_few_gates_kernel(int64_t places, i
   gweight[i] = v;
 }
 
-// Up to 512 nodes (us, fp32, 8 experts, 2 of a node, against the tiles: 64 channels at lmax 3, 256 nodes 10 / 38, 512 nodes
-// 15 / 28, 1024 nodes 28 / 28; 128 channels at lmax 0, 512 nodes 12 / 15, 1024 nodes 21 / 15; bf16, 128 channels at lmax
-// 3, 512 nodes 38 / 37).
+// Up to 512 nodes.  Forward, us, against the tiles: fp32, two experts of a node: 64 channels at lmax 3, 128, 256 and 512
+// nodes 6 / 33, 9 / 29 and 16 / 25 (1024 nodes 28 / 28); 128 channels at lmax 6, 512 nodes 194 / 1052, at lmax 0 12 / 12.
+// bf16: 64 channels at lmax 3, one expert 4 / 8, 5 / 8 and 8 / 8, two 6 / 13, 7 / 12 and 12 / 11.  The gradients of h
+// and gates are as near.  A node's work here grows with its experts, and the tiles' hardly: from 8 of them on the tiles
+// would be faster (fp32, 64 channels at lmax 3, 256 and 512 nodes 27 / 43 and 53 / 44; bf16 19 / 15 and 40 / 16; bf16, 128
+// channels at lmax 0, 32 nodes 22 / 10).
 static bool expert_few(int64_t N) { return N <= 512; }
 // The other way round the weights are read an element at a time (us, gradients of 128 channels at lmax 3: 32 nodes 27, with
 // the transposed copy 20; one node 17, 20).
