@@ -873,8 +873,7 @@ typedef struct eqtp_expert_desc {
  *   grad_weight [N, top_k] fp32 = <grad_out, W h> (0 at places without an expert);
  *   grad_W      [X, lmax+1, C, C] fp32, summed over slots in a fixed order
  *               (needs slots and ptr; zeros for experts without places).  With
- *               bf16 operands weight * grad_out enters in two bf16 parts: 2^-16
- *               of a term at most is lost.
+ *               bf16 operands weight * grad_out keeps fp32's 24 bits.
  *   grad_out    [N, C, K] (x_dtype).
  *   workspace   eqtp_expert_linear_backward_workspace_bytes(d, N) bytes,
  *               16-byte aligned.

@@ -15,11 +15,12 @@
 // us (3.1 TB/s) and 6 for the lines' sums; 100k nodes x 32 x 16 bf16, 2 of 8,
 // 68 us (410 MB, 6.1 TB/s, half of it found in the L2s) and 7.
 // fp32: the products' operands are fp32.  bf16: a gate's product with the
-// gradient is held in two bf16 parts, both multiplied: 2^-16 of a term at most
-// is lost.  Where an infinity meets them (inf - inf is the second part of an
-// infinite product, and the two parts of one may have different signs) a sum
-// comes out as NaN: the wave then goes over its places again, carefully, and
-// what is still NaN is one by the formula.
+// gradient is held in three bf16 parts, all multiplied, so it keeps its 24 bits
+// (two parts would lose 2^-18 of a term, as much as a sum of few terms in all;
+// they took 69 us, three 70 to 71).  Where an infinity meets them (inf - inf is
+// the second part of an infinite product, and an infinity times a part that is 0
+// is NaN) a sum comes out as NaN: the wave then goes over its places again,
+// carefully, and what is still NaN is one by the formula.
 // Chunks go to lines of part, which a second kernel adds in a fixed
 // order: no atomics, the same bits from call to call.
 #include <type_traits>
@@ -112,7 +113,8 @@ __device__ __forceinline__ uint32_t not_finite(uint32_t v) {
 
 template <bool GATES>
 struct Comps<__bf16, GATES> {
-  uint32_t x[8], lo[GATES ? 8 : 1];  // pairs of components; what the first part of a product leaves
+  // pairs of components; what the first part of a product leaves, in two parts
+  uint32_t x[8], lo[GATES ? 8 : 1], lo2[GATES ? 8 : 1];
   __device__ __forceinline__ void load(const __bf16* p, int np) {
     const uint16_t* h = reinterpret_cast<const uint16_t*>(p);
 #pragma unroll
@@ -132,22 +134,25 @@ struct Comps<__bf16, GATES> {
       }
     }
   }
-  // CAREFUL: an infinite product has no second part, and a finite one beyond bf16's largest a finite first one
+  // The 24 bits of a product in three parts of 8, cut, not rounded: nothing is lost, and a finite one has finite parts.
+  // CAREFUL: an infinite one has a first part only.  (Parts of places past the chunk are cleared where there are any:
+  // 70 us, in every step 73; in fp32 and without gates that is slower, 33 us instead of 26.)
   template <bool CAREFUL>
   __device__ __forceinline__ void gate(float w, bool live) {
+    auto high = [](float a) { return __uint_as_float(__float_as_uint(a) & 0xffff0000u); };
+    auto pair = [](float a, float b) { return __builtin_amdgcn_perm(__float_as_uint(b), __float_as_uint(a), 0x07060302u); };
 #pragma unroll
     for (int q = 0; q < 8; ++q) {
       if constexpr (GATES) {
         const float a = w * __uint_as_float(x[q] << 16), b = w * __uint_as_float(x[q] & 0xffff0000u);
-        typedef __bf16 b2 __attribute__((ext_vector_type(2)));
-        uint32_t hi = __builtin_bit_cast(uint32_t, b2{(__bf16)a, (__bf16)b});
-        if constexpr (CAREFUL)
-          hi -= (fabsf(a) < __builtin_inff() && (hi & 0x7fffu) == 0x7f80u ? 1u : 0u) +
-                (fabsf(b) < __builtin_inff() && (hi & 0x7fff0000u) == 0x7f800000u ? 0x10000u : 0u);
-        const float ra = a - __uint_as_float(hi << 16), rb = b - __uint_as_float(hi & 0xffff0000u);
-        x[q] = live ? hi : 0u;
-        lo[q] = live ? __builtin_bit_cast(uint32_t, b2{(__bf16)ra, (__bf16)rb}) : 0u;
-        if constexpr (CAREFUL) lo[q] &= ~not_finite(hi);
+        const float a1 = a - high(a), b1 = b - high(b), a2 = a1 - high(a1), b2 = b1 - high(b1);
+        x[q] = pair(a, b);
+        lo[q] = pair(a1, b1);
+        lo2[q] = pair(a2, b2);
+        if constexpr (CAREFUL) {
+          lo[q] &= ~not_finite(x[q]);
+          lo2[q] &= ~not_finite(x[q]);
+        }
       } else {
         x[q] = live ? x[q] : 0u;
       }
@@ -155,30 +160,44 @@ struct Comps<__bf16, GATES> {
   }
   __device__ __forceinline__ void clear(bool live) {
 #pragma unroll
-    for (int q = 0; q < 8; ++q) x[q] = live ? x[q] : 0u;
-  }
-  // the words that hold components first .. first + n - 1, eight components from word `at` on, others cleared
-  static __device__ __forceinline__ bf16x8 part(const uint32_t (&v)[8], int at, int first, int n) {
-    uint32_t o[4];
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const int m = 2 * (at + q);
-      const uint32_t keep = (m >= first && m < first + n ? 0xffffu : 0u) | (m + 1 >= first && m + 1 < first + n ? 0xffff0000u : 0u);
-      o[q] = at + q < 8 ? v[(at + q) & 7] & keep : 0u;
+    for (int q = 0; q < 8; ++q) {
+      x[q] = live ? x[q] : 0u;
+      if constexpr (GATES) {
+        lo[q] = live ? lo[q] : 0u;
+        lo2[q] = live ? lo2[q] : 0u;
+      }
     }
-    return __builtin_bit_cast(bf16x8, uint4{o[0], o[1], o[2], o[3]});
   }
-  // CAREFUL: an infinity of b meets the first parts only
+  // word `at` of v, its components outside first .. first + n - 1 cleared
+  static __device__ __forceinline__ uint32_t word(const uint32_t (&v)[8], int at, int first, int n) {
+    const int m = 2 * at;
+    return v[at] & ((m >= first && m < first + n ? 0xffffu : 0u) | (m + 1 >= first && m + 1 < first + n ? 0xffff0000u : 0u));
+  }
+  // Four words of components are one product's operand; where a degree has one or two, its parts stand beside each other
+  // in them.  CAREFUL: an infinity of b meets the first parts only.
   template <bool CAREFUL>
   __device__ __forceinline__ void add(const Comps& b, int first, int n, f4& acc) const {
+    constexpr int PARTS = GATES ? 3 : 1;
+    const int end = (first + n + 1) / 2;
 #pragma unroll
-    for (int at = first / 2; 2 * at < first + n; at += 4) {
-      const bf16x8 bv = part(b.x, at, first, n);
-      acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(part(x, at, first, n), bv, acc, 0, 0, 0);
-      if constexpr (GATES) {
-        uint4 t = __builtin_bit_cast(uint4, bv);
-        if constexpr (CAREFUL) t = {t.x & ~not_finite(t.x), t.y & ~not_finite(t.y), t.z & ~not_finite(t.z), t.w & ~not_finite(t.w)};
-        acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(part(lo, at, first, n), __builtin_bit_cast(bf16x8, t), acc, 0, 0, 0);
+    for (int at = first / 2; at < end; at += 4) {
+      const int words = end - at < 4 ? end - at : 4, beside = 4 / words;
+#pragma unroll
+      for (int p0 = 0; p0 < PARTS; p0 += beside) {
+        uint32_t u[4], v[4];
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+          const int p = p0 + s / words, w = at + s % words;
+          const bool is = s < beside * words && p < PARTS;
+          u[s] = v[s] = 0u;
+          if (!is) continue;
+          if constexpr (GATES) u[s] = p == 0 ? word(x, w, first, n) : (p == 1 ? word(lo, w, first, n) : word(lo2, w, first, n));
+          else u[s] = word(x, w, first, n);
+          v[s] = word(b.x, w, first, n);
+          if (CAREFUL && p > 0) v[s] &= ~not_finite(v[s]);
+        }
+        acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, uint4{u[0], u[1], u[2], u[3]}),
+                                                      __builtin_bit_cast(bf16x8, uint4{v[0], v[1], v[2], v[3]}), acc, 0, 0, 0);
       }
     }
   }
@@ -237,9 +256,13 @@ __device__ __forceinline__ void expert_grad_walk(const ExpertGradArgs& a, const 
         }
 #pragma unroll
         for (int r = 0; r < RT; ++r) g[r].template gate<CAREFUL>(w, live);
-        if (s0 + 4 * st + 4 > ch.s1)  // places past the chunk read its last one's rows: an infinity of h times 0 is none of it
+        if (s0 + 4 * st + 4 > ch.s1) {  // places past the chunk read its last one's rows: none of it, infinities neither
+          if constexpr (GATES && !std::is_same<S, float>::value)
+#pragma unroll
+            for (int r = 0; r < RT; ++r) g[r].clear(live);
 #pragma unroll
           for (int t = 0; t < CTC; ++t) h[t].clear(live);
+        }
 #pragma unroll
         for (int l = 0; l < LN; ++l)
 #pragma unroll

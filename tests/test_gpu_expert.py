@@ -306,6 +306,25 @@ def test_products_beyond_the_largest_bf16():
     assert ((gW[0, 0].double() - want).abs() <= (2.0 ** -16 + 8 * 2.0 ** -24) * want.abs()).all()
 
 
+@pytest.mark.parametrize("N,C,lmax", [(1, 64, 3), (3, 32, 0), (2, 16, 6), (1, 128, 1), (2, 64, 2), (1, 8, 4), (2, 32, 5)])
+def test_gated_gradients_keep_fp32(N, C, lmax):
+    """Few terms, so that what a term loses shows: a gate's product with a bf16 gradient keeps its 24 bits.  Each enters as
+    three products, so a sum has three additions a term, which may cut (two half steps), and the gate's product is rounded."""
+    eq = _eq()
+    _say("gated gradients keep fp32, N=%d C=%d lmax=%d" % (N, C, lmax))
+    m = Mix(N, C, lmax, 2, 2, "bf16", True, seed=C + lmax, holes=False)
+    m.idx[:] = [0, 1]
+    m.ti.copy_(m.ti.new_tensor(m.idx))
+    gW = _get(m.grads(eq, eq.eqtp_expert_plan(m.ti, 2))[1])
+    for e in range(2):
+        for l in range(lmax + 1):
+            s = slice(l * l, (l + 1) ** 2)
+            t = m.w[1][:, e, None, None] * m.g[1][:, :, s]
+            want = np.tensordot(t, m.h[1][:, :, s], axes=((0, 2), (0, 2)))
+            size = np.tensordot(np.abs(t), np.abs(m.h[1][:, :, s]), axes=((0, 2), (0, 2)))
+            _within(gW[e, l], want, ref.u * (6 * N * (2 * l + 1) + 3) * size, "grad_W")
+
+
 def _far_reference(m):
     """The statement of mix_reference, expert by expert: (out, grad_h, grad_W, grad_weight), the sums of their terms'
     sizes, and each expert's places."""
