@@ -9,8 +9,10 @@
 // Both passes read 12 bytes an edge and write or read 4 H.  Forward: 5.24M edges
 // x 8 heads, 64 buckets, 41 us, 5.7 TB/s, a copy's rate; 266k x 4, 33 buckets
 // 4.6 us; 20k x 4 3.4 us, a launch.
-// Backward: the same cases 88 us (2.6 TB/s: vector ALUs and LDS) and 12 us, and
-// 4 to 5 us for the lines' sums.
+// Backward: the same cases 88 to 93 us (2.6 TB/s: vector ALUs and LDS) and 12 us,
+// and 4 to 5 us for the lines' sums.  A lane adds its own edges of a bucket in
+// fp32 (E / (64 waves) of them and a few times as many with many heads), all that
+// follows is in 64 bits.
 #include "eqtp_device.hpp"
 #include "eqtp_kernels.hpp"
 

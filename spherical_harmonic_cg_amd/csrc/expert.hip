@@ -22,17 +22,21 @@
 // Four forms:
 //   few nodes (up to 512): a thread an output, on the vector ALUs;
 //   fp32 rows that fit (expert_f32_kernel): rows go through LDS, operands are
-//     read 16 channels at a time.  10k nodes x 64 x 16, one of 10 experts: 38 to
-//     41 us, 34 TFLOP/s (bytes 15 us, products 9): 626 tiles on 512 workgroups
+//     read 16 channels at a time.  10k nodes x 64 x 16, one of 10 experts: 37 to
+//     41 us, 35 TFLOP/s (bytes 15 us, products 9): 626 tiles on 512 workgroups
 //     at a time, and LDS reads between a wave's products;
 //   bf16 rows that fit, without the gates' gradient (expert_staged_kernel): rows
-//     through LDS, tiles one after the other.  100k nodes x 32 x 16, 2 of 8: 59
-//     us, 3.5 TB/s, where the direct form took 71;
+//     through LDS, tiles one after the other.  100k nodes x 32 x 16, 2 of 8: 57
+//     to 59 us, 3.6 TB/s, where the direct form took 71;
 //   the rest (expert_kernel: rows that do not fit, lmax 4 and above, and bf16
 //     with the gates' gradient): runs from and to memory, no barriers.  The
-//     gradients of h and of the gates of that case: 96 us, 3.2 TB/s; with the
+//     gradients of h and of the gates of that case: 94 us, 3.3 TB/s; with the
 //     gradient's rows through LDS a tile ahead 113, with both tensors' rows
 //     through LDS, a tile a workgroup, 115.
+// At 128 channels above lmax 0 a wave's operands, weights and sums are more than
+// its registers in most forms: 10k nodes, two of 8, forward and gradients of h
+// and gates, fp32 at lmax 3 and 4 210 + 270 and 1220 + 1690 us, bf16 100 + 220 and
+// 260 + 520.
 #include <atomic>
 #include <type_traits>
 

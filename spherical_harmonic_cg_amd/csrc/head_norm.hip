@@ -15,11 +15,11 @@
 //
 // Each element is read and written once; what a long row takes is the cache's
 // and HBM's time, a short one its fixed work.  Forward: 10k nodes x 64 channels
-// x 16, q and k, 33 us (5.0 TB/s); 100k x (32 + 16) x 16 bf16 72 us (4.2 TB/s);
-// 100k rows of 128 + 32 bf16 26 us (2.4 TB/s: a thread's sixteen elements carry
-// a norm and eight angles).  Backward, with the weights' gradients: the first 71
-// us (3.5 TB/s, vector ALUs some 40 of them), the last 51; 5 us for the lines'
-// sums.
+// x 16, q and k, 33 us (5.0 TB/s); 100k x (32 + 16) x 16 bf16 70 us (4.4 TB/s);
+// 100k rows of 128 + 32 bf16 22 us (2.9 TB/s: a thread's sixteen elements carry
+// a norm and eight angles), of fp32 40 us.  Backward, with the weights'
+// gradients: the first 74 us (3.3 TB/s, vector ALUs some 40 of them), the second
+// 185, the rows 51 (fp32 60); 5 us for the lines' sums.
 //
 // A group of T threads
 // holds a head's row in registers as pairs: quad i of the row's first half
